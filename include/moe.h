@@ -398,6 +398,38 @@ int moe_forward_threshold(const moe_config *cfg, const void *x, const float *Wg,
                           moe_stream_t stream);
 
 /*
+ * The flat layer for a few tokens (T <= MOE_FEW_MAX_TOKENS), such as one
+ * decoding step of as many sequences: one cooperative launch instead of
+ * moe_forward's chain, bound by reading the weights of the experts in use
+ * once. Arguments, outputs and definition are moe_forward's without the
+ * balancing losses, which belong to training: the same gate, capacity,
+ * token-order slots (pos, keep) and output, with the expert terms summed in
+ * fp32 (moe_forward rounds them to bf16 where it may), so the two agree to
+ * rounding, not bit for bit. A larger T returns MOE_ERR_UNSUPPORTED (use
+ * moe_forward). ws holds moe_few_workspace_size bytes and needs no
+ * initialisation; the status word at its start is cleared first. The launch
+ * takes every SM while it runs; calls on other streams wait for one another.
+ */
+#define MOE_FEW_MAX_TOKENS 64
+int moe_few_workspace_size(const moe_config *cfg, size_t *bytes);
+int moe_forward_few(const moe_config *cfg, const void *x, const float *Wg, const float *Wnoise,
+                    const float *noise, const float *logit_bias, const void *W1, const void *b1,
+                    const void *W2, const void *b2, void *y, int32_t *expert_idx, float *gate,
+                    int32_t *pos, uint8_t *keep, void *ws, moe_stream_t stream);
+
+/*
+ * The threshold mask for a few tokens: moe_forward_threshold's arguments,
+ * outputs and definition (picks P_i > T_i in expert order, at most k of them,
+ * gates renormalised, no capacity), run as moe_forward_few runs, with the same
+ * bound on T and a workspace of moe_few_workspace_size bytes.
+ */
+int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float *Wg,
+                              const float *logit_bias, const float *thresholds, const void *W1,
+                              const void *b1, const void *W2, const void *b2, void *y,
+                              int32_t *expert_idx, float *gate, uint32_t *mask_out, void *ws,
+                              moe_stream_t stream);
+
+/*
  * Backward of the flat layer ("Outrageously Large Neural Networks", section
  * 3.4, "Training the gating network": plain back-propagation, gradients reach
  * W_g through the selected softmax gates and W_noise through the smooth load

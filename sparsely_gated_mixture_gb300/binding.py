@@ -30,7 +30,8 @@ EXPORTS = ("moe_status_string", "moe_capacity", "moe_workspace_size", "moe_gate"
            "moe_backward_workspace_size", "moe_backward", "moe_gate_backward",
            "moe_noalloc_last_status", "moe_eval_normal_cdf", "moe_threshold_workspace_size",
            "moe_forward_threshold", "moe_expert_counts", "moe_dispatch_ranked",
-           "moe_aux_totals", "moe_aux_from_totals")
+           "moe_aux_totals", "moe_aux_from_totals", "moe_few_workspace_size",
+           "moe_forward_few", "moe_forward_threshold_few")
 
 
 class MoEError(RuntimeError):
@@ -115,6 +116,9 @@ def lib():
             F = ctypes.c_float
             L.moe_backward.argtypes = [CP] + [P] * 12 + [F, F, F] + [P] * 12
             L.moe_gate_backward.argtypes = [CP] + [P] * 7 + [F, F] + [P] * 7
+            L.moe_few_workspace_size.argtypes = [CP, ctypes.POINTER(ctypes.c_size_t)]
+            L.moe_forward_few.argtypes = [CP] + [P] * 16
+            L.moe_forward_threshold_few.argtypes = [CP] + [P] * 14
             for name in EXPORTS[1:]:
                 getattr(L, name).restype = I
             _lib = L
@@ -304,6 +308,35 @@ def moe_forward_threshold(cfg, x, Wg, logit_bias, thresholds, W1, b1, W2, b2, y,
                                        _p(expert_idx), _p(gate), _p(mask_out), _p(ws),
                                        _stream(stream)),
            "moe_forward_threshold")
+
+
+FEW_MAX_TOKENS = 64
+
+
+def moe_few_workspace_size(cfg) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_few_workspace_size")
+    return n.value
+
+
+def moe_forward_few(cfg, x, Wg, Wnoise, noise, logit_bias, W1, b1, W2, b2, y, ws,
+                    expert_idx=None, gate=None, pos=None, keep=None, stream=None):
+    """The flat layer for up to FEW_MAX_TOKENS tokens, in one launch."""
+    _check(lib().moe_forward_few(ctypes.byref(cfg), _p(x), _p(Wg), _p(Wnoise), _p(noise),
+                                 _p(logit_bias), _p(W1), _p(b1), _p(W2), _p(b2), _p(y),
+                                 _p(expert_idx), _p(gate), _p(pos), _p(keep), _p(ws),
+                                 _stream(stream)), "moe_forward_few")
+
+
+def moe_forward_threshold_few(cfg, x, Wg, logit_bias, thresholds, W1, b1, W2, b2, y, ws,
+                              expert_idx=None, gate=None, mask_out=None, stream=None):
+    """The threshold-mask layer for up to FEW_MAX_TOKENS tokens, in one launch."""
+    _check(lib().moe_forward_threshold_few(ctypes.byref(cfg), _p(x), _p(Wg), _p(logit_bias),
+                                           _p(thresholds), _p(W1), _p(b1), _p(W2), _p(b2), _p(y),
+                                           _p(expert_idx), _p(gate), _p(mask_out), _p(ws),
+                                           _stream(stream)),
+           "moe_forward_threshold_few")
 
 
 def moe_expert_counts(cfg, expert_idx, expert_count, ws, stream=None):

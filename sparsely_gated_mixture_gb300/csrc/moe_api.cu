@@ -311,6 +311,13 @@ static moe_config thr_layer(const moe_config &c) {
   return r;
 }
 
+// ----------------------------------------------------------------------------- few tokens
+static int check_few(const moe_config *c) {
+  const int r = check_cfg(c);
+  if (r != MOE_OK) return r;
+  return c->T <= MOE_FEW_MAX_TOKENS ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+
 // ----------------------------------------------------------------------------- backward
 struct BwdLayout {
   size_t poff, dY, dU, dP, dX, dgpart, dg, coef, dc, dz, dxr, rpart, bpart, cpart, total;
@@ -897,6 +904,47 @@ int moe_forward_threshold(const moe_config *cfg, const void *x, const float *Wg,
   // 3. Slots (token order, no capacity), gather, expert GEMMs, combine.
   return expert_path(c, L, ws, x, idx, g, ws_at<int32_t>(ws, L.pos), ws_at<uint8_t>(ws, L.keep),
                      W1, b1, W2, b2, y, st, s, true);
+}
+
+int moe_few_workspace_size(const moe_config *cfg, size_t *bytes) {
+  const int r = check_few(cfg);
+  if (r != MOE_OK) return r;
+  if (!bytes) return MOE_ERR_ARG;
+  *bytes = few_layout(*cfg).total;
+  return MOE_OK;
+}
+
+int moe_forward_few(const moe_config *cfg, const void *x, const float *Wg, const float *Wnoise,
+                    const float *noise, const float *logit_bias, const void *W1, const void *b1,
+                    const void *W2, const void *b2, void *y, int32_t *expert_idx, float *gate,
+                    int32_t *pos, uint8_t *keep, void *ws, moe_stream_t stream) {
+  const int r = check_few(cfg);
+  if (r != MOE_OK) return r;
+  MOE_REQ(x); MOE_REQ(Wg); MOE_OPT(Wnoise); MOE_OPT(noise); MOE_OPT(logit_bias);
+  MOE_REQ(W1); MOE_OPT(b1); MOE_REQ(W2); MOE_OPT(b2); MOE_REQ(y);
+  MOE_OPT(expert_idx); MOE_OPT(gate); MOE_OPT(pos); MOE_OPT(keep);
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
+  if ((Wnoise == nullptr) != (noise == nullptr)) return MOE_ERR_ARG;
+  const FewCall q{*cfg, host_capacity(*cfg), x, Wg, Wnoise, noise, logit_bias, nullptr, W1, b1,
+                  W2, b2, y, expert_idx, gate, pos, keep, nullptr, ws};
+  MOE_CUDA(launch_few(q, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float *Wg,
+                              const float *logit_bias, const float *thresholds, const void *W1,
+                              const void *b1, const void *W2, const void *b2, void *y,
+                              int32_t *expert_idx, float *gate, uint32_t *mask_out, void *ws,
+                              moe_stream_t stream) {
+  const int r = check_few(cfg);
+  if (r != MOE_OK) return r;
+  MOE_REQ(x); MOE_REQ(Wg); MOE_OPT(logit_bias); MOE_REQ(thresholds); MOE_REQ(W1); MOE_OPT(b1);
+  MOE_REQ(W2); MOE_OPT(b2); MOE_REQ(y); MOE_OPT(expert_idx); MOE_OPT(gate); MOE_OPT(mask_out);
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
+  const FewCall q{*cfg, cfg->T, x, Wg, nullptr, nullptr, logit_bias, thresholds, W1, b1, W2, b2,
+                  y, expert_idx, gate, nullptr, nullptr, mask_out, ws};
+  MOE_CUDA(launch_few(q, (cudaStream_t)stream));
+  return MOE_OK;
 }
 
 int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes) {

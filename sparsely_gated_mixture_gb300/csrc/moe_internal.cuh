@@ -246,6 +246,29 @@ cudaError_t launch_ffn_tc(const moe_config &cfg, int C, const void *xbuf, const 
                           bool z_bf16, DeviceStatus *st,
                           cudaStream_t s);  // z_bf16: Z in bf16 (else fp32)
 
+// ----------------------------------------------------------------------------- few tokens
+// k_few.cu: the whole layer for T <= 64 tokens in one cooperative launch.
+// thr: the threshold mask's [E] thresholds (null: the flat layer's gate).
+struct FewLayout {
+  size_t status, flags, idx, gate, rpart, hpart, zpart, h, total;
+};
+FewLayout few_layout(const moe_config &cfg);
+struct FewCall {
+  moe_config cfg;
+  int capacity;
+  const void *x;
+  const float *Wg, *Wn, *noise, *bias, *thr;
+  const void *W1, *b1, *W2, *b2;
+  void *y;
+  int32_t *idx;
+  float *gate;
+  int32_t *pos;
+  uint8_t *keep;
+  uint32_t *mask;
+  void *ws;
+};
+cudaError_t launch_few(const FewCall &q, cudaStream_t s);
+
 // ----------------------------------------------------------------------------- backward
 // Padded row blocks of the backward's row buffers: each expert's rows start at
 // poff[e] and take max(64, roundup(rows, 64)) rows, pad rows zero.
