@@ -491,6 +491,68 @@ int moe_gate_backward(const moe_config *cfg, const void *x, const float *Wg, con
                       moe_stream_t stream);
 
 /*
+ * Activation checkpoints in 8 bits. What the backward needs of a forward and
+ * cannot rebuild cheaply is the experts' hidden rows H [rows, d_ff]; the
+ * router's logits, the slots and the gathered x rows follow from x and the
+ * choices at a few percent of the step. So a stack of layers shares one
+ * workspace: after each moe_forward the layer's H goes into a checkpoint of
+ * about half its bf16 bytes, the layer keeps x, expert_idx and gate, and
+ * moe_backward_checkpoint rebuilds the rest.
+ *
+ * Format.  h8 [rows, d_ff]: e4m3 (bias 7, no infinities) bytes; hscale [rows,
+ *   ceil(d_ff/32)]: one byte e + 127 per 32 columns of a row; the value is
+ *   e4m3(h8) * 2^e. e is the smallest exponent, at least -124, with 448 * 2^e
+ *   >= the block's largest value; values round to nearest, ties to even, but
+ *   one over zero is never stored as zero (the ReLU's pattern survives, and
+ *   with it every gradient that uses only the pattern). Values <= 0 are
+ *   stored as 0. A block holding an Inf or NaN gets hscale 255, loads as NaN
+ *   and is recorded as MOE_ERR_NONFINITE (detail = the value's flat index).
+ *   Loading is exact in bf16 and fp32.
+ * rows = min(T*k, E*C) at most (moe_checkpoint_size, which also gives the two
+ *   arrays' bytes); rows past expert_offset[E] are neither read nor written.
+ *
+ * moe_checkpoint_save: H -> h8, hscale. hbuf [T*k, d_ff] and expert_offset
+ *   [E+1] as moe_expert_ffn and moe_dispatch wrote them, or both NULL for
+ *   those that the last moe_forward left in ws.
+ * moe_checkpoint_load: h8, hscale -> hbuf (act_dtype); both NULL: into ws,
+ *   under the offsets there.
+ * With hbuf and expert_offset given, only the status word of ws is used
+ * (256 bytes suffice); it is not cleared.
+ */
+int moe_checkpoint_size(const moe_config *cfg, int64_t *rows, size_t *h8_bytes,
+                        size_t *hscale_bytes);
+int moe_checkpoint_save(const moe_config *cfg, const void *hbuf, const int32_t *expert_offset,
+                        uint8_t *h8, uint8_t *hscale, void *ws, moe_stream_t stream);
+int moe_checkpoint_load(const moe_config *cfg, const uint8_t *h8, const uint8_t *hscale,
+                        const int32_t *expert_offset, void *hbuf, void *ws,
+                        moe_stream_t stream);
+
+/*
+ * moe_backward from a checkpoint: the same gradients of the same L, with the
+ * hidden rows' stored values in place of the rows (dW2 and dgate see them;
+ * dW1, db1, db2 and the experts' share of dx are those of the unrounded rows).
+ * Inputs as moe_forward had them (x, Wg, Wnoise, noise, logit_bias and the
+ * unchanged weights W1, W2, b2), its outputs expert_idx and gate [T,k] (both
+ * required: the choices and slots are theirs; only the logits around them are
+ * recomputed, with moe_gate's kernels) and the checkpoint. cfg->capacity_factor
+ * and min_capacity are the forward's. ws (moe_workspace_size) is scratch here:
+ * it need not hold that forward, nor be initialised, and its status word is
+ * cleared first. dW1, db1, dW2 and db2 are in act_dtype (bf16 layers: fp32
+ * sums rounded once, half moe_backward's gradient bytes); dx act_dtype; dWg,
+ * dWnoise, dlogit_bias, dgate fp32; db1, db2, dlogit_bias and dgate may be
+ * NULL. An expert_idx outside [0, E) is recorded as MOE_ERR_BOUNDS. bws as for
+ * moe_backward.
+ */
+int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *Wg,
+                            const float *Wnoise, const float *noise, const float *logit_bias,
+                            const void *W1, const void *W2, const void *b2,
+                            const int32_t *expert_idx, const float *gate, const uint8_t *h8,
+                            const uint8_t *hscale, const void *dy, float w_importance,
+                            float w_load, float w_aux, void *dx, float *dWg, float *dWnoise,
+                            float *dlogit_bias, void *dW1, void *db1, void *dW2, void *db2,
+                            float *dgate, void *ws, void *bws, moe_stream_t stream);
+
+/*
  * Diagnostic: out[i] = Phi(u[i]) for i < n, the standard normal CDF exactly as
  * the balancing kernels evaluate it inside the load estimator P(x, i) =
  * Phi((c_i - kth_excluding(H, k, i)) / sigma_i) ("Outrageously Large", Eq. 9),

@@ -31,7 +31,8 @@ EXPORTS = ("moe_status_string", "moe_capacity", "moe_workspace_size", "moe_gate"
            "moe_noalloc_last_status", "moe_eval_normal_cdf", "moe_threshold_workspace_size",
            "moe_forward_threshold", "moe_expert_counts", "moe_dispatch_ranked",
            "moe_aux_totals", "moe_aux_from_totals", "moe_few_workspace_size",
-           "moe_forward_few", "moe_forward_threshold_few")
+           "moe_forward_few", "moe_forward_threshold_few", "moe_checkpoint_size",
+           "moe_checkpoint_save", "moe_checkpoint_load", "moe_backward_checkpoint")
 
 
 class MoEError(RuntimeError):
@@ -119,6 +120,12 @@ def lib():
             L.moe_few_workspace_size.argtypes = [CP, ctypes.POINTER(ctypes.c_size_t)]
             L.moe_forward_few.argtypes = [CP] + [P] * 16
             L.moe_forward_threshold_few.argtypes = [CP] + [P] * 14
+            L.moe_checkpoint_size.argtypes = [CP, ctypes.POINTER(ctypes.c_int64),
+                                              ctypes.POINTER(ctypes.c_size_t),
+                                              ctypes.POINTER(ctypes.c_size_t)]
+            L.moe_checkpoint_save.argtypes = [CP] + [P] * 6
+            L.moe_checkpoint_load.argtypes = [CP] + [P] * 6
+            L.moe_backward_checkpoint.argtypes = [CP] + [P] * 13 + [F, F, F] + [P] * 12
             for name in EXPORTS[1:]:
                 getattr(L, name).restype = I
             _lib = L
@@ -257,6 +264,39 @@ def moe_gate_backward(cfg, x, Wg, Wnoise, noise, expert_idx, gate, dgate, w_load
                                    float(w_aux), _p(dWg), _p(dWnoise), _p(dlogit_bias),
                                    _p(dx_gate), _p(ws), _p(bws), _stream(stream)),
            "moe_gate_backward")
+
+
+def moe_checkpoint_size(cfg):
+    """(rows, bytes of h8, bytes of hscale) of a checkpoint, at most."""
+    rows, h8, hs = ctypes.c_int64(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_checkpoint_size(ctypes.byref(cfg), ctypes.byref(rows), ctypes.byref(h8),
+                                     ctypes.byref(hs)), "moe_checkpoint_size")
+    return rows.value, h8.value, hs.value
+
+
+def moe_checkpoint_save(cfg, hbuf, expert_offset, h8, hscale, ws, stream=None):
+    """Hidden rows to 8 bits (hbuf and expert_offset None: the copies in ws)."""
+    _check(lib().moe_checkpoint_save(ctypes.byref(cfg), _p(hbuf), _p(expert_offset), _p(h8),
+                                     _p(hscale), _p(ws), _stream(stream)), "moe_checkpoint_save")
+
+
+def moe_checkpoint_load(cfg, h8, hscale, expert_offset, hbuf, ws, stream=None):
+    """Hidden rows from 8 bits (expert_offset and hbuf None: those in ws)."""
+    _check(lib().moe_checkpoint_load(ctypes.byref(cfg), _p(h8), _p(hscale), _p(expert_offset),
+                                     _p(hbuf), _p(ws), _stream(stream)), "moe_checkpoint_load")
+
+
+def moe_backward_checkpoint(cfg, x, Wg, Wnoise, noise, logit_bias, W1, W2, b2, expert_idx, gate,
+                            h8, hscale, dy, w_importance, w_load, w_aux, dx, dWg, dWnoise,
+                            dlogit_bias, dW1, db1, dW2, db2, dgate, ws, bws, stream=None):
+    """moe_backward from x, the choices and a checkpoint; weight gradients in
+    the layer's type."""
+    _check(lib().moe_backward_checkpoint(
+        ctypes.byref(cfg), _p(x), _p(Wg), _p(Wnoise), _p(noise), _p(logit_bias), _p(W1), _p(W2),
+        _p(b2), _p(expert_idx), _p(gate), _p(h8), _p(hscale), _p(dy), float(w_importance),
+        float(w_load), float(w_aux), _p(dx), _p(dWg), _p(dWnoise), _p(dlogit_bias), _p(dW1),
+        _p(db1), _p(dW2), _p(db2), _p(dgate), _p(ws), _p(bws), _stream(stream)),
+        "moe_backward_checkpoint")
 
 
 NOALLOC_SCRATCH_BYTES = 4 << 20

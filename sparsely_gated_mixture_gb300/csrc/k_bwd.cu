@@ -634,15 +634,19 @@ k_bwd_colsum(int E, int cols, int chunks, const int32_t *__restrict__ offset,
   pdl_trigger();
 }
 
+__device__ __forceinline__ void store_f(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_f(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <typename O>
 __global__ void k_bwd_colsum_reduce(int E, int cols, int chunks, const float *__restrict__ part,
-                                    float *__restrict__ out) {
+                                    O *__restrict__ out) {
   pdl_wait();
   const long long n = (long long)E * cols;
   for (long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x; u < n;
        u += (long long)gridDim.x * blockDim.x) {
     float s = 0.f;
     for (int q = 0; q < chunks; ++q) s += part[(size_t)q * n + u];
-    out[u] = s;
+    store_f(out + u, s);
   }
   pdl_trigger();
 }
@@ -800,7 +804,8 @@ cudaError_t launch_bwd_router(const moe_config &c, bool noisy, const void *x, co
 
 cudaError_t launch_bwd_colsum(const moe_config &c, int cols, int chunks, const int32_t *offset,
                               const int32_t *poff, const float *row_gate, const void *src,
-                              bool src_f32, float *part, float *out, cudaStream_t s) {
+                              bool src_f32, float *part, void *out, bool out_bf16,
+                              cudaStream_t s) {
   const dim3 g((cols + 255) / 256, c.E, chunks);
   cudaError_t err =
       src_f32 ? launch_pdl(k_bwd_colsum<float>, g, 256, 0, s, c.E, cols, chunks, offset, poff,
@@ -808,8 +813,12 @@ cudaError_t launch_bwd_colsum(const moe_config &c, int cols, int chunks, const i
               : launch_pdl(k_bwd_colsum<__nv_bfloat16>, g, 256, 0, s, c.E, cols, chunks, offset,
                            poff, row_gate, static_cast<const __nv_bfloat16 *>(src), part);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_bwd_colsum_reduce, grid_for((long long)c.E * cols, 256), 256, 0, s, c.E,
-                    cols, chunks, (const float *)part, out);
+  const int rg = grid_for((long long)c.E * cols, 256);
+  if (out_bf16)
+    return launch_pdl(k_bwd_colsum_reduce<__nv_bfloat16>, rg, 256, 0, s, c.E, cols, chunks,
+                      (const float *)part, static_cast<__nv_bfloat16 *>(out));
+  return launch_pdl(k_bwd_colsum_reduce<float>, rg, 256, 0, s, c.E, cols, chunks,
+                    (const float *)part, static_cast<float *>(out));
 }
 
 // Launched in plain stream order (no programmatic dependent launch): it

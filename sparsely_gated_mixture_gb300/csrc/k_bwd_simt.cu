@@ -167,11 +167,12 @@ k_bs_dgrad(int K, int N, int E, const int32_t *__restrict__ offset,
 }
 
 // out[e][m][n] = sum over the expert's real rows r of A[offset[e] + r][m] *
-// B[poff[e] + r][n]; A: the forward's packed rows (T), B: padded rows (fp32).
-template <typename T>
+// B[poff[e] + r][n]; A: the forward's packed rows (T), B: padded rows (fp32);
+// out in O (fp32, or the layer's bf16).
+template <typename T, typename O>
 __global__ void __launch_bounds__(kThreads)
 k_bs_wgrad(int M, int N, const int32_t *__restrict__ offset, const int32_t *__restrict__ poff,
-           const T *__restrict__ A, const float *__restrict__ B, float *__restrict__ out,
+           const T *__restrict__ A, const float *__restrict__ B, O *__restrict__ out,
            DeviceStatus *st) {
   pdl_wait();
   __shared__ float As[TK][TM + 4];
@@ -217,7 +218,7 @@ k_bs_wgrad(int M, int N, const int32_t *__restrict__ offset, const int32_t *__re
       const int n = n0 + tn + j;
       if (n >= N) continue;
       bad |= !isfinite(acc[i][j]);
-      out[((size_t)e * M + m) * N + n] = acc[i][j];
+      out[((size_t)e * M + m) * N + n] = st_val<O>(acc[i][j]);
     }
   }
   if (bad) record_error(st, MOE_ERR_NONFINITE, (long long)e);
@@ -304,7 +305,7 @@ cudaError_t launch_bwd_simt_front(const moe_config &c, const BwdSimt &p, cudaStr
                                  : run_simt_bwd<float>(c, p, s);
 }
 
-template <typename T>
+template <typename T, typename O>
 static cudaError_t simt_back(const moe_config &c, const BwdSimt &p, cudaStream_t s) {
   const int rblk = (int)((p.P_max + TM - 1) / TM);
   const dim3 g1((c.d + TN - 1) / TN, rblk);
@@ -314,16 +315,20 @@ static cudaError_t simt_back(const moe_config &c, const BwdSimt &p, cudaStream_t
                                  (float *)nullptr, p.st);
   if (err != cudaSuccess) return err;
   const dim3 g2((c.d + TN - 1) / TN, (c.d_ff + TM - 1) / TM, c.E);
-  err = launch_pdl_c(kPdlGemm, k_bs_wgrad<T>, g2, kThreads, 0, s, c.d_ff, c.d, p.offset, p.poff,
-                     static_cast<const T *>(p.hbuf), (const float *)p.dU, p.dW2, p.st);
+  err = launch_pdl_c(kPdlGemm, k_bs_wgrad<T, O>, g2, kThreads, 0, s, c.d_ff, c.d, p.offset,
+                     p.poff, static_cast<const T *>(p.hbuf), (const float *)p.dU,
+                     static_cast<O *>(p.dW2), p.st);
   if (err != cudaSuccess) return err;
   const dim3 g3((c.d_ff + TN - 1) / TN, (c.d + TM - 1) / TM, c.E);
-  return launch_pdl_c(kPdlGemm, k_bs_wgrad<T>, g3, kThreads, 0, s, c.d, c.d_ff, p.offset,
-                      p.poff, static_cast<const T *>(p.xbuf), (const float *)p.dP, p.dW1, p.st);
+  return launch_pdl_c(kPdlGemm, k_bs_wgrad<T, O>, g3, kThreads, 0, s, c.d, c.d_ff, p.offset,
+                      p.poff, static_cast<const T *>(p.xbuf), (const float *)p.dP,
+                      static_cast<O *>(p.dW1), p.st);
 }
 
 cudaError_t launch_bwd_simt_back(const moe_config &c, const BwdSimt &p, cudaStream_t s) {
-  return c.act_dtype == MOE_BF16 ? simt_back<__nv_bfloat16>(c, p, s) : simt_back<float>(c, p, s);
+  if (c.act_dtype != MOE_BF16) return simt_back<float, float>(c, p, s);
+  return p.dw_bf16 ? simt_back<__nv_bfloat16, __nv_bfloat16>(c, p, s)
+                   : simt_back<__nv_bfloat16, float>(c, p, s);
 }
 
 cudaError_t launch_bwd_simt_dg(const moe_config &c, const BwdSimt &p, float *dg, cudaStream_t s) {

@@ -59,7 +59,7 @@ struct BParams {
   const float *row_gate;  // mode 0: [packed rows]
   const __nv_bfloat16 *hbuf;  // mode 0: [packed rows, N]
   void *out;      // mode 0: bf16 [padded rows, N]; mode 1: fp32 [padded rows, N];
-                  // mode 2: fp32 [E, M, N]
+                  // mode 2: fp32 (or bf16) [E, M, N]
   float *dgpart;  // mode 0: [padded rows, n_blocks]
   DeviceStatus *st;
   unsigned long long wait_ns;
@@ -146,6 +146,15 @@ __device__ __forceinline__ BTile locate(const BParams &p, const int *start, int 
   return t;
 }
 
+// 32 fp32 sums of a weight gradient, rounded once to bf16.
+__device__ __forceinline__ void pack_bf16(const float (&f)[32], uint32_t (&packed)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+    packed[j] = *reinterpret_cast<uint32_t *>(&b);
+  }
+}
+
 // One lane's row m of a finished tile: 32 accumulator columns at a time from
 // TMEM (lane_addr: this warp's lanes, this accumulator), stored as the mode
 // asks. Warp-collective (every lane loads). Modes 0 and 1 in the CTA-pair
@@ -153,7 +162,7 @@ __device__ __forceinline__ BTile locate(const BParams &p, const int *start, int 
 // rows, N]) and cnt: the warp's 32 rows, inside the expert's padded block
 // (its size is a multiple of 64), then leave by TMA store, mode 1's pad rows
 // included (zero, as dpre's pad rows are).
-template <int MODE>
+template <int MODE, bool OB = false>
 __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, int m,
                                               uint32_t lane_addr, float *stg = nullptr,
                                               const CUtensorMap *tmO = nullptr,
@@ -230,6 +239,15 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
       if (tma) {
         stage_store_f32(tmO, stg + (*cnt & 1u) * 1024, f, n, t.prow0 + m0);
         ++*cnt;
+      } else if constexpr (OB) {
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                             ((size_t)t.e * p.M + m) * p.N + n);
+        uint32_t packed[16];
+        pack_bf16(f, packed);
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          o[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
+                            packed[4 * w + 3]);
       } else {
         float *o = MODE == 1
                        ? static_cast<float *>(p.out) + pr * p.N + n
@@ -245,7 +263,8 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
   if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)(MODE == 2 ? m : (long long)pr));
 }
 
-template <int MODE>
+// OB (mode 2): the weight gradient in bf16.
+template <int MODE, bool OB = false>
 __global__ void __launch_bounds__(kThreads, 1)
 k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
          const BParams p) {
@@ -405,8 +424,8 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
       if (!ready) break;
       tc_fence_after();
       const int m = t.mb * BM + r_in_tile;
-      epilogue_rows<MODE>(p, t, m, tmem_base + ((uint32_t)(quad * 32) << 16) +
-                                       (uint32_t)(buf * BN));
+      epilogue_rows<MODE, OB>(p, t, m, tmem_base + ((uint32_t)(quad * 32) << 16) +
+                                           (uint32_t)(buf * BN));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
@@ -503,6 +522,8 @@ __device__ __forceinline__ BTile locate_pair(const BParams &p, const int *start,
 // here each store writes whole 128-byte row segments, and the fp32 output
 // (4 bytes per product of a K = rows-per-expert reduction) no longer holds
 // the tensor pipe back. cnt counts this warp's staged chunks (buffer parity).
+// OB: the tile in bf16 (64-byte rows, 64-byte swizzle), rounded once here.
+template <bool OB>
 __device__ __forceinline__ void epilogue_wgrad_tma(const BParams &p, const BTile &t, int m0,
                                                    uint32_t lane_addr, float *stg,
                                                    const CUtensorMap *tmO, uint32_t &cnt) {
@@ -517,13 +538,31 @@ __device__ __forceinline__ void epilogue_wgrad_tma(const BParams &p, const BTile
     float *buf = stg + (cnt & 1u) * P_STG_TILE;
     if (lane == 0) bulk_wait_read_but1();  // this buffer's previous store has read it
     __syncwarp();
-    float4 *row = reinterpret_cast<float4 *>(buf + lane * 32);
+    if constexpr (OB) {
+      float f[32];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const float4 f = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                   __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-      bad |= !isfinite(f.x) || !isfinite(f.y) || !isfinite(f.z) || !isfinite(f.w);
-      row[q ^ (lane & 7)] = f;
+      for (int j = 0; j < 32; ++j) {
+        f[j] = __uint_as_float(v[j]);
+        bad |= !isfinite(f[j]);
+      }
+      uint32_t packed[16];
+      pack_bf16(f, packed);
+      uint4 *row = reinterpret_cast<uint4 *>(buf) + lane * 4;
+      const int x = (lane >> 1) & 3;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        row[q ^ x] = make_uint4(packed[4 * q], packed[4 * q + 1], packed[4 * q + 2],
+                                packed[4 * q + 3]);
+    } else {
+      float4 *row = reinterpret_cast<float4 *>(buf + lane * 32);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 f = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                     __uint_as_float(v[4 * q + 2]),
+                                     __uint_as_float(v[4 * q + 3]));
+        bad |= !isfinite(f.x) || !isfinite(f.y) || !isfinite(f.z) || !isfinite(f.w);
+        row[q ^ (lane & 7)] = f;
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -539,7 +578,7 @@ __device__ __forceinline__ void epilogue_wgrad_tma(const BParams &p, const BTile
 // tmO: mode 2's output dW as [E, M, N] fp32, box [1, 32, 32], 128-byte
 // swizzle; modes 0 and 1: the output [padded rows, N] (bf16 / fp32), box [32,
 // 32], when p.tma_out is set.
-template <int MODE>
+template <int MODE, bool OB = false>
 __global__ void __launch_bounds__(kThreads, 1)
 k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const BParams p) {
@@ -790,7 +829,7 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       const uint32_t lane_addr =
           tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
       if constexpr (MODE == 2)
-        epilogue_wgrad_tma(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
+        epilogue_wgrad_tma<OB>(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
       else
         epilogue_rows<MODE>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
       tc_fence_before();
@@ -863,12 +902,12 @@ int pair_clusters_bwd(size_t smem) {
   return n;
 }
 
-template <int MODE>
+template <int MODE, bool OB = false>
 cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
                              const BParams &p, int clusters, cudaStream_t s) {
   const size_t smem = bwd_smem_bytes_pair(p.E, MODE);
   cudaError_t err = cudaFuncSetAttribute(
-      k_bwd_tc_pair<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      k_bwd_tc_pair<MODE, OB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
@@ -880,32 +919,35 @@ cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const C
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled(kPdlGemm) ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_bwd_tc_pair<MODE>, a, b, o, p);
+  return cudaLaunchKernelEx(&cfg, k_bwd_tc_pair<MODE, OB>, a, b, o, p);
 }
 
-template <int MODE>
+template <int MODE, bool OB = false>
 cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p,
                         cudaStream_t s) {
   const size_t smem = bwd_smem_bytes(p.E);
-  cudaError_t err = cudaFuncSetAttribute(k_bwd_tc<MODE>,
+  cudaError_t err = cudaFuncSetAttribute(k_bwd_tc<MODE, OB>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
-  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE>, sm_count(), kThreads, smem, s, a, b, p);
+  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB>, sm_count(), kThreads, smem, s, a, b, p);
   return cudaGetLastError();
 }
 
-// 3-D fp32 tensor [E, M, N] (N % 4 == 0): the weight gradient, box [1, 32
-// rows, 32 columns] in the 128-byte swizzle, for the CTA-pair kernel's TMA
-// stores (rows past M and columns past N of a box are not written).
-bool make_out_map3(CUtensorMap *m, float *base, int E, int M, int N) {
+// 3-D tensor [E, M, N], fp32 (N % 4 == 0) or bf16 (N % 8 == 0): the weight
+// gradient, box [1, 32 rows, 32 columns] in the 128-byte (bf16: 64-byte)
+// swizzle, for the CTA-pair kernel's TMA stores (rows past M and columns past
+// N of a box are not written).
+bool make_out_map3(CUtensorMap *m, void *base, int E, int M, int N, bool bf16) {
   auto fn = encode_fn();
-  if (!fn || N % 4 != 0) return false;
+  if (!fn || N % (bf16 ? 8 : 4) != 0) return false;
+  const cuuint64_t eb = bf16 ? 2 : 4;
   cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)M, (cuuint64_t)E};
-  cuuint64_t strides[2] = {(cuuint64_t)N * 4, (cuuint64_t)M * N * 4};
+  cuuint64_t strides[2] = {(cuuint64_t)N * eb, (cuuint64_t)M * N * eb};
   cuuint32_t box[3] = {32, 32, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base,
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -972,9 +1014,10 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
     const int cl = pick_pair<2>(g, g.k_len, (long long)g.E * ((g.M + 255) / 256) * nb);
     CUtensorMap to;
     if (cl > 0 && (uintptr_t)g.out % 16 == 0 &&
-        make_out_map3(&to, static_cast<float *>(g.out), g.E, g.M, g.N))
-      return launch_mode_pair<2>(ta, tb, to, p, cl, s);
-    return launch_mode<2>(ta, tb, p, s);
+        make_out_map3(&to, g.out, g.E, g.M, g.N, g.out_bf16))
+      return g.out_bf16 ? launch_mode_pair<2, true>(ta, tb, to, p, cl, s)
+                        : launch_mode_pair<2>(ta, tb, to, p, cl, s);
+    return g.out_bf16 ? launch_mode<2, true>(ta, tb, p, s) : launch_mode<2>(ta, tb, p, s);
   }
   // A: padded rows [a_rows, K]; B: the weight as [E*N rows, K] (the pair
   // kernel loads half of a tile's 256 B rows per CTA).

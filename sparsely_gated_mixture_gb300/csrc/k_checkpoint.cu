@@ -1,0 +1,313 @@
+// Hidden activations in 8 bits between the forward and the backward.
+//
+// A row's columns form blocks of 32; a block stores its values as e4m3 with
+// one scale 2^e, e the smallest exponent (at least -124) whose largest e4m3
+// value, 448 * 2^e, reaches the block's largest. So a value keeps 4
+// significant bits unless it is below 2^-6 * 2^e, that is some 2^-14 of the
+// block's largest. Two properties that the backward relies on:
+//   - a value over zero is never stored as zero (it is lifted to the smallest
+//     one, 2^-9 * 2^e): the ReLU pattern [h > 0], and with it dpre, db1, dW1
+//     and the experts' share of dx, is exactly that of the unrounded rows;
+//   - every stored value is exact in bf16 (4 significant bits, exponent at
+//     least -133), so loading rounds nothing.
+// Values at or below zero (the rows are ReLU outputs) are stored as zero. A
+// block with a non-finite value gets the scale byte 255 and loads as NaN.
+// Scale bytes: e + 127.
+//
+// Both directions are HBM streams: one warp moves 1024 columns of a row,
+// every 16-byte (fp32: 32-byte) load issued before the first is used; 4 lanes
+// of 8 columns make a block. Widths that are not a multiple of 8 go one
+// column per lane.
+#include "moe_internal.cuh"
+
+#include <cuda_fp8.h>
+
+namespace moe {
+namespace {
+
+constexpr int kLow = -124;      // smallest scale exponent
+constexpr int kWarps = 8;
+constexpr int kPasses = 4;      // passes of 256 columns per warp
+constexpr int kSeg = 256 * kPasses;
+
+// Scale exponent of a block from its largest value (finite, >= 0): amax =
+// 1.m * 2^(E - 127) and 448 = 1.75 * 2^8.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return max(e, kLow);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// v / 2^e for e4m3: positive values stay positive; where 448 * 2^e passes the
+// largest float (e >= 120) the result stops at 240, whose value is finite.
+__device__ __forceinline__ float scaled(float v, float inv, float cap) {
+  return v > 0.f ? fminf(fmaxf(v * inv, 0.001953125f), cap) : 0.f;
+}
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+// What a scale byte multiplies by.
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
+}
+
+template <typename T>
+struct Oct;
+template <>
+struct Oct<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(w[j] << 16);
+      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      w[j] = *reinterpret_cast<uint32_t *>(&b);
+    }
+    v = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Oct<float> {
+  float4 a, b;
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+k_ckpt_save(int cols, int segs, const int32_t *__restrict__ rows, const T *__restrict__ h,
+            uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
+            DeviceStatus *st) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
+  const long long row = u / segs;
+  const int seg = (int)(u - row * segs);
+  if (row >= max_rows || row >= *rows) return;
+  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const T *src = h + row * cols;
+  uint8_t *dst = q + row * cols;
+  Oct<T> in[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int c = seg * kSeg + i * 256 + lane * 8;
+    if (c < cols) in[i] = *reinterpret_cast<const Oct<T> *>(src + c);
+  }
+  uint32_t mine = 0;  // the scale byte of block `lane` of this segment
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int c = seg * kSeg + i * 256 + lane * 8;
+    float f[8] = {};
+    if (c < cols) in[i].get(f);
+    float top = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      top = fmaxf(top, f[j]);
+      bad |= !isfinite(f[j]);
+    }
+    if (bad) top = INFINITY;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool fine = top < INFINITY;
+    const int e = fine ? scale_exp(top) : 0;
+    const float inv = pow2(-e), cap = e >= 120 ? 240.f : 448.f;
+    const uint32_t byte = fine ? (uint32_t)(e + 127) : 255u;
+    const uint32_t got = __shfl_sync(0xffffffffu, byte, 4 * (lane & 7));
+    if ((lane >> 3) == i) mine = got;
+    if (c < cols) {
+      uint2 o;
+      o.x = e4m3x2(scaled(f[0], inv, cap), scaled(f[1], inv, cap)) |
+            e4m3x2(scaled(f[2], inv, cap), scaled(f[3], inv, cap)) << 16;
+      o.y = e4m3x2(scaled(f[4], inv, cap), scaled(f[5], inv, cap)) |
+            e4m3x2(scaled(f[6], inv, cap), scaled(f[7], inv, cap)) << 16;
+      *reinterpret_cast<uint2 *>(dst + c) = o;
+    }
+    if (bad) record_error(st, MOE_ERR_NONFINITE, row * cols + c);
+  }
+  const int b = seg * (kSeg / kCkptBlock) + lane;
+  if (b < nb) scale[row * nb + b] = (uint8_t)mine;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+k_ckpt_load(int cols, int segs, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
+            const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
+  const long long row = u / segs;
+  const int seg = (int)(u - row * segs);
+  if (row >= max_rows || row >= *rows) return;
+  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const uint8_t *src = q + row * cols;
+  T *dst = h + row * cols;
+  uint2 in[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int c = seg * kSeg + i * 256 + lane * 8;
+    if (c < cols) in[i] = *reinterpret_cast<const uint2 *>(src + c);
+  }
+  const int b = seg * (kSeg / kCkptBlock) + lane;
+  const float mine = b < nb ? scale_of(scale[row * nb + b]) : 0.f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int c = seg * kSeg + i * 256 + lane * 8;
+    const float s = __shfl_sync(0xffffffffu, mine, i * 8 + (lane >> 2));
+    if (c >= cols) continue;
+    const uint32_t w[4] = {in[i].x & 0xffffu, in[i].x >> 16, in[i].y & 0xffffu, in[i].y >> 16};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 v = from_e4m3x2(w[j]);
+      f[2 * j] = v.x * s;
+      f[2 * j + 1] = v.y * s;
+    }
+    Oct<T> o;
+    o.set(f);
+    *reinterpret_cast<Oct<T> *>(dst + c) = o;
+  }
+}
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Any width: a warp per block of 32 columns, one column per lane.
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+k_ckpt_save_any(int cols, const int32_t *__restrict__ rows, const T *__restrict__ h,
+                uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
+                DeviceStatus *st) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
+  const long long row = u / nb;
+  const int b = (int)(u - row * nb);
+  if (row >= max_rows || row >= *rows) return;
+  const int c = b * kCkptBlock + lane;
+  const float v = c < cols ? to_f(h[row * cols + c]) : 0.f;
+  const bool bad = !isfinite(v);
+  float top = bad ? INFINITY : fmaxf(v, 0.f);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const bool fine = top < INFINITY;
+  const int e = fine ? scale_exp(top) : 0;
+  if (c < cols)
+    q[row * cols + c] = (uint8_t)e4m3x2(scaled(v, pow2(-e), e >= 120 ? 240.f : 448.f), 0.f);
+  if (lane == 0) scale[u] = fine ? (uint8_t)(e + 127) : (uint8_t)255;
+  if (bad) record_error(st, MOE_ERR_NONFINITE, row * cols + c);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWarps * 32)
+k_ckpt_load_any(int cols, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
+                const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
+  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
+  const long long row = u / nb;
+  const int c = (int)(u - row * nb) * kCkptBlock + lane;
+  if (row >= max_rows || row >= *rows || c >= cols) return;
+  put(h + row * cols + c, from_e4m3x2(q[row * cols + c]).x * scale_of(scale[u]));
+}
+
+__global__ void k_ckpt_choices(int n, int E, const int32_t *__restrict__ idx,
+                               int32_t *__restrict__ out, DeviceStatus *st) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const int e = idx[i];
+  const bool ok = e >= 0 && e < E;
+  if (!ok) record_error(st, MOE_ERR_BOUNDS, i);
+  out[i] = ok ? e : 0;
+}
+
+// Blocks of kWarps warps for `units` warps; false past the grid's limit.
+bool grid_of(long long units, dim3 &g) {
+  const long long b = (units + kWarps - 1) / kWarps;
+  if (b > 0x7fffffffLL) return false;
+  g = dim3((unsigned)b);
+  return true;
+}
+
+template <typename T>
+cudaError_t run_save(long long max_rows, int cols, const int32_t *rows, const void *h, uint8_t *q,
+                     uint8_t *scale, DeviceStatus *st, cudaStream_t s) {
+  const T *src = static_cast<const T *>(h);
+  dim3 g;
+  if (cols % 8 == 0) {
+    const int segs = (cols + kSeg - 1) / kSeg;
+    if (!grid_of(max_rows * segs, g)) return cudaErrorInvalidValue;
+    return launch_pdl(k_ckpt_save<T>, g, kWarps * 32, 0, s, cols, segs, rows, src, q, scale,
+                      max_rows, st);
+  }
+  if (!grid_of(max_rows * ((cols + kCkptBlock - 1) / kCkptBlock), g)) return cudaErrorInvalidValue;
+  return launch_pdl(k_ckpt_save_any<T>, g, kWarps * 32, 0, s, cols, rows, src, q, scale, max_rows,
+                    st);
+}
+
+template <typename T>
+cudaError_t run_load(long long max_rows, int cols, const int32_t *rows, const uint8_t *q,
+                     const uint8_t *scale, void *h, cudaStream_t s) {
+  T *dst = static_cast<T *>(h);
+  dim3 g;
+  if (cols % 8 == 0) {
+    const int segs = (cols + kSeg - 1) / kSeg;
+    if (!grid_of(max_rows * segs, g)) return cudaErrorInvalidValue;
+    return launch_pdl(k_ckpt_load<T>, g, kWarps * 32, 0, s, cols, segs, rows, q, scale, dst,
+                      max_rows);
+  }
+  if (!grid_of(max_rows * ((cols + kCkptBlock - 1) / kCkptBlock), g)) return cudaErrorInvalidValue;
+  return launch_pdl(k_ckpt_load_any<T>, g, kWarps * 32, 0, s, cols, rows, q, scale, dst, max_rows);
+}
+
+}  // namespace
+
+cudaError_t launch_checkpoint_save(bool bf16, long long max_rows, int cols, const int32_t *rows,
+                                   const void *h, uint8_t *q, uint8_t *scale, DeviceStatus *st,
+                                   cudaStream_t s) {
+  return bf16 ? run_save<__nv_bfloat16>(max_rows, cols, rows, h, q, scale, st, s)
+              : run_save<float>(max_rows, cols, rows, h, q, scale, st, s);
+}
+
+cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, const int32_t *rows,
+                                   const uint8_t *q, const uint8_t *scale, void *h,
+                                   cudaStream_t s) {
+  return bf16 ? run_load<__nv_bfloat16>(max_rows, cols, rows, q, scale, h, s)
+              : run_load<float>(max_rows, cols, rows, q, scale, h, s);
+}
+
+cudaError_t launch_checkpoint_choices(int n, int E, const int32_t *idx, int32_t *out,
+                                      DeviceStatus *st, cudaStream_t s) {
+  return launch_pdl(k_ckpt_choices, dim3((n + 255) / 256), 256, 0, s, n, E, idx, out, st);
+}
+
+}  // namespace moe

@@ -325,6 +325,12 @@ struct BwdLayout {
   int n_blocks2, chunks;
 };
 
+// Rows an 8-bit checkpoint of the hidden activations holds at most.
+static long long checkpoint_rows(const moe_config &c) {
+  const long long A = (long long)c.T * c.k, full = (long long)c.E * host_capacity(c);
+  return A < full ? A : full;
+}
+
 // The expert backward runs on the tensor cores for bf16 layers whose widths
 // are multiples of 64, else on the CUDA cores (fp32 row buffers).
 static bool bwd_tc_shape(const moe_config &c) {
@@ -980,6 +986,118 @@ static int gate_bwd_impl(const moe_config &c, const WsLayout &L, const BwdLayout
   return MOE_OK;
 }
 
+// The backward of the flat layer from the state in q.ws (routing, packed rows,
+// hidden rows) and the selection given: moe_backward's, and
+// moe_backward_checkpoint's once it has rebuilt that state.
+struct BwdCall {
+  const void *x;
+  const float *Wg, *Wnoise, *noise;
+  const void *W1, *W2, *b2;
+  const int32_t *idx;
+  const float *gate;
+  const int32_t *pos;
+  const uint8_t *keep;
+  const void *dy;
+  float w_importance, w_load, w_aux;
+  void *dx;
+  float *dWg, *dWnoise, *dlogit_bias;
+  void *dW1, *db1, *dW2, *db2;
+  float *dgate;
+  void *ws, *bws;
+  bool dw_bf16;  // dW1, db1, dW2, db2 in bf16 (else fp32)
+};
+
+static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &q,
+                         cudaStream_t s) {
+  const bool tc = bwd_tc_shape(c);
+  const BwdLayout B = bwd_layout(c);
+  void *ws = q.ws, *bws = q.bws;
+  DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
+  const int32_t *offset = ws_at<int32_t>(ws, L.offset);
+  const int32_t *row_token = ws_at<int32_t>(ws, L.row_token);
+  const float *row_gate = ws_at<float>(ws, L.row_gate);
+  void *xbuf = ws_at<char>(ws, L.xbuf), *hbuf = ws_at<char>(ws, L.hbuf);
+  int32_t *poff = ws_at<int32_t>(bws, B.poff);
+  void *dY = ws_at<char>(bws, B.dY), *dU = ws_at<char>(bws, B.dU), *dP = ws_at<char>(bws, B.dP);
+  float *dX = ws_at<float>(bws, B.dX), *dgpart = ws_at<float>(bws, B.dgpart);
+  float *dg = ws_at<float>(bws, B.dg), *dxr = ws_at<float>(bws, B.dxr);
+  const long long A_rows = (long long)c.T * c.k;
+  const long long cap = host_capacity(c);  // rows per expert at most
+  // CUDA-core form (fp32 rows): the same steps, in k_bwd_simt.cu.
+  const BwdSimt sp{B.P_max, offset, poff, row_token, row_gate, q.dy, q.W1, q.W2, q.b2, xbuf,
+                   hbuf, static_cast<float *>(dY), static_cast<float *>(dU), static_cast<float *>(dP),
+                   dX, dgpart, q.dW1, q.dW2, st, q.dw_bf16};
+  // 1. Padded row blocks, finite K tails, the dy rows (plain and gate-scaled);
+  // 2. through W2: D = dY W2^T, the gate partials <D, h> and dpre = g D [h > 0].
+  MOE_CUDA(launch_bwd_offsets(c.E, offset, poff, s));
+  if (tc) {
+    MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, s));
+    MOE_CUDA(launch_bwd_gather(c, B.P_max, offset, poff, row_token, row_gate, q.dy, dY, dU,
+                               s));
+    BwdGemm g0{0, c.d, c.d_ff, 0, c.E, B.P_max, 0, 0, dY, q.W2, offset, poff, row_gate, hbuf,
+               dP, dgpart, false};
+    MOE_CUDA(launch_bwd_gemm(g0, st, s));
+  } else {
+    MOE_CUDA(launch_bwd_simt_front(c, sp, s));
+  }
+  // From here two independent branches. On the side stream (the library's,
+  // as in moe_forward; `stream` itself if none could be made): the gate's
+  // backward from the dgate partials -- <dy, U> per kept choice, the gate,
+  // load and Switch terms, the router's weight gradients and its share of dx
+  // -- and the bias column sums. Their small kernels fit beside the
+  // persistent GEMM CTAs of the other branch, which stays on `stream`.
+  SideStream *side = nullptr;
+  std::unique_lock<std::mutex> side_lock;
+  side = side_stream(side_lock, s);
+  cudaStream_t fs = s;
+  if (side) {
+    MOE_CUDA(cudaEventRecord(side->fork, s));
+    MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
+    fs = side->s;
+  }
+  if (tc)
+    MOE_CUDA(launch_bwd_dg(c, B.n_blocks2, offset, poff, row_token, dgpart, q.dy, q.b2, dg,
+                           fs));
+  else
+    MOE_CUDA(launch_bwd_simt_dg(c, sp, dg, fs));
+  const int r = gate_bwd_impl(c, L, B, ws, bws, q.x, q.Wg, q.Wnoise, q.noise, q.idx, q.gate,
+                              q.keep, dg, false, q.w_importance, q.w_load, q.w_aux, q.dgate,
+                              q.dWg, q.dWnoise, q.dlogit_bias, dxr, fs);
+  if (r != MOE_OK) return r;
+  float *cpart = ws_at<float>(bws, B.cpart);
+  if (q.db2)
+    MOE_CUDA(launch_bwd_colsum(c, c.d, B.chunks, offset, poff, row_gate, dY, !tc, cpart, q.db2,
+                               q.dw_bf16, fs));
+  if (q.db1)
+    MOE_CUDA(launch_bwd_colsum(c, c.d_ff, B.chunks, offset, poff, nullptr, dP, !tc, cpart, q.db1,
+                               q.dw_bf16, fs));
+  // 3. Through W1: dX = dpre W1^T; weight gradients dW2[e] = h^T (g dY),
+  //    dW1[e] = x^T dpre.
+  if (tc) {
+    BwdGemm g1{1, c.d_ff, c.d, 0, c.E, B.P_max, 0, 0, dP, q.W1, offset, poff, nullptr, nullptr,
+               dX, nullptr, false};
+    MOE_CUDA(launch_bwd_gemm(g1, st, s));
+    BwdGemm g2{2, 0, c.d, c.d_ff, c.E, A_rows, B.P_max, cap, hbuf, dU, offset, poff, nullptr,
+               nullptr, q.dW2, nullptr, q.dw_bf16};
+    MOE_CUDA(launch_bwd_gemm(g2, st, s));
+    BwdGemm g3{2, 0, c.d_ff, c.d, c.E, A_rows, B.P_max, cap, xbuf, dP, offset, poff, nullptr,
+               nullptr, q.dW1, nullptr, q.dw_bf16};
+    MOE_CUDA(launch_bwd_gemm(g3, st, s));
+  } else {
+    MOE_CUDA(launch_bwd_simt_back(c, sp, s));
+  }
+  if (side) {
+    MOE_CUDA(cudaEventRecord(side->join, side->s));
+    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
+  }
+  // 4. dx = dy + the router's share + the kept experts' rows.
+  if (tc)
+    MOE_CUDA(launch_bwd_dx(c, q.idx, q.pos, q.keep, poff, dX, dxr, q.dy, q.dx, s));
+  else
+    MOE_CUDA(launch_bwd_simt_dx(c, sp, q.idx, q.pos, q.keep, dxr, q.dx, s));
+  return MOE_OK;
+}
+
 int moe_gate_backward(const moe_config *cfg, const void *x, const float *Wg, const float *Wnoise,
                       const float *noise, const int32_t *expert_idx, const float *gate,
                       const float *dgate, float w_load, float w_aux, float *dWg, float *dWnoise,
@@ -1021,96 +1139,112 @@ int moe_backward(const moe_config *cfg, const void *x, const float *Wg, const fl
     return MOE_ERR_ARG;
   if (!isfinite(w_importance) || !isfinite(w_load) || !isfinite(w_aux)) return MOE_ERR_ARG;
   const moe_config &c = *cfg;
-  const bool tc = bwd_tc_shape(c);
-  if (tc && !bwd_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
+  if (bwd_tc_shape(c) && !bwd_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
   const WsLayout L = ws_layout(c);
-  const BwdLayout B = bwd_layout(c);
+  const BwdCall q{x, Wg, Wnoise, noise, W1, W2, b2,
+                  expert_idx ? expert_idx : ws_at<int32_t>(ws, L.idx),
+                  gate ? gate : ws_at<float>(ws, L.gate), pos ? pos : ws_at<int32_t>(ws, L.pos),
+                  keep ? keep : ws_at<uint8_t>(ws, L.keep), dy, w_importance, w_load, w_aux, dx,
+                  dWg, dWnoise, dlogit_bias, dW1, db1, dW2, db2, dgate, ws, bws, false};
+  return backward_impl(c, L, q, (cudaStream_t)stream);
+}
+
+int moe_checkpoint_size(const moe_config *cfg, int64_t *rows, size_t *h8_bytes,
+                        size_t *hscale_bytes) {
+  const int r = check_cfg(cfg);
+  if (r != MOE_OK) return r;
+  if (!rows || !h8_bytes || !hscale_bytes) return MOE_ERR_ARG;
+  const long long n = checkpoint_rows(*cfg);
+  *rows = n;
+  *h8_bytes = (size_t)n * cfg->d_ff;
+  *hscale_bytes = (size_t)n * ((cfg->d_ff + kCkptBlock - 1) / kCkptBlock);
+  return MOE_OK;
+}
+
+int moe_checkpoint_save(const moe_config *cfg, const void *hbuf, const int32_t *expert_offset,
+                        uint8_t *h8, uint8_t *hscale, void *ws, moe_stream_t stream) {
+  const int r = check_cfg(cfg);
+  if (r != MOE_OK) return r;
+  MOE_OPT(hbuf); MOE_OPT(expert_offset); MOE_REQ(h8); MOE_REQ(hscale);
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
+  if ((hbuf == nullptr) != (expert_offset == nullptr)) return MOE_ERR_ARG;
+  const moe_config &c = *cfg;
+  const WsLayout L = ws_layout(c);
+  const void *h = hbuf ? hbuf : ws_at<char>(ws, L.hbuf);
+  const int32_t *off = expert_offset ? expert_offset : ws_at<int32_t>(ws, L.offset);
+  MOE_CUDA(launch_checkpoint_save(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff, off + c.E,
+                                  h, h8, hscale, ws_at<DeviceStatus>(ws, L.status),
+                                  (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+int moe_checkpoint_load(const moe_config *cfg, const uint8_t *h8, const uint8_t *hscale,
+                        const int32_t *expert_offset, void *hbuf, void *ws,
+                        moe_stream_t stream) {
+  const int r = check_cfg(cfg);
+  if (r != MOE_OK) return r;
+  MOE_REQ(h8); MOE_REQ(hscale); MOE_OPT(expert_offset); MOE_OPT(hbuf);
+  if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
+  if ((hbuf == nullptr) != (expert_offset == nullptr)) return MOE_ERR_ARG;
+  const moe_config &c = *cfg;
+  const WsLayout L = ws_layout(c);
+  void *h = hbuf ? hbuf : ws_at<char>(ws, L.hbuf);
+  const int32_t *off = expert_offset ? expert_offset : ws_at<int32_t>(ws, L.offset);
+  MOE_CUDA(launch_checkpoint_load(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff, off + c.E,
+                                  h8, hscale, h, (cudaStream_t)stream));
+  return MOE_OK;
+}
+
+int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *Wg,
+                            const float *Wnoise, const float *noise, const float *logit_bias,
+                            const void *W1, const void *W2, const void *b2,
+                            const int32_t *expert_idx, const float *gate, const uint8_t *h8,
+                            const uint8_t *hscale, const void *dy, float w_importance,
+                            float w_load, float w_aux, void *dx, float *dWg, float *dWnoise,
+                            float *dlogit_bias, void *dW1, void *db1, void *dW2, void *db2,
+                            float *dgate, void *ws, void *bws, moe_stream_t stream) {
+  int r = check_cfg(cfg);
+  if (r != MOE_OK) return r;
+  MOE_REQ(x); MOE_REQ(Wg); MOE_OPT(Wnoise); MOE_OPT(noise); MOE_OPT(logit_bias); MOE_REQ(W1);
+  MOE_REQ(W2); MOE_OPT(b2); MOE_REQ(expert_idx); MOE_REQ(gate); MOE_REQ(h8); MOE_REQ(hscale);
+  MOE_REQ(dy); MOE_REQ(dx); MOE_REQ(dWg); MOE_OPT(dWnoise); MOE_OPT(dlogit_bias); MOE_REQ(dW1);
+  MOE_OPT(db1); MOE_REQ(dW2); MOE_OPT(db2); MOE_OPT(dgate);
+  if (!ws || !aligned(ws, 256) || !bws || !aligned(bws, 256)) return MOE_ERR_ARG;
+  if ((Wnoise == nullptr) != (noise == nullptr) || (Wnoise == nullptr) != (dWnoise == nullptr))
+    return MOE_ERR_ARG;
+  if (!isfinite(w_importance) || !isfinite(w_load) || !isfinite(w_aux)) return MOE_ERR_ARG;
+  const moe_config &c = *cfg;
+  if (bwd_tc_shape(c) && !bwd_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
+  const WsLayout L = ws_layout(c);
   cudaStream_t s = (cudaStream_t)stream;
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
-  const int32_t *idx = expert_idx ? expert_idx : ws_at<int32_t>(ws, L.idx);
-  const float *g = gate ? gate : ws_at<float>(ws, L.gate);
-  const int32_t *ps = pos ? pos : ws_at<int32_t>(ws, L.pos);
-  const uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.keep);
-  const int32_t *offset = ws_at<int32_t>(ws, L.offset);
-  const int32_t *row_token = ws_at<int32_t>(ws, L.row_token);
-  const float *row_gate = ws_at<float>(ws, L.row_gate);
-  void *xbuf = ws_at<char>(ws, L.xbuf), *hbuf = ws_at<char>(ws, L.hbuf);
-  int32_t *poff = ws_at<int32_t>(bws, B.poff);
-  void *dY = ws_at<char>(bws, B.dY), *dU = ws_at<char>(bws, B.dU), *dP = ws_at<char>(bws, B.dP);
-  float *dX = ws_at<float>(bws, B.dX), *dgpart = ws_at<float>(bws, B.dgpart);
-  float *dg = ws_at<float>(bws, B.dg), *dxr = ws_at<float>(bws, B.dxr);
-  const long long A_rows = (long long)c.T * c.k;
-  const long long cap = host_capacity(c);  // rows per expert at most
-  // CUDA-core form (fp32 rows): the same steps, in k_bwd_simt.cu.
-  const BwdSimt sp{B.P_max, offset, poff, row_token, row_gate, dy, W1, W2, b2, xbuf, hbuf,
-                   static_cast<float *>(dY), static_cast<float *>(dU), static_cast<float *>(dP),
-                   dX, dgpart, dW1, dW2, st};
-  // 1. Padded row blocks, finite K tails, the dy rows (plain and gate-scaled);
-  // 2. through W2: D = dY W2^T, the gate partials <D, h> and dpre = g D [h > 0].
-  MOE_CUDA(launch_bwd_offsets(c.E, offset, poff, s));
-  if (tc) {
-    MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, s));
-    MOE_CUDA(launch_bwd_gather(c, B.P_max, offset, poff, row_token, row_gate, dy, dY, dU, s));
-    BwdGemm g0{0, c.d, c.d_ff, 0, c.E, B.P_max, 0, 0, dY, W2, offset, poff, row_gate, hbuf, dP,
-               dgpart};
-    MOE_CUDA(launch_bwd_gemm(g0, st, s));
-  } else {
-    MOE_CUDA(launch_bwd_simt_front(c, sp, s));
-  }
-  // From here two independent branches. On the side stream (the library's,
-  // as in moe_forward; `stream` itself if none could be made): the gate's
-  // backward from the dgate partials -- <dy, U> per kept choice, the gate,
-  // load and Switch terms, the router's weight gradients and its share of dx
-  // -- and the bias column sums. Their small kernels fit beside the
-  // persistent GEMM CTAs of the other branch, which stays on `stream`.
-  SideStream *side = nullptr;
-  std::unique_lock<std::mutex> side_lock;
-  side = side_stream(side_lock, s);
-  cudaStream_t fs = s;
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->fork, s));
-    MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
-    fs = side->s;
-  }
-  if (tc)
-    MOE_CUDA(launch_bwd_dg(c, B.n_blocks2, offset, poff, row_token, dgpart, dy, b2, dg, fs));
-  else
-    MOE_CUDA(launch_bwd_simt_dg(c, sp, dg, fs));
-  r = gate_bwd_impl(c, L, B, ws, bws, x, Wg, Wnoise, noise, idx, g, kp, dg, false, w_importance,
-                    w_load, w_aux, dgate, dWg, dWnoise, dlogit_bias, dxr, fs);
+  // The router's logits and balancing totals, as the forward computed them
+  // (its kernels, in its order: the same bits). The choices are the caller's.
+  const bool losses = w_importance != 0.f || w_load != 0.f || w_aux != 0.f;
+  r = gate_impl(c, x, Wg, Wnoise, noise, logit_bias, ws_at<int32_t>(ws, L.idx),
+                ws_at<float>(ws, L.gate), ws_at<float>(ws, L.thr), ws, losses, s);
   if (r != MOE_OK) return r;
-  float *cpart = ws_at<float>(bws, B.cpart);
-  if (db2)
-    MOE_CUDA(launch_bwd_colsum(c, c.d, B.chunks, offset, poff, row_gate, dY, !tc, cpart, db2,
-                               fs));
-  if (db1)
-    MOE_CUDA(launch_bwd_colsum(c, c.d_ff, B.chunks, offset, poff, nullptr, dP, !tc, cpart, db1,
-                               fs));
-  // 3. Through W1: dX = dpre W1^T; weight gradients dW2[e] = h^T (g dY),
-  //    dW1[e] = x^T dpre.
-  if (tc) {
-    BwdGemm g1{1, c.d_ff, c.d, 0, c.E, B.P_max, 0, 0, dP, W1, offset, poff, nullptr, nullptr, dX,
-               nullptr};
-    MOE_CUDA(launch_bwd_gemm(g1, st, s));
-    BwdGemm g2{2, 0, c.d, c.d_ff, c.E, A_rows, B.P_max, cap, hbuf, dU, offset, poff, nullptr,
-               nullptr, dW2, nullptr};
-    MOE_CUDA(launch_bwd_gemm(g2, st, s));
-    BwdGemm g3{2, 0, c.d_ff, c.d, c.E, A_rows, B.P_max, cap, xbuf, dP, offset, poff, nullptr,
-               nullptr, dW1, nullptr};
-    MOE_CUDA(launch_bwd_gemm(g3, st, s));
-  } else {
-    MOE_CUDA(launch_bwd_simt_back(c, sp, s));
-  }
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->join, side->s));
-    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
-  }
-  // 4. dx = dy + the router's share + the kept experts' rows.
-  if (tc)
-    MOE_CUDA(launch_bwd_dx(c, idx, ps, kp, poff, dX, dxr, dy, dx, s));
-  else
-    MOE_CUDA(launch_bwd_simt_dx(c, sp, idx, ps, kp, dxr, dx, s));
-  return MOE_OK;
+  if (losses)
+    MOE_CUDA(launch_aux_finalize(c, ws_at<float>(ws, L.partials), L.n_aux_blocks,
+                                 ws_at<float>(ws, L.out3s), nullptr, nullptr,
+                                 ws_at<float2>(ws, L.aux_vec), st, s));
+  // The packed rows of the choices, x's gathered and the hidden ones loaded.
+  int32_t *offset = ws_at<int32_t>(ws, L.offset), *pos = ws_at<int32_t>(ws, L.pos);
+  uint8_t *keep = ws_at<uint8_t>(ws, L.keep);
+  MOE_CUDA(launch_slots(c, host_capacity(c), expert_idx, gate, ws_at<int32_t>(ws, L.hist),
+                        ws_at<int32_t>(ws, L.chunk_base), ws_at<int32_t>(ws, L.count), offset,
+                        ws_at<int32_t>(ws, L.mtiles), pos, keep, ws_at<int32_t>(ws, L.row_token),
+                        ws_at<float>(ws, L.row_gate), L.n_chunks, st, s));
+  MOE_CUDA(launch_gather(c, x, offset, ws_at<int32_t>(ws, L.row_token), ws_at<char>(ws, L.xbuf),
+                         st, s));
+  MOE_CUDA(launch_checkpoint_load(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff,
+                                  offset + c.E, h8, hscale, ws_at<char>(ws, L.hbuf), s));
+  int32_t *idx = ws_at<int32_t>(ws, L.idx);
+  MOE_CUDA(launch_checkpoint_choices(c.T * c.k, c.E, expert_idx, idx, st, s));
+  const BwdCall q{x, Wg, Wnoise, noise, W1, W2, b2, idx, gate, pos, keep, dy, w_importance,
+                  w_load, w_aux, dx, dWg, dWnoise, dlogit_bias, dW1, db1, dW2, db2, dgate, ws,
+                  bws, c.act_dtype == MOE_BF16};
+  return backward_impl(c, L, q, s);
 }
 
 int moe_last_device_status(void *ws, moe_stream_t stream, int64_t *detail) {

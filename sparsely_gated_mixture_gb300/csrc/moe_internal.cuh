@@ -289,6 +289,7 @@ struct BwdGemm {
   const void *hbuf;
   void *out;
   float *dgpart;
+  bool out_bf16;  // mode 2: the weight gradient in bf16
 };
 bool bwd_tc_supported(const moe_config &cfg);
 cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s);
@@ -300,8 +301,10 @@ struct BwdSimt {
   const int32_t *offset, *poff, *row_token;
   const float *row_gate;
   const void *dy, *W1, *W2, *b2, *xbuf, *hbuf;
-  float *dY, *dU, *dP, *dX, *dgpart, *dW1, *dW2;
+  float *dY, *dU, *dP, *dX, *dgpart;
+  void *dW1, *dW2;  // fp32, or bf16 with dw_bf16
   DeviceStatus *st;
+  bool dw_bf16;
 };
 int simt_dgate_blocks(const moe_config &c);  // column blocks of the dgate partials
 // gather and the dgrad through W2 (dpre, dgate partials)
@@ -340,12 +343,28 @@ cudaError_t launch_bwd_router(const moe_config &c, bool noisy, const void *x, co
                               const float *Wn, const float *dc, const float *dz, float *part,
                               float *bpart, float *dWg, float *dWn, float *dbias, float *dxr,
                               cudaStream_t s);
-// src rows are bf16, or fp32 when src_f32.
+// src rows are bf16, or fp32 when src_f32; out fp32 or bf16.
 cudaError_t launch_bwd_colsum(const moe_config &c, int cols, int chunks, const int32_t *offset,
                               const int32_t *poff, const float *row_gate, const void *src,
-                              bool src_f32, float *part, float *out, cudaStream_t s);
+                              bool src_f32, float *part, void *out, bool out_bf16,
+                              cudaStream_t s);
 cudaError_t launch_bwd_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                           const uint8_t *keep, const int32_t *poff, const float *dX,
                           const float *dxr, const void *dy, void *dx, cudaStream_t s);
+
+// ----------------------------------------------------------------------------- checkpoint
+// k_checkpoint.cu: hidden rows in 8 bits (e4m3 values, one power-of-two scale
+// per 32 columns), and back. Rows [0, *rows) of at most max_rows.
+constexpr int kCkptBlock = 32;
+cudaError_t launch_checkpoint_save(bool bf16, long long max_rows, int cols, const int32_t *rows,
+                                   const void *h, uint8_t *q, uint8_t *scale, DeviceStatus *st,
+                                   cudaStream_t s);
+cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, const int32_t *rows,
+                                   const uint8_t *q, const uint8_t *scale, void *h,
+                                   cudaStream_t s);
+// The caller's choices with an index outside [0, E) replaced by 0 (recorded as
+// MOE_ERR_BOUNDS), for kernels that index by expert.
+cudaError_t launch_checkpoint_choices(int n, int E, const int32_t *idx, int32_t *out,
+                                      DeviceStatus *st, cudaStream_t s);
 
 }  // namespace moe
