@@ -78,18 +78,17 @@ __device__ __forceinline__ void few_start(const FewArgs &p) {
   }
 }
 
-// Arrive at barrier b: everything this block wrote before is visible to a
-// block that has waited.
+// Arrive at barrier b (one thread, after a barrier of the block's threads that
+// wrote): what they wrote before is visible to a block that has waited.
 __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    few_flag_set(p.flags + (size_t)b * kFewMaxGrid + blockIdx.x, p.nonce);
-  }
+  __threadfence();
+  few_flag_set(p.flags + (size_t)b * kFewMaxGrid + blockIdx.x, p.nonce);
 }
 
-// Wait for barrier b (all threads of the block); false: leave the kernel.
-__device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n_threads) {
+// Wait for barrier b (threads tid of n_threads of the block); false: leave the
+// kernel. With an abort flag, a set one ends the wait too.
+__device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n_threads,
+                                         volatile int *abort_flag = nullptr) {
   bool ok = true;
   unsigned long long t0 = 0;
   for (int i = tid; i < (int)gridDim.x && ok; i += n_threads) {
@@ -97,6 +96,10 @@ __device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n
     while (few_flag_get(f) != p.nonce) {
       const unsigned long long now = globaltimer();
       if (t0 == 0) t0 = now;
+      if (abort_flag && *abort_flag) {
+        ok = false;
+        break;
+      }
       if (now - t0 >= p.wait_ns) {
         record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
         ok = false;
@@ -108,7 +111,8 @@ __device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n
 }
 
 __device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
-  few_arrive(p, b);
+  __syncthreads();
+  if (threadIdx.x == 0) few_arrive(p, b);
   const bool ok = few_wait(p, b, threadIdx.x, blockDim.x);
   const bool fail = __syncthreads_or(!ok);
   if (threadIdx.x == 0 && (b == 1 || fail))
@@ -366,11 +370,12 @@ struct FewRows {
   int *expert;                 // [<= kFewRows] experts in use
   int *first;                  // [<= kFewRows + 1] their first packed row
   int *base;                   // [E] first packed row of every expert
+  uint16_t *owner;             // [<= kFewRows] each packed row's place in `expert`
   uint8_t *token;              // [<= kFewRows] token of each packed row
   int n, rows;                 // experts in use; rows
 };
-constexpr size_t few_rows_bytes(int E) {
-  return (size_t)E * 8 + (size_t)E * 4 + (size_t)(2 * kFewRows + 2) * 4 + kFewRows + 64;
+constexpr size_t few_rows_bytes(int E, int A) {
+  return ((size_t)E * 12 + ((size_t)2 * A + 2) * 4 + (size_t)A * 3 + 63) / 64 * 64;
 }
 
 __device__ FewRows few_rows(const FewArgs &p, char *smem) {
@@ -378,11 +383,12 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   R.tokens = reinterpret_cast<unsigned long long *>(smem);
   R.base = reinterpret_cast<int *>(R.tokens + p.E);
   R.expert = R.base + p.E;
-  R.first = R.expert + kFewRows;
-  R.token = reinterpret_cast<uint8_t *>(R.first + kFewRows + 1);
+  const int A = p.T * p.k;
+  R.first = R.expert + A;
+  R.owner = reinterpret_cast<uint16_t *>(R.first + A + 1);
+  R.token = reinterpret_cast<uint8_t *>(R.owner + A);
   __shared__ int scan[8][2], total[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int A = p.T * p.k;
   for (int e = tid; e < p.E; e += kFewThreads) R.tokens[e] = 0;
   __syncthreads();
   for (int a = tid; a < A; a += kFewThreads) {
@@ -432,6 +438,7 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
     if (n > 0) {
       R.expert[bu] = e;
       R.first[bu] = br;
+      for (int r = 0; r < n; ++r) R.owner[br + r] = (uint16_t)bu;
       ++bu;
       br += n;
     }
@@ -455,53 +462,116 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
 }
 
 // ----------------------------------------------------------------------------- hidden, combine
-// h[r] = ReLU(sum of the slices + b1), rounded once to the layer's type.
-// slices_of(i): the number of partial slices of expert i of R (all equal in
-// the CUDA-core form).
-template <typename T>
-__device__ void few_hidden(const FewArgs &p, const FewRows &R, int slices) {
+// V floats at p (aligned to V floats).
+template <int V>
+__device__ __forceinline__ void few_add(const float *p, float (&v)[V]) {
+  if constexpr (V == 4) {
+    const float4 f = *reinterpret_cast<const float4 *>(p);
+    v[0] += f.x;
+    v[1] += f.y;
+    v[2] += f.z;
+    v[3] += f.w;
+  } else if constexpr (V == 2) {
+    const float2 f = *reinterpret_cast<const float2 *>(p);
+    v[0] += f.x;
+    v[1] += f.y;
+  } else {
+    v[0] += *p;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void few_ld(const T *p, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = few_f(p[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ void few_st(T *p, const float (&v)[V]) {
+  struct alignas(sizeof(T) * V) Pack {
+    T t[V];
+  } o;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o.t[i] = few_t<T>(v[i]);
+  *reinterpret_cast<Pack *>(p) = o;
+}
+
+// h[r] = ReLU(sum of the partial sums + b1), rounded once to the layer's
+// type, V columns at a time, by threads tid of n_threads of each block.
+// pieces(j, c): the number of partial sums of column c of expert j of R.
+template <typename T, int V, typename PF>
+__device__ __forceinline__ void few_hidden(const FewArgs &p, const FewRows &R, const PF &pieces,
+                                           int tid, int n_threads) {
   const T *b1 = static_cast<const T *>(p.b1);
   T *h = static_cast<T *>(p.h);
-  const size_t n = (size_t)R.rows * p.F;
-  for (int i = 0; i < R.n; ++i) {
-    const int e = R.expert[i];
-    const size_t lo = (size_t)R.first[i] * p.F, hi = (size_t)R.first[i + 1] * p.F;
-    for (size_t j = lo + (size_t)blockIdx.x * kFewThreads + threadIdx.x; j < hi;
-         j += (size_t)gridDim.x * kFewThreads) {
-      float v = 0.f;
-      for (int s = 0; s < slices; ++s) v += p.hpart[s * n + j];
-      if (b1) v += few_f(b1[(size_t)e * p.F + j % p.F]);
-      h[j] = few_t<T>(fmaxf(v, 0.f));
+  const unsigned cols = p.F / V, total = R.rows * cols;
+  const size_t step = (size_t)R.rows * p.F;
+  for (unsigned i = blockIdx.x * n_threads + tid; i < total; i += gridDim.x * n_threads) {
+    const unsigned row = i / cols, c = (i - row * cols) * V;
+    const int j = R.owner[row], np = pieces(j, (int)c);
+    const float *src = p.hpart + (size_t)row * p.F + c;
+    float v[V] = {};
+#pragma unroll 4
+    for (int s = 0; s < np; ++s) few_add<V>(src + s * step, v);
+    if (b1) {
+      float b[V];
+      few_ld<T, V>(b1 + (size_t)R.expert[j] * p.F + c, b);
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] += b[q];
     }
+#pragma unroll
+    for (int q = 0; q < V; ++q) v[q] = fmaxf(v[q], 0.f);
+    few_st<T, V>(h + (size_t)row * p.F + c, v);
   }
 }
 
 // y[t] = x[t] + sum over the kept choices, in order, of gate * (sum of the
-// slices + b2), in fp32, rounded once.
-template <typename T>
-__device__ void few_combine(const FewArgs &p, const FewRows &R, int slices) {
+// partial sums + b2), in fp32, rounded once.
+template <typename T, int V, typename PF>
+__device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
+                                            const PF &pieces) {
   const T *x = static_cast<const T *>(p.x), *b2 = static_cast<const T *>(p.b2);
   T *y = static_cast<T *>(p.y);
-  const size_t n = (size_t)R.rows * p.d;
-  for (size_t j = (size_t)blockIdx.x * kFewThreads + threadIdx.x; j < (size_t)p.T * p.d;
-       j += (size_t)gridDim.x * kFewThreads) {
-    const int t = (int)(j / p.d), c = (int)(j % p.d);
-    float acc = few_f(x[j]);
+  const unsigned cols = p.d / V, total = p.T * cols;
+  const size_t step = (size_t)R.rows * p.d;
+  for (unsigned i = blockIdx.x * kFewThreads + threadIdx.x; i < total;
+       i += gridDim.x * kFewThreads) {
+    const unsigned t = i / cols, c = (i - t * cols) * V;
+    float acc[V];
+    few_ld<T, V>(x + (size_t)t * p.d + c, acc);
     for (int q = 0; q < p.k; ++q) {
       const int e = p.idx[t * p.k + q];
       if (e < 0 || e >= p.E) continue;
       const int pos = __popcll(R.tokens[e] & ((1ull << t) - 1));
       if (pos >= p.C) continue;
-      const size_t at = (size_t)(R.base[e] + pos) * p.d + c;
-      float v = 0.f;
-      for (int s = 0; s < slices; ++s) v += p.zpart[s * n + at];
-      if (b2) v += few_f(b2[(size_t)e * p.d + c]);
-      acc += p.gate[t * p.k + q] * v;
+      const int row = R.base[e] + pos, np = pieces(R.owner[row], (int)c);
+      const float *src = p.zpart + (size_t)row * p.d + c;
+      float v[V] = {};
+#pragma unroll 4
+      for (int s = 0; s < np; ++s) few_add<V>(src + s * step, v);
+      if (b2) {
+        float b[V];
+        few_ld<T, V>(b2 + (size_t)e * p.d + c, b);
+#pragma unroll
+        for (int z = 0; z < V; ++z) v[z] += b[z];
+      }
+      const float g = p.gate[t * p.k + q];
+#pragma unroll
+      for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[z], acc[z]);
     }
-    if (!isfinite(acc)) record_error(p.st, MOE_ERR_NONFINITE, t);
-    y[j] = few_t<T>(acc);
+    bool bad = false;
+#pragma unroll
+    for (int z = 0; z < V; ++z) bad |= !isfinite(acc[z]);
+    if (bad) record_error(p.st, MOE_ERR_NONFINITE, t);
+    few_st<T, V>(y + (size_t)t * p.d + c, acc);
   }
 }
 
 }  // namespace
+
+// Launches a kernel of one cooperative grid of kFewThreads-thread blocks.
+cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
+                            cudaStream_t s);
+// k_few_tc.cu: bf16 layers whose widths are multiples of 8, experts on tcgen05.
+bool few_tc_supported(const moe_config &cfg);
+cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s);
+
 }  // namespace moe

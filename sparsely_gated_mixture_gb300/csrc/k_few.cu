@@ -45,18 +45,6 @@ struct FewVec<float, 1> {
   __device__ void get(float (&f)[1]) const { f[0] = v; }
 };
 template <>
-struct FewVec<__nv_bfloat16, 8> {
-  uint4 v;
-  __device__ void get(float (&f)[8]) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  }
-};
-template <>
 struct FewVec<__nv_bfloat16, 2> {
   uint32_t v;
   __device__ void get(float (&f)[2]) const {
@@ -70,7 +58,7 @@ struct FewVec<__nv_bfloat16, 1> {
   __device__ void get(float (&f)[1]) const { f[0] = __bfloat162float(v); }
 };
 
-// smem: xs [kUnitRows][8], red [8 warps][8 rows][32 * VEC / 2 columns at a time].
+// smem: xs [kUnitRows][8], red [8 warps][8 rows][VEC][32 lanes].
 constexpr int kSimtSmemFloats = kUnitRows * 8 + 8 * 8 * 32 * 4;
 
 template <typename T, int VEC>
@@ -128,26 +116,21 @@ __device__ void few_product(const FewRows &R, const T *A, bool by_token, const T
           }
         }
       }
-      // Join the warps, up to 4 columns of each lane at a time.
+      // Join the warps.
+      __syncthreads();
 #pragma unroll
-      for (int v0 = 0; v0 < VEC; v0 += 4) {
-        constexpr int PV = VEC < 4 ? VEC : 4;
-        __syncthreads();
+      for (int r = 0; r < 8; ++r)
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
+        for (int v = 0; v < VEC; ++v) red[((warp * 8 + r) * VEC + v) * 32 + lane] = acc[r][v];
+      __syncthreads();
+      for (int j = tid; j < 8 * VEC * 32; j += kFewThreads) {
+        const int r = j / (VEC * 32), l = j % 32, v = j / 32 % VEC;
+        const int col = cb * COLS + l * VEC + v;
+        if (r0 + r >= r1 || col >= N) continue;
+        float sum = 0.f;
 #pragma unroll
-          for (int v = 0; v < PV; ++v)
-            red[((warp * 8 + r) * PV + v) * 32 + lane] = acc[r][v0 + v];
-        __syncthreads();
-        for (int j = tid; j < 8 * PV * 32; j += kFewThreads) {
-          const int r = j / (PV * 32), l = j % 32, v = j / 32 % PV;
-          const int col = cb * COLS + l * VEC + v0 + v;
-          if (r0 + r >= r1 || col >= N) continue;
-          float sum = 0.f;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) sum += red[((x * 8 + r) * PV + v) * 32 + l];
-          out[((size_t)s * R.rows + r0 + r) * N + col] = sum;
-        }
+        for (int x = 0; x < 8; ++x) sum += red[((x * 8 + r) * VEC + v) * 32 + l];
+        out[((size_t)s * R.rows + r0 + r) * N + col] = sum;
       }
     }
   }
@@ -166,16 +149,33 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
   few_product<T, VEC>(R, static_cast<const T *>(p.x), true, static_cast<const T *>(p.W1), p.d,
                       p.F, p.hpart, work);
   if (!few_barrier(p, 2)) return;
-  few_hidden<T>(p, R, few_units(R.n, p.d, p.F, 32 * VEC, gridDim.x).slices);
+  constexpr int V = VEC < 4 ? VEC : 4;
+  const int s1 = few_units(R.n, p.d, p.F, 32 * VEC, gridDim.x).slices;
+  const int s2 = few_units(R.n, p.F, p.d, 32 * VEC, gridDim.x).slices;
+  few_hidden<T, V>(p, R, [&](int, int) { return s1; }, threadIdx.x, kFewThreads);
   if (!few_barrier(p, 3)) return;
   few_product<T, VEC>(R, static_cast<const T *>(p.h), false, static_cast<const T *>(p.W2), p.F,
                       p.d, p.zpart, work);
   if (!few_barrier(p, 4)) return;
-  few_combine<T>(p, R, few_units(R.n, p.F, p.d, 32 * VEC, gridDim.x).slices);
+  few_combine<T, V>(p, R, [&](int, int) { return s2; });
 }
 
-cudaError_t launch_coop(const void *kernel, const FewArgs &p, int grid, size_t smem,
-                        cudaStream_t s) {
+template <typename T, int VEC>
+cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
+  const size_t smem = kSimtSmemFloats * 4 + few_rows_bytes(p.E, p.T * p.k);
+  int grid = 2 * sm_count();  // two blocks fit an SM (launch bounds, 62 KB at most)
+  if (grid > kFewMaxGrid) grid = kFewMaxGrid;
+  void *args[1] = {const_cast<FewArgs *>(&p)};
+  return launch_few_grid(reinterpret_cast<const void *>(k_few_simt<T, VEC>), args, grid, smem, s);
+}
+
+}  // namespace
+
+cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
+                            cudaStream_t s) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kFewThreads);
@@ -186,27 +186,8 @@ cudaError_t launch_coop(const void *kernel, const FewArgs &p, int grid, size_t s
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void *args[1] = {const_cast<FewArgs *>(&p)};
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
-
-template <typename T, int VEC>
-cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
-  size_t smem = kSimtSmemFloats * 4 + few_rows_bytes(p.E);
-  const void *kernel = reinterpret_cast<const void *>(k_few_simt<T, VEC>);
-  cudaError_t err = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (err != cudaSuccess) return err;
-  int per_sm = 0;
-  err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kFewThreads, smem);
-  if (err != cudaSuccess) return err;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  int grid = sm_count() * (per_sm < 2 ? per_sm : 2);
-  if (grid > kFewMaxGrid) grid = kFewMaxGrid;
-  return launch_coop(kernel, p, grid, smem, s);
-}
-
-}  // namespace
 
 FewLayout few_layout(const moe_config &c) {
   FewLayout L{};
@@ -223,11 +204,11 @@ FewLayout few_layout(const moe_config &c) {
   L.gate = take(A * 4);
   // Router: slices * columns <= (grid + groups) * 32, with noise or without.
   L.rpart = take(T * 32 * (kFewMaxGrid + 2 * (2 * E + 31) / 32 + 1) * 4);
-  // A layer's partials: slices <= 2 grid / (experts in use * column blocks) + 1
-  // and rows <= T * experts in use (and <= T k), so slices * rows * N <=
-  // T * 2 grid * (columns of a block) + T k N.
-  L.hpart = take((T * 2 * kFewMaxGrid * kFewColsMax + A * F) * 4);
-  L.zpart = take((T * 2 * kFewMaxGrid * kFewColsMax + A * d) * 4);
+  // A layer's partials: with at most 2 grid / (experts in use * column blocks)
+  // + 2 of them per column (both forms) and rows <= T * experts in use (and <=
+  // T k), partials * rows * N <= T * 2 grid * (columns of a block) + 2 T k N.
+  L.hpart = take((T * 2 * kFewMaxGrid * kFewColsMax + 2 * A * F) * 4);
+  L.zpart = take((T * 2 * kFewMaxGrid * kFewColsMax + 2 * A * d) * 4);
   L.h = take(A * F * elem_bytes(c.act_dtype));
   L.total = off;
   return L;
@@ -275,7 +256,7 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
     if (c.d % 4 == 0 && c.d_ff % 4 == 0) return run_simt<float, 4>(p, s);
     return run_simt<float, 1>(p, s);
   }
-  if (c.d % 8 == 0 && c.d_ff % 8 == 0) return run_simt<__nv_bfloat16, 8>(p, s);
+  if (few_tc_supported(c)) return launch_few_tc(p, s);
   if (c.d % 2 == 0 && c.d_ff % 2 == 0) return run_simt<__nv_bfloat16, 2>(p, s);
   return run_simt<__nv_bfloat16, 1>(p, s);
 }

@@ -1,0 +1,432 @@
+// The few-token layer with the experts on tcgen05: bf16 layers whose widths
+// are multiples of 8.
+//
+// The products are bound by reading the weights once, so the weights are the
+// tall operand: D[n, token] = sum_k W[k, n] A[token, k] with M = 128 weight
+// columns on the TMEM lanes and the tokens as the instruction's N (16 to 64).
+// Weight tiles go from HBM by TMA straight into the MMA's shared memory, and
+// no thread touches them.
+//
+// The work of a layer, (experts in use) x (256-column tiles) x (64-row chunks
+// of K), is one line of units of 32 KB of weights that the blocks share in
+// equal contiguous runs; a run's share of a tile leaves as a partial sum, and
+// the few partials of a column are added in order by whoever needs them next.
+//
+// Warps: 0 weight producer (TMA), 1 MMA issuer and TMEM owner, 2 producer of
+// the token operand (TMA: x for layer 1, H for layer 2), 4-7 epilogue. The
+// weight producer knows both layers' tiles once the experts are selected, so
+// it runs ahead into layer 2 while the grid joins layer 1's partials: the ring
+// of stages holds some 4 us of HBM time per SM, which covers the two barriers
+// between the layers.
+#include "few.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 256;                    // weight columns of a unit
+constexpr int kChunk = 64;                    // rows of K of a unit
+constexpr int kWBytes = kTile * kChunk * 2;   // 32 KB
+constexpr int kBoxBytes = 64 * kChunk * 2;    // one [64 x 64] box, 8 KB
+constexpr int kMaxStages = 8;
+constexpr int kTmemCols = 256;                // 2 buffers x 2 halves x 64 tokens
+constexpr int kEpiThreads = 128;
+
+// D = A B with fp32 accumulation, bf16 operands, A (weights) MN-major, B
+// (tokens) K-major, M = 128, N tokens.
+__device__ __forceinline__ uint32_t few_idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void few_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void few_tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                           int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// Eight TMEM columns of this warp's lanes, at any addresses, and one wait.
+__device__ __forceinline__ void few_tmem8(const uint32_t (&a)[8], uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%8];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%9];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%2}, [%10];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%3}, [%11];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%4}, [%12];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%5}, [%13];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%6}, [%14];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%7}, [%15];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
+      : "memory");
+}
+
+// Whether v holds for all threads of the four epilogue warps (and a barrier of
+// them).
+__device__ __forceinline__ bool epi_all(bool v) {
+  uint32_t out;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.and.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(out)
+      : "r"((uint32_t)v), "n"(kEpiThreads)
+      : "memory");
+  return out != 0;
+}
+
+// One layer's units and this block's run of them. G: the blocks that get any
+// (every one of them at least one unit). Units are fewer than 2^31 / 512:
+// their weights would not fit the device otherwise.
+struct FewLine {
+  int N, KC, NT;
+  unsigned total, G;
+  __device__ FewLine(int n_experts, int K, int n, int grid) {
+    N = n;
+    KC = (K + kChunk - 1) / kChunk;
+    NT = (n + kTile - 1) / kTile;
+    total = (unsigned)n_experts * NT * KC;
+    G = min((unsigned)grid, total);
+  }
+  __device__ unsigned lo(unsigned b) const {
+    return b >= G ? total : (unsigned)((unsigned long long)total * b / G);
+  }
+  // The block whose run holds unit u: the largest b with lo(b) <= u.
+  __device__ unsigned owner(unsigned u) const {
+    return (unsigned)(((unsigned long long)(u + 1) * G - 1) / total);
+  }
+  // Partial sums of column c of expert j.
+  __device__ int pieces(int j, int c) const {
+    const unsigned tile = (unsigned)j * NT + c / kTile;
+    return (int)(owner(tile * KC + KC - 1) - owner(tile * KC)) + 1;
+  }
+};
+
+// A run's share of one tile: expert j, columns from n0, chunks [kb0, kb1), the
+// piece it makes.
+struct FewSeg {
+  int j, n0, kb0, kb1, piece;
+};
+__device__ __forceinline__ FewSeg few_seg(const FewLine &l, unsigned u, unsigned hi) {
+  FewSeg s;
+  const unsigned tile = u / l.KC;
+  s.j = tile / l.NT;
+  s.n0 = (int)(tile - (unsigned)s.j * l.NT) * kTile;
+  s.kb0 = (int)(u - tile * l.KC);
+  s.kb1 = min(l.KC, s.kb0 + (int)(hi - u));
+  s.piece = (int)(blockIdx.x - l.owner(tile * l.KC));
+  return s;
+}
+
+struct FewTc {
+  int stages, tok_bytes;  // ring stages; bytes of a stage's token operand
+};
+
+// tmX: x [T, d], box [roundup(T, 16), 64]; tmH: H [T k, d_ff], box [16, 64];
+// tm1, tm2: W1 [E, d, d_ff], W2 [E, d_ff, d], box [1, 64, 64]. All bf16 in the
+// 128-byte swizzle; out-of-range rows and columns read as zero.
+__global__ void __launch_bounds__(kFewThreads, 1)
+k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmH,
+         const __grid_constant__ CUtensorMap tm1, const __grid_constant__ CUtensorMap tm2,
+         const __grid_constant__ FewArgs p, const FewTc q) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint64_t full_w[kMaxStages], full_t[kMaxStages], empty[kMaxStages];
+  __shared__ uint64_t acc_full[2], acc_empty[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int *abort_flag = &abort_word;
+  uint8_t *ring = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int stage = kWBytes + q.tok_bytes, S = q.stages;
+  uint8_t *rows_mem = ring + (size_t)S * stage;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  few_start(p);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full_w[s], 1);
+      mbar_init(&full_t[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(&drain, 1);
+    abort_word = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&tmem_slot)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  // The ring's memory serves the router and the selection first.
+  float *work = reinterpret_cast<float *>(ring);
+  few_route<__nv_bfloat16>(p, work);
+  bool ok = few_barrier(p, 0);
+  if (ok) {
+    few_select<__nv_bfloat16>(p, work);
+    ok = few_barrier(p, 1);
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  FewRows R{};
+  if (ok) R = few_rows(p, reinterpret_cast<char *>(rows_mem));
+  fence_proxy_async_smem();  // generic accesses to the ring come before TMA's
+  __syncthreads();
+  if (ok && R.n > 0) {
+    const FewLine line[2] = {FewLine(R.n, p.d, p.F, gridDim.x), FewLine(R.n, p.F, p.d, gridDim.x)};
+    if (warp == 0) {
+      if (lane == 0) {
+        // ------------------------------------------------------ weight producer
+        uint32_t it = 0;
+        bool go = true;
+        for (int layer = 0; layer < 2 && go; ++layer) {
+          const FewLine &l = line[layer];
+          const CUtensorMap *tm = layer ? &tm2 : &tm1;
+          const unsigned hi = l.lo(blockIdx.x + 1);
+          for (unsigned u = l.lo(blockIdx.x); u < hi && go;) {
+            const FewSeg s = few_seg(l, u, hi);
+            const int e = R.expert[s.j], boxes = min(4, (l.N - s.n0 + 63) / 64);
+            for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+              const int st = it % S;
+              if (!mbar_wait(&empty[st], ((it / S) & 1u) ^ 1u, abort_flag, p.st, 111, p.wait_ns)) {
+                go = false;
+                break;
+              }
+              mbar_expect_tx(&full_w[st], boxes * kBoxBytes);
+              for (int b = 0; b < boxes; ++b)
+                few_tma_3d(ring + (size_t)st * stage + b * kBoxBytes, tm, &full_w[st],
+                           s.n0 + b * 64, kb * kChunk, e);
+            }
+            u += s.kb1 - s.kb0;
+          }
+        }
+        for (uint32_t i = it > (uint32_t)S ? it - S : 0; i < it; ++i)
+          mbar_drain(&full_w[i % S], (i / S) & 1u);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // ------------------------------------------------------ MMA issuer
+        uint32_t it = 0;
+        int local = 0;
+        bool go = true;
+        for (int layer = 0; layer < 2 && go; ++layer) {
+          const FewLine &l = line[layer];
+          const unsigned hi = l.lo(blockIdx.x + 1);
+          for (unsigned u = l.lo(blockIdx.x); u < hi && go; ++local) {
+            const FewSeg s = few_seg(l, u, hi);
+            const int buf = local & 1;
+            if (!mbar_wait(&acc_empty[buf], ((local >> 1) & 1u) ^ 1u, abort_flag, p.st, 112,
+                           p.wait_ns))
+              break;
+            tc_fence_after();
+            const int toks = layer ? R.first[s.j + 1] - R.first[s.j] : p.T;
+            const uint32_t idesc = few_idesc((toks + 15) / 16 * 16);
+            const uint32_t d0 = tmem + (uint32_t)(buf * 128);
+            const int halves = l.N - s.n0 > 128 ? 2 : 1;
+            for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+              const int st = it % S;
+              const uint32_t ph = (it / S) & 1u;
+              if (!mbar_wait(&full_w[st], ph, abort_flag, p.st, 113, p.wait_ns) ||
+                  !mbar_wait(&full_t[st], ph, abort_flag, p.st, 114, p.wait_ns)) {
+                go = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t a0 = smem_u32(ring + (size_t)st * stage);
+              const uint32_t b0 = a0 + kWBytes;
+              for (int h = 0; h < halves; ++h)
+#pragma unroll
+                for (int kk = 0; kk < kChunk / 16; ++kk)
+                  few_mma(d0 + h * 64, sdesc(a0 + h * 2 * kBoxBytes + kk * 2048, kBoxBytes, 1024),
+                          sdesc(b0 + kk * 32, 16, 1024), idesc, (kb > s.kb0 || kk) ? 1u : 0u);
+              umma_commit(&empty[st]);
+            }
+            if (go) umma_commit(&acc_full[buf]);
+            u += s.kb1 - s.kb0;
+          }
+        }
+        umma_commit(&drain);
+        mbar_drain(&drain, 0);
+      }
+    } else if (warp == 2) {
+      // -------------------------------------------------------- token producer
+      uint32_t it = 0;
+      bool go = true;
+      for (int layer = 0; layer < 2 && go; ++layer) {
+        const FewLine &l = line[layer];
+        if (layer) {
+          // H is complete when every block has passed barrier 3.
+          const bool done = few_wait(p, 3, lane, 32, abort_flag);
+          if (!__all_sync(0xffffffffu, done)) {
+            *abort_flag = 1;
+            break;
+          }
+          asm volatile("fence.proxy.async.global;" ::: "memory");
+        }
+        const unsigned hi = l.lo(blockIdx.x + 1);
+        for (unsigned u = l.lo(blockIdx.x); u < hi && go;) {
+          const FewSeg s = few_seg(l, u, hi);
+          if (lane == 0) {
+            const int r0 = R.first[s.j], rows = R.first[s.j + 1] - r0;
+            const int boxes = layer ? (rows + 15) / 16 : 1;
+            const uint32_t bytes = layer ? boxes * 2048 : q.tok_bytes;
+            for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+              const int st = it % S;
+              if (!mbar_wait(&empty[st], ((it / S) & 1u) ^ 1u, abort_flag, p.st, 115, p.wait_ns)) {
+                go = false;
+                break;
+              }
+              uint8_t *dst = ring + (size_t)st * stage + kWBytes;
+              mbar_expect_tx(&full_t[st], bytes);
+              for (int b = 0; b < boxes; ++b)
+                tma_load_2d(dst + b * 2048, layer ? &tmH : &tmX, &full_t[st], kb * kChunk,
+                            layer ? r0 + b * 16 : 0);
+            }
+          }
+          go = __shfl_sync(0xffffffffu, go, 0);
+          u += s.kb1 - s.kb0;
+        }
+      }
+      if (lane == 0)
+        for (uint32_t i = it > (uint32_t)S ? it - S : 0; i < it; ++i)
+          mbar_drain(&full_t[i % S], (i / S) & 1u);
+    } else if (warp >= 4) {
+      // -------------------------------------------------------- epilogue
+      const int quad = warp & 3, et = threadIdx.x - 128;
+      int local = 0;
+      bool go = true;
+      for (int layer = 0; layer < 2 && go; ++layer) {
+        const FewLine &l = line[layer];
+        float *part = layer ? p.zpart : p.hpart;
+        const unsigned hi = l.lo(blockIdx.x + 1);
+        for (unsigned u = l.lo(blockIdx.x); u < hi; ++local) {
+          const FewSeg s = few_seg(l, u, hi);
+          const int buf = local & 1;
+          go = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1u, abort_flag,
+                                                 p.st, 116, p.wait_ns));
+          if (!go) break;
+          tc_fence_after();
+          const int r0 = R.first[s.j], rows = R.first[s.j + 1] - r0;
+          const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * 128);
+          float *out = part + ((size_t)s.piece * R.rows + r0) * l.N;
+          for (int h = 0; h < 2; ++h) {
+            if (s.n0 + h * 128 >= l.N) break;
+            const int n = s.n0 + h * 128 + quad * 32 + lane;
+            for (int r = 0; r < rows; r += 8) {
+              uint32_t a[8], v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int rr = min(r + i, rows - 1);
+                a[i] = lanes + h * 64 + (uint32_t)(layer ? rr : R.token[r0 + rr]);
+              }
+              few_tmem8(a, v);
+              if (n < l.N) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (r + i < rows) out[(size_t)(r + i) * l.N + n] = __uint_as_float(v[i]);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[buf]);
+          u += s.kb1 - s.kb0;
+        }
+        if (layer == 0) {
+          // Join layer 1's partials into H between two barriers of the grid.
+          // Every decision to go on is taken by all four warps together.
+          go = epi_all(go && *abort_flag == 0);
+          if (go) {
+            if (et == 0) few_arrive(p, 2);
+            go = epi_all(few_wait(p, 2, et, kEpiThreads, abort_flag));
+          }
+          if (!go) {
+            *abort_flag = 1;
+          } else {
+            few_hidden<__nv_bfloat16, 4>(
+                p, R, [&](int j, int c) { return line[0].pieces(j, c); }, et, kEpiThreads);
+            asm volatile("fence.proxy.async.global;" ::: "memory");  // H is read by TMA
+            epi_all(true);
+            if (et == 0) few_arrive(p, 3);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+  }
+  if (!ok || *abort_flag) {
+    if (threadIdx.x == 0) p.flags[blockIdx.x] = 0;
+    return;
+  }
+  if (!few_barrier(p, 4)) return;
+  const FewLine l2(R.n > 0 ? R.n : 1, p.F, p.d, gridDim.x);
+  few_combine<__nv_bfloat16, 4>(p, R, [&](int j, int c) { return l2.pieces(j, c); });
+}
+
+// 3-D bf16 tensor [E, K, N], box [1, 64, 64], 128-byte swizzle; rows past K of
+// an expert and columns past N read as zero.
+bool make_weight_map(CUtensorMap *m, const void *base, int E, int K, int N) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)K, (cuuint64_t)E};
+  cuuint64_t strides[2] = {(cuuint64_t)N * 2, (cuuint64_t)K * N * 2};
+  cuuint32_t box[3] = {64, kChunk, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kSmemMax = 227 * 1024 - 1024;  // less the static part
+
+}  // namespace
+
+bool few_tc_supported(const moe_config &c) {
+  return c.act_dtype == MOE_BF16 && c.d % 8 == 0 && c.d_ff % 8 == 0 && encode_fn() != nullptr;
+}
+
+cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s) {
+  const int box = (p.T + 15) / 16 * 16;
+  FewTc q;
+  q.tok_bytes = box * kChunk * 2;
+  const size_t rows = few_rows_bytes(p.E, p.T * p.k);
+  const size_t stage = kWBytes + q.tok_bytes;
+  q.stages = (int)((kSmemMax - 1024 - rows) / stage);
+  if (q.stages > kMaxStages) q.stages = kMaxStages;
+  CUtensorMap tx, th, t1, t2;
+  if (!make_map(&tx, p.x, (uint64_t)p.T, (uint64_t)p.d, (uint32_t)box) ||
+      !make_map(&th, p.h, (uint64_t)p.T * p.k, (uint64_t)p.F, 16) ||
+      !make_weight_map(&t1, p.W1, p.E, p.d, p.F) || !make_weight_map(&t2, p.W2, p.E, p.F, p.d))
+    return cudaErrorInvalidValue;
+  int grid = sm_count();
+  if (grid > kFewMaxGrid) grid = kFewMaxGrid;
+  void *args[6] = {&tx, &th, &t1, &t2, const_cast<FewArgs *>(&p), &q};
+  return launch_few_grid(reinterpret_cast<const void *>(k_few_tc), args, grid,
+                         1024 + q.stages * stage + rows, s);
+}
+
+}  // namespace moe
