@@ -25,6 +25,7 @@ constexpr int kFewRows = 1024;     // T * k at most (k <= 16)
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxGrid = 512;   // blocks at most (sizes the partial buffers)
 constexpr int kFewBarriers = 5;
+constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 128-byte line
 constexpr int kFewColsMax = 256;   // columns of one unit of the experts' products at most
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
@@ -41,7 +42,9 @@ struct FewArgs {
   uint32_t *mask;  // [T, ceil(E/32)] or null (threshold)
   // Workspace.
   DeviceStatus *st;
-  unsigned long long *flags;  // [kFewBarriers][kFewMaxGrid]
+  unsigned long long *flags;  // [kFewBarriers][kFewMaxGrid][kFewFlag], the first word of each
+  uint32_t *tiles;            // pieces of layer 1's tiles that are written (tensor-core form)
+  int n_tiles;
   float *rpart;               // router partials [slices][T][columns]
   float *hpart, *zpart;       // partials of the layers [slices][rows][N]
   void *h;                    // [rows, F], the layer's type
@@ -53,7 +56,9 @@ namespace {
 // ----------------------------------------------------------------------------- grid barrier
 // Every block has one flag per barrier; it arrives by storing the launch's
 // nonce there and waits until all blocks' flags hold it: one hop, where a
-// shared counter would take one atomic per block in turn. The workspace need
+// shared counter would take one atomic per block in turn, and each flag has a
+// 128-byte line of its own (152 blocks polling 152 flags on ten lines took 2
+// to 5 us a barrier: every poll went to the same few L2 slices). The workspace need
 // not be zeroed: flags of an earlier call hold another nonce, and for a
 // replayed graph, whose nonce is the same each time, the flags are cleared:
 // a block clears its flags of the barriers after the first before it arrives
@@ -70,19 +75,23 @@ __device__ __forceinline__ unsigned long long few_flag_get(const unsigned long l
   return v;
 }
 
+__device__ __forceinline__ unsigned long long *few_flag(const FewArgs &p, int b, int block) {
+  return p.flags + ((size_t)b * kFewMaxGrid + block) * kFewFlag;
+}
+
 __device__ __forceinline__ void few_start(const FewArgs &p) {
-  if (threadIdx.x == 0) {
-    for (int b = 1; b < kFewBarriers; ++b)
-      p.flags[(size_t)b * kFewMaxGrid + blockIdx.x] = 0;
-    if (blockIdx.x == 0) *p.st = DeviceStatus{};
-  }
+  if (threadIdx.x > 0 && threadIdx.x < kFewBarriers) *few_flag(p, threadIdx.x, blockIdx.x) = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.st = DeviceStatus{};
+  for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_tiles;
+       i += gridDim.x * kFewThreads)
+    p.tiles[i] = 0;
 }
 
 // Arrive at barrier b (one thread, after a barrier of the block's threads that
 // wrote): what they wrote before is visible to a block that has waited.
 __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
   __threadfence();
-  few_flag_set(p.flags + (size_t)b * kFewMaxGrid + blockIdx.x, p.nonce);
+  few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);
 }
 
 // Wait for barrier b (threads tid of n_threads of the block); false: leave the
@@ -92,7 +101,7 @@ __device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n
   bool ok = true;
   unsigned long long t0 = 0;
   for (int i = tid; i < (int)gridDim.x && ok; i += n_threads) {
-    const unsigned long long *f = p.flags + (size_t)b * kFewMaxGrid + i;
+    const unsigned long long *f = few_flag(p, b, i);
     while (few_flag_get(f) != p.nonce) {
       const unsigned long long now = globaltimer();
       if (t0 == 0) t0 = now;
@@ -115,8 +124,7 @@ __device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
   if (threadIdx.x == 0) few_arrive(p, b);
   const bool ok = few_wait(p, b, threadIdx.x, blockDim.x);
   const bool fail = __syncthreads_or(!ok);
-  if (threadIdx.x == 0 && (b == 1 || fail))
-    p.flags[blockIdx.x] = 0;
+  if (threadIdx.x == 0 && (b == 1 || fail)) *few_flag(p, 0, blockIdx.x) = 0;
   return !fail;
 }
 
@@ -133,11 +141,13 @@ __device__ __forceinline__ __nv_bfloat16 few_t<__nv_bfloat16>(float v) {
 }
 
 // ----------------------------------------------------------------------------- router
-// Columns: E of W_g, then E of W_noise. A unit is 32 columns (or the next
-// power of two over their number, the warp's lanes then also covering rows)
-// and one slice of d; the block's warps share the slice's rows, each thread
-// holding the sums of 8 tokens in registers, and are summed in shared memory.
-constexpr int kRtRows = 128;  // rows of x staged at a time
+// Columns: E of W_g, then E of W_noise. A unit is 32 columns (or, for fewer,
+// the power of two from their number on, a warp's lanes then covering several
+// rows) and one slice of d, as many units as blocks where that is possible.
+// 64 rows of the weights and of x (for every token) are staged in shared
+// memory at a time; a warp takes 8 tokens, and with fewer than 64 tokens the
+// warps of the same tokens share the rows. Every product is fp32.
+constexpr int kRtRows = 64;
 
 struct FewRouter {
   int NC, cw, groups, slices, rows_per_slice;
@@ -148,69 +158,125 @@ __host__ __device__ inline FewRouter few_router(int d, int E, bool noisy, int gr
   r.cw = 1;
   while (r.cw < 32 && r.cw < r.NC) r.cw *= 2;
   r.groups = (r.NC + r.cw - 1) / r.cw;
-  int s = (grid + r.groups - 1) / r.groups;
+  int s = grid / r.groups;
   const int most = (d + 31) / 32;  // slices of at least 32 rows
   if (s > most) s = most;
-  r.rows_per_slice = (d + s - 1) / s;
+  if (s < 1) s = 1;
+  r.rows_per_slice = ((d + s - 1) / s + 7) / 8 * 8;
   r.slices = (d + r.rows_per_slice - 1) / r.rows_per_slice;
   return r;
 }
 
-// smem: xs [kRtRows][8] floats, red [8 warps][8][32] floats (12 KB).
+// x[t, k .. k+7] as floats, zero past the end.
 template <typename T>
-__device__ void few_route(const FewArgs &p, float *smem) {
+__device__ __forceinline__ void few_x8(const T *x, int d, int k, float (&f)[8]) {
+  if (d % 8 == 0 && k + 8 <= d) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(x + k);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    } else {
+      const float4 a = *reinterpret_cast<const float4 *>(x + k);
+      const float4 b = *reinterpret_cast<const float4 *>(x + k + 4);
+      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = k + j < d ? few_f(x[k + j]) : 0.f;
+  }
+}
+
+// smem: xs [kRtRows][tokens, a multiple of 8], w [kRtRows][cw], red [8 warps][8][32]:
+// 32 KB at most.
+template <typename T>
+__device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
   const FewRouter r = few_router(p.d, p.E, p.Wn != nullptr, gridDim.x);
-  float *xs = smem;
-  float *red = smem + kRtRows * 8;
+  const int tg = (p.T + 7) / 8, tp = tg * 8;
+  int tgp = 1;  // warps side by side over the tokens: 1, 2, 4 or 8
+  while (tgp < tg) tgp *= 2;
+  const int ks = 8 / tgp;  // warps that share a token group's rows
+  float *xs = smem, *ws = xs + kRtRows * tp, *red = ws + kRtRows * r.cw;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lr = lane / r.cw, lrows = 32 / r.cw;  // this lane's row among the warp's
+  const int tgi = warp & (tgp - 1), kp = warp / tgp;
+  const int lrows = 32 / r.cw, lr = lane / r.cw, lc = lane & (r.cw - 1);
   const T *x = static_cast<const T *>(p.x);
   for (int u = blockIdx.x; u < r.groups * r.slices; u += gridDim.x) {
     const int g = u % r.groups, s = u / r.groups;
     const int k0 = s * r.rows_per_slice, k1 = min(p.d, k0 + r.rows_per_slice);
-    const int col = g * r.cw + (lane & (r.cw - 1));
-    const float *W = nullptr;
-    if (col < p.E) W = p.Wg + col;
-    else if (col < r.NC) W = p.Wn + (col - p.E);
-    for (int t0 = 0; t0 < p.T; t0 += 8) {
-      float acc[8] = {};
-      for (int kb = k0; kb < k1; kb += kRtRows) {
-        const int n = min(kRtRows, k1 - kb);
-        __syncthreads();
-        for (int i = tid; i < 8 * n; i += kFewThreads) {
-          const int t = i / n, kk = i - t * n;
-          xs[kk * 8 + t] = t0 + t < p.T ? few_f(x[(size_t)(t0 + t) * p.d + kb + kk]) : 0.f;
-        }
-        __syncthreads();
-        if (W) {
-#pragma unroll 4
-          for (int kk = warp * lrows + lr; kk < n; kk += 8 * lrows) {
-            const float w = W[(size_t)(kb + kk) * p.E];
-            const float4 a = *reinterpret_cast<const float4 *>(xs + kk * 8);
-            const float4 b = *reinterpret_cast<const float4 *>(xs + kk * 8 + 4);
-            acc[0] = fmaf(w, a.x, acc[0]);
-            acc[1] = fmaf(w, a.y, acc[1]);
-            acc[2] = fmaf(w, a.z, acc[2]);
-            acc[3] = fmaf(w, a.w, acc[3]);
-            acc[4] = fmaf(w, b.x, acc[4]);
-            acc[5] = fmaf(w, b.y, acc[5]);
-            acc[6] = fmaf(w, b.z, acc[6]);
-            acc[7] = fmaf(w, b.w, acc[7]);
-          }
-        }
-      }
-      __syncthreads();
+    float acc[8] = {};
+    for (int kb = k0; kb < k1; kb += kRtRows) {
+      const int n = min(kRtRows, k1 - kb);
+      // The weights' loads are issued before anything is waited for.
+      float wv[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) red[(warp * 8 + t) * 32 + lane] = acc[t];
-      __syncthreads();
-      // Thread (t, column): the sum over the warps and the lanes' rows.
-      const int t = tid >> 5;
-      if (lane < r.cw && t0 + t < p.T && col < r.NC) {
-        float v = 0.f;
-        for (int w = 0; w < 8; ++w)
-          for (int q = 0; q < lrows; ++q) v += red[(w * 8 + t) * 32 + q * r.cw + lane];
-        p.rpart[((size_t)s * p.T + t0 + t) * r.NC + col] = v;
+      for (int i = 0; i < 8; ++i) {
+        const int at = i * kFewThreads + tid, kk = at / r.cw, col = g * r.cw + (at & (r.cw - 1));
+        wv[i] = 0.f;
+        if (at < kRtRows * r.cw && kk < n && col < r.NC)
+          wv[i] = col < p.E ? p.Wg[(size_t)(kb + kk) * p.E + col]
+                            : p.Wn[(size_t)(kb + kk) * p.E + col - p.E];
       }
+      float xv[2][8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = i * kFewThreads + tid, t = at % tp, ko = at / tp * 8;
+        if (ko < kRtRows && t < p.T && ko < n) {
+          few_x8<T>(x + (size_t)t * p.d, p.d, kb + ko, xv[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) xv[i][j] = 0.f;
+        }
+      }
+      __syncthreads();  // the previous rows have been used
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = i * kFewThreads + tid;
+        if (at < kRtRows * r.cw) ws[at] = wv[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = i * kFewThreads + tid, t = at % tp, ko = at / tp * 8;
+        if (ko < kRtRows)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) xs[(ko + j) * tp + t] = xv[i][j];
+      }
+      __syncthreads();
+      if (tgi < tg) {
+#pragma unroll 4
+        for (int kk = kp * lrows + lr; kk < n; kk += ks * lrows) {
+          const float w = ws[kk * r.cw + lc];
+          const float4 a = *reinterpret_cast<const float4 *>(xs + kk * tp + tgi * 8);
+          const float4 b = *reinterpret_cast<const float4 *>(xs + kk * tp + tgi * 8 + 4);
+          acc[0] = fmaf(w, a.x, acc[0]);
+          acc[1] = fmaf(w, a.y, acc[1]);
+          acc[2] = fmaf(w, a.z, acc[2]);
+          acc[3] = fmaf(w, a.w, acc[3]);
+          acc[4] = fmaf(w, b.x, acc[4]);
+          acc[5] = fmaf(w, b.y, acc[5]);
+          acc[6] = fmaf(w, b.z, acc[6]);
+          acc[7] = fmaf(w, b.w, acc[7]);
+        }
+      }
+    }
+    // Over the lanes' rows, then over the warps of the same tokens.
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      for (int o = r.cw; o < 32; o <<= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+    if (lr == 0)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) red[(warp * 8 + t) * 32 + lc] = acc[t];
+    __syncthreads();
+    for (int i = tid; i < tp * r.cw; i += kFewThreads) {
+      const int t = i / r.cw, c = i & (r.cw - 1), col = g * r.cw + c;
+      if (t >= p.T || col >= r.NC) continue;
+      float v = 0.f;
+      for (int w = 0; w < ks; ++w) v += red[((w * tgp + t / 8) * 8 + t % 8) * 32 + c];
+      p.rpart[((size_t)s * p.T + t) * r.NC + col] = v;
     }
   }
 }
@@ -242,32 +308,52 @@ __device__ __forceinline__ float few_block(float v, float *red) {
 //   Switch:    the largest, its gate from the softmax over all experts;
 //   threshold: the experts with Softmax(H) > thr, in order, renormalised.
 // A NaN logit ranks last; a non-finite one is recorded.
-// smem: H [E] floats, red [8], taken words [32].
+// smem: H [E] floats, red [8], taken words [32], sums [2][256].
 template <typename T>
-__device__ void few_select(const FewArgs &p, float *smem) {
+__device__ __forceinline__ void few_select(const FewArgs &p, float *smem) {
   const FewRouter r = few_router(p.d, p.E, p.Wn != nullptr, gridDim.x);
   float *H = smem;
   float *red = smem + p.E;
   uint32_t *words = reinterpret_cast<uint32_t *>(red + 8);
+  float *sums = red + 40;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Threads side by side over the experts, the rest over the slices.
+  int pe = 1;
+  while (pe < p.E && pe < kFewThreads) pe *= 2;
+  const int nl = kFewThreads / pe, sl = tid / pe;
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     float mx = -INFINITY;
     __syncthreads();
-    for (int e = tid; e < p.E; e += kFewThreads) {
-      const float *q = p.rpart + (size_t)t * r.NC + e;
-      const size_t step = (size_t)p.T * r.NC;
+    for (int e0 = 0; e0 < p.E; e0 += pe) {
+      const int e = e0 + (tid & (pe - 1));
       float c = 0.f, z = 0.f;
+      if (e < p.E) {
+        const float *q = p.rpart + (size_t)t * r.NC + e;
+        const size_t step = (size_t)p.T * r.NC;
 #pragma unroll 8
-      for (int s = 0; s < r.slices; ++s) c += q[s * step];
-      if (p.bias) c += p.bias[e];
-      if (p.Wn) {
-#pragma unroll 8
-        for (int s = 0; s < r.slices; ++s) z += q[s * step + p.E];
-        c = fmaf(p.noise[(size_t)t * p.E + e], few_softplus(z), c);
+        for (int s = sl; s < r.slices; s += nl) {
+          c += q[s * step];
+          if (p.Wn) z += q[s * step + p.E];
+        }
       }
-      if (!isfinite(c)) record_error(p.st, MOE_ERR_NONFINITE, (long long)t * p.E + e);
-      H[e] = c;
-      mx = fmaxf(mx, c);
+      if (nl > 1) {
+        __syncthreads();
+        sums[tid] = c;
+        sums[kFewThreads + tid] = z;
+        __syncthreads();
+        if (sl == 0)
+          for (int i = 1; i < nl; ++i) {
+            c += sums[i * pe + tid];
+            z += sums[kFewThreads + i * pe + tid];
+          }
+      }
+      if (sl == 0 && e < p.E) {
+        if (p.bias) c += p.bias[e];
+        if (p.Wn) c = fmaf(p.noise[(size_t)t * p.E + e], few_softplus(z), c);
+        if (!isfinite(c)) record_error(p.st, MOE_ERR_NONFINITE, (long long)t * p.E + e);
+        H[e] = c;
+        mx = fmaxf(mx, c);
+      }
     }
     int32_t *oi = p.idx + (size_t)t * p.k;
     float *og = p.gate + (size_t)t * p.k;
@@ -319,21 +405,27 @@ __device__ void few_select(const FewArgs &p, float *smem) {
         if (total > p.k && lane == 0) record_error(p.st, MOE_ERR_BOUNDS, t);
       }
     } else if (warp == 0) {
-      // Lane l ranks experts l, l + 32, ...; `done` marks the chosen ones.
+      // Lane l ranks experts l, l + 32, ...; `done` marks the chosen ones. A
+      // lane looks its experts through again only after it gave one away.
       uint32_t done = 0;
-      float top = 0.f, g = 0.f, sum = 0.f;
-      int mine = 0;
+      float top = 0.f, g = 0.f, sum = 0.f, lv = -INFINITY;
+      int mine = 0, le = 0x7fffffff;
+      bool look = true;
       for (int j = 0; j < p.k; ++j) {
-        float bv = -INFINITY;
-        int be = 0x7fffffff;
-        for (int e = lane, q = 0; e < p.E; e += 32, ++q) {
-          if ((done >> q) & 1u) continue;
-          const float v = isnan(H[e]) ? -INFINITY : H[e];
-          if (be == 0x7fffffff || v > bv) {
-            bv = v;
-            be = e;
+        if (look) {
+          lv = -INFINITY;
+          le = 0x7fffffff;
+          for (int e = lane, q = 0; e < p.E; e += 32, ++q) {
+            if ((done >> q) & 1u) continue;
+            const float v = isnan(H[e]) ? -INFINITY : H[e];
+            if (le == 0x7fffffff || v > lv) {
+              lv = v;
+              le = e;
+            }
           }
         }
+        float bv = lv;
+        int be = le;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
           const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
@@ -343,7 +435,8 @@ __device__ void few_select(const FewArgs &p, float *smem) {
             be = oe;
           }
         }
-        if ((be & 31) == lane) done |= 1u << (be >> 5);
+        look = (be & 31) == lane;
+        if (look) done |= 1u << (be >> 5);
         if (j == 0) top = bv;
         const float w = expf(bv - top);
         sum += w;
@@ -371,11 +464,13 @@ struct FewRows {
   int *first;                  // [<= kFewRows + 1] their first packed row
   int *base;                   // [E] first packed row of every expert
   uint16_t *owner;             // [<= kFewRows] each packed row's place in `expert`
+  int16_t *row;                // [T k] packed row of each choice, or -1
+  float *gate;                 // [T k]
   uint8_t *token;              // [<= kFewRows] token of each packed row
   int n, rows;                 // experts in use; rows
 };
 constexpr size_t few_rows_bytes(int E, int A) {
-  return ((size_t)E * 12 + ((size_t)2 * A + 2) * 4 + (size_t)A * 3 + 63) / 64 * 64;
+  return ((size_t)E * 12 + ((size_t)2 * A + 2) * 4 + (size_t)A * 9 + 63) / 64 * 64;
 }
 
 __device__ FewRows few_rows(const FewArgs &p, char *smem) {
@@ -385,16 +480,25 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   R.expert = R.base + p.E;
   const int A = p.T * p.k;
   R.first = R.expert + A;
-  R.owner = reinterpret_cast<uint16_t *>(R.first + A + 1);
-  R.token = reinterpret_cast<uint8_t *>(R.owner + A);
+  R.gate = reinterpret_cast<float *>(R.first + A + 1);
+  R.owner = reinterpret_cast<uint16_t *>(R.gate + A);
+  R.row = reinterpret_cast<int16_t *>(R.owner + A);
+  R.token = reinterpret_cast<uint8_t *>(R.row + A);
   __shared__ int scan[8][2], total[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int choice[kFewRows / kFewThreads];
+#pragma unroll
+  for (int i = 0; i < kFewRows / kFewThreads; ++i) {
+    const int a = i * kFewThreads + tid;
+    choice[i] = a < A ? p.idx[a] : -1;
+    if (a < A) R.gate[a] = p.gate[a];
+  }
   for (int e = tid; e < p.E; e += kFewThreads) R.tokens[e] = 0;
   __syncthreads();
-  for (int a = tid; a < A; a += kFewThreads) {
-    const int e = p.idx[a];
-    if (e >= 0 && e < p.E) atomicOr(&R.tokens[e], 1ull << (a / p.k));
-  }
+#pragma unroll
+  for (int i = 0; i < kFewRows / kFewThreads; ++i)
+    if (choice[i] >= 0 && choice[i] < p.E)
+      atomicOr(&R.tokens[choice[i]], 1ull << ((i * kFewThreads + tid) / p.k));
   __syncthreads();
   // Exclusive sums over the experts of (in use, rows), 4 experts a thread.
   int use = 0, rows = 0;
@@ -446,11 +550,14 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   __syncthreads();
   R.n = total[0];
   R.rows = total[1];
-  for (int a = tid; a < A; a += kFewThreads) {
-    const int e = p.idx[a], t = a / p.k;
+#pragma unroll
+  for (int i = 0; i < kFewRows / kFewThreads; ++i) {
+    const int a = i * kFewThreads + tid, e = choice[i], t = a / p.k;
+    if (a >= A) break;
     const bool some = e >= 0 && e < p.E;
     const int pos = some ? __popcll(R.tokens[e] & ((1ull << t) - 1)) : -1;
     const bool kept = some && pos < p.C;
+    R.row[a] = kept ? (int16_t)(R.base[e] + pos) : (int16_t)-1;
     if (kept) R.token[R.base[e] + pos] = (uint8_t)t;
     if (blockIdx.x == 0) {
       if (p.pos) p.pos[a] = pos;
@@ -462,21 +569,21 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
 }
 
 // ----------------------------------------------------------------------------- hidden, combine
-// V floats at p (aligned to V floats).
+// V floats at p (aligned to V floats), written by other blocks: from L2.
 template <int V>
 __device__ __forceinline__ void few_add(const float *p, float (&v)[V]) {
   if constexpr (V == 4) {
-    const float4 f = *reinterpret_cast<const float4 *>(p);
+    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
     v[0] += f.x;
     v[1] += f.y;
     v[2] += f.z;
     v[3] += f.w;
   } else if constexpr (V == 2) {
-    const float2 f = *reinterpret_cast<const float2 *>(p);
+    const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
     v[0] += f.x;
     v[1] += f.y;
   } else {
-    v[0] += *p;
+    v[0] += __ldcg(p);
   }
 }
 template <typename T, int V>
@@ -537,25 +644,35 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
     const unsigned t = i / cols, c = (i - t * cols) * V;
     float acc[V];
     few_ld<T, V>(x + (size_t)t * p.d + c, acc);
-    for (int q = 0; q < p.k; ++q) {
-      const int e = p.idx[t * p.k + q];
-      if (e < 0 || e >= p.E) continue;
-      const int pos = __popcll(R.tokens[e] & ((1ull << t) - 1));
-      if (pos >= p.C) continue;
-      const int row = R.base[e] + pos, np = pieces(R.owner[row], (int)c);
-      const float *src = p.zpart + (size_t)row * p.d + c;
-      float v[V] = {};
-#pragma unroll 4
-      for (int s = 0; s < np; ++s) few_add<V>(src + s * step, v);
-      if (b2) {
-        float b[V];
-        few_ld<T, V>(b2 + (size_t)e * p.d + c, b);
+    // Four choices side by side, so that their loads overlap; each choice's
+    // partials are added in order, then the choices in order.
+    for (int q0 = 0; q0 < p.k; q0 += 4) {
+      float v[4][V] = {};
+      int row[4], np[4], most = 0;
 #pragma unroll
-        for (int z = 0; z < V; ++z) v[z] += b[z];
+      for (int q = 0; q < 4; ++q) {
+        row[q] = q0 + q < p.k ? R.row[t * p.k + q0 + q] : -1;
+        np[q] = row[q] >= 0 ? pieces(R.owner[row[q]], (int)c) : 0;
+        most = max(most, np[q]);
       }
-      const float g = p.gate[t * p.k + q];
+#pragma unroll 2
+      for (int s = 0; s < most; ++s)
 #pragma unroll
-      for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[z], acc[z]);
+        for (int q = 0; q < 4; ++q)
+          if (s < np[q]) few_add<V>(p.zpart + s * step + (size_t)row[q] * p.d + c, v[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (row[q] < 0) continue;
+        if (b2) {
+          float b[V];
+          few_ld<T, V>(b2 + (size_t)R.expert[R.owner[row[q]]] * p.d + c, b);
+#pragma unroll
+          for (int z = 0; z < V; ++z) v[q][z] += b[z];
+        }
+        const float g = R.gate[t * p.k + q0 + q];
+#pragma unroll
+        for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[q][z], acc[z]);
+      }
     }
     bool bad = false;
 #pragma unroll
@@ -572,6 +689,7 @@ cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t sm
                             cudaStream_t s);
 // k_few_tc.cu: bf16 layers whose widths are multiples of 8, experts on tcgen05.
 bool few_tc_supported(const moe_config &cfg);
+int few_tc_tiles(const moe_config &cfg);  // layer 1's tiles at most
 cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s);
 
 }  // namespace moe

@@ -199,7 +199,9 @@ FewLayout few_layout(const moe_config &c) {
     return o;
   };
   L.status = take(sizeof(DeviceStatus));
-  L.flags = take((size_t)kFewBarriers * kFewMaxGrid * 8);
+  L.flags = take((size_t)kFewBarriers * kFewMaxGrid * kFewFlag * 8);
+  L.n_tiles = few_tc_supported(c) ? few_tc_tiles(c) : 0;
+  L.tiles = take((size_t)L.n_tiles * 4);
   L.idx = take(A * 4);
   L.gate = take(A * 4);
   // Router: slices * columns <= (grid + groups) * 32, with noise or without.
@@ -243,6 +245,8 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.mask = q.mask;
   p.st = ws_at<DeviceStatus>(q.ws, L.status);
   p.flags = ws_at<unsigned long long>(q.ws, L.flags);
+  p.tiles = ws_at<uint32_t>(q.ws, L.tiles);
+  p.n_tiles = L.n_tiles;
   p.rpart = ws_at<float>(q.ws, L.rpart);
   p.hpart = ws_at<float>(q.ws, L.hpart);
   p.zpart = ws_at<float>(q.ws, L.zpart);

@@ -9,8 +9,10 @@
 //
 // The work of a layer, (experts in use) x (256-column tiles) x (64-row chunks
 // of K), is one line of units of 32 KB of weights that the blocks share in
-// equal contiguous runs; a run's share of a tile leaves as a partial sum, and
-// the few partials of a column are added in order by whoever needs them next.
+// equal contiguous runs. A tile that one run holds whole goes on directly; the
+// parts of a shared one leave as partial sums, added in order of K: for layer
+// 1 by the block that writes the tile's last part, which then makes H of them,
+// for layer 2 in the combine.
 //
 // Warps: 0 weight producer (TMA), 1 MMA issuer and TMEM owner, 2 producer of
 // the token operand (TMA: x for layer 1, H for layer 2), 4-7 epilogue. The
@@ -85,8 +87,8 @@ __device__ __forceinline__ bool epi_all(bool v) {
 }
 
 // One layer's units and this block's run of them. G: the blocks that get any
-// (every one of them at least one unit). Units are fewer than 2^31 / 512:
-// their weights would not fit the device otherwise.
+// (every one of them at least one unit). total * G stays below 2^32: 2^32 / 512
+// units of 32 KB would not fit the device.
 struct FewLine {
   int N, KC, NT;
   unsigned total, G;
@@ -98,11 +100,11 @@ struct FewLine {
     G = min((unsigned)grid, total);
   }
   __device__ unsigned lo(unsigned b) const {
-    return b >= G ? total : (unsigned)((unsigned long long)total * b / G);
+    return b >= G ? total : total * b / G;
   }
   // The block whose run holds unit u: the largest b with lo(b) <= u.
   __device__ unsigned owner(unsigned u) const {
-    return (unsigned)(((unsigned long long)(u + 1) * G - 1) / total);
+    return ((u + 1) * G - 1) / total;
   }
   // Partial sums of column c of expert j.
   __device__ int pieces(int j, int c) const {
@@ -143,6 +145,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   __shared__ uint64_t acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
+  __shared__ bool last_part;
   volatile int *abort_flag = &abort_word;
   uint8_t *ring = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -165,7 +168,12 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     abort_word = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (threadIdx.x == 32) {
+    for (const CUtensorMap *m : {&tmX, &tmH, &tm1, &tm2})
+      asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory");
+  }
   if (warp == 1) {
+    __syncwarp();
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&tmem_slot)),
                  "r"(kTmemCols)
@@ -271,8 +279,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       for (int layer = 0; layer < 2 && go; ++layer) {
         const FewLine &l = line[layer];
         if (layer) {
-          // H is complete when every block has passed barrier 3.
-          const bool done = few_wait(p, 3, lane, 32, abort_flag);
+          // H is complete when every block has arrived at barrier 2.
+          const bool done = few_wait(p, 2, lane, 32, abort_flag);
           if (!__all_sync(0xffffffffu, done)) {
             *abort_flag = 1;
             break;
@@ -309,6 +317,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     } else if (warp >= 4) {
       // -------------------------------------------------------- epilogue
       const int quad = warp & 3, et = threadIdx.x - 128;
+      const __nv_bfloat16 *b1 = static_cast<const __nv_bfloat16 *>(p.b1);
+      __nv_bfloat16 *hout = static_cast<__nv_bfloat16 *>(p.h);
       int local = 0;
       bool go = true;
       for (int layer = 0; layer < 2 && go; ++layer) {
@@ -318,16 +328,23 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         for (unsigned u = l.lo(blockIdx.x); u < hi; ++local) {
           const FewSeg s = few_seg(l, u, hi);
           const int buf = local & 1;
-          go = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], (local >> 1) & 1u, abort_flag,
-                                                 p.st, 116, p.wait_ns));
+          // In layer 1 the four warps meet below: they go on or leave together.
+          go = mbar_wait(&acc_full[buf], (local >> 1) & 1u, abort_flag, p.st, 116, p.wait_ns);
+          go = layer ? __all_sync(0xffffffffu, go) : epi_all(go);
           if (!go) break;
           tc_fence_after();
           const int r0 = R.first[s.j], rows = R.first[s.j + 1] - r0;
           const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * 128);
           float *out = part + ((size_t)s.piece * R.rows + r0) * l.N;
+          // A whole tile of layer 1 becomes H here; a part of one leaves as a
+          // partial sum, and whoever writes a tile's last part joins them.
+          const bool whole = layer == 0 && s.kb0 == 0 && s.kb1 == l.KC;
+          const int e = R.expert[s.j];
           for (int h = 0; h < 2; ++h) {
             if (s.n0 + h * 128 >= l.N) break;
             const int n = s.n0 + h * 128 + quad * 32 + lane;
+            const float bias =
+                whole && b1 && n < l.N ? __bfloat162float(b1[(size_t)e * l.N + n]) : 0.f;
             for (int r = 0; r < rows; r += 8) {
               uint32_t a[8], v[8];
 #pragma unroll
@@ -337,34 +354,61 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
               }
               few_tmem8(a, v);
               if (n < l.N) {
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (r + i < rows) out[(size_t)(r + i) * l.N + n] = __uint_as_float(v[i]);
+                  for (int i = 0; i < 8; ++i)
+                    if (r + i < rows)
+                      hout[(size_t)(r0 + r + i) * l.N + n] =
+                          __float2bfloat16_rn(fmaxf(__uint_as_float(v[i]) + bias, 0.f));
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    if (r + i < rows) out[(size_t)(r + i) * l.N + n] = __uint_as_float(v[i]);
+                }
               }
             }
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[buf]);
+          if (layer == 0 && !whole) {
+            const int np = l.pieces(s.j, s.n0);
+            epi_all(true);  // the part is written
+            if (et == 0) {
+              __threadfence();
+              last_part = atomicAdd(p.tiles + s.j * l.NT + s.n0 / kTile, 1u) == (unsigned)np - 1;
+              __threadfence();
+            }
+            epi_all(true);
+            if (last_part) {
+              const int cols = min(kTile, l.N - s.n0) / 4;
+              const size_t step = (size_t)R.rows * l.N;
+              const float *src = part + (size_t)r0 * l.N + s.n0;
+              for (int i = et; i < rows * cols; i += kEpiThreads) {
+                const int r = i / cols, c = (i - r * cols) * 4;
+                float v[4] = {};
+#pragma unroll 4
+                for (int z = 0; z < np; ++z) few_add<4>(src + z * step + (size_t)r * l.N + c, v);
+                if (b1) {
+                  float b[4];
+                  few_ld<__nv_bfloat16, 4>(b1 + (size_t)e * l.N + s.n0 + c, b);
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) v[z] += b[z];
+                }
+#pragma unroll
+                for (int z = 0; z < 4; ++z) v[z] = fmaxf(v[z], 0.f);
+                few_st<__nv_bfloat16, 4>(hout + (size_t)(r0 + r) * l.N + s.n0 + c, v);
+              }
+            }
+          }
           u += s.kb1 - s.kb0;
         }
         if (layer == 0) {
-          // Join layer 1's partials into H between two barriers of the grid.
-          // Every decision to go on is taken by all four warps together.
+          // H's share of this block is written: TMA of every block may read it.
+          asm volatile("fence.proxy.async.global;" ::: "memory");
           go = epi_all(go && *abort_flag == 0);
-          if (go) {
-            if (et == 0) few_arrive(p, 2);
-            go = epi_all(few_wait(p, 2, et, kEpiThreads, abort_flag));
-          }
-          if (!go) {
-            *abort_flag = 1;
-          } else {
-            few_hidden<__nv_bfloat16, 4>(
-                p, R, [&](int j, int c) { return line[0].pieces(j, c); }, et, kEpiThreads);
-            asm volatile("fence.proxy.async.global;" ::: "memory");  // H is read by TMA
-            epi_all(true);
-            if (et == 0) few_arrive(p, 3);
-          }
+          if (!go) *abort_flag = 1;
+          else if (et == 0) few_arrive(p, 2);
         }
       }
     }
@@ -379,10 +423,10 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                  : "memory");
   }
   if (!ok || *abort_flag) {
-    if (threadIdx.x == 0) p.flags[blockIdx.x] = 0;
+    if (threadIdx.x == 0) *few_flag(p, 0, blockIdx.x) = 0;
     return;
   }
-  if (!few_barrier(p, 4)) return;
+  if (!few_barrier(p, 3)) return;
   const FewLine l2(R.n > 0 ? R.n : 1, p.F, p.d, gridDim.x);
   few_combine<__nv_bfloat16, 4>(p, R, [&](int j, int c) { return l2.pieces(j, c); });
 }
@@ -404,6 +448,11 @@ bool make_weight_map(CUtensorMap *m, const void *base, int E, int K, int N) {
 constexpr size_t kSmemMax = 227 * 1024 - 1024;  // less the static part
 
 }  // namespace
+
+int few_tc_tiles(const moe_config &c) {
+  const long long A = (long long)c.T * c.k;
+  return (int)((A < c.E ? A : c.E) * ((c.d_ff + kTile - 1) / kTile));
+}
 
 bool few_tc_supported(const moe_config &c) {
   return c.act_dtype == MOE_BF16 && c.d % 8 == 0 && c.d_ff % 8 == 0 && encode_fn() != nullptr;

@@ -250,7 +250,8 @@ cudaError_t launch_ffn_tc(const moe_config &cfg, int C, const void *xbuf, const 
 // k_few.cu: the whole layer for T <= 64 tokens in one cooperative launch.
 // thr: the threshold mask's [E] thresholds (null: the flat layer's gate).
 struct FewLayout {
-  size_t status, flags, idx, gate, rpart, hpart, zpart, h, total;
+  size_t status, flags, tiles, idx, gate, rpart, hpart, zpart, h, total;
+  int n_tiles;
 };
 FewLayout few_layout(const moe_config &cfg);
 struct FewCall {
