@@ -29,8 +29,32 @@ constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 
 constexpr int kFewColsMax = 256;   // columns of one unit of the experts' products at most
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
+// Division by a number that is fixed for the call, as a multiplication: the
+// quotient from floor((2^32 - 1) / d) is at most one too small. (A plain
+// division is some 150 cycles of latency, which the phases of a one-token call
+// would pay a dozen times in a row.)
+struct FewDiv {
+  unsigned d, inv;
+  __host__ __device__ FewDiv() : d(1), inv(0xffffffffu) {}
+  __host__ __device__ explicit FewDiv(unsigned v) : d(v), inv(0xffffffffu / v) {}
+  __device__ unsigned operator()(unsigned n) const {
+    const unsigned q = __umulhi(n, inv);
+    return q + (n - q * d >= d ? 1u : 0u);
+  }
+};
+
+// The router's units (few_router).
+struct FewRouter {
+  int NC, groups, slices, rows_per_slice;
+  int lcw;  // log2 of the columns of a unit
+  int lt;   // log2 of the warps side by side over the tokens
+  FewDiv by_group;
+};
+
 struct FewArgs {
   int T, d, E, F, k, C, mode;
+  FewRouter rt;
+  FewDiv by_k, by_d4, by_f4;  // k; d / 4 and d_ff / 4 (1 where they are not whole)
   const void *x;
   const float *Wg, *Wn, *noise, *bias, *thr;
   const void *W1, *b1, *W2, *b2;
@@ -69,9 +93,10 @@ namespace {
 __device__ __forceinline__ void few_flag_set(unsigned long long *f, unsigned long long v) {
   asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(f), "l"(v) : "memory");
 }
+// Relaxed: several can be in flight; the caller fences once it has seen them.
 __device__ __forceinline__ unsigned long long few_flag_get(const unsigned long long *f) {
   unsigned long long v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f) : "memory");
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(f) : "memory");
   return v;
 }
 
@@ -90,33 +115,35 @@ __device__ __forceinline__ void few_start(const FewArgs &p) {
 // Arrive at barrier b (one thread, after a barrier of the block's threads that
 // wrote): what they wrote before is visible to a block that has waited.
 __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
-  __threadfence();
-  few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);
+  few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);  // a release, cumulative over the barrier
 }
 
 // Wait for barrier b (threads tid of n_threads of the block); false: leave the
 // kernel. With an abort flag, a set one ends the wait too.
 __device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n_threads,
                                          volatile int *abort_flag = nullptr) {
-  bool ok = true;
   unsigned long long t0 = 0;
-  for (int i = tid; i < (int)gridDim.x && ok; i += n_threads) {
-    const unsigned long long *f = few_flag(p, b, i);
-    while (few_flag_get(f) != p.nonce) {
+  for (int i0 = tid; i0 < (int)gridDim.x; i0 += 8 * n_threads) {
+    for (;;) {
+      // Up to eight flags a thread, looked at together.
+      bool all = true;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = i0 + j * n_threads;
+        if (i < (int)gridDim.x) all &= few_flag_get(few_flag(p, b, i)) == p.nonce;
+      }
+      if (all) break;
       const unsigned long long now = globaltimer();
       if (t0 == 0) t0 = now;
-      if (abort_flag && *abort_flag) {
-        ok = false;
-        break;
-      }
+      if (abort_flag && *abort_flag) return false;
       if (now - t0 >= p.wait_ns) {
         record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
-        ok = false;
-        break;
+        return false;
       }
     }
   }
-  return ok;
+  __threadfence();  // the flags' acquire
+  return true;
 }
 
 __device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
@@ -149,21 +176,21 @@ __device__ __forceinline__ __nv_bfloat16 few_t<__nv_bfloat16>(float v) {
 // warps of the same tokens share the rows. Every product is fp32.
 constexpr int kRtRows = 64;
 
-struct FewRouter {
-  int NC, cw, groups, slices, rows_per_slice;
-};
-__host__ __device__ inline FewRouter few_router(int d, int E, bool noisy, int grid) {
+inline FewRouter few_router(int T, int d, int E, bool noisy, int grid) {
   FewRouter r;
   r.NC = noisy ? 2 * E : E;
-  r.cw = 1;
-  while (r.cw < 32 && r.cw < r.NC) r.cw *= 2;
-  r.groups = (r.NC + r.cw - 1) / r.cw;
+  r.lcw = 0;
+  while (r.lcw < 5 && (1 << r.lcw) < r.NC) ++r.lcw;
+  r.groups = (r.NC + (1 << r.lcw) - 1) >> r.lcw;
   int s = grid / r.groups;
   const int most = (d + 31) / 32;  // slices of at least 32 rows
   if (s > most) s = most;
   if (s < 1) s = 1;
   r.rows_per_slice = ((d + s - 1) / s + 7) / 8 * 8;
   r.slices = (d + r.rows_per_slice - 1) / r.rows_per_slice;
+  r.lt = 0;
+  while ((8 << r.lt) < T) ++r.lt;
+  r.by_group = FewDiv((unsigned)r.groups);
   return r;
 }
 
@@ -195,61 +222,68 @@ __device__ __forceinline__ void few_x8(const T *x, int d, int k, float (&f)[8]) 
 // 32 KB at most.
 template <typename T>
 __device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
-  const FewRouter r = few_router(p.d, p.E, p.Wn != nullptr, gridDim.x);
-  const int tg = (p.T + 7) / 8, tp = tg * 8;
-  int tgp = 1;  // warps side by side over the tokens: 1, 2, 4 or 8
-  while (tgp < tg) tgp *= 2;
-  const int ks = 8 / tgp;  // warps that share a token group's rows
-  float *xs = smem, *ws = xs + kRtRows * tp, *red = ws + kRtRows * r.cw;
+  const FewRouter &r = p.rt;
+  const int tgp = 1 << r.lt, tp = 8 << r.lt;  // warps, tokens side by side
+  const int ks = 8 >> r.lt;                   // warps that share a token group's rows
+  const int cw = 1 << r.lcw;
+  float *xs = smem, *ws = xs + kRtRows * tp, *red = ws + kRtRows * cw;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tgi = warp & (tgp - 1), kp = warp / tgp;
-  const int lrows = 32 / r.cw, lr = lane / r.cw, lc = lane & (r.cw - 1);
+  const int tgi = warp & (tgp - 1), kp = warp >> r.lt;
+  const int lrows = 32 >> r.lcw, lr = lane >> r.lcw, lc = lane & (cw - 1);
   const T *x = static_cast<const T *>(p.x);
+  int xt[2], xo[2];  // the token and the 8 columns that this thread stages
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xo[i] = ((i * kFewThreads + tid) >> (3 + r.lt)) * 8;
+    xt[i] = (i * kFewThreads + tid) & (tp - 1);
+  }
   for (int u = blockIdx.x; u < r.groups * r.slices; u += gridDim.x) {
-    const int g = u % r.groups, s = u / r.groups;
+    const int s = (int)r.by_group(u), g = u - s * r.groups;
     const int k0 = s * r.rows_per_slice, k1 = min(p.d, k0 + r.rows_per_slice);
+    const int col0 = g << r.lcw;
     float acc[8] = {};
-    for (int kb = k0; kb < k1; kb += kRtRows) {
+    float wv[8], xv[2][8];
+    // The next 64 rows are in flight while these are multiplied.
+    auto fetch = [&](int kb) {
       const int n = min(kRtRows, k1 - kb);
-      // The weights' loads are issued before anything is waited for.
-      float wv[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int at = i * kFewThreads + tid, kk = at / r.cw, col = g * r.cw + (at & (r.cw - 1));
+        const int at = i * kFewThreads + tid, kk = at >> r.lcw, col = col0 + (at & (cw - 1));
         wv[i] = 0.f;
-        if (at < kRtRows * r.cw && kk < n && col < r.NC)
+        if (kk < n && col < r.NC)
           wv[i] = col < p.E ? p.Wg[(size_t)(kb + kk) * p.E + col]
                             : p.Wn[(size_t)(kb + kk) * p.E + col - p.E];
       }
-      float xv[2][8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int at = i * kFewThreads + tid, t = at % tp, ko = at / tp * 8;
-        if (ko < kRtRows && t < p.T && ko < n) {
-          few_x8<T>(x + (size_t)t * p.d, p.d, kb + ko, xv[i]);
+        if (xt[i] < p.T && xo[i] < n) {
+          few_x8<T>(x + (size_t)xt[i] * p.d, p.d, kb + xo[i], xv[i]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) xv[i][j] = 0.f;
         }
       }
+    };
+    fetch(k0);
+    for (int kb = k0; kb < k1; kb += kRtRows) {
+      const int n = min(kRtRows, k1 - kb);
       __syncthreads();  // the previous rows have been used
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int at = i * kFewThreads + tid;
-        if (at < kRtRows * r.cw) ws[at] = wv[i];
+        if (at < kRtRows * cw) ws[at] = wv[i];
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int at = i * kFewThreads + tid, t = at % tp, ko = at / tp * 8;
-        if (ko < kRtRows)
+      for (int i = 0; i < 2; ++i)
+        if (xo[i] < kRtRows)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) xs[(ko + j) * tp + t] = xv[i][j];
-      }
+          for (int j = 0; j < 8; ++j) xs[(xo[i] + j) * tp + xt[i]] = xv[i][j];
       __syncthreads();
-      if (tgi < tg) {
+      if (kb + kRtRows < k1) fetch(kb + kRtRows);
+      if (tgi * 8 < p.T) {
 #pragma unroll 4
         for (int kk = kp * lrows + lr; kk < n; kk += ks * lrows) {
-          const float w = ws[kk * r.cw + lc];
+          const float w = ws[kk * cw + lc];
           const float4 a = *reinterpret_cast<const float4 *>(xs + kk * tp + tgi * 8);
           const float4 b = *reinterpret_cast<const float4 *>(xs + kk * tp + tgi * 8 + 4);
           acc[0] = fmaf(w, a.x, acc[0]);
@@ -266,13 +300,13 @@ __device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
     // Over the lanes' rows, then over the warps of the same tokens.
 #pragma unroll
     for (int t = 0; t < 8; ++t)
-      for (int o = r.cw; o < 32; o <<= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
+      for (int o = cw; o < 32; o <<= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
     if (lr == 0)
 #pragma unroll
       for (int t = 0; t < 8; ++t) red[(warp * 8 + t) * 32 + lc] = acc[t];
     __syncthreads();
-    for (int i = tid; i < tp * r.cw; i += kFewThreads) {
-      const int t = i / r.cw, c = i & (r.cw - 1), col = g * r.cw + c;
+    for (int i = tid; i < tp * cw; i += kFewThreads) {
+      const int t = i >> r.lcw, c = i & (cw - 1), col = col0 + c;
       if (t >= p.T || col >= r.NC) continue;
       float v = 0.f;
       for (int w = 0; w < ks; ++w) v += red[((w * tgp + t / 8) * 8 + t % 8) * 32 + c];
@@ -284,6 +318,12 @@ __device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
 // ----------------------------------------------------------------------------- selection
 __device__ __forceinline__ float few_softplus(float z) {
   return fmaxf(z, 0.f) + log1pf(expf(-fabsf(z)));
+}
+
+// A float's order as an unsigned number; NaN is lowest.
+__device__ __forceinline__ uint32_t few_key(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return isnan(v) ? 0u : b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // Block reduction of a float over 256 threads (red: 8 floats of shared memory).
@@ -311,49 +351,80 @@ __device__ __forceinline__ float few_block(float v, float *red) {
 // smem: H [E] floats, red [8], taken words [32], sums [2][256].
 template <typename T>
 __device__ __forceinline__ void few_select(const FewArgs &p, float *smem) {
-  const FewRouter r = few_router(p.d, p.E, p.Wn != nullptr, gridDim.x);
+  const FewRouter &r = p.rt;
   float *H = smem;
   float *red = smem + p.E;
   uint32_t *words = reinterpret_cast<uint32_t *>(red + 8);
   float *sums = red + 40;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // Threads side by side over the experts, the rest over the slices.
-  int pe = 1;
-  while (pe < p.E && pe < kFewThreads) pe *= 2;
-  const int nl = kFewThreads / pe, sl = tid / pe;
+  const int lpe = min(8, 32 - __clz(p.E - 1)), pe = 1 << lpe;
+  const int nl = kFewThreads >> lpe, sl = tid >> lpe;
   for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
     float mx = -INFINITY;
     __syncthreads();
-    for (int e0 = 0; e0 < p.E; e0 += pe) {
-      const int e = e0 + (tid & (pe - 1));
-      float c = 0.f, z = 0.f;
-      if (e < p.E) {
-        const float *q = p.rpart + (size_t)t * r.NC + e;
-        const size_t step = (size_t)p.T * r.NC;
-#pragma unroll 8
-        for (int s = sl; s < r.slices; s += nl) {
-          c += q[s * step];
-          if (p.Wn) z += q[s * step + p.E];
+    // Up to four experts a thread, four slices at a time, all the loads of a
+    // round in flight together (places past the end read the first one).
+    float c[4] = {}, z[4] = {}, add[4] = {}, noise[4] = {};
+    const int e0 = tid & (pe - 1);
+    const float *q = p.rpart + (size_t)t * r.NC;
+    const size_t step = (size_t)p.T * r.NC;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i * pe;
+      if (sl == 0 && e < p.E) {
+        if (p.bias) add[i] = p.bias[e];
+        if (p.Wn) noise[i] = p.noise[(size_t)t * p.E + e];
+      }
+    }
+    for (int s0 = sl; s0 < r.slices; s0 += 4 * nl) {
+      float vc[4][4], vz[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i * pe >= p.E) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = e0 + i * pe, s = s0 + j * nl;
+          const float *at = q + (s < r.slices ? s * step : 0) + (e < p.E ? e : 0);
+          vc[i][j] = __ldcg(at);
+          if (p.Wn) vz[i][j] = __ldcg(at + p.E);
         }
       }
-      if (nl > 1) {
-        __syncthreads();
-        sums[tid] = c;
-        sums[kFewThreads + tid] = z;
-        __syncthreads();
-        if (sl == 0)
-          for (int i = 1; i < nl; ++i) {
-            c += sums[i * pe + tid];
-            z += sums[kFewThreads + i * pe + tid];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i * pe >= p.E) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (s0 + j * nl < r.slices) {
+            c[i] += vc[i][j];
+            if (p.Wn) z[i] += vz[i][j];
           }
       }
-      if (sl == 0 && e < p.E) {
-        if (p.bias) c += p.bias[e];
-        if (p.Wn) c = fmaf(p.noise[(size_t)t * p.E + e], few_softplus(z), c);
-        if (!isfinite(c)) record_error(p.st, MOE_ERR_NONFINITE, (long long)t * p.E + e);
-        H[e] = c;
-        mx = fmaxf(mx, c);
+    }
+    if (nl > 1) {  // then E <= 128: one expert a thread
+      sums[tid] = c[0];
+      sums[kFewThreads + tid] = z[0];
+      __syncthreads();
+      if (sl == 0) {
+        float cs = 0.f, zs = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < nl; ++i) {
+          cs += sums[i * pe + tid];
+          zs += sums[kFewThreads + i * pe + tid];
+        }
+        c[0] = cs;
+        z[0] = zs;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + i * pe;
+      if (sl != 0 || e >= p.E) continue;
+      float h = c[i] + add[i];
+      if (p.Wn) h = fmaf(noise[i], few_softplus(z[i]), h);
+      if (!isfinite(h)) record_error(p.st, MOE_ERR_NONFINITE, (long long)t * p.E + e);
+      H[e] = h;
+      mx = fmaxf(mx, h);
     }
     int32_t *oi = p.idx + (size_t)t * p.k;
     float *og = p.gate + (size_t)t * p.k;
@@ -406,48 +477,40 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem) {
       }
     } else if (warp == 0) {
       // Lane l ranks experts l, l + 32, ...; `done` marks the chosen ones. A
-      // lane looks its experts through again only after it gave one away.
-      uint32_t done = 0;
-      float top = 0.f, g = 0.f, sum = 0.f, lv = -INFINITY;
-      int mine = 0, le = 0x7fffffff;
+      // lane looks its experts through again only after it gave one away. The
+      // warp's choice is two integer reductions: the largest key, then the
+      // lowest index that has it.
+      uint32_t done = 0, lk = 0;
+      int le = 0x7fffffff, mine = 0;
       bool look = true;
       for (int j = 0; j < p.k; ++j) {
         if (look) {
-          lv = -INFINITY;
+          lk = 0;
           le = 0x7fffffff;
+#pragma unroll 4
           for (int e = lane, q = 0; e < p.E; e += 32, ++q) {
-            if ((done >> q) & 1u) continue;
-            const float v = isnan(H[e]) ? -INFINITY : H[e];
-            if (le == 0x7fffffff || v > lv) {
-              lv = v;
+            const uint32_t key = few_key(H[e]);
+            if (!((done >> q) & 1u) && (le == 0x7fffffff || key > lk)) {
+              lk = key;
               le = e;
             }
           }
         }
-        float bv = lv;
-        int be = le;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-          const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-          if (oe != 0x7fffffff && (be == 0x7fffffff || ov > bv || (ov == bv && oe < be))) {
-            bv = ov;
-            be = oe;
-          }
-        }
-        look = (be & 31) == lane;
-        if (look) done |= 1u << (be >> 5);
-        if (j == 0) top = bv;
-        const float w = expf(bv - top);
-        sum += w;
-        if (lane == j) {
-          g = w;
-          mine = be;
-        }
+        const uint32_t best = __reduce_max_sync(0xffffffffu, lk);
+        const int e = (int)__reduce_min_sync(0xffffffffu, lk == best ? (uint32_t)le : 0x7fffffffu);
+        look = (e & 31) == lane;
+        if (look) done |= 1u << (e >> 5);
+        if (lane == j) mine = e;
       }
+      const float v = lane < p.k ? H[mine] : -INFINITY;
+      const float top = __shfl_sync(0xffffffffu, v, 0);  // every lane takes part
+      const float w = lane < p.k ? expf(v - top) : 0.f;
+      float sum = w;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane < p.k) {
         oi[lane] = mine;
-        og[lane] = p.mode == kFewSwitch ? 1.f / se : g / sum;
+        og[lane] = p.mode == kFewSwitch ? 1.f / se : w / sum;
       }
     }
   }
@@ -459,10 +522,11 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem) {
 // token. A token picks an expert at most once, so a choice's slot is the
 // number of earlier tokens in the expert's 64-bit mask.
 struct FewRows {
-  unsigned long long *tokens;  // [E] tokens of each expert
+  unsigned long long *tokens;  // [E] tokens of each expert (bit t)
   int *expert;                 // [<= kFewRows] experts in use
   int *first;                  // [<= kFewRows + 1] their first packed row
   int *base;                   // [E] first packed row of every expert
+  int16_t *place;              // [E] its place in `expert`
   uint16_t *owner;             // [<= kFewRows] each packed row's place in `expert`
   int16_t *row;                // [T k] packed row of each choice, or -1
   float *gate;                 // [T k]
@@ -470,7 +534,7 @@ struct FewRows {
   int n, rows;                 // experts in use; rows
 };
 constexpr size_t few_rows_bytes(int E, int A) {
-  return ((size_t)E * 12 + ((size_t)2 * A + 2) * 4 + (size_t)A * 9 + 63) / 64 * 64;
+  return ((size_t)E * 14 + ((size_t)2 * A + 2) * 4 + (size_t)A * 9 + 63) / 64 * 64;
 }
 
 __device__ FewRows few_rows(const FewArgs &p, char *smem) {
@@ -483,7 +547,8 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   R.gate = reinterpret_cast<float *>(R.first + A + 1);
   R.owner = reinterpret_cast<uint16_t *>(R.gate + A);
   R.row = reinterpret_cast<int16_t *>(R.owner + A);
-  R.token = reinterpret_cast<uint8_t *>(R.row + A);
+  R.place = R.row + A;
+  R.token = reinterpret_cast<uint8_t *>(R.place + p.E);
   __shared__ int scan[8][2], total[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int choice[kFewRows / kFewThreads];
@@ -497,8 +562,10 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kFewRows / kFewThreads; ++i)
-    if (choice[i] >= 0 && choice[i] < p.E)
-      atomicOr(&R.tokens[choice[i]], 1ull << ((i * kFewThreads + tid) / p.k));
+    if (choice[i] >= 0 && choice[i] < p.E) {
+      const int t = (int)p.by_k(i * kFewThreads + tid);  // 32-bit halves: one native atomic each
+      atomicOr(reinterpret_cast<uint32_t *>(&R.tokens[choice[i]]) + (t >> 5), 1u << (t & 31));
+    }
   __syncthreads();
   // Exclusive sums over the experts of (in use, rows), 4 experts a thread.
   int use = 0, rows = 0;
@@ -542,7 +609,7 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
     if (n > 0) {
       R.expert[bu] = e;
       R.first[bu] = br;
-      for (int r = 0; r < n; ++r) R.owner[br + r] = (uint16_t)bu;
+      R.place[e] = (int16_t)bu;
       ++bu;
       br += n;
     }
@@ -552,13 +619,16 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   R.rows = total[1];
 #pragma unroll
   for (int i = 0; i < kFewRows / kFewThreads; ++i) {
-    const int a = i * kFewThreads + tid, e = choice[i], t = a / p.k;
+    const int a = i * kFewThreads + tid, e = choice[i], t = (int)p.by_k(a);
     if (a >= A) break;
     const bool some = e >= 0 && e < p.E;
     const int pos = some ? __popcll(R.tokens[e] & ((1ull << t) - 1)) : -1;
     const bool kept = some && pos < p.C;
     R.row[a] = kept ? (int16_t)(R.base[e] + pos) : (int16_t)-1;
-    if (kept) R.token[R.base[e] + pos] = (uint8_t)t;
+    if (kept) {
+      R.token[R.base[e] + pos] = (uint8_t)t;
+      R.owner[R.base[e] + pos] = (uint16_t)R.place[e];
+    }
     if (blockIdx.x == 0) {
       if (p.pos) p.pos[a] = pos;
       if (p.keep) p.keep[a] = kept;
@@ -610,9 +680,10 @@ __device__ __forceinline__ void few_hidden(const FewArgs &p, const FewRows &R, c
   const T *b1 = static_cast<const T *>(p.b1);
   T *h = static_cast<T *>(p.h);
   const unsigned cols = p.F / V, total = R.rows * cols;
+  const FewDiv by = V == 4 ? p.by_f4 : FewDiv(cols);
   const size_t step = (size_t)R.rows * p.F;
   for (unsigned i = blockIdx.x * n_threads + tid; i < total; i += gridDim.x * n_threads) {
-    const unsigned row = i / cols, c = (i - row * cols) * V;
+    const unsigned row = by(i), c = (i - row * cols) * V;
     const int j = R.owner[row], np = pieces(j, (int)c);
     const float *src = p.hpart + (size_t)row * p.F + c;
     float v[V] = {};
@@ -631,7 +702,10 @@ __device__ __forceinline__ void few_hidden(const FewArgs &p, const FewRows &R, c
 }
 
 // y[t] = x[t] + sum over the kept choices, in order, of gate * (sum of the
-// partial sums + b2), in fp32, rounded once.
+// partial sums + b2), in fp32, rounded once. V columns a thread; where that
+// leaves most threads idle (few tokens, whose partials are many), 8 lanes
+// share the partials of the same columns, each adding every 8th, joined in a
+// fixed order.
 template <typename T, int V, typename PF>
 __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
                                             const PF &pieces) {
@@ -639,11 +713,16 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
   T *y = static_cast<T *>(p.y);
   const unsigned cols = p.d / V, total = p.T * cols;
   const size_t step = (size_t)R.rows * p.d;
-  for (unsigned i = blockIdx.x * kFewThreads + threadIdx.x; i < total;
-       i += gridDim.x * kFewThreads) {
-    const unsigned t = i / cols, c = (i - t * cols) * V;
-    float acc[V];
-    few_ld<T, V>(x + (size_t)t * p.d + c, acc);
+  const FewDiv by = V == 4 ? p.by_d4 : FewDiv(cols);
+  const unsigned lshare = total * 8 <= gridDim.x * kFewThreads ? 3 : 0, share = 1u << lshare;
+  const unsigned sub = threadIdx.x & (share - 1), lane = threadIdx.x & 31;
+  for (unsigned w = blockIdx.x * kFewThreads + threadIdx.x; w - lane < total * share;
+       w += gridDim.x * kFewThreads) {  // whole warps go round together
+    const unsigned i = w >> lshare;
+    const bool live = i < total;
+    const unsigned t = live ? by(i) : 0, c = live ? (i - t * cols) * V : 0;
+    float acc[V] = {};
+    if (live) few_ld<T, V>(x + (size_t)t * p.d + c, acc);
     // Four choices side by side, so that their loads overlap; each choice's
     // partials are added in order, then the choices in order.
     for (int q0 = 0; q0 < p.k; q0 += 4) {
@@ -651,15 +730,22 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
       int row[4], np[4], most = 0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        row[q] = q0 + q < p.k ? R.row[t * p.k + q0 + q] : -1;
+        row[q] = live && q0 + q < p.k ? R.row[t * p.k + q0 + q] : -1;
         np[q] = row[q] >= 0 ? pieces(R.owner[row[q]], (int)c) : 0;
         most = max(most, np[q]);
       }
-#pragma unroll 2
-      for (int s = 0; s < most; ++s)
+#pragma unroll 4
+      for (int s = (int)sub; s < most; s += (int)share)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (s < np[q]) few_add<V>(p.zpart + s * step + (size_t)row[q] * p.d + c, v[q]);
+      if (share == 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int z = 0; z < V; ++z)
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) v[q][z] += __shfl_xor_sync(0xffffffffu, v[q][z], o);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (row[q] < 0) continue;
@@ -674,6 +760,7 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
         for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[q][z], acc[z]);
       }
     }
+    if (!live || sub) continue;
     bool bad = false;
 #pragma unroll
     for (int z = 0; z < V; ++z) bad |= !isfinite(acc[z]);

@@ -165,7 +165,9 @@ cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
   const size_t smem = kSimtSmemFloats * 4 + few_rows_bytes(p.E, p.T * p.k);
   int grid = 2 * sm_count();  // two blocks fit an SM (launch bounds, 62 KB at most)
   if (grid > kFewMaxGrid) grid = kFewMaxGrid;
-  void *args[1] = {const_cast<FewArgs *>(&p)};
+  FewArgs a = p;
+  a.rt = few_router(p.T, p.d, p.E, p.Wn != nullptr, grid);
+  void *args[1] = {&a};
   return launch_few_grid(reinterpret_cast<const void *>(k_few_simt<T, VEC>), args, grid, smem, s);
 }
 
@@ -227,6 +229,9 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.k = c.k;
   p.C = q.capacity;
   p.mode = q.thr ? kFewThreshold : c.gate_mode == MOE_GATE_SWITCH ? kFewSwitch : kFewTopk;
+  p.by_k = FewDiv(c.k);
+  p.by_d4 = FewDiv(c.d % 4 == 0 ? c.d / 4 : 1);
+  p.by_f4 = FewDiv(c.d_ff % 4 == 0 ? c.d_ff / 4 : 1);
   p.x = q.x;
   p.Wg = q.Wg;
   p.Wn = q.Wn;

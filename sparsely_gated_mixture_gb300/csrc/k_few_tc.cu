@@ -47,11 +47,14 @@ __device__ __forceinline__ void few_mma(uint32_t d, uint64_t a, uint64_t b, uint
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// A box of weights, first to leave L2: each is read once, and what the blocks
+// exchange should stay (40 tokens over 1024 experts 93 -> 87 us).
 __device__ __forceinline__ void few_tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
                                            int y, int z) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "{\n .reg .b64 pol;\n createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n"
+      " cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], pol;\n}\n" ::"r"(smem_u32(dst)),
       "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
@@ -86,48 +89,67 @@ __device__ __forceinline__ bool epi_all(bool v) {
   return out != 0;
 }
 
-// One layer's units and this block's run of them. G: the blocks that get any
-// (every one of them at least one unit). total * G stays below 2^32: 2^32 / 512
-// units of 32 KB would not fit the device.
+// One layer's units and this block's run of them, [lo, hi). G: the blocks that
+// get any (every one of them at least two units, unless there is but one: with
+// one unit each, the smallest layers gain less from the wider load than the
+// doubled partial sums cost, 34.2 against 31.7 us for the noisy top-4 layer's
+// token). total * G stays below 2^32: 2^32 / 512 units of 32 KB would not fit
+// the device.
 struct FewLine {
   int N, KC, NT;
-  unsigned total, G;
-  __device__ FewLine(int n_experts, int K, int n, int grid) {
+  unsigned total, G, lo, hi;
+  FewDiv by_total;
+  // Where the run begins: expert j of those in use, column tile nt, chunk kb;
+  // the piece of its tile that it makes.
+  int j, nt, kb, piece;
+
+  // By one thread, for all others to use.
+  __device__ void make(int n_experts, int K, int n, int grid) {
     N = n;
     KC = (K + kChunk - 1) / kChunk;
     NT = (n + kTile - 1) / kTile;
     total = (unsigned)n_experts * NT * KC;
-    G = min((unsigned)grid, total);
+    G = max(1u, min((unsigned)grid, total / 2));
+    by_total = FewDiv(total);
+    const FewDiv by_g(G);
+    const unsigned b = min((unsigned)blockIdx.x, G);
+    lo = b == G ? total : by_g(total * b);
+    hi = b == G ? total : by_g(total * (b + 1));
+    const unsigned tile = lo / KC;
+    j = (int)(tile / NT);
+    nt = (int)(tile - (unsigned)j * NT);
+    kb = (int)(lo - tile * KC);
+    piece = (int)(blockIdx.x - owner(tile * KC));
   }
-  __device__ unsigned lo(unsigned b) const {
-    return b >= G ? total : total * b / G;
-  }
-  // The block whose run holds unit u: the largest b with lo(b) <= u.
-  __device__ unsigned owner(unsigned u) const {
-    return ((u + 1) * G - 1) / total;
-  }
-  // Partial sums of column c of expert j.
-  __device__ int pieces(int j, int c) const {
-    const unsigned tile = (unsigned)j * NT + c / kTile;
-    return (int)(owner(tile * KC + KC - 1) - owner(tile * KC)) + 1;
+  // The block whose run holds unit u: the largest b with floor(total b / G) <= u.
+  __device__ unsigned owner(unsigned u) const { return by_total((u + 1) * G - 1); }
+  // Partial sums of column c of expert jj.
+  __device__ int pieces(int jj, int c) const {
+    const unsigned u = ((unsigned)jj * NT + c / kTile) * KC;
+    return (int)(owner(u + KC - 1) - owner(u)) + 1;
   }
 };
 
-// A run's share of one tile: expert j, columns from n0, chunks [kb0, kb1), the
-// piece it makes.
+// The shares of tiles that make up a block's run, in order: expert j, columns
+// from nt * kTile, chunks [kb0, kb1), and which piece of the tile it is.
 struct FewSeg {
-  int j, n0, kb0, kb1, piece;
+  int j, nt, kb0, kb1, piece;
+  unsigned left;  // units from kb0 to the run's end
+  __device__ explicit FewSeg(const FewLine &l)
+      : j(l.j), nt(l.nt), kb0(l.kb), piece(l.piece), left(l.hi - l.lo) {
+    kb1 = (int)min((unsigned)l.KC, kb0 + left);
+  }
+  __device__ bool more() const { return left > 0; }
+  __device__ void next(const FewLine &l) {
+    left -= kb1 - kb0;
+    kb0 = piece = 0;  // a tile begun by this run: its first piece
+    if (++nt == l.NT) {
+      nt = 0;
+      ++j;
+    }
+    kb1 = (int)min((unsigned)l.KC, left);
+  }
 };
-__device__ __forceinline__ FewSeg few_seg(const FewLine &l, unsigned u, unsigned hi) {
-  FewSeg s;
-  const unsigned tile = u / l.KC;
-  s.j = tile / l.NT;
-  s.n0 = (int)(tile - (unsigned)s.j * l.NT) * kTile;
-  s.kb0 = (int)(u - tile * l.KC);
-  s.kb1 = min(l.KC, s.kb0 + (int)(hi - u));
-  s.piece = (int)(blockIdx.x - l.owner(tile * l.KC));
-  return s;
-}
 
 struct FewTc {
   int stages, tok_bytes;  // ring stages; bytes of a stage's token operand
@@ -146,6 +168,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ bool last_part;
+  __shared__ __align__(16) unsigned char line_mem[2 * sizeof(FewLine)];
+  FewLine *line = reinterpret_cast<FewLine *>(line_mem);
   volatile int *abort_flag = &abort_word;
   uint8_t *ring = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -194,10 +218,11 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   const uint32_t tmem = tmem_slot;
   FewRows R{};
   if (ok) R = few_rows(p, reinterpret_cast<char *>(rows_mem));
+  if (ok && R.n > 0 && lane == 0 && warp < 2)
+    line[warp].make(R.n, warp ? p.F : p.d, warp ? p.d : p.F, gridDim.x);
   fence_proxy_async_smem();  // generic accesses to the ring come before TMA's
   __syncthreads();
   if (ok && R.n > 0) {
-    const FewLine line[2] = {FewLine(R.n, p.d, p.F, gridDim.x), FewLine(R.n, p.F, p.d, gridDim.x)};
     if (warp == 0) {
       if (lane == 0) {
         // ------------------------------------------------------ weight producer
@@ -206,10 +231,9 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         for (int layer = 0; layer < 2 && go; ++layer) {
           const FewLine &l = line[layer];
           const CUtensorMap *tm = layer ? &tm2 : &tm1;
-          const unsigned hi = l.lo(blockIdx.x + 1);
-          for (unsigned u = l.lo(blockIdx.x); u < hi && go;) {
-            const FewSeg s = few_seg(l, u, hi);
-            const int e = R.expert[s.j], boxes = min(4, (l.N - s.n0 + 63) / 64);
+          for (FewSeg s(l); s.more() && go; s.next(l)) {
+            const int n0 = s.nt * kTile;
+            const int e = R.expert[s.j], boxes = min(4, (l.N - n0 + 63) / 64);
             for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
               const int st = it % S;
               if (!mbar_wait(&empty[st], ((it / S) & 1u) ^ 1u, abort_flag, p.st, 111, p.wait_ns)) {
@@ -219,9 +243,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
               mbar_expect_tx(&full_w[st], boxes * kBoxBytes);
               for (int b = 0; b < boxes; ++b)
                 few_tma_3d(ring + (size_t)st * stage + b * kBoxBytes, tm, &full_w[st],
-                           s.n0 + b * 64, kb * kChunk, e);
+                           n0 + b * 64, kb * kChunk, e);
             }
-            u += s.kb1 - s.kb0;
           }
         }
         for (uint32_t i = it > (uint32_t)S ? it - S : 0; i < it; ++i)
@@ -235,9 +258,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         bool go = true;
         for (int layer = 0; layer < 2 && go; ++layer) {
           const FewLine &l = line[layer];
-          const unsigned hi = l.lo(blockIdx.x + 1);
-          for (unsigned u = l.lo(blockIdx.x); u < hi && go; ++local) {
-            const FewSeg s = few_seg(l, u, hi);
+          for (FewSeg s(l); s.more() && go; s.next(l), ++local) {
             const int buf = local & 1;
             if (!mbar_wait(&acc_empty[buf], ((local >> 1) & 1u) ^ 1u, abort_flag, p.st, 112,
                            p.wait_ns))
@@ -246,7 +267,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
             const int toks = layer ? R.first[s.j + 1] - R.first[s.j] : p.T;
             const uint32_t idesc = few_idesc((toks + 15) / 16 * 16);
             const uint32_t d0 = tmem + (uint32_t)(buf * 128);
-            const int halves = l.N - s.n0 > 128 ? 2 : 1;
+            const int halves = l.N - s.nt * kTile > 128 ? 2 : 1;
             for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
               const int st = it % S;
               const uint32_t ph = (it / S) & 1u;
@@ -266,7 +287,6 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
               umma_commit(&empty[st]);
             }
             if (go) umma_commit(&acc_full[buf]);
-            u += s.kb1 - s.kb0;
           }
         }
         umma_commit(&drain);
@@ -287,9 +307,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           }
           asm volatile("fence.proxy.async.global;" ::: "memory");
         }
-        const unsigned hi = l.lo(blockIdx.x + 1);
-        for (unsigned u = l.lo(blockIdx.x); u < hi && go;) {
-          const FewSeg s = few_seg(l, u, hi);
+        for (FewSeg s(l); s.more() && go; s.next(l)) {
           if (lane == 0) {
             const int r0 = R.first[s.j], rows = R.first[s.j + 1] - r0;
             const int boxes = layer ? (rows + 15) / 16 : 1;
@@ -308,7 +326,6 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
             }
           }
           go = __shfl_sync(0xffffffffu, go, 0);
-          u += s.kb1 - s.kb0;
         }
       }
       if (lane == 0)
@@ -324,10 +341,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       for (int layer = 0; layer < 2 && go; ++layer) {
         const FewLine &l = line[layer];
         float *part = layer ? p.zpart : p.hpart;
-        const unsigned hi = l.lo(blockIdx.x + 1);
-        for (unsigned u = l.lo(blockIdx.x); u < hi; ++local) {
-          const FewSeg s = few_seg(l, u, hi);
-          const int buf = local & 1;
+        for (FewSeg s(l); s.more(); s.next(l), ++local) {
+          const int buf = local & 1, n0 = s.nt * kTile;
           // In layer 1 the four warps meet below: they go on or leave together.
           go = mbar_wait(&acc_full[buf], (local >> 1) & 1u, abort_flag, p.st, 116, p.wait_ns);
           go = layer ? __all_sync(0xffffffffu, go) : epi_all(go);
@@ -341,8 +356,8 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           const bool whole = layer == 0 && s.kb0 == 0 && s.kb1 == l.KC;
           const int e = R.expert[s.j];
           for (int h = 0; h < 2; ++h) {
-            if (s.n0 + h * 128 >= l.N) break;
-            const int n = s.n0 + h * 128 + quad * 32 + lane;
+            if (n0 + h * 128 >= l.N) break;
+            const int n = n0 + h * 128 + quad * 32 + lane;
             const float bias =
                 whole && b1 && n < l.N ? __bfloat162float(b1[(size_t)e * l.N + n]) : 0.f;
             for (int r = 0; r < rows; r += 8) {
@@ -372,36 +387,49 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[buf]);
           if (layer == 0 && !whole) {
-            const int np = l.pieces(s.j, s.n0);
+            const int np = l.pieces(s.j, n0);
             epi_all(true);  // the part is written
             if (et == 0) {
               __threadfence();
-              last_part = atomicAdd(p.tiles + s.j * l.NT + s.n0 / kTile, 1u) == (unsigned)np - 1;
+              last_part = atomicAdd(p.tiles + s.j * l.NT + s.nt, 1u) == (unsigned)np - 1;
               __threadfence();
             }
             epi_all(true);
             if (last_part) {
-              const int cols = min(kTile, l.N - s.n0) / 4;
+              const int cols = min(kTile, l.N - n0) / 4;
               const size_t step = (size_t)R.rows * l.N;
-              const float *src = part + (size_t)r0 * l.N + s.n0;
-              for (int i = et; i < rows * cols; i += kEpiThreads) {
-                const int r = i / cols, c = (i - r * cols) * 4;
-                float v[4] = {};
-#pragma unroll 4
-                for (int z = 0; z < np; ++z) few_add<4>(src + z * step + (size_t)r * l.N + c, v);
-                if (b1) {
-                  float b[4];
-                  few_ld<__nv_bfloat16, 4>(b1 + (size_t)e * l.N + s.n0 + c, b);
+              const float *src = part + (size_t)r0 * l.N + n0;
+              // Four places a thread at a time, so that their loads overlap.
+              for (int i0 = et; i0 < rows * cols; i0 += 4 * kEpiThreads) {
+                float v[4][4] = {};
+                int r[4], c[4];
 #pragma unroll
-                  for (int z = 0; z < 4; ++z) v[z] += b[z];
+                for (int m = 0; m < 4; ++m) {
+                  const int i = i0 + m * kEpiThreads;
+                  r[m] = i < rows * cols ? (cols == kTile / 4 ? i / (kTile / 4) : i / cols) : -1;
+                  c[m] = (i - r[m] * cols) * 4;
                 }
+#pragma unroll 2
+                for (int z = 0; z < np; ++z)
 #pragma unroll
-                for (int z = 0; z < 4; ++z) v[z] = fmaxf(v[z], 0.f);
-                few_st<__nv_bfloat16, 4>(hout + (size_t)(r0 + r) * l.N + s.n0 + c, v);
+                  for (int m = 0; m < 4; ++m)
+                    if (r[m] >= 0) few_add<4>(src + z * step + (size_t)r[m] * l.N + c[m], v[m]);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                  if (r[m] < 0) continue;
+                  if (b1) {
+                    float b[4];
+                    few_ld<__nv_bfloat16, 4>(b1 + (size_t)e * l.N + n0 + c[m], b);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) v[m][z] += b[z];
+                  }
+#pragma unroll
+                  for (int z = 0; z < 4; ++z) v[m][z] = fmaxf(v[m][z], 0.f);
+                  few_st<__nv_bfloat16, 4>(hout + (size_t)(r0 + r[m]) * l.N + n0 + c[m], v[m]);
+                }
               }
             }
           }
-          u += s.kb1 - s.kb0;
         }
         if (layer == 0) {
           // H's share of this block is written: TMA of every block may read it.
@@ -427,8 +455,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     return;
   }
   if (!few_barrier(p, 3)) return;
-  const FewLine l2(R.n > 0 ? R.n : 1, p.F, p.d, gridDim.x);
-  few_combine<__nv_bfloat16, 4>(p, R, [&](int j, int c) { return l2.pieces(j, c); });
+  few_combine<__nv_bfloat16, 4>(p, R, [&](int j, int c) { return line[1].pieces(j, c); });
 }
 
 // 3-D bf16 tensor [E, K, N], box [1, 64, 64], 128-byte swizzle; rows past K of
@@ -473,7 +500,9 @@ cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   int grid = sm_count();
   if (grid > kFewMaxGrid) grid = kFewMaxGrid;
-  void *args[6] = {&tx, &th, &t1, &t2, const_cast<FewArgs *>(&p), &q};
+  FewArgs a = p;
+  a.rt = few_router(p.T, p.d, p.E, p.Wn != nullptr, grid);
+  void *args[6] = {&tx, &th, &t1, &t2, &a, &q};
   return launch_few_grid(reinterpret_cast<const void *>(k_few_tc), args, grid,
                          1024 + q.stages * stage + rows, s);
 }
