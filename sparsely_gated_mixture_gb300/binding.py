@@ -142,8 +142,9 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
+        # The handle without a Stream object around it (3 us a call less).
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
