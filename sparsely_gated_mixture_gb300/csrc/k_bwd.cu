@@ -214,16 +214,21 @@ __global__ void __launch_bounds__(256)
 k_bwd_coef(int T, int E, const float2 *__restrict__ aux, float w_imp, float w_load, float w_aux,
            float *__restrict__ coef) {
   pdl_wait();
-  __shared__ double stat[4];
+  __shared__ double stat[4], sum[2][1024];  // E <= 1024
   const float wq[2] = {w_imp, w_load};
+  for (int u = threadIdx.x; u < 2 * E; u += blockDim.x) {
+    const int q = u >= E;
+    if (wq[q] != 0.f) sum[q][u - q * E] = (double)aux[u].x + (double)aux[u].y;
+  }
+  __syncthreads();
   if (threadIdx.x < 2 && wq[threadIdx.x] != 0.f) {
     const int q = threadIdx.x;
     double m = 0.0;
-    for (int e = 0; e < E; ++e) m += (double)aux[q * E + e].x + (double)aux[q * E + e].y;
+    for (int e = 0; e < E; ++e) m += sum[q][e];
     m /= E;
     double var = 0.0;
     for (int e = 0; e < E; ++e) {
-      const double v = (double)aux[q * E + e].x + (double)aux[q * E + e].y - m;
+      const double v = sum[q][e] - m;
       var += v * v;
     }
     stat[2 * q] = m;
@@ -535,6 +540,7 @@ __global__ void k_bwd_xtd_reduce(int d, int E, int NC, int S, const float *__res
        u += (long long)gridDim.x * blockDim.x) {
     if (u < n) {
       float s = 0.f;
+#pragma unroll 8
       for (int q = 0; q < S; ++q) s += part[(size_t)q * n + u];
       const int i = (int)(u / NC), col = (int)(u % NC);
       if (col < E) dWg[(size_t)i * E + col] = s;
@@ -625,9 +631,21 @@ k_bwd_colsum(int E, int cols, int chunks, const int32_t *__restrict__ offset,
     const int rows = offset[e + 1] - offset[e];
     const int m0 = ch * kColRows, m1 = min(rows, m0 + kColRows);
     float s = 0.f;
-    for (int m = m0; m < m1; ++m) {
-      const float v = to_f(src[((size_t)poff[e] + m) * cols + c]);
-      s = row_gate ? fmaf(row_gate[offset[e] + m], v, s) : s + v;
+    const S *col = src + (size_t)poff[e] * cols + c;
+    const float *g = row_gate ? row_gate + offset[e] : nullptr;
+    // Sixteen rows in flight; the sum stays in row order (33 -> 8 us for 16 K
+    // rows of 512, 15 -> 9 us for 16 K rows of 1024).
+    for (int m = m0; m < m1; m += 16) {
+      float v[16], w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int mi = min(m + i, m1 - 1);
+        v[i] = to_f(col[(size_t)mi * cols]);
+        w[i] = g ? g[mi] : 1.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (m + i < m1) s = g ? fmaf(w[i], v[i], s) : s + v[i];
     }
     part[((size_t)ch * E + e) * cols + c] = s;
   }

@@ -18,6 +18,7 @@ namespace moe {
 namespace {
 
 constexpr int TM = 64, TN = 64, TK = 16, kThreads = 256;
+constexpr int kLoads = TM * TK / kThreads;  // of each operand, per thread and chunk (TM == TN)
 
 template <typename T>
 __device__ __forceinline__ float ld(const T *p, size_t i);
@@ -103,16 +104,27 @@ k_bs_dgrad(int K, int N, int E, const int32_t *__restrict__ offset,
   const int tid = threadIdx.x;
   const int tm = (tid / 16) * 4, tn = (tid % 16) * 4;
   float acc[4][4] = {};
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    for (int i = tid; i < TM * TK; i += kThreads) {
-      const int m = i / TK, kk = i % TK, kx = k0 + kk;
-      As[kk][m] = kx < K ? A[(size_t)(pr0 + m) * K + kx] : 0.f;
+  // The next chunk's loads, all issued together, are in flight while this one
+  // is multiplied (per-step loads in a loop took four latencies one by one).
+  float ra[kLoads], rb[kLoads];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = tid + j * kThreads, m = i / TK, kx = k0 + i % TK;
+      ra[j] = kx < K ? A[(size_t)(pr0 + m) * K + kx] : 0.f;
+      rb[j] = (kx < K && n0 + m < N) ? ld(W, ((size_t)e * N + n0 + m) * K + kx) : 0.f;
     }
-    for (int i = tid; i < TN * TK; i += kThreads) {
-      const int n = i / TK, kk = i % TK, kx = k0 + kk;
-      Bs[kk][n] = (kx < K && n0 + n < N) ? ld(W, ((size_t)e * N + n0 + n) * K + kx) : 0.f;
+  };
+  fetch(0);
+  for (int k0 = 0; k0 < K; k0 += TK) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = tid + j * kThreads, m = i / TK, kk = i % TK;
+      As[kk][m] = ra[j];
+      Bs[kk][m] = rb[j];
     }
     __syncthreads();
+    if (k0 + TK < K) fetch(k0 + TK);
 #pragma unroll
     for (int kk = 0; kk < TK; ++kk) {
       float a[4], b[4];
@@ -183,16 +195,25 @@ k_bs_wgrad(int M, int N, const int32_t *__restrict__ offset, const int32_t *__re
   const int tid = threadIdx.x;
   const int tm = (tid / 16) * 4, tn = (tid % 16) * 4;
   float acc[4][4] = {};
-  for (int r0 = 0; r0 < rows; r0 += TK) {
-    for (int i = tid; i < TK * TM; i += kThreads) {
-      const int kk = i / TM, m = i % TM, r = r0 + kk;
-      As[kk][m] = (r < rows && m0 + m < M) ? ld(A, (size_t)(a0 + r) * M + m0 + m) : 0.f;
+  float ra[kLoads], rb[kLoads];  // the next chunk, as in the dgrad
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = tid + j * kThreads, m = i % TM, r = r0 + i / TM;
+      ra[j] = (r < rows && m0 + m < M) ? ld(A, (size_t)(a0 + r) * M + m0 + m) : 0.f;
+      rb[j] = (r < rows && n0 + m < N) ? B[(size_t)(b0 + r) * N + n0 + m] : 0.f;
     }
-    for (int i = tid; i < TK * TN; i += kThreads) {
-      const int kk = i / TN, n = i % TN, r = r0 + kk;
-      Bs[kk][n] = (r < rows && n0 + n < N) ? B[(size_t)(b0 + r) * N + n0 + n] : 0.f;
+  };
+  fetch(0);
+  for (int r0 = 0; r0 < rows; r0 += TK) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = tid + j * kThreads, kk = i / TM, m = i % TM;
+      As[kk][m] = ra[j];
+      Bs[kk][m] = rb[j];
     }
     __syncthreads();
+    if (r0 + TK < rows) fetch(r0 + TK);
 #pragma unroll
     for (int kk = 0; kk < TK; ++kk) {
       float a[4], b[4];

@@ -30,6 +30,7 @@
 // MMA issuer, warps 2-5 epilogue.
 #include "moe_internal.cuh"
 #include "tc_ptx.cuh"
+#include "checkpoint.cuh"
 
 #include <stdlib.h>
 
@@ -58,6 +59,7 @@ struct BParams {
   const int32_t *poff;    // [E+1] padded row offsets
   const float *row_gate;  // mode 0: [packed rows]
   const __nv_bfloat16 *hbuf;  // mode 0: [packed rows, N]
+  const uint8_t *h8, *hscale;  // mode 0: the same in 8 bits [packed rows, N], [.., N / 32]
   void *out;      // mode 0: bf16 [padded rows, N]; mode 1: fp32 [padded rows, N];
                   // mode 2: fp32 (or bf16) [E, M, N]
   float *dgpart;  // mode 0: [padded rows, n_blocks]
@@ -189,7 +191,24 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
     if (!valid || n >= p.N) continue;
     if (MODE == 0) {
       float h[32];
-      if (real) {
+      if (real && OB) {
+        // e4m3 values of one block of 32 and its scale: exactly hbuf's values.
+        const uint4 *hp = reinterpret_cast<const uint4 *>(p.h8 + q * p.N + n);
+        const float sc = ckpt_scale(p.hscale[q * (p.N / kCkptBlock) + n / kCkptBlock]);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint4 u = hp[w];
+          const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 lo = ckpt_e4m3x2(uu[j] & 0xffffu), hi = ckpt_e4m3x2(uu[j] >> 16);
+            h[16 * w + 4 * j] = lo.x * sc;
+            h[16 * w + 4 * j + 1] = lo.y * sc;
+            h[16 * w + 4 * j + 2] = hi.x * sc;
+            h[16 * w + 4 * j + 3] = hi.y * sc;
+          }
+        }
+      } else if (real) {
         const uint4 *hp = reinterpret_cast<const uint4 *>(p.hbuf + q * p.N + n);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -263,7 +282,8 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
   if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)(MODE == 2 ? m : (long long)pr));
 }
 
-// OB (mode 2): the weight gradient in bf16.
+// OB: in mode 2 the weight gradient is written in bf16, in mode 0 the hidden
+// rows are read in 8 bits (a checkpoint's).
 template <int MODE, bool OB = false>
 __global__ void __launch_bounds__(kThreads, 1)
 k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -831,7 +851,7 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       if constexpr (MODE == 2)
         epilogue_wgrad_tma<OB>(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
       else
-        epilogue_rows<MODE>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
+        epilogue_rows<MODE, OB>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(buf ? acc_empty_leader1 : acc_empty_leader0);
@@ -993,6 +1013,8 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
   p.poff = g.poff;
   p.row_gate = g.row_gate;
   p.hbuf = static_cast<const __nv_bfloat16 *>(g.hbuf);
+  p.h8 = g.h8;
+  p.hscale = g.hscale;
   p.out = g.out;
   p.dgpart = g.dgpart;
   p.st = st;
@@ -1029,9 +1051,11 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
   if (cl > 0) {
     CUtensorMap to = ta;  // unused unless p.tma_out
     p.tma_out = make_rows_map(&to, g.out, (uint64_t)g.a_rows, (uint64_t)g.N, g.mode == 1) ? 1 : 0;
+    if (g.mode == 0 && g.h8) return launch_mode_pair<0, true>(ta, tb, to, p, cl, s);
     return g.mode == 0 ? launch_mode_pair<0>(ta, tb, to, p, cl, s)
                        : launch_mode_pair<1>(ta, tb, to, p, cl, s);
   }
+  if (g.mode == 0 && g.h8) return launch_mode<0, true>(ta, tb, p, s);
   return g.mode == 0 ? launch_mode<0>(ta, tb, p, s) : launch_mode<1>(ta, tb, p, s);
 }
 

@@ -18,9 +18,8 @@
 // every 16-byte (fp32: 32-byte) load issued before the first is used; 4 lanes
 // of 8 columns make a block. Widths that are not a multiple of 8 go one
 // column per lane.
+#include "checkpoint.cuh"
 #include "moe_internal.cuh"
-
-#include <cuda_fp8.h>
 
 namespace moe {
 namespace {
@@ -47,15 +46,6 @@ __device__ __forceinline__ float scaled(float v, float inv, float cap) {
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)v, __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-// What a scale byte multiplies by.
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return byte == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
-}
-
 template <typename T>
 struct Oct;
 template <>
@@ -170,7 +160,7 @@ k_ckpt_load(int cols, int segs, const int32_t *__restrict__ rows, const uint8_t 
     if (c < cols) in[i] = *reinterpret_cast<const uint2 *>(src + c);
   }
   const int b = seg * (kSeg / kCkptBlock) + lane;
-  const float mine = b < nb ? scale_of(scale[row * nb + b]) : 0.f;
+  const float mine = b < nb ? ckpt_scale(scale[row * nb + b]) : 0.f;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int c = seg * kSeg + i * 256 + lane * 8;
@@ -180,7 +170,7 @@ k_ckpt_load(int cols, int segs, const int32_t *__restrict__ rows, const uint8_t 
     float f[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 v = from_e4m3x2(w[j]);
+      const float2 v = ckpt_e4m3x2(w[j]);
       f[2 * j] = v.x * s;
       f[2 * j + 1] = v.y * s;
     }
@@ -235,14 +225,16 @@ k_ckpt_load_any(int cols, const int32_t *__restrict__ rows, const uint8_t *__res
   const long long row = u / nb;
   const int c = (int)(u - row * nb) * kCkptBlock + lane;
   if (row >= max_rows || row >= *rows || c >= cols) return;
-  put(h + row * cols + c, from_e4m3x2(q[row * cols + c]).x * scale_of(scale[u]));
+  put(h + row * cols + c, ckpt_e4m3x2(q[row * cols + c]).x * ckpt_scale(scale[u]));
 }
 
 __global__ void k_ckpt_choices(int n, int E, const int32_t *__restrict__ idx,
-                               int32_t *__restrict__ out, DeviceStatus *st) {
+                               int32_t *__restrict__ out, DeviceStatus *st,
+                               const DeviceStatus *other) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i == 0 && other && other->code) record_error(st, other->code, other->detail);
   if (i >= n) return;
   const int e = idx[i];
   const bool ok = e >= 0 && e < E;
@@ -306,8 +298,9 @@ cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, cons
 }
 
 cudaError_t launch_checkpoint_choices(int n, int E, const int32_t *idx, int32_t *out,
-                                      DeviceStatus *st, cudaStream_t s) {
-  return launch_pdl(k_ckpt_choices, dim3((n + 255) / 256), 256, 0, s, n, E, idx, out, st);
+                                      DeviceStatus *st, const DeviceStatus *other,
+                                      cudaStream_t s) {
+  return launch_pdl(k_ckpt_choices, dim3((n + 255) / 256), 256, 0, s, n, E, idx, out, st, other);
 }
 
 }  // namespace moe

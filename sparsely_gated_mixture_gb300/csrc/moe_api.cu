@@ -120,9 +120,9 @@ static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 static int gate_impl(const moe_config &c, const void *x, const float *Wg, const float *Wn,
                      const float *noise, const float *bias, int32_t *idx, float *gate, float *thr,
-                     void *ws, bool partials, cudaStream_t s) {
+                     void *ws, bool partials, cudaStream_t s, DeviceStatus *st = nullptr) {
   const WsLayout L = ws_layout(c);
-  DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
+  if (!st) st = ws_at<DeviceStatus>(ws, L.status);
   float *cc = ws_at<float>(ws, L.c), *sg = ws_at<float>(ws, L.sigma), *H = ws_at<float>(ws, L.H);
   float *rs = ws_at<float>(ws, L.rowstat);
   float *part = ws_at<float>(ws, L.partials);  // launch_router clears the status word first
@@ -320,7 +320,7 @@ static int check_few(const moe_config *c) {
 
 // ----------------------------------------------------------------------------- backward
 struct BwdLayout {
-  size_t poff, dY, dU, dP, dX, dgpart, dg, coef, dc, dz, dxr, rpart, bpart, cpart, total;
+  size_t poff, dY, dU, dP, dX, dgpart, dg, coef, dc, dz, dxr, rpart, bpart, cpart, st2, total;
   long long P_max;  // padded rows: T*k + 64*E bounds sum_e max(64, roundup(rows_e, 64))
   int n_blocks2, chunks;
 };
@@ -371,6 +371,7 @@ static BwdLayout bwd_layout(const moe_config &cfg) {
   L.rpart = take(rp * d * 4);
   L.bpart = take(rp * 4);
   L.cpart = take((size_t)L.chunks * E * (d > dff ? d : dff) * 4);
+  L.st2 = take(sizeof(DeviceStatus));  // a router run beside the rest
   L.total = off;
   return L;
 }
@@ -1007,8 +1008,42 @@ struct BwdCall {
   bool dw_bf16;  // dW1, db1, dW2, db2 in bf16 (else fp32)
 };
 
+// What moe_backward_checkpoint rebuilds the state from. q.idx is then a copy
+// in ws, q.pos and q.keep are ws's, and all are written here.
+struct CkptCall {
+  const float *logit_bias;
+  const int32_t *expert_idx;
+  const uint8_t *h8, *hscale;
+};
+
+// The router's part of that state (its status in st2, carried over to ws's
+// status word), needed by the losses, the noise and the Switch softmax only.
+static int ckpt_router(const moe_config &c, const WsLayout &L, const BwdLayout &B,
+                       const BwdCall &q, const CkptCall &ck, cudaStream_t s) {
+  void *ws = q.ws;
+  DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
+  DeviceStatus *st2 = ws_at<DeviceStatus>(q.bws, B.st2);
+  const bool losses = q.w_importance != 0.f || q.w_load != 0.f || q.w_aux != 0.f;
+  const bool router = losses || q.Wnoise || c.gate_mode == MOE_GATE_SWITCH;
+  if (router) {
+    // The logits and balancing totals, as the forward computed them (its
+    // kernels, in its order: the same bits). The choices stay the caller's.
+    const int r = gate_impl(c, q.x, q.Wg, q.Wnoise, q.noise, ck.logit_bias,
+                            ws_at<int32_t>(ws, L.idx), ws_at<float>(ws, L.gate),
+                            ws_at<float>(ws, L.thr), ws, losses, s, st2);
+    if (r != MOE_OK) return r;
+    if (losses)
+      MOE_CUDA(launch_aux_finalize(c, ws_at<float>(ws, L.partials), L.n_aux_blocks,
+                                   ws_at<float>(ws, L.out3s), nullptr, nullptr,
+                                   ws_at<float2>(ws, L.aux_vec), st2, s));
+  }
+  MOE_CUDA(launch_checkpoint_choices(c.T * c.k, c.E, ck.expert_idx, ws_at<int32_t>(ws, L.idx), st,
+                                     router ? st2 : nullptr, s));
+  return MOE_OK;
+}
+
 static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &q,
-                         cudaStream_t s) {
+                         cudaStream_t s, const CkptCall *ck = nullptr) {
   const bool tc = bwd_tc_shape(c);
   const BwdLayout B = bwd_layout(c);
   void *ws = q.ws, *bws = q.bws;
@@ -1027,15 +1062,53 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
   const BwdSimt sp{B.P_max, offset, poff, row_token, row_gate, q.dy, q.W1, q.W2, q.b2, xbuf,
                    hbuf, static_cast<float *>(dY), static_cast<float *>(dU), static_cast<float *>(dP),
                    dX, dgpart, q.dW1, q.dW2, st, q.dw_bf16};
+  SideStream *side = nullptr;
+  std::unique_lock<std::mutex> side_lock;
+  cudaStream_t fs = s;
+  const auto fork = [&]() -> int {  // work enqueued on fs from here follows that on s
+    if (!side) return MOE_OK;
+    MOE_CUDA(cudaEventRecord(side->fork, s));
+    MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
+    return MOE_OK;
+  };
+  if (ck) {
+    // From a checkpoint: the choices' slots first. Beside them and the first
+    // GEMM, on the side stream, what only later steps read: the router, the
+    // packed x rows and the hidden rows in the layer's type (the tensor-core
+    // dgrad reads them in 8 bits).
+    side = side_stream(side_lock, s);
+    if (side) fs = side->s;
+    MOE_CUDA(cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s));
+    int r = fork();
+    if (r == MOE_OK) r = ckpt_router(c, L, B, q, *ck, fs);
+    if (r != MOE_OK) return r;
+    MOE_CUDA(launch_slots(c, host_capacity(c), ck->expert_idx, q.gate, ws_at<int32_t>(ws, L.hist),
+                          ws_at<int32_t>(ws, L.chunk_base), ws_at<int32_t>(ws, L.count),
+                          ws_at<int32_t>(ws, L.offset), ws_at<int32_t>(ws, L.mtiles),
+                          ws_at<int32_t>(ws, L.pos), ws_at<uint8_t>(ws, L.keep),
+                          ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate),
+                          L.n_chunks, st, s));
+    r = fork();
+    if (r != MOE_OK) return r;
+    MOE_CUDA(launch_gather(c, q.x, offset, row_token, xbuf, st, fs));
+    MOE_CUDA(launch_checkpoint_load(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff,
+                                    offset + c.E, ck->h8, ck->hscale, hbuf, tc ? fs : s));
+    if (tc) MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, fs));
+    if (side) MOE_CUDA(cudaEventRecord(side->join, side->s));
+  }
   // 1. Padded row blocks, finite K tails, the dy rows (plain and gate-scaled);
   // 2. through W2: D = dY W2^T, the gate partials <D, h> and dpre = g D [h > 0].
   MOE_CUDA(launch_bwd_offsets(c.E, offset, poff, s));
   if (tc) {
-    MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, s));
+    if (!ck) MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, s));
     MOE_CUDA(launch_bwd_gather(c, B.P_max, offset, poff, row_token, row_gate, q.dy, dY, dU,
                                s));
     BwdGemm g0{0, c.d, c.d_ff, 0, c.E, B.P_max, 0, 0, dY, q.W2, offset, poff, row_gate, hbuf,
                dP, dgpart, false};
+    if (ck) {
+      g0.h8 = ck->h8;
+      g0.hscale = ck->hscale;
+    }
     MOE_CUDA(launch_bwd_gemm(g0, st, s));
   } else {
     MOE_CUDA(launch_bwd_simt_front(c, sp, s));
@@ -1046,21 +1119,17 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
   // load and Switch terms, the router's weight gradients and its share of dx
   // -- and the bias column sums. Their small kernels fit beside the
   // persistent GEMM CTAs of the other branch, which stays on `stream`.
-  SideStream *side = nullptr;
-  std::unique_lock<std::mutex> side_lock;
-  side = side_stream(side_lock, s);
-  cudaStream_t fs = s;
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->fork, s));
-    MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
-    fs = side->s;
-  }
+  if (!ck) side = side_stream(side_lock, s);
+  if (side) fs = side->s;
+  int r = fork();
+  if (r != MOE_OK) return r;
+  if (ck && side) MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));  // the packed rows
   if (tc)
     MOE_CUDA(launch_bwd_dg(c, B.n_blocks2, offset, poff, row_token, dgpart, q.dy, q.b2, dg,
                            fs));
   else
     MOE_CUDA(launch_bwd_simt_dg(c, sp, dg, fs));
-  const int r = gate_bwd_impl(c, L, B, ws, bws, q.x, q.Wg, q.Wnoise, q.noise, q.idx, q.gate,
+  r = gate_bwd_impl(c, L, B, ws, bws, q.x, q.Wg, q.Wnoise, q.noise, q.idx, q.gate,
                               q.keep, dg, false, q.w_importance, q.w_load, q.w_aux, q.dgate,
                               q.dWg, q.dWnoise, q.dlogit_bias, dxr, fs);
   if (r != MOE_OK) return r;
@@ -1216,35 +1285,12 @@ int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *W
   const moe_config &c = *cfg;
   if (bwd_tc_shape(c) && !bwd_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
   const WsLayout L = ws_layout(c);
-  cudaStream_t s = (cudaStream_t)stream;
-  DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
-  // The router's logits and balancing totals, as the forward computed them
-  // (its kernels, in its order: the same bits). The choices are the caller's.
-  const bool losses = w_importance != 0.f || w_load != 0.f || w_aux != 0.f;
-  r = gate_impl(c, x, Wg, Wnoise, noise, logit_bias, ws_at<int32_t>(ws, L.idx),
-                ws_at<float>(ws, L.gate), ws_at<float>(ws, L.thr), ws, losses, s);
-  if (r != MOE_OK) return r;
-  if (losses)
-    MOE_CUDA(launch_aux_finalize(c, ws_at<float>(ws, L.partials), L.n_aux_blocks,
-                                 ws_at<float>(ws, L.out3s), nullptr, nullptr,
-                                 ws_at<float2>(ws, L.aux_vec), st, s));
-  // The packed rows of the choices, x's gathered and the hidden ones loaded.
-  int32_t *offset = ws_at<int32_t>(ws, L.offset), *pos = ws_at<int32_t>(ws, L.pos);
-  uint8_t *keep = ws_at<uint8_t>(ws, L.keep);
-  MOE_CUDA(launch_slots(c, host_capacity(c), expert_idx, gate, ws_at<int32_t>(ws, L.hist),
-                        ws_at<int32_t>(ws, L.chunk_base), ws_at<int32_t>(ws, L.count), offset,
-                        ws_at<int32_t>(ws, L.mtiles), pos, keep, ws_at<int32_t>(ws, L.row_token),
-                        ws_at<float>(ws, L.row_gate), L.n_chunks, st, s));
-  MOE_CUDA(launch_gather(c, x, offset, ws_at<int32_t>(ws, L.row_token), ws_at<char>(ws, L.xbuf),
-                         st, s));
-  MOE_CUDA(launch_checkpoint_load(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff,
-                                  offset + c.E, h8, hscale, ws_at<char>(ws, L.hbuf), s));
-  int32_t *idx = ws_at<int32_t>(ws, L.idx);
-  MOE_CUDA(launch_checkpoint_choices(c.T * c.k, c.E, expert_idx, idx, st, s));
-  const BwdCall q{x, Wg, Wnoise, noise, W1, W2, b2, idx, gate, pos, keep, dy, w_importance,
+  const BwdCall q{x, Wg, Wnoise, noise, W1, W2, b2, ws_at<int32_t>(ws, L.idx), gate,
+                  ws_at<int32_t>(ws, L.pos), ws_at<uint8_t>(ws, L.keep), dy, w_importance,
                   w_load, w_aux, dx, dWg, dWnoise, dlogit_bias, dW1, db1, dW2, db2, dgate, ws,
                   bws, c.act_dtype == MOE_BF16};
-  return backward_impl(c, L, q, s);
+  const CkptCall ck{logit_bias, expert_idx, h8, hscale};
+  return backward_impl(c, L, q, (cudaStream_t)stream, &ck);
 }
 
 int moe_last_device_status(void *ws, moe_stream_t stream, int64_t *detail) {

@@ -291,6 +291,7 @@ struct BwdGemm {
   void *out;
   float *dgpart;
   bool out_bf16;  // mode 2: the weight gradient in bf16
+  const uint8_t *h8 = nullptr, *hscale = nullptr;  // mode 0: hbuf's values in 8 bits instead
 };
 bool bwd_tc_supported(const moe_config &cfg);
 cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s);
@@ -364,8 +365,10 @@ cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, cons
                                    const uint8_t *q, const uint8_t *scale, void *h,
                                    cudaStream_t s);
 // The caller's choices with an index outside [0, E) replaced by 0 (recorded as
-// MOE_ERR_BOUNDS), for kernels that index by expert.
+// MOE_ERR_BOUNDS), for kernels that index by expert; an error in `other` (may be
+// null) is carried over to st.
 cudaError_t launch_checkpoint_choices(int n, int E, const int32_t *idx, int32_t *out,
-                                      DeviceStatus *st, cudaStream_t s);
+                                      DeviceStatus *st, const DeviceStatus *other,
+                                      cudaStream_t s);
 
 }  // namespace moe
