@@ -620,21 +620,32 @@ k_bwd_dxr(int T, int d, int E, int NC, const float *__restrict__ dc, const float
 // chunks of 128 rows, then the chunks in order.
 constexpr int kColRows = 128;
 
+// The two bias gradients go in one launch: blocks of x < nx0 are job 0's.
+template <typename S>
+struct ColJob {
+  int cols;
+  const float *row_gate;
+  const S *src;
+  float *part;
+};
+
 template <typename S>
 __global__ void __launch_bounds__(256)
-k_bwd_colsum(int E, int cols, int chunks, const int32_t *__restrict__ offset,
-             const int32_t *__restrict__ poff, const float *__restrict__ row_gate,
-             const S *__restrict__ src, float *__restrict__ part) {
+k_bwd_colsum(int E, int nx0, const int32_t *__restrict__ offset,
+             const int32_t *__restrict__ poff, const ColJob<S> j0, const ColJob<S> j1) {
   pdl_wait();
-  const int c = blockIdx.x * 256 + threadIdx.x, e = blockIdx.y, ch = blockIdx.z;
+  const bool first = (int)blockIdx.x < nx0;
+  const ColJob<S> job = first ? j0 : j1;
+  const int cols = job.cols;
+  const int c = ((int)blockIdx.x - (first ? 0 : nx0)) * 256 + threadIdx.x;
+  const int e = blockIdx.y, ch = blockIdx.z;
   if (c < cols) {
     const int rows = offset[e + 1] - offset[e];
     const int m0 = ch * kColRows, m1 = min(rows, m0 + kColRows);
     float s = 0.f;
-    const S *col = src + (size_t)poff[e] * cols + c;
-    const float *g = row_gate ? row_gate + offset[e] : nullptr;
-    // Sixteen rows in flight; the sum stays in row order (33 -> 8 us for 16 K
-    // rows of 512, 15 -> 9 us for 16 K rows of 1024).
+    const S *col = job.src + (size_t)poff[e] * cols + c;
+    const float *g = job.row_gate ? job.row_gate + offset[e] : nullptr;
+    // Sixteen rows in flight; the sum stays in row order.
     for (int m = m0; m < m1; m += 16) {
       float v[16], w[16];
 #pragma unroll
@@ -647,7 +658,7 @@ k_bwd_colsum(int E, int cols, int chunks, const int32_t *__restrict__ offset,
       for (int i = 0; i < 16; ++i)
         if (m + i < m1) s = g ? fmaf(w[i], v[i], s) : s + v[i];
     }
-    part[((size_t)ch * E + e) * cols + c] = s;
+    job.part[((size_t)ch * E + e) * cols + c] = s;
   }
   pdl_trigger();
 }
@@ -656,15 +667,20 @@ __device__ __forceinline__ void store_f(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_f(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 template <typename O>
-__global__ void k_bwd_colsum_reduce(int E, int cols, int chunks, const float *__restrict__ part,
-                                    O *__restrict__ out) {
+__global__ void k_bwd_colsum_reduce(int chunks, long long n0, long long n1,
+                                    const float *__restrict__ part0,
+                                    const float *__restrict__ part1, O *__restrict__ out0,
+                                    O *__restrict__ out1) {
   pdl_wait();
-  const long long n = (long long)E * cols;
-  for (long long u = blockIdx.x * (long long)blockDim.x + threadIdx.x; u < n;
-       u += (long long)gridDim.x * blockDim.x) {
+  for (long long w = blockIdx.x * (long long)blockDim.x + threadIdx.x; w < n0 + n1;
+       w += (long long)gridDim.x * blockDim.x) {
+    const bool first = w < n0;
+    const long long u = first ? w : w - n0, n = first ? n0 : n1;
+    const float *part = first ? part0 : part1;
     float s = 0.f;
+#pragma unroll 8
     for (int q = 0; q < chunks; ++q) s += part[(size_t)q * n + u];
-    store_f(out + u, s);
+    store_f((first ? out0 : out1) + u, s);
   }
   pdl_trigger();
 }
@@ -820,23 +836,39 @@ cudaError_t launch_bwd_router(const moe_config &c, bool noisy, const void *x, co
   return launch_pdl(k_bwd_dxr, g2, 256, 0, s, c.T, c.d, c.E, NC, dc, dz, Wg, Wn, dxr);
 }
 
-cudaError_t launch_bwd_colsum(const moe_config &c, int cols, int chunks, const int32_t *offset,
-                              const int32_t *poff, const float *row_gate, const void *src,
-                              bool src_f32, float *part, void *out, bool out_bf16,
+template <typename S>
+static cudaError_t run_colsum(const moe_config &c, int chunks, const int32_t *offset,
+                              const int32_t *poff, const float *row_gate, const void *dY,
+                              const void *dP, float *part, void *db2, void *db1, bool out_bf16,
                               cudaStream_t s) {
-  const dim3 g((cols + 255) / 256, c.E, chunks);
-  cudaError_t err =
-      src_f32 ? launch_pdl(k_bwd_colsum<float>, g, 256, 0, s, c.E, cols, chunks, offset, poff,
-                           row_gate, static_cast<const float *>(src), part)
-              : launch_pdl(k_bwd_colsum<__nv_bfloat16>, g, 256, 0, s, c.E, cols, chunks, offset,
-                           poff, row_gate, static_cast<const __nv_bfloat16 *>(src), part);
+  const int d = db2 ? c.d : 0, f = db1 ? c.d_ff : 0;  // a gradient not asked for has no columns
+  const long long n0 = (long long)c.E * d, n1 = (long long)c.E * f;
+  float *part1 = part + chunks * n0;
+  const ColJob<S> j0{d, row_gate, static_cast<const S *>(dY), part};
+  const ColJob<S> j1{f, nullptr, static_cast<const S *>(dP), part1};
+  const int nx0 = (d + 255) / 256, nx1 = (f + 255) / 256;
+  const cudaError_t err = launch_pdl(k_bwd_colsum<S>, dim3(nx0 + nx1, c.E, chunks), 256, 0, s,
+                                     c.E, nx0, offset, poff, j0, j1);
   if (err != cudaSuccess) return err;
-  const int rg = grid_for((long long)c.E * cols, 256);
+  const int rg = grid_for(n0 + n1, 256);
   if (out_bf16)
-    return launch_pdl(k_bwd_colsum_reduce<__nv_bfloat16>, rg, 256, 0, s, c.E, cols, chunks,
-                      (const float *)part, static_cast<__nv_bfloat16 *>(out));
-  return launch_pdl(k_bwd_colsum_reduce<float>, rg, 256, 0, s, c.E, cols, chunks,
-                    (const float *)part, static_cast<float *>(out));
+    return launch_pdl(k_bwd_colsum_reduce<__nv_bfloat16>, rg, 256, 0, s, chunks, n0, n1,
+                      (const float *)part, (const float *)part1,
+                      static_cast<__nv_bfloat16 *>(db2), static_cast<__nv_bfloat16 *>(db1));
+  return launch_pdl(k_bwd_colsum_reduce<float>, rg, 256, 0, s, chunks, n0, n1,
+                    (const float *)part, (const float *)part1, static_cast<float *>(db2),
+                    static_cast<float *>(db1));
+}
+
+cudaError_t launch_bwd_colsum(const moe_config &c, int chunks, const int32_t *offset,
+                              const int32_t *poff, const float *row_gate, const void *dY,
+                              const void *dP, bool src_f32, float *part, void *db2, void *db1,
+                              bool out_bf16, cudaStream_t s) {
+  if (!db1 && !db2) return cudaSuccess;
+  return src_f32 ? run_colsum<float>(c, chunks, offset, poff, row_gate, dY, dP, part, db2, db1,
+                                     out_bf16, s)
+                 : run_colsum<__nv_bfloat16>(c, chunks, offset, poff, row_gate, dY, dP, part, db2,
+                                             db1, out_bf16, s);
 }
 
 // Launched in plain stream order (no programmatic dependent launch): it

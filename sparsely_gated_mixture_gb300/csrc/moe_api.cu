@@ -370,7 +370,7 @@ static BwdLayout bwd_layout(const moe_config &cfg) {
   L.dxr = take(T * d * 4);
   L.rpart = take(rp * d * 4);
   L.bpart = take(rp * 4);
-  L.cpart = take((size_t)L.chunks * E * (d > dff ? d : dff) * 4);
+  L.cpart = take((size_t)L.chunks * E * (d + dff) * 4);
   L.st2 = take(sizeof(DeviceStatus));  // a router run beside the rest
   L.total = off;
   return L;
@@ -970,12 +970,13 @@ static int gate_bwd_impl(const moe_config &c, const WsLayout &L, const BwdLayout
                          const float *noise, const int32_t *idx, const float *g,
                          const uint8_t *kp, const float *dg, bool dg_total, float w_imp,
                          float w_load, float w_aux, float *dgate_out, float *dWg, float *dWn,
-                         float *dbias, float *dxr, cudaStream_t s) {
+                         float *dbias, float *dxr, cudaStream_t s, bool coef_done = false) {
   const bool noisy = Wn != nullptr;
   const bool load_on = noisy && c.k < c.E && w_load != 0.f;
   const bool aux_on = w_aux != 0.f;
   float *coef = ws_at<float>(bws, B.coef);
-  MOE_CUDA(launch_bwd_coef(c, ws_at<float2>(ws, L.aux_vec), w_imp, w_load, w_aux, coef, s));
+  if (!coef_done)
+    MOE_CUDA(launch_bwd_coef(c, ws_at<float2>(ws, L.aux_vec), w_imp, w_load, w_aux, coef, s));
   float *dc = ws_at<float>(bws, B.dc), *dz = ws_at<float>(bws, B.dz);
   MOE_CUDA(launch_bwd_gate(c, noisy, load_on, aux_on, dg_total, ws_at<float>(ws, L.H),
                            ws_at<float>(ws, L.c), ws_at<float>(ws, L.sigma), noise,
@@ -1039,6 +1040,8 @@ static int ckpt_router(const moe_config &c, const WsLayout &L, const BwdLayout &
   }
   MOE_CUDA(launch_checkpoint_choices(c.T * c.k, c.E, ck.expert_idx, ws_at<int32_t>(ws, L.idx), st,
                                      router ? st2 : nullptr, s));
+  MOE_CUDA(launch_bwd_coef(c, ws_at<float2>(ws, L.aux_vec), q.w_importance, q.w_load, q.w_aux,
+                           ws_at<float>(q.bws, B.coef), s));
   return MOE_OK;
 }
 
@@ -1131,15 +1134,10 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
     MOE_CUDA(launch_bwd_simt_dg(c, sp, dg, fs));
   r = gate_bwd_impl(c, L, B, ws, bws, q.x, q.Wg, q.Wnoise, q.noise, q.idx, q.gate,
                               q.keep, dg, false, q.w_importance, q.w_load, q.w_aux, q.dgate,
-                              q.dWg, q.dWnoise, q.dlogit_bias, dxr, fs);
+                              q.dWg, q.dWnoise, q.dlogit_bias, dxr, fs, ck != nullptr);
   if (r != MOE_OK) return r;
-  float *cpart = ws_at<float>(bws, B.cpart);
-  if (q.db2)
-    MOE_CUDA(launch_bwd_colsum(c, c.d, B.chunks, offset, poff, row_gate, dY, !tc, cpart, q.db2,
-                               q.dw_bf16, fs));
-  if (q.db1)
-    MOE_CUDA(launch_bwd_colsum(c, c.d_ff, B.chunks, offset, poff, nullptr, dP, !tc, cpart, q.db1,
-                               q.dw_bf16, fs));
+  MOE_CUDA(launch_bwd_colsum(c, B.chunks, offset, poff, row_gate, dY, dP, !tc,
+                             ws_at<float>(bws, B.cpart), q.db2, q.db1, q.dw_bf16, fs));
   // 3. Through W1: dX = dpre W1^T; weight gradients dW2[e] = h^T (g dY),
   //    dW1[e] = x^T dpre.
   if (tc) {

@@ -345,11 +345,13 @@ cudaError_t launch_bwd_router(const moe_config &c, bool noisy, const void *x, co
                               const float *Wn, const float *dc, const float *dz, float *part,
                               float *bpart, float *dWg, float *dWn, float *dbias, float *dxr,
                               cudaStream_t s);
-// src rows are bf16, or fp32 when src_f32; out fp32 or bf16.
-cudaError_t launch_bwd_colsum(const moe_config &c, int cols, int chunks, const int32_t *offset,
-                              const int32_t *poff, const float *row_gate, const void *src,
-                              bool src_f32, float *part, void *out, bool out_bf16,
-                              cudaStream_t s);
+// The bias gradients db2 [E, d] = column sums of gate * dY, db1 [E, d_ff] = of
+// dP, over each expert's rows; either may be null. The rows are bf16, or fp32
+// when src_f32; out fp32 or bf16; part: chunks * E * (d + d_ff) floats.
+cudaError_t launch_bwd_colsum(const moe_config &c, int chunks, const int32_t *offset,
+                              const int32_t *poff, const float *row_gate, const void *dY,
+                              const void *dP, bool src_f32, float *part, void *db2, void *db1,
+                              bool out_bf16, cudaStream_t s);
 cudaError_t launch_bwd_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                           const uint8_t *keep, const int32_t *poff, const float *dX,
                           const float *dxr, const void *dy, void *dx, cudaStream_t s);
