@@ -12,25 +12,43 @@ namespace {
 
 // ----------------------------------------------------------------------------- experts
 // out[s][row][n] = sum over slice s of K of A[row][k] W[e][k][n]. A unit is an
-// expert, a block of 32 * VEC columns and a slice of K; the block's 8 warps
-// share the slice's rows (each loads whole 32 * VEC column segments), and
-// their sums are joined in shared memory in warp order.
-constexpr int kUnitRows = 256;  // rows of K staged at a time: 32 a warp
+// expert, a block of 32 * VEC columns and a slice of K. The block stages a
+// chunk of K of up to 8 rows of A in shared memory, transposed; each of its 8
+// warps takes an eighth of the chunk's K and has all its weights (32 values a
+// lane) in flight before the rows are staged. The warps' sums are joined in
+// shared memory in warp order.
+template <int VEC>
+struct FewChunk {
+  static constexpr int per_warp = 32 / VEC;  // 4 KB in flight a warp (fp32)
+  static constexpr int rows = 8 * per_warp;
+};
 
+// The slices of K: as many as make the fewest rows of K for the busiest block,
+// a unit's own cost (staging, joining) counted as 64 rows.
 struct FewUnits {
   int blocks, slices, per;  // column blocks, slices of K, rows of K per slice
+  int total;
+  FewDiv by_blocks, by_tile;  // column blocks; units of an expert
+  __device__ void make(int n_experts, int K, int N, int cols, int grid) {
+    blocks = (N + cols - 1) / cols;
+    const int tiles = n_experts * blocks;
+    int best = 0x7fffffff;
+    slices = 1;
+    per = K;
+    for (int s = 1; s <= 8; ++s) {
+      const int rows = ((K + s - 1) / s + 31) / 32 * 32, n = (K + rows - 1) / rows;
+      const int cost = (tiles * n + grid - 1) / grid * (rows + 64);
+      if (cost < best) {
+        best = cost;
+        slices = n;
+        per = rows;
+      }
+    }
+    total = tiles * slices;
+    by_blocks = FewDiv(blocks);
+    by_tile = FewDiv(blocks * slices);
+  }
 };
-__host__ __device__ inline FewUnits few_units(int n_experts, int K, int N, int cols, int grid) {
-  FewUnits u;
-  u.blocks = (N + cols - 1) / cols;
-  const int tiles = n_experts * u.blocks;
-  int s = tiles > 0 ? (2 * grid + tiles - 1) / tiles : 1;
-  const int most = (K + kUnitRows - 1) / kUnitRows;
-  if (s > most) s = most;
-  u.per = ((K + s - 1) / s + kUnitRows - 1) / kUnitRows * kUnitRows;
-  u.slices = (K + u.per - 1) / u.per;
-  return u;
-}
 
 template <typename T, int VEC>
 struct FewVec;
@@ -38,6 +56,11 @@ template <>
 struct FewVec<float, 4> {
   float4 v;
   __device__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <>
+struct FewVec<float, 2> {
+  float2 v;
+  __device__ void get(float (&f)[2]) const { f[0] = v.x; f[1] = v.y; }
 };
 template <>
 struct FewVec<float, 1> {
@@ -58,79 +81,102 @@ struct FewVec<__nv_bfloat16, 1> {
   __device__ void get(float (&f)[1]) const { f[0] = __bfloat162float(v); }
 };
 
-// smem: xs [kUnitRows][8], red [8 warps][8 rows][VEC][32 lanes].
-constexpr int kSimtSmemFloats = kUnitRows * 8 + 8 * 8 * 32 * 4;
+// smem: xs [chunk rows][8], red [8 warps][8 rows][VEC][32 lanes].
+constexpr int kSimtSmemFloats = 256 * 8 + 8 * 8 * 32 * 4;
 
-template <typename T, int VEC>
-__device__ void few_product(const FewRows &R, const T *A, bool by_token, const T *Wall, int K,
-                            int N, float *out, float *smem) {
-  constexpr int COLS = 32 * VEC;
+// One unit's sums of rows r0 .. r0 + R - 1 (those below r1).
+template <typename T, int VEC, int R>
+__device__ __forceinline__ void few_unit(const FewRows &rows, const T *A, bool by_token,
+                                         const T *W, bool live, int K, int N, int k0, int k1,
+                                         int r0, int r1, int c0, float *out, float *smem) {
   using V = FewVec<T, VEC>;
-  const FewUnits u = few_units(R.n, K, N, COLS, gridDim.x);
-  float *xs = smem, *red = smem + kUnitRows * 8;
+  constexpr int PW = FewChunk<VEC>::per_warp, CH = FewChunk<VEC>::rows;
+  float *xs = smem, *red = smem + CH * 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int total = R.n * u.blocks * u.slices;
-  for (int w = blockIdx.x; w < total; w += gridDim.x) {
-    const int i = w / (u.blocks * u.slices), q = w % (u.blocks * u.slices);
-    const int cb = q % u.blocks, s = q / u.blocks;
-    const int k0 = s * u.per, k1 = min(K, k0 + u.per);
-    const int c = cb * COLS + lane * VEC;
-    const T *W = Wall + (size_t)R.expert[i] * K * N + c;
-    const int r1 = R.first[i + 1];
-    for (int r0 = R.first[i]; r0 < r1; r0 += 8) {
-      float acc[8][VEC] = {};
-      for (int kb = k0; kb < k1; kb += kUnitRows) {
-        const int n = min(kUnitRows, k1 - kb);
-        __syncthreads();
-        for (int j = tid; j < 8 * kUnitRows; j += kFewThreads) {
-          const int r = j / kUnitRows, kk = j % kUnitRows;
-          float v = 0.f;
-          if (r0 + r < r1 && kk < n) {
-            const size_t row = by_token ? R.token[r0 + r] : r0 + r;
-            v = few_f(A[row * K + kb + kk]);
-          }
-          xs[kk * 8 + r] = v;
-        }
-        __syncthreads();
-        if (c < N) {
-          const int m0 = warp * 32, m1 = min(n, m0 + 32);
-          for (int m = m0; m < m1; m += 8) {
-            V wv[8];
+  float acc[R][VEC] = {};
+  for (int kb = k0; kb < k1; kb += CH) {
+    const int n = min(CH, k1 - kb), m0 = warp * PW;
+    V wv[PW];
 #pragma unroll
-            for (int z = 0; z < 8; ++z)
-              if (m + z < m1)
-                wv[z] = *reinterpret_cast<const V *>(W + (size_t)(kb + m + z) * N);
+    for (int z = 0; z < PW; ++z)
+      if (live && m0 + z < n) wv[z] = *reinterpret_cast<const V *>(W + (size_t)(kb + m0 + z) * N);
+    constexpr int NX = (R * CH + kFewThreads - 1) / kFewThreads;
+    float xv[NX];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) {
-              if (m + z >= m1) break;
-              float f[VEC];
-              wv[z].get(f);
-              const float4 a = *reinterpret_cast<const float4 *>(xs + (m + z) * 8);
-              const float4 b = *reinterpret_cast<const float4 *>(xs + (m + z) * 8 + 4);
-              const float xr[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-              for (int r = 0; r < 8; ++r)
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) acc[r][v] = fmaf(xr[r], f[v], acc[r][v]);
-            }
-          }
-        }
+    for (int j = 0; j < NX; ++j) {
+      const int i = j * kFewThreads + tid, r = i / CH, kk = i % CH;
+      xv[j] = 0.f;
+      if (r < R && r0 + r < r1 && kk < n) {
+        const size_t row = by_token ? rows.token[r0 + r] : r0 + r;
+        xv[j] = few_f(A[row * K + kb + kk]);
       }
-      // Join the warps.
-      __syncthreads();
+    }
+    __syncthreads();
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
+    for (int j = 0; j < NX; ++j) {
+      const int i = j * kFewThreads + tid;
+      if (i < R * CH) xs[i % CH * R + i / CH] = xv[j];
+    }
+    __syncthreads();
+    if (live) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) red[((warp * 8 + r) * VEC + v) * 32 + lane] = acc[r][v];
-      __syncthreads();
-      for (int j = tid; j < 8 * VEC * 32; j += kFewThreads) {
-        const int r = j / (VEC * 32), l = j % 32, v = j / 32 % VEC;
-        const int col = cb * COLS + l * VEC + v;
-        if (r0 + r >= r1 || col >= N) continue;
-        float sum = 0.f;
+      for (int z = 0; z < PW; ++z) {
+        if (m0 + z >= n) break;
+        float f[VEC], x[R];
+        wv[z].get(f);
+        if constexpr (R == 8) {
+          const float4 a = *reinterpret_cast<const float4 *>(xs + (m0 + z) * 8);
+          const float4 b = *reinterpret_cast<const float4 *>(xs + (m0 + z) * 8 + 4);
+          x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+          x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        } else {
+          const float2 a = *reinterpret_cast<const float2 *>(xs + (m0 + z) * 2);
+          x[0] = a.x; x[1] = a.y;
+        }
 #pragma unroll
-        for (int x = 0; x < 8; ++x) sum += red[((x * 8 + r) * VEC + v) * 32 + l];
-        out[((size_t)s * R.rows + r0 + r) * N + col] = sum;
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) acc[r][v] = fmaf(x[r], f[v], acc[r][v]);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) red[((warp * R + r) * VEC + v) * 32 + lane] = acc[r][v];
+  __syncthreads();
+  for (int j = tid; j < R * VEC * 32; j += kFewThreads) {
+    const int r = j / (VEC * 32), l = j % 32, v = j / 32 % VEC;
+    const int col = c0 + l * VEC + v;
+    if (r0 + r >= r1 || col >= N) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sum += red[((x * R + r) * VEC + v) * 32 + l];
+    out[(size_t)(r0 + r) * N + col] = sum;
+  }
+}
+
+// One or two rows, the usual number, cost a quarter of eight's arithmetic.
+template <typename T, int VEC>
+__device__ void few_product(const FewRows &R, const FewUnits &u, const T *A, bool by_token,
+                            const T *Wall, int K, int N, float *out, float *smem) {
+  constexpr int COLS = 32 * VEC;
+  const int lane = threadIdx.x & 31;
+  for (int w = blockIdx.x; w < u.total; w += gridDim.x) {
+    const int i = (int)u.by_tile(w), q = w - i * u.blocks * u.slices;
+    const int s = (int)u.by_blocks(q), cb = q - s * u.blocks;
+    const int k0 = s * u.per, k1 = min(K, k0 + u.per), c = cb * COLS + lane * VEC;
+    const T *W = Wall + (size_t)R.expert[i] * K * N + c;
+    float *o = out + (size_t)s * R.rows * N;
+    const int r1 = R.first[i + 1];
+    for (int r0 = R.first[i]; r0 < r1;) {
+      if (r1 - r0 <= 2) {
+        few_unit<T, VEC, 2>(R, A, by_token, W, c < N, K, N, k0, k1, r0, r1, cb * COLS, o, smem);
+        r0 += 2;
+      } else {
+        few_unit<T, VEC, 8>(R, A, by_token, W, c < N, K, N, k0, k1, r0, r1, cb * COLS, o, smem);
+        r0 += 8;
       }
     }
   }
@@ -146,18 +192,23 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
   few_select<T>(p, work);
   if (!few_barrier(p, 1)) return;
   const FewRows R = few_rows(p, smem + kSimtSmemFloats * 4);
-  few_product<T, VEC>(R, static_cast<const T *>(p.x), true, static_cast<const T *>(p.W1), p.d,
-                      p.F, p.hpart, work);
+  __shared__ __align__(8) unsigned char unit_mem[2 * sizeof(FewUnits)];
+  FewUnits *u = reinterpret_cast<FewUnits *>(unit_mem);
+  if (threadIdx.x < 64 && threadIdx.x % 32 == 0) {
+    const bool second = threadIdx.x == 32;
+    u[second].make(R.n, second ? p.F : p.d, second ? p.d : p.F, 32 * VEC, gridDim.x);
+  }
+  __syncthreads();
+  few_product<T, VEC>(R, u[0], static_cast<const T *>(p.x), true, static_cast<const T *>(p.W1),
+                      p.d, p.F, p.hpart, work);
   if (!few_barrier(p, 2)) return;
-  constexpr int V = VEC < 4 ? VEC : 4;
-  const int s1 = few_units(R.n, p.d, p.F, 32 * VEC, gridDim.x).slices;
-  const int s2 = few_units(R.n, p.F, p.d, 32 * VEC, gridDim.x).slices;
-  few_hidden<T, V>(p, R, [&](int, int) { return s1; }, threadIdx.x, kFewThreads);
+  constexpr int V = VEC;
+  few_hidden<T, V>(p, R, [&](int, int) { return u[0].slices; }, threadIdx.x, kFewThreads);
   if (!few_barrier(p, 3)) return;
-  few_product<T, VEC>(R, static_cast<const T *>(p.h), false, static_cast<const T *>(p.W2), p.F,
-                      p.d, p.zpart, work);
+  few_product<T, VEC>(R, u[1], static_cast<const T *>(p.h), false, static_cast<const T *>(p.W2),
+                      p.F, p.d, p.zpart, work);
   if (!few_barrier(p, 4)) return;
-  few_combine<T, V>(p, R, [&](int, int) { return s2; });
+  few_combine<T, V>(p, R, [&](int, int) { return u[1].slices; });
 }
 
 template <typename T, int VEC>
@@ -263,6 +314,7 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.wait_ns = wait_limit_ns();
   if (c.act_dtype == MOE_F32) {
     if (c.d % 4 == 0 && c.d_ff % 4 == 0) return run_simt<float, 4>(p, s);
+    if (c.d % 2 == 0 && c.d_ff % 2 == 0) return run_simt<float, 2>(p, s);
     return run_simt<float, 1>(p, s);
   }
   if (few_tc_supported(c)) return launch_few_tc(p, s);
