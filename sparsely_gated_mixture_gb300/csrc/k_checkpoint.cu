@@ -228,6 +228,12 @@ k_ckpt_load_any(int cols, const int32_t *__restrict__ rows, const uint8_t *__res
   put(h + row * cols + c, ckpt_e4m3x2(q[row * cols + c]).x * ckpt_scale(scale[u]));
 }
 
+__global__ void k_ckpt_begin(DeviceStatus *st) {
+  pdl_wait();
+  if (threadIdx.x == 0) *st = DeviceStatus{};
+  pdl_trigger();
+}
+
 __global__ void k_ckpt_choices(int n, int E, const int32_t *__restrict__ idx,
                                int32_t *__restrict__ out, DeviceStatus *st,
                                const DeviceStatus *other) {
@@ -295,6 +301,10 @@ cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, cons
                                    cudaStream_t s) {
   return bf16 ? run_load<__nv_bfloat16>(max_rows, cols, rows, q, scale, h, s)
               : run_load<float>(max_rows, cols, rows, q, scale, h, s);
+}
+
+cudaError_t launch_checkpoint_begin(DeviceStatus *st, cudaStream_t s) {
+  return launch_pdl(k_ckpt_begin, dim3(1), 32, 0, s, st);
 }
 
 cudaError_t launch_checkpoint_choices(int n, int E, const int32_t *idx, int32_t *out,

@@ -1081,7 +1081,7 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
     // dgrad reads them in 8 bits).
     side = side_stream(side_lock, s);
     if (side) fs = side->s;
-    MOE_CUDA(cudaMemsetAsync(st, 0, sizeof(DeviceStatus), s));
+    MOE_CUDA(launch_checkpoint_begin(st, s));
     int r = fork();
     if (r == MOE_OK) r = ckpt_router(c, L, B, q, *ck, fs);
     if (r != MOE_OK) return r;

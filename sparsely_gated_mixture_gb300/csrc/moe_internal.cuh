@@ -366,6 +366,10 @@ cudaError_t launch_checkpoint_save(bool bf16, long long max_rows, int cols, cons
 cudaError_t launch_checkpoint_load(bool bf16, long long max_rows, int cols, const int32_t *rows,
                                    const uint8_t *q, const uint8_t *scale, void *h,
                                    cudaStream_t s);
+// Clears a status word: a kernel, for its place in the chain of dependent
+// launches (a memset in its place takes 10 us more of the noisy top-4 layer's
+// backward).
+cudaError_t launch_checkpoint_begin(DeviceStatus *st, cudaStream_t s);
 // The caller's choices with an index outside [0, E) replaced by 0 (recorded as
 // MOE_ERR_BOUNDS), for kernels that index by expert; an error in `other` (may be
 // null) is carried over to st.
