@@ -7,8 +7,8 @@
 //   selection  one block per token: logits, top-k or threshold mask, gates
 //   (every block then derives the capacity's slots and the experts' rows)
 //   layer 1    partial sums of x W1 over slices of d, for the experts in use
-//   hidden     H = ReLU(sum + b1), rounded to the layer's type
-//   layer 2    partial sums of H W2 over slices of d_ff
+//   layer 2    H = ReLU(sum + b1), rounded to the layer's type, and the partial
+//              sums of H W2 over slices of d_ff
 //   combine    y = x + sum of gate * (sum + b2)
 // with a barrier over the grid after each but the last.
 #pragma once
@@ -24,7 +24,7 @@ constexpr int kFewTokens = 64;     // T at most: an expert's tokens are one 64-b
 constexpr int kFewRows = 1024;     // T * k at most (k <= 16)
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxGrid = 512;   // blocks at most (sizes the partial buffers)
-constexpr int kFewBarriers = 5;
+constexpr int kFewBarriers = 4;
 constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 128-byte line
 constexpr int kFewColsMax = 256;   // columns of one unit of the experts' products at most
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
@@ -54,7 +54,7 @@ struct FewRouter {
 struct FewArgs {
   int T, d, E, F, k, C, mode;
   FewRouter rt;
-  FewDiv by_k, by_d4, by_f4;  // k; d / 4 and d_ff / 4 (1 where they are not whole)
+  FewDiv by_k, by_d4;  // k; d / 4 (1 where it is not whole)
   const void *x;
   const float *Wg, *Wn, *noise, *bias, *thr;
   const void *W1, *b1, *W2, *b2;
@@ -638,7 +638,7 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem) {
   return R;
 }
 
-// ----------------------------------------------------------------------------- hidden, combine
+// ----------------------------------------------------------------------------- combine
 // V floats at p (aligned to V floats), written by other blocks: from L2.
 template <int V>
 __device__ __forceinline__ void few_add(const float *p, float (&v)[V]) {
@@ -669,36 +669,6 @@ __device__ __forceinline__ void few_st(T *p, const float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) o.t[i] = few_t<T>(v[i]);
   *reinterpret_cast<Pack *>(p) = o;
-}
-
-// h[r] = ReLU(sum of the partial sums + b1), rounded once to the layer's
-// type, V columns at a time, by threads tid of n_threads of each block.
-// pieces(j, c): the number of partial sums of column c of expert j of R.
-template <typename T, int V, typename PF>
-__device__ __forceinline__ void few_hidden(const FewArgs &p, const FewRows &R, const PF &pieces,
-                                           int tid, int n_threads) {
-  const T *b1 = static_cast<const T *>(p.b1);
-  T *h = static_cast<T *>(p.h);
-  const unsigned cols = p.F / V, total = R.rows * cols;
-  const FewDiv by = V == 4 ? p.by_f4 : FewDiv(cols);
-  const size_t step = (size_t)R.rows * p.F;
-  for (unsigned i = blockIdx.x * n_threads + tid; i < total; i += gridDim.x * n_threads) {
-    const unsigned row = by(i), c = (i - row * cols) * V;
-    const int j = R.owner[row], np = pieces(j, (int)c);
-    const float *src = p.hpart + (size_t)row * p.F + c;
-    float v[V] = {};
-#pragma unroll 4
-    for (int s = 0; s < np; ++s) few_add<V>(src + s * step, v);
-    if (b1) {
-      float b[V];
-      few_ld<T, V>(b1 + (size_t)R.expert[j] * p.F + c, b);
-#pragma unroll
-      for (int q = 0; q < V; ++q) v[q] += b[q];
-    }
-#pragma unroll
-    for (int q = 0; q < V; ++q) v[q] = fmaxf(v[q], 0.f);
-    few_st<T, V>(h + (size_t)row * p.F + c, v);
-  }
 }
 
 // y[t] = x[t] + sum over the kept choices, in order, of gate * (sum of the

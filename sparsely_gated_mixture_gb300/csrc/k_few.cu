@@ -84,11 +84,39 @@ struct FewVec<__nv_bfloat16, 1> {
 // smem: xs [chunk rows][8], red [8 warps][8 rows][VEC][32 lanes].
 constexpr int kSimtSmemFloats = 256 * 8 + 8 * 8 * 32 * 4;
 
-// One unit's sums of rows r0 .. r0 + R - 1 (those below r1).
-template <typename T, int VEC, int R>
-__device__ __forceinline__ void few_unit(const FewRows &rows, const T *A, bool by_token,
-                                         const T *W, bool live, int K, int N, int k0, int k1,
-                                         int r0, int r1, int c0, float *out, float *smem) {
+// The rows of a product's left operand: layer 1's are tokens' x; layer 2's the
+// hidden ones, made of layer 1's partial sums where they are staged (ReLU of
+// their sum and b1, rounded once to the layer's type).
+template <typename T>
+struct FewX {
+  const FewRows &rows;
+  const T *x;
+  int K;
+  __device__ float operator()(int row, int k, int) const {
+    return few_f(x[(size_t)rows.token[row] * K + k]);
+  }
+};
+template <typename T>
+struct FewH {
+  const float *part;
+  size_t step;  // between the slices
+  const T *b1;
+  int K, slices;
+  __device__ float operator()(int row, int k, int e) const {
+    const float *p = part + (size_t)row * K + k;
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) v += __ldcg(p + s * step);
+    if (b1) v += few_f(b1[(size_t)e * K + k]);
+    return few_f(few_t<T>(fmaxf(v, 0.f)));
+  }
+};
+
+// One unit's sums of rows r0 .. r0 + R - 1 (those below r1) of expert e.
+template <typename T, int VEC, int R, typename AF>
+__device__ __forceinline__ void few_unit(const AF &A, int e, const T *W, bool live, int N, int k0,
+                                         int k1, int r0, int r1, int c0, float *out,
+                                         float *smem) {
   using V = FewVec<T, VEC>;
   constexpr int PW = FewChunk<VEC>::per_warp, CH = FewChunk<VEC>::rows;
   float *xs = smem, *red = smem + CH * 8;
@@ -106,10 +134,7 @@ __device__ __forceinline__ void few_unit(const FewRows &rows, const T *A, bool b
     for (int j = 0; j < NX; ++j) {
       const int i = j * kFewThreads + tid, r = i / CH, kk = i % CH;
       xv[j] = 0.f;
-      if (r < R && r0 + r < r1 && kk < n) {
-        const size_t row = by_token ? rows.token[r0 + r] : r0 + r;
-        xv[j] = few_f(A[row * K + kb + kk]);
-      }
+      if (r < R && r0 + r < r1 && kk < n) xv[j] = A(r0 + r, kb + kk, e);
     }
     __syncthreads();
 #pragma unroll
@@ -158,24 +183,25 @@ __device__ __forceinline__ void few_unit(const FewRows &rows, const T *A, bool b
 }
 
 // One or two rows, the usual number, cost a quarter of eight's arithmetic.
-template <typename T, int VEC>
-__device__ void few_product(const FewRows &R, const FewUnits &u, const T *A, bool by_token,
-                            const T *Wall, int K, int N, float *out, float *smem) {
+template <typename T, int VEC, typename AF>
+__device__ void few_product(const FewRows &R, const FewUnits &u, const AF &A, const T *Wall, int K,
+                            int N, float *out, float *smem) {
   constexpr int COLS = 32 * VEC;
   const int lane = threadIdx.x & 31;
   for (int w = blockIdx.x; w < u.total; w += gridDim.x) {
     const int i = (int)u.by_tile(w), q = w - i * u.blocks * u.slices;
     const int s = (int)u.by_blocks(q), cb = q - s * u.blocks;
     const int k0 = s * u.per, k1 = min(K, k0 + u.per), c = cb * COLS + lane * VEC;
-    const T *W = Wall + (size_t)R.expert[i] * K * N + c;
+    const int e = R.expert[i];
+    const T *W = Wall + (size_t)e * K * N + c;
     float *o = out + (size_t)s * R.rows * N;
     const int r1 = R.first[i + 1];
     for (int r0 = R.first[i]; r0 < r1;) {
       if (r1 - r0 <= 2) {
-        few_unit<T, VEC, 2>(R, A, by_token, W, c < N, K, N, k0, k1, r0, r1, cb * COLS, o, smem);
+        few_unit<T, VEC, 2>(A, e, W, c < N, N, k0, k1, r0, r1, cb * COLS, o, smem);
         r0 += 2;
       } else {
-        few_unit<T, VEC, 8>(R, A, by_token, W, c < N, K, N, k0, k1, r0, r1, cb * COLS, o, smem);
+        few_unit<T, VEC, 8>(A, e, W, c < N, N, k0, k1, r0, r1, cb * COLS, o, smem);
         r0 += 8;
       }
     }
@@ -199,15 +225,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
     u[second].make(R.n, second ? p.F : p.d, second ? p.d : p.F, 32 * VEC, gridDim.x);
   }
   __syncthreads();
-  few_product<T, VEC>(R, u[0], static_cast<const T *>(p.x), true, static_cast<const T *>(p.W1),
-                      p.d, p.F, p.hpart, work);
+  const FewX<T> x{R, static_cast<const T *>(p.x), p.d};
+  few_product<T, VEC>(R, u[0], x, static_cast<const T *>(p.W1), p.d, p.F, p.hpart, work);
   if (!few_barrier(p, 2)) return;
-  constexpr int V = VEC;
-  few_hidden<T, V>(p, R, [&](int, int) { return u[0].slices; }, threadIdx.x, kFewThreads);
+  const FewH<T> h{p.hpart, (size_t)R.rows * p.F, static_cast<const T *>(p.b1), p.F, u[0].slices};
+  few_product<T, VEC>(R, u[1], h, static_cast<const T *>(p.W2), p.F, p.d, p.zpart, work);
   if (!few_barrier(p, 3)) return;
-  few_product<T, VEC>(R, u[1], static_cast<const T *>(p.h), false, static_cast<const T *>(p.W2),
-                      p.F, p.d, p.zpart, work);
-  if (!few_barrier(p, 4)) return;
+  constexpr int V = VEC;
   few_combine<T, V>(p, R, [&](int, int) { return u[1].slices; });
 }
 
@@ -282,7 +306,6 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.mode = q.thr ? kFewThreshold : c.gate_mode == MOE_GATE_SWITCH ? kFewSwitch : kFewTopk;
   p.by_k = FewDiv(c.k);
   p.by_d4 = FewDiv(c.d % 4 == 0 ? c.d / 4 : 1);
-  p.by_f4 = FewDiv(c.d_ff % 4 == 0 ? c.d_ff / 4 : 1);
   p.x = q.x;
   p.Wg = q.Wg;
   p.Wn = q.Wn;
