@@ -215,9 +215,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
   few_start(p);
   few_route<T>(p, work);
   if (!few_barrier(p, 0)) return;
-  few_select<T>(p, work);
-  if (!few_barrier(p, 1)) return;
-  const FewRows R = few_rows(p, smem + kSimtSmemFloats * 4);
+  __shared__ FewAlone alone;
+  few_select<T>(p, work, alone);
+  if (p.T == 1) __syncthreads();
+  else if (!few_barrier(p, 1)) return;
+  const FewRows R = few_rows(p, smem + kSimtSmemFloats * 4, alone);
   __shared__ __align__(8) unsigned char unit_mem[2 * sizeof(FewUnits)];
   FewUnits *u = reinterpret_cast<FewUnits *>(unit_mem);
   if (threadIdx.x < 64 && threadIdx.x % 32 == 0) {

@@ -168,6 +168,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   __shared__ bool last_part;
+  __shared__ FewAlone alone;
   __shared__ __align__(16) unsigned char line_mem[2 * sizeof(FewLine)];
   FewLine *line = reinterpret_cast<FewLine *>(line_mem);
   volatile int *abort_flag = &abort_word;
@@ -211,14 +212,14 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   few_route<__nv_bfloat16>(p, work);
   bool ok = few_barrier(p, 0);
   if (ok) {
-    few_select<__nv_bfloat16>(p, work);
-    ok = few_barrier(p, 1);
+    few_select<__nv_bfloat16>(p, work, alone);
+    if (p.T > 1) ok = few_barrier(p, 1);
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   FewRows R{};
-  if (ok) R = few_rows(p, reinterpret_cast<char *>(rows_mem));
+  if (ok) R = few_rows(p, reinterpret_cast<char *>(rows_mem), alone);
   if (ok && R.n > 0 && lane == 0 && warp < 2)
     line[warp].make(R.n, warp ? p.F : p.d, warp ? p.d : p.F, gridDim.x);
   fence_proxy_async_smem();  // generic accesses to the ring come before TMA's
