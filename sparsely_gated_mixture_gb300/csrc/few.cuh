@@ -46,8 +46,8 @@ struct FewDiv {
 // The router's units (few_router).
 struct FewRouter {
   int NC, groups, slices, rows_per_slice;
-  int lcw;  // log2 of the columns of a unit
-  int lt;   // log2 of the warps side by side over the tokens
+  int lcw;  // log2 of the columns of a unit (8 to 32)
+  int lt;   // log2 of the groups of 8 tokens (2 to 8)
   FewDiv by_group;
 };
 
@@ -168,18 +168,17 @@ __device__ __forceinline__ __nv_bfloat16 few_t<__nv_bfloat16>(float v) {
 }
 
 // ----------------------------------------------------------------------------- router
-// Columns: E of W_g, then E of W_noise. A unit is 32 columns (or, for fewer,
-// the power of two from their number on, a warp's lanes then covering several
-// rows) and one slice of d, as many units as blocks where that is possible.
+// Columns: E of W_g, then E of W_noise. A unit is 32 columns (8 or 16 where
+// there are no more) and one slice of d, as many units as blocks where that is
+// possible.
 // 64 rows of the weights and of x (for every token) are staged in shared
-// memory at a time; a warp takes 8 tokens, and with fewer than 64 tokens the
-// warps of the same tokens share the rows. Every product is fp32.
+// memory at a time.
 constexpr int kRtRows = 64;
 
 inline FewRouter few_router(int T, int d, int E, bool noisy, int grid) {
   FewRouter r;
   r.NC = noisy ? 2 * E : E;
-  r.lcw = 0;
+  r.lcw = 3;
   while (r.lcw < 5 && (1 << r.lcw) < r.NC) ++r.lcw;
   r.groups = (r.NC + (1 << r.lcw) - 1) >> r.lcw;
   int s = grid / r.groups;
@@ -188,7 +187,7 @@ inline FewRouter few_router(int T, int d, int E, bool noisy, int grid) {
   if (s < 1) s = 1;
   r.rows_per_slice = ((d + s - 1) / s + 7) / 8 * 8;
   r.slices = (d + r.rows_per_slice - 1) / r.rows_per_slice;
-  r.lt = 0;
+  r.lt = 1;
   while ((8 << r.lt) < T) ++r.lt;
   r.by_group = FewDiv((unsigned)r.groups);
   return r;
@@ -218,10 +217,12 @@ __device__ __forceinline__ void few_x8(const T *x, int d, int k, float (&f)[8]) 
   }
 }
 
+// fp32 x, on the CUDA cores: a warp takes 8 tokens, and with fewer than 64
+// tokens the warps of the same tokens share the rows.
 // smem: xs [kRtRows][tokens, a multiple of 8], w [kRtRows][cw], red [8 warps][8][32]:
 // 32 KB at most.
 template <typename T>
-__device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
+__device__ __forceinline__ void few_route_f32(const FewArgs &p, float *smem) {
   const FewRouter &r = p.rt;
   const int tgp = 1 << r.lt, tp = 8 << r.lt;  // warps, tokens side by side
   const int ks = 8 >> r.lt;                   // warps that share a token group's rows
@@ -313,6 +314,156 @@ __device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
       p.rpart[((size_t)s * p.T + t) * r.NC + col] = v;
     }
   }
+}
+
+__device__ __forceinline__ void few_mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// bf16 x: a weight is the exact sum of three bf16 numbers, so three bf16
+// products with fp32 accumulation give the fp32 product. The CUDA-core form
+// above is bound by its shared-memory reads (9 for 8 multiply-adds: 8 us for 40
+// tokens and 1024 columns); here a 16-row step takes 28 for the whole block's
+// 64 tokens x 16 columns. The products are too small and the weights too few
+// for tcgen05's operands (they would first have to be split into memory).
+// Warps: 4 steps of 16 rows x 2 halves of the columns; joined in shared memory.
+// smem: xs bf16 [tokens][72], w bf16 [3][cw][72] (rows of 64 with a pad that
+// spreads the fragments' reads over the banks); then red [4][tokens][cw] floats.
+__device__ __forceinline__ void few_route_bf16(const FewArgs &p, float *smem) {
+  const FewRouter &r = p.rt;
+  const int tp = 8 << r.lt, mt = tp >> 4, cw = 1 << r.lcw, nt = cw >> 3;
+  constexpr int P = 36;  // 32-bit words of a staged row
+  uint32_t *xs = reinterpret_cast<uint32_t *>(smem), *ws = xs + tp * P;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int step = warp & 3, nh = warp >> 2, g = lane >> 2, q = lane & 3;
+  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x);
+  int xt[2], xo[2];  // the token and the 8 columns that this thread stages
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    xo[i] = ((i * kFewThreads + tid) >> (3 + r.lt)) * 8;
+    xt[i] = (i * kFewThreads + tid) & (tp - 1);
+  }
+  for (int u = blockIdx.x; u < r.groups * r.slices; u += gridDim.x) {
+    const int s = (int)r.by_group(u), gr = u - s * r.groups;
+    const int k0 = s * r.rows_per_slice, k1 = min(p.d, k0 + r.rows_per_slice);
+    const int col0 = gr << r.lcw;
+    float acc[4][2][4] = {};
+    float wv[4][2], xv[2][8];
+    // The next 64 rows are in flight while these are multiplied.
+    auto fetch = [&](int kb) {
+      const int n = min(kRtRows, k1 - kb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = i * kFewThreads + tid, kk = (at >> r.lcw) * 2, col = col0 + (at & (cw - 1));
+        const float *w = col < p.E ? p.Wg + col : p.Wn + col - p.E;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          wv[i][j] = kk + j < n && col < r.NC ? w[(size_t)(kb + kk + j) * p.E] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (xt[i] < p.T && xo[i] < n) {
+          few_x8(x + (size_t)xt[i] * p.d, p.d, kb + xo[i], xv[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) xv[i][j] = 0.f;
+        }
+      }
+    };
+    fetch(k0);
+    for (int kb = k0; kb < k1; kb += kRtRows) {
+      __syncthreads();  // the previous rows have been used
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = i * kFewThreads + tid;
+        if (at >= (kRtRows / 2) << r.lcw) break;
+        uint32_t *dst = ws + (at & (cw - 1)) * P + (at >> r.lcw);
+        float a = wv[i][0], b = wv[i][1];
+#pragma unroll
+        for (int z = 0; z < 3; ++z) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+          dst[z * cw * P] = *reinterpret_cast<const uint32_t *>(&h);
+          a -= __low2float(h);
+          b -= __high2float(h);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (xo[i] < kRtRows) {
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(xv[i][2 * j], xv[i][2 * j + 1]);  // exact
+            o[j] = *reinterpret_cast<const uint32_t *>(&h);
+          }
+          *reinterpret_cast<uint4 *>(xs + xt[i] * P + xo[i] / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      __syncthreads();
+      if (kb + kRtRows < k1) fetch(kb + kRtRows);
+      if (nh < nt) {
+        uint32_t b[2][3][2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          if (nh + 2 * n >= nt) break;
+#pragma unroll
+          for (int z = 0; z < 3; ++z) {
+            const uint32_t *w = ws + (z * cw + (nh + 2 * n) * 8 + g) * P + step * 8 + q;
+            b[n][z][0] = w[0];
+            b[n][z][1] = w[4];
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (m >= mt) break;
+          const uint32_t *at = xs + (m * 16 + g) * P + step * 8 + q;
+          const uint32_t a[4] = {at[0], at[8 * P], at[4], at[8 * P + 4]};
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (nh + 2 * n >= nt) break;
+#pragma unroll
+            for (int z = 2; z >= 0; --z) few_mma16816(acc[m][n], a, b[n][z][0], b[n][z][1]);
+          }
+        }
+      }
+    }
+    __syncthreads();  // the staged rows have been used: red takes their place
+    float *red = smem;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (m >= mt) break;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        if (nh + 2 * n >= nt) break;
+        float *o = red + ((step * tp + m * 16 + g) << r.lcw) + (nh + 2 * n) * 8 + q * 2;
+        o[0] = acc[m][n][0];
+        o[1] = acc[m][n][1];
+        o[8 << r.lcw] = acc[m][n][2];
+        o[(8 << r.lcw) + 1] = acc[m][n][3];
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < tp << r.lcw; i += kFewThreads) {
+      const int t = i >> r.lcw, col = col0 + (i & (cw - 1));
+      if (t >= p.T || col >= r.NC) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += red[(w * tp << r.lcw) + i];
+      p.rpart[((size_t)s * p.T + t) * r.NC + col] = v;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void few_route(const FewArgs &p, float *smem) {
+  if constexpr (sizeof(T) == 2)
+    few_route_bf16(p, smem);
+  else
+    few_route_f32<T>(p, smem);
 }
 
 // ----------------------------------------------------------------------------- selection
