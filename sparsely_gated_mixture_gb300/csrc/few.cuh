@@ -23,10 +23,10 @@ namespace moe {
 constexpr int kFewTokens = 64;     // T at most: an expert's tokens are one 64-bit mask
 constexpr int kFewRows = 1024;     // T * k at most (k <= 16)
 constexpr int kFewThreads = 256;
-constexpr int kFewMaxGrid = 512;   // blocks at most (sizes the partial buffers)
+constexpr int kFewMaxGrid = 320;   // blocks at most (sizes the flags and partial sums)
 constexpr int kFewBarriers = 4;
 constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 128-byte line
-constexpr int kFewColsMax = 256;   // columns of one unit of the experts' products at most
+constexpr int kFewTile = 256;      // weight columns of a unit on the tensor cores
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
 // Division by a number that is fixed for the call, as a multiplication: the

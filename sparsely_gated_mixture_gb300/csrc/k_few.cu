@@ -23,7 +23,9 @@ struct FewChunk {
   static constexpr int rows = 8 * per_warp;
 };
 
-// The slices of K: as many as make the fewest rows of K for the busiest block,
+constexpr int kSlices = 8;
+
+// The slices of K, up to kSlices: as many as make the fewest rows of K for the busiest block,
 // a unit's own cost (staging, joining) counted as 64 rows.
 struct FewUnits {
   int blocks, slices, per;  // column blocks, slices of K, rows of K per slice
@@ -35,7 +37,7 @@ struct FewUnits {
     int best = 0x7fffffff;
     slices = 1;
     per = K;
-    for (int s = 1; s <= 8; ++s) {
+    for (int s = 1; s <= kSlices; ++s) {
       const int rows = ((K + s - 1) / s + 31) / 32 * 32, n = (K + rows - 1) / rows;
       const int cost = (tiles * n + grid - 1) / grid * (rows + 64);
       if (cost < best) {
@@ -252,7 +254,7 @@ cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
 
 cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
                             cudaStream_t s) {
-  const cudaError_t err =
+  cudaError_t err =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -265,7 +267,9 @@ cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t sm
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, kernel, args);
+  err = cudaLaunchKernelExC(&cfg, kernel, args);
+  if (err != cudaSuccess) cudaGetLastError();  // reported here, not by the next call
+  return err;
 }
 
 FewLayout few_layout(const moe_config &c) {
@@ -285,11 +289,16 @@ FewLayout few_layout(const moe_config &c) {
   L.gate = take(A * 4);
   // Router: slices * columns <= (grid + groups) * 32, with noise or without.
   L.rpart = take(T * 32 * (kFewMaxGrid + 2 * (2 * E + 31) / 32 + 1) * 4);
-  // A layer's partials: with at most 2 grid / (experts in use * column blocks)
-  // + 2 of them per column (both forms) and rows <= T * experts in use (and <=
-  // T k), partials * rows * N <= T * 2 grid * (columns of a block) + 2 T k N.
-  L.hpart = take((T * 2 * kFewMaxGrid * kFewColsMax + 2 * A * F) * 4);
-  L.zpart = take((T * 2 * kFewMaxGrid * kFewColsMax + 2 * A * d) * 4);
+  // A layer's partial sums. On the CUDA cores: at most kSlices of every value.
+  // On the tensor cores a tile has at most KC / (a run's length) + 2, and a run
+  // at least 2 / 3 of total / G units (total / G rounded down, 2 at least); with
+  // total = experts in use * NT * KC and rows <= T * experts in use that is
+  // 1.5 T G kFewTile floats and two of every value.
+  const auto partials = [&](size_t N) {
+    return few_tc_supported(c) ? T * 2 * kFewMaxGrid * kFewTile + 2 * A * N : kSlices * A * N;
+  };
+  L.hpart = take(partials(F) * 4);
+  L.zpart = take(partials(d) * 4);
   L.h = take(A * F * elem_bytes(c.act_dtype));
   L.total = off;
   return L;

@@ -25,7 +25,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 256;                    // weight columns of a unit
+constexpr int kTile = kFewTile;               // weight columns of a unit
 constexpr int kChunk = 64;                    // rows of K of a unit
 constexpr int kWBytes = kTile * kChunk * 2;   // 32 KB
 constexpr int kBoxBytes = 64 * kChunk * 2;    // one [64 x 64] box, 8 KB

@@ -26,6 +26,14 @@ def test_workspace_sizes(lib):
     assert lib.moe_few_workspace_size(ctypes.byref(B.config(1, 64, 8, 128, 2, 1.0)), None) == 1
 
 
+def test_workspace_holds_the_cuda_cores_partial_sums(lib):
+    """Up to 8 slices of K of both products, whatever share of the rows the
+    experts get (widths that the tensor cores do not take)."""
+    for act, d, d_ff in ((B.MOE_BF16, 4098, 2050), (B.MOE_F32, 8192, 4096)):
+        cfg = B.config(64, d, 16, d_ff, 16, 1.0, act_dtype=act)
+        assert B.moe_few_workspace_size(cfg) >= 8 * 64 * 16 * (d + d_ff) * 4
+
+
 @pytest.mark.parametrize("bad", [
     {0: None}, {0: F + 8}, {1: None}, {2: F}, {3: F}, {4: F + 4}, {5: None}, {6: F + 2}, {7: None},
     {9: None}, {10: F + 4}, {11: F + 4}, {12: F + 4}, {13: F + 1}, {14: None}, {14: F + 16}])

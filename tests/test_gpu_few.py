@@ -102,6 +102,9 @@ CASES = {
     "many_experts_odd": _w(50, 40, 999, 24, 16, cf=64.0, noisy=True),
     "switch_noisy": _w(31, 128, 12, 96, 1, cf=1.0, mode=wl.SWITCH, noisy=True),
     "k16": _w(64, 128, 40, 64, 16, cf=1.0),
+    "largest": _w(64, 72, 1024, 24, 16, cf=1024.0, noisy=True),
+    "largest_odd": _w(64, 67, 1024, 23, 16, cf=1024.0, noisy=True),
+    "largest_f32": _w(64, 68, 1024, 24, 16, cf=1024.0, dtype="f32"),
 }
 
 
