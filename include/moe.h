@@ -505,8 +505,9 @@ int moe_gate_backward(const moe_config *cfg, const void *x, const float *Wg, con
  *   >= the block's largest value; values round to nearest, ties to even, but
  *   one over zero is never stored as zero (the ReLU's pattern survives, and
  *   with it every gradient that uses only the pattern). Values <= 0 are
- *   stored as 0. A block holding an Inf or NaN gets hscale 255, loads as NaN
- *   and is recorded as MOE_ERR_NONFINITE (detail = the value's flat index).
+ *   stored as 0. A block holding a NaN or a positive Inf gets hscale 255,
+ *   loads as NaN and is recorded as MOE_ERR_NONFINITE (detail = a flat index in
+ *   it).
  *   Loading is exact in bf16 and fp32.
  * rows = min(T*k, E*C) at most (moe_checkpoint_size, which also gives the two
  *   arrays' bytes); rows past expert_offset[E] are neither read nor written.

@@ -11,13 +11,16 @@
 //   - every stored value is exact in bf16 (4 significant bits, exponent at
 //     least -133), so loading rounds nothing.
 // Values at or below zero (the rows are ReLU outputs) are stored as zero. A
-// block with a non-finite value gets the scale byte 255 and loads as NaN.
-// Scale bytes: e + 127.
+// block with a NaN or an infinity over zero gets the scale byte 255 and loads
+// as NaN. Scale bytes: e + 127.
 //
 // Both directions are HBM streams: one warp moves 1024 columns of a row,
 // every 16-byte (fp32: 32-byte) load issued before the first is used; 4 lanes
 // of 8 columns make a block. Widths that are not a multiple of 8 go one
-// column per lane.
+// column per lane. Saving was bound by its instructions before it was by memory
+// (some 10 a value: 135 us for the large-expert layer's rows, loading 98); the
+// largest value and the ReLU now take one packed instruction for two bf16
+// values, the lift over zero two a value.
 #include "checkpoint.cuh"
 #include "moe_internal.cuh"
 
@@ -38,10 +41,21 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// v / 2^e for e4m3: positive values stay positive; where 448 * 2^e passes the
-// largest float (e >= 120) the result stops at 240, whose value is finite.
-__device__ __forceinline__ float scaled(float v, float inv, float cap) {
-  return v > 0.f ? fminf(fmaxf(v * inv, 0.001953125f), cap) : 0.f;
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// v / 2^e (v >= 0) for e4m3, at least 2^-9 where v is over zero. Saturates in
+// the conversion; where 448 * 2^e passes the largest float (e >= 120) it stops
+// at 240, whose value is finite.
+constexpr float kLeast = 0.001953125f;
+template <typename T>
+__device__ __forceinline__ float scaled(float v, float inv) {
+  // Any bf16 over zero (2^-133 on) times 2^127 is over 2^-9.
+  if constexpr (sizeof(T) == 2) return fmaxf(v * inv, fminf(v * 0x1p127f, kLeast));
+  return fmaxf(v * inv, v > 0.f ? kLeast : 0.f);
 }
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -51,6 +65,15 @@ struct Oct;
 template <>
 struct Oct<__nv_bfloat16> {
   uint4 v;
+  // Values below zero become zero; the largest of all, NaN if one is.
+  __device__ __forceinline__ float relu_top() {
+    __nv_bfloat162 *w = reinterpret_cast<__nv_bfloat162 *>(&v);
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __hmax2_nan(w[j], zero);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
+    return max_nan(__low2float(m), __high2float(m));
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -72,6 +95,17 @@ struct Oct<__nv_bfloat16> {
 template <>
 struct Oct<float> {
   float4 a, b;
+  __device__ __forceinline__ float relu_top() {
+    float f[8], top = 0.f;
+    get(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      f[j] = max_nan(f[j], 0.f);
+      top = max_nan(top, f[j]);
+    }
+    set(f);
+    return top;
+  }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
@@ -107,31 +141,27 @@ k_ckpt_save(int cols, int segs, const int32_t *__restrict__ rows, const T *__res
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int c = seg * kSeg + i * 256 + lane * 8;
-    float f[8] = {};
-    if (c < cols) in[i].get(f);
-    float top = 0.f;
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      top = fmaxf(top, f[j]);
-      bad |= !isfinite(f[j]);
-    }
+    float f[8], top = 0.f;
+    if (c < cols) top = in[i].relu_top();
+    const bool bad = !(top < INFINITY);
     if (bad) top = INFINITY;
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const bool fine = top < INFINITY;
     const int e = fine ? scale_exp(top) : 0;
-    const float inv = pow2(-e), cap = e >= 120 ? 240.f : 448.f;
+    const float inv = pow2(-e);
     const uint32_t byte = fine ? (uint32_t)(e + 127) : 255u;
     const uint32_t got = __shfl_sync(0xffffffffu, byte, 4 * (lane & 7));
     if ((lane >> 3) == i) mine = got;
     if (c < cols) {
-      uint2 o;
-      o.x = e4m3x2(scaled(f[0], inv, cap), scaled(f[1], inv, cap)) |
-            e4m3x2(scaled(f[2], inv, cap), scaled(f[3], inv, cap)) << 16;
-      o.y = e4m3x2(scaled(f[4], inv, cap), scaled(f[5], inv, cap)) |
-            e4m3x2(scaled(f[6], inv, cap), scaled(f[7], inv, cap)) << 16;
-      *reinterpret_cast<uint2 *>(dst + c) = o;
+      in[i].get(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = scaled<T>(f[j], inv);
+      if (e >= 120)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fminf(f[j], 240.f);
+      *reinterpret_cast<uint2 *>(dst + c) = make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16,
+                                                       e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
     }
     if (bad) record_error(st, MOE_ERR_NONFINITE, row * cols + c);
   }
@@ -200,15 +230,16 @@ k_ckpt_save_any(int cols, const int32_t *__restrict__ rows, const T *__restrict_
   const int b = (int)(u - row * nb);
   if (row >= max_rows || row >= *rows) return;
   const int c = b * kCkptBlock + lane;
-  const float v = c < cols ? to_f(h[row * cols + c]) : 0.f;
-  const bool bad = !isfinite(v);
-  float top = bad ? INFINITY : fmaxf(v, 0.f);
+  const float v = c < cols ? max_nan(to_f(h[row * cols + c]), 0.f) : 0.f;
+  const bool bad = !(v < INFINITY);
+  float top = bad ? INFINITY : v;
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const bool fine = top < INFINITY;
   const int e = fine ? scale_exp(top) : 0;
   if (c < cols)
-    q[row * cols + c] = (uint8_t)e4m3x2(scaled(v, pow2(-e), e >= 120 ? 240.f : 448.f), 0.f);
+    q[row * cols + c] =
+        (uint8_t)e4m3x2(fminf(scaled<T>(v, pow2(-e)), e >= 120 ? 240.f : 448.f), 0.f);
   if (lane == 0) scale[u] = fine ? (uint8_t)(e + 127) : (uint8_t)255;
   if (bad) record_error(st, MOE_ERR_NONFINITE, row * cols + c);
 }

@@ -28,14 +28,14 @@ def quantise(h):
         for b in range(nb):
             c = slice(b * BLOCK, min(F, (b + 1) * BLOCK))
             x = h[r, c]
-            if not np.all(np.isfinite(x)):
+            if np.any(np.isnan(x) | (x == np.inf)):
                 s[r, b], v[r, c] = 255, np.nan
                 continue
             top = max(0.0, x.max())
             e = LOW
             while 448.0 * 2.0 ** e < top:
                 e += 1
-            z = np.where(x > 0, x, 0.0) / 2.0 ** e
+            z = np.maximum(x, 0.0) / 2.0 ** e
             i = np.searchsorted(mid, z)  # nearest, the lower one on ties
             tie = (i < 126) & (z == mid[np.minimum(i, 125)])
             i = np.where(tie & (i % 2 == 1), i + 1, i)

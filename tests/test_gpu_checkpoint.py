@@ -70,6 +70,24 @@ def test_format_against_fp64(dtype, F):
     assert bool((out[n:] == -5).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("F", [64, 50])
+def test_values_below_zero_are_stored_as_zero(dtype, F):
+    cfg = B.config(4, 8, 1, F, 1, 1.0, act_dtype=B.MOE_BF16 if dtype == "bf16" else B.MOE_F32)
+    h = np.random.default_rng(2).standard_normal((4, F)).astype(np.float32)
+    h[1] = -np.abs(h[1])
+    h[2, 3], h[2, 40], h[3, 0] = -np.inf, -0.0, -1e-38
+    bits = wl.f32_to_bf16_bits(h) if dtype == "bf16" else h
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    h8, hs, _ = checkpoint(cfg)
+    B.moe_checkpoint_save(cfg, dev_act(bits, dtype), off, h8, hs, ws)
+    q, s, _ = ref.quantise(few.f64(bits, dtype))
+    assert B.moe_last_device_status(ws)[0] == 0
+    assert np.array_equal(h8.cpu().numpy().reshape(4, F), q)
+    assert np.array_equal(hs.cpu().numpy().reshape(4, -1), s)
+
+
 @pytest.mark.parametrize("F", [64, 50])
 def test_nonfinite_rows_are_recorded_and_load_as_nan(F):
     cfg = B.config(4, 8, 1, F, 1, 1.0)
