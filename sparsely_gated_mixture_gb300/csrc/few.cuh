@@ -29,32 +29,18 @@ constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 
 constexpr int kFewTile = 256;      // weight columns of a unit on the tensor cores
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
-// Division by a number that is fixed for the call, as a multiplication: the
-// quotient from floor((2^32 - 1) / d) is at most one too small. (A plain
-// division is some 150 cycles of latency, which the phases of a one-token call
-// would pay a dozen times in a row.)
-struct FewDiv {
-  unsigned d, inv;
-  __host__ __device__ FewDiv() : d(1), inv(0xffffffffu) {}
-  __host__ __device__ explicit FewDiv(unsigned v) : d(v), inv(0xffffffffu / v) {}
-  __device__ unsigned operator()(unsigned n) const {
-    const unsigned q = __umulhi(n, inv);
-    return q + (n - q * d >= d ? 1u : 0u);
-  }
-};
-
 // The router's units (few_router).
 struct FewRouter {
   int NC, groups, slices, rows_per_slice;
   int lcw;  // log2 of the columns of a unit (8 to 32)
   int lt;   // log2 of the groups of 8 tokens (2 to 8)
-  FewDiv by_group;
+  FixedDiv by_group;
 };
 
 struct FewArgs {
   int T, d, E, F, k, C, mode;
   FewRouter rt;
-  FewDiv by_k, by_d4;  // k; d / 4 (1 where it is not whole)
+  FixedDiv by_k, by_d4;  // k; d / 4 (1 where it is not whole)
   const void *x;
   const float *Wg, *Wn, *noise, *bias, *thr;
   const void *W1, *b1, *W2, *b2;
@@ -189,7 +175,7 @@ inline FewRouter few_router(int T, int d, int E, bool noisy, int grid) {
   r.slices = (d + r.rows_per_slice - 1) / r.rows_per_slice;
   r.lt = 1;
   while ((8 << r.lt) < T) ++r.lt;
-  r.by_group = FewDiv((unsigned)r.groups);
+  r.by_group = FixedDiv((unsigned)r.groups);
   return r;
 }
 
@@ -847,7 +833,7 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
   T *y = static_cast<T *>(p.y);
   const unsigned cols = p.d / V, total = p.T * cols;
   const size_t step = (size_t)R.rows * p.d;
-  const FewDiv by = V == 4 ? p.by_d4 : FewDiv(cols);
+  const FixedDiv by = V == 4 ? p.by_d4 : FixedDiv(cols);
   const unsigned lshare = total * 8 <= gridDim.x * kFewThreads ? 3 : 0, share = 1u << lshare;
   const unsigned sub = threadIdx.x & (share - 1), lane = threadIdx.x & 31;
   for (unsigned w = blockIdx.x * kFewThreads + threadIdx.x; w - lane < total * share;

@@ -17,10 +17,11 @@
 // Both directions are HBM streams: one warp moves 1024 columns of a row,
 // every 16-byte (fp32: 32-byte) load issued before the first is used; 4 lanes
 // of 8 columns make a block. Widths that are not a multiple of 8 go one
-// column per lane. Saving was bound by its instructions before it was by memory
-// (some 10 a value: 135 us for the large-expert layer's rows, loading 98); the
-// largest value and the ReLU now take one packed instruction for two bf16
-// values, the lift over zero two a value.
+// column per lane. Saving and loading the 16384 rows of 14336 of the large-expert
+// layer take 215 us for 1.42 GB, 6.6 TB/s. Saving was bound by its instructions
+// first (some 10 a value, 227 us for both): the ReLU and the largest value now
+// take one packed instruction for two bf16 values, the lift over zero two a
+// value, and a warp's row no 64-bit division.
 #include "checkpoint.cuh"
 #include "moe_internal.cuh"
 
@@ -118,15 +119,15 @@ struct Oct<float> {
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_save(int cols, int segs, const int32_t *__restrict__ rows, const T *__restrict__ h,
+k_ckpt_save(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, const T *__restrict__ h,
             uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
             DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-  const long long row = u / segs;
-  const int seg = (int)(u - row * segs);
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5), r = by_seg(u);
+  const long long row = r;
+  const int seg = (int)(u - r * by_seg.d);
   if (row >= max_rows || row >= *rows) return;
   const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const T *src = h + row * cols;
@@ -171,14 +172,14 @@ k_ckpt_save(int cols, int segs, const int32_t *__restrict__ rows, const T *__res
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_load(int cols, int segs, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
+k_ckpt_load(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
             const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-  const long long row = u / segs;
-  const int seg = (int)(u - row * segs);
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5), r = by_seg(u);
+  const long long row = r;
+  const int seg = (int)(u - r * by_seg.d);
   if (row >= max_rows || row >= *rows) return;
   const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
   const uint8_t *src = q + row * cols;
@@ -218,16 +219,15 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // Any width: a warp per block of 32 columns, one column per lane.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_save_any(int cols, const int32_t *__restrict__ rows, const T *__restrict__ h,
+k_ckpt_save_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows, const T *__restrict__ h,
                 uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
                 DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-  const long long row = u / nb;
-  const int b = (int)(u - row * nb);
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5), r = by_block(u);
+  const long long row = r;
+  const int b = (int)(u - r * by_block.d);
   if (row >= max_rows || row >= *rows) return;
   const int c = b * kCkptBlock + lane;
   const float v = c < cols ? max_nan(to_f(h[row * cols + c]), 0.f) : 0.f;
@@ -246,15 +246,14 @@ k_ckpt_save_any(int cols, const int32_t *__restrict__ rows, const T *__restrict_
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_load_any(int cols, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
+k_ckpt_load_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
                 const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int nb = (cols + kCkptBlock - 1) / kCkptBlock;
-  const long long u = blockIdx.x * (long long)kWarps + (threadIdx.x >> 5);
-  const long long row = u / nb;
-  const int c = (int)(u - row * nb) * kCkptBlock + lane;
+  const unsigned u = blockIdx.x * kWarps + (threadIdx.x >> 5), r = by_block(u);
+  const long long row = r;
+  const int c = (int)(u - r * by_block.d) * kCkptBlock + lane;
   if (row >= max_rows || row >= *rows || c >= cols) return;
   put(h + row * cols + c, ckpt_e4m3x2(q[row * cols + c]).x * ckpt_scale(scale[u]));
 }
@@ -279,11 +278,12 @@ __global__ void k_ckpt_choices(int n, int E, const int32_t *__restrict__ idx,
   out[i] = ok ? e : 0;
 }
 
-// Blocks of kWarps warps for `units` warps; false past the grid's limit.
-bool grid_of(long long units, dim3 &g) {
-  const long long b = (units + kWarps - 1) / kWarps;
-  if (b > 0x7fffffffLL) return false;
-  g = dim3((unsigned)b);
+// Blocks of kWarps warps for max_rows * per_row warps; false past 2^32 warps
+// (rows that no device holds).
+bool grid_of(long long max_rows, int per_row, dim3 &g) {
+  const long long units = max_rows * per_row;
+  if (units >= (1ll << 32) - kWarps) return false;
+  g = dim3((unsigned)((units + kWarps - 1) / kWarps));
   return true;
 }
 
@@ -291,31 +291,22 @@ template <typename T>
 cudaError_t run_save(long long max_rows, int cols, const int32_t *rows, const void *h, uint8_t *q,
                      uint8_t *scale, DeviceStatus *st, cudaStream_t s) {
   const T *src = static_cast<const T *>(h);
+  const int per_row = cols % 8 == 0 ? (cols + kSeg - 1) / kSeg : (cols + kCkptBlock - 1) / kCkptBlock;
   dim3 g;
-  if (cols % 8 == 0) {
-    const int segs = (cols + kSeg - 1) / kSeg;
-    if (!grid_of(max_rows * segs, g)) return cudaErrorInvalidValue;
-    return launch_pdl(k_ckpt_save<T>, g, kWarps * 32, 0, s, cols, segs, rows, src, q, scale,
-                      max_rows, st);
-  }
-  if (!grid_of(max_rows * ((cols + kCkptBlock - 1) / kCkptBlock), g)) return cudaErrorInvalidValue;
-  return launch_pdl(k_ckpt_save_any<T>, g, kWarps * 32, 0, s, cols, rows, src, q, scale, max_rows,
-                    st);
+  if (!grid_of(max_rows, per_row, g)) return cudaErrorInvalidValue;
+  return launch_pdl(cols % 8 == 0 ? k_ckpt_save<T> : k_ckpt_save_any<T>, g, kWarps * 32, 0, s, cols,
+                    FixedDiv((unsigned)per_row), rows, src, q, scale, max_rows, st);
 }
 
 template <typename T>
 cudaError_t run_load(long long max_rows, int cols, const int32_t *rows, const uint8_t *q,
                      const uint8_t *scale, void *h, cudaStream_t s) {
   T *dst = static_cast<T *>(h);
+  const int per_row = cols % 8 == 0 ? (cols + kSeg - 1) / kSeg : (cols + kCkptBlock - 1) / kCkptBlock;
   dim3 g;
-  if (cols % 8 == 0) {
-    const int segs = (cols + kSeg - 1) / kSeg;
-    if (!grid_of(max_rows * segs, g)) return cudaErrorInvalidValue;
-    return launch_pdl(k_ckpt_load<T>, g, kWarps * 32, 0, s, cols, segs, rows, q, scale, dst,
-                      max_rows);
-  }
-  if (!grid_of(max_rows * ((cols + kCkptBlock - 1) / kCkptBlock), g)) return cudaErrorInvalidValue;
-  return launch_pdl(k_ckpt_load_any<T>, g, kWarps * 32, 0, s, cols, rows, q, scale, dst, max_rows);
+  if (!grid_of(max_rows, per_row, g)) return cudaErrorInvalidValue;
+  return launch_pdl(cols % 8 == 0 ? k_ckpt_load<T> : k_ckpt_load_any<T>, g, kWarps * 32, 0, s, cols,
+                    FixedDiv((unsigned)per_row), rows, q, scale, dst, max_rows);
 }
 
 }  // namespace

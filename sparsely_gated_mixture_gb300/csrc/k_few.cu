@@ -30,7 +30,7 @@ constexpr int kSlices = 8;
 struct FewUnits {
   int blocks, slices, per;  // column blocks, slices of K, rows of K per slice
   int total;
-  FewDiv by_blocks, by_tile;  // column blocks; units of an expert
+  FixedDiv by_blocks, by_tile;  // column blocks; units of an expert
   __device__ void make(int n_experts, int K, int N, int cols, int grid) {
     blocks = (N + cols - 1) / cols;
     const int tiles = n_experts * blocks;
@@ -47,8 +47,8 @@ struct FewUnits {
       }
     }
     total = tiles * slices;
-    by_blocks = FewDiv(blocks);
-    by_tile = FewDiv(blocks * slices);
+    by_blocks = FixedDiv(blocks);
+    by_tile = FixedDiv(blocks * slices);
   }
 };
 
@@ -315,8 +315,8 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.k = c.k;
   p.C = q.capacity;
   p.mode = q.thr ? kFewThreshold : c.gate_mode == MOE_GATE_SWITCH ? kFewSwitch : kFewTopk;
-  p.by_k = FewDiv(c.k);
-  p.by_d4 = FewDiv(c.d % 4 == 0 ? c.d / 4 : 1);
+  p.by_k = FixedDiv(c.k);
+  p.by_d4 = FixedDiv(c.d % 4 == 0 ? c.d / 4 : 1);
   p.x = q.x;
   p.Wg = q.Wg;
   p.Wn = q.Wn;

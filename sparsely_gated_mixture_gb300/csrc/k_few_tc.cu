@@ -98,7 +98,7 @@ __device__ __forceinline__ bool epi_all(bool v) {
 struct FewLine {
   int N, KC, NT;
   unsigned total, G, lo, hi;
-  FewDiv by_total;
+  FixedDiv by_total;
   // Where the run begins: expert j of those in use, column tile nt, chunk kb;
   // the piece of its tile that it makes.
   int j, nt, kb, piece;
@@ -110,8 +110,8 @@ struct FewLine {
     NT = (n + kTile - 1) / kTile;
     total = (unsigned)n_experts * NT * KC;
     G = max(1u, min((unsigned)grid, total / 2));
-    by_total = FewDiv(total);
-    const FewDiv by_g(G);
+    by_total = FixedDiv(total);
+    const FixedDiv by_g(G);
     const unsigned b = min((unsigned)blockIdx.x, G);
     lo = b == G ? total : by_g(total * b);
     hi = b == G ? total : by_g(total * (b + 1));

@@ -109,6 +109,20 @@ inline T *ws_at(void *ws, size_t off) {
 
 inline int elem_bytes(int dtype) { return dtype == MOE_BF16 ? 2 : 4; }
 
+// Division by a number that is fixed for the call, as a multiplication: the
+// quotient from floor((2^32 - 1) / d) is at most one too small. (A plain
+// division is some 150 cycles of latency, which the phases of a one-token call
+// would pay a dozen times in a row.)
+struct FixedDiv {
+  unsigned d, inv;
+  __host__ __device__ FixedDiv() : d(1), inv(0xffffffffu) {}
+  __host__ __device__ explicit FixedDiv(unsigned v) : d(v), inv(0xffffffffu / v) {}
+  __device__ unsigned operator()(unsigned n) const {
+    const unsigned q = __umulhi(n, inv);
+    return q + (n - q * d >= d ? 1u : 0u);
+  }
+};
+
 // ----------------------------------------------------------------------------- launchers
 // Each returns a cudaError_t from the launch (cudaSuccess if nothing failed).
 
