@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe.so: the forward path of the sparsely-gated
  * Mixture-of-Experts layer on one NVIDIA GB300 (sm_103a), its hierarchical
- * and strictly balanced variants, and the flat layer's backward.
+ * and strictly balanced variants, its form for a few tokens, and the flat
+ * layer's backward, also from 8-bit activation checkpoints.
  *
  * The layer, as the pages state it ("Outrageously Large Neural Networks: The
  * Sparsely-Gated Mixture-of-Experts Layer", section 3.4; "Switch Transformer",
@@ -24,7 +25,8 @@
  *   balancing-loss finalize on a side stream, forked from `stream` after the
  *   gate and joined back before it returns (so later work on `stream`, and
  *   stream capture, see one ordered forward); moe_backward forks its gate
- *   branch onto the side stream and joins it back before its last kernel.
+ *   branch onto the side stream and joins it back before its last kernel, as
+ *   moe_backward_checkpoint does that and part of what it rebuilds.
  *   Each device has a pool of 8 side streams, made on the first such call
  *   that is not under stream capture (make one call before capturing if the
  *   captured graph should keep the overlap) and kept; each serves one caller
@@ -39,16 +41,17 @@
  *   gates and zbuf are always fp32.
  * Errors.  A bad argument returns MOE_ERR_ARG (or MOE_ERR_UNSUPPORTED) before
  *   anything is enqueued. A failed launch returns MOE_ERR_CUDA; work enqueued
- *   before the failure (on `stream` and, in moe_forward and moe_backward, on
+ *   before the failure (on `stream` and, in moe_forward and the backwards, on
  *   the library's side stream) may still run, so synchronise the device before
  *   reusing the call's buffers. Conditions found
  *   on the device -- a non-finite router logit, expert output or layer output
  *   (the Switch page raises on each), an index out of range, or a bounded wait
  *   that ran out -- are recorded in a status word inside `ws`;
- *   moe_last_device_status() reads it. moe_gate() and moe_forward() clear it
- *   when they start, moe_last_device_status() after reading it; a caller whose
- *   first call on a fresh workspace is another stage zero-fills the workspace
- *   (or calls moe_last_device_status) first. Each bounded wait inside the
+ *   moe_last_device_status() reads it. moe_gate(), moe_forward(), the few-token
+ *   calls and moe_backward_checkpoint() clear it when they start,
+ *   moe_last_device_status() after reading it; a caller whose first call on a
+ *   fresh workspace is another stage zero-fills the workspace (or calls
+ *   moe_last_device_status) first. Each bounded wait inside the
  *   tensor-core kernels gives up after 2 s, or after MOE_WAIT_LIMIT_NS
  *   nanoseconds if that environment variable is set when the call is made
  *   (a diagnostic: 0 makes the first wait that is not already satisfied run

@@ -854,6 +854,7 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
         np[q] = row[q] >= 0 ? pieces(R.owner[row[q]], (int)c) : 0;
         most = max(most, np[q]);
       }
+      if (!__any_sync(0xffffffffu, most > 0)) continue;  // places past the last pick
 #pragma unroll 4
       for (int s = (int)sub; s < most; s += (int)share)
 #pragma unroll
@@ -895,7 +896,9 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
 cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
                             cudaStream_t s);
 // k_few_tc.cu: bf16 layers whose widths are multiples of 8, experts on tcgen05.
-bool few_tc_supported(const moe_config &cfg);
+inline bool few_on_tc(const moe_config &c) {
+  return c.act_dtype == MOE_BF16 && c.d % 8 == 0 && c.d_ff % 8 == 0;
+}
 int few_tc_tiles(const moe_config &cfg);  // layer 1's tiles at most
 cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s);
 

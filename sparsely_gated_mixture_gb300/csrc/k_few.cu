@@ -283,7 +283,7 @@ FewLayout few_layout(const moe_config &c) {
   };
   L.status = take(sizeof(DeviceStatus));
   L.flags = take((size_t)kFewBarriers * kFewMaxGrid * kFewFlag * 8);
-  L.n_tiles = few_tc_supported(c) ? few_tc_tiles(c) : 0;
+  L.n_tiles = few_on_tc(c) ? few_tc_tiles(c) : 0;
   L.tiles = take((size_t)L.n_tiles * 4);
   L.idx = take(A * 4);
   L.gate = take(A * 4);
@@ -295,7 +295,7 @@ FewLayout few_layout(const moe_config &c) {
   // total = experts in use * NT * KC and rows <= T * experts in use that is
   // 1.5 T G kFewTile floats and two of every value.
   const auto partials = [&](size_t N) {
-    return few_tc_supported(c) ? T * 2 * kFewMaxGrid * kFewTile + 2 * A * N : kSlices * A * N;
+    return few_on_tc(c) ? T * 2 * kFewMaxGrid * kFewTile + 2 * A * N : kSlices * A * N;
   };
   L.hpart = take(partials(F) * 4);
   L.zpart = take(partials(d) * 4);
@@ -351,7 +351,7 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
     if (c.d % 2 == 0 && c.d_ff % 2 == 0) return run_simt<float, 2>(p, s);
     return run_simt<float, 1>(p, s);
   }
-  if (few_tc_supported(c)) return launch_few_tc(p, s);
+  if (few_on_tc(c)) return launch_few_tc(p, s);
   if (c.d % 2 == 0 && c.d_ff % 2 == 0) return run_simt<__nv_bfloat16, 2>(p, s);
   return run_simt<__nv_bfloat16, 1>(p, s);
 }

@@ -483,10 +483,6 @@ int few_tc_tiles(const moe_config &c) {
   return (int)((A < c.E ? A : c.E) * ((c.d_ff + kTile - 1) / kTile));
 }
 
-bool few_tc_supported(const moe_config &c) {
-  return c.act_dtype == MOE_BF16 && c.d % 8 == 0 && c.d_ff % 8 == 0 && encode_fn() != nullptr;
-}
-
 cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s) {
   const int box = (p.T + 15) / 16 * 16;
   FewTc q;

@@ -330,6 +330,27 @@ def test_backward_in_a_graph():
             assert torch.equal(v, g[n]), n
 
 
+def test_backward_on_more_streams_than_side_streams():
+    """The library pairs eight caller streams with side streams; further ones
+    run everything on their own, with the same bits."""
+    w, inp, d, _, dy = setup("tc_top2")
+    f = forward(w, d, inp)
+    want, _ = backward(w, d, f, dy)
+    torch.cuda.synchronize()
+    cfg = B.config_for(w)
+    lanes = [(torch.cuda.Stream(), scratch(B.moe_workspace_size(cfg)),
+              scratch(B.moe_backward_workspace_size(cfg)), grads(w)) for _ in range(10)]
+    torch.cuda.synchronize()
+    for s, ws, bws, g in lanes:
+        backward(w, d, f, dy, ws=ws, bws=bws, stream=s, g=g)
+    torch.cuda.synchronize()
+    for s, ws, _, g in lanes:
+        assert B.moe_last_device_status(ws, s)[0] == 0
+        for n, v in want.items():
+            if v is not None:
+                assert torch.equal(v, g[n]), n
+
+
 def test_optional_outputs():
     w, inp, d, _, dy = setup("tc_clean")
     f = forward(w, d, inp)
