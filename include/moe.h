@@ -408,12 +408,13 @@ int moe_forward_threshold(const moe_config *cfg, const void *x, const float *Wg,
  * balancing losses, which belong to training: the same gate, capacity,
  * token-order slots (pos, keep) and output, with the expert terms summed in
  * fp32 (moe_forward rounds them to bf16 where it may), so the two agree to
- * rounding, not bit for bit. A larger T returns MOE_ERR_UNSUPPORTED (use
- * moe_forward). ws holds moe_few_workspace_size bytes and needs no
+ * rounding, not bit for bit. y may be x. A larger T, or a d or d_ff over
+ * MOE_FEW_MAX_WIDTH, returns MOE_ERR_UNSUPPORTED (use moe_forward). ws holds moe_few_workspace_size bytes and needs no
  * initialisation; the status word at its start is cleared first. The launch
  * takes every SM while it runs; calls on other streams wait for one another.
  */
 #define MOE_FEW_MAX_TOKENS 64
+#define MOE_FEW_MAX_WIDTH 524288
 int moe_few_workspace_size(const moe_config *cfg, size_t *bytes);
 int moe_forward_few(const moe_config *cfg, const void *x, const float *Wg, const float *Wnoise,
                     const float *noise, const float *logit_bias, const void *W1, const void *b1,
@@ -424,7 +425,7 @@ int moe_forward_few(const moe_config *cfg, const void *x, const float *Wg, const
  * The threshold mask for a few tokens: moe_forward_threshold's arguments,
  * outputs and definition (picks P_i > T_i in expert order, at most k of them,
  * gates renormalised, no capacity), run as moe_forward_few runs, with the same
- * bound on T and a workspace of moe_few_workspace_size bytes.
+ * bounds on T, d and d_ff and a workspace of moe_few_workspace_size bytes.
  */
 int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float *Wg,
                               const float *logit_bias, const float *thresholds, const void *W1,
@@ -514,6 +515,7 @@ int moe_gate_backward(const moe_config *cfg, const void *x, const float *Wg, con
  *   Loading is exact in bf16 and fp32.
  * rows = min(T*k, E*C) at most (moe_checkpoint_size, which also gives the two
  *   arrays' bytes); rows past expert_offset[E] are neither read nor written.
+ *   MOE_ERR_UNSUPPORTED past 2^32 blocks of 32 or a d_ff over 2^30.
  *
  * moe_checkpoint_save: H -> h8, hscale. hbuf [T*k, d_ff] and expert_offset
  *   [E+1] as moe_expert_ffn and moe_dispatch wrote them, or both NULL for

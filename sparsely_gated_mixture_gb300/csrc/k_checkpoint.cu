@@ -119,9 +119,9 @@ struct Oct<float> {
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_save(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, const T *__restrict__ h,
-            uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
-            DeviceStatus *st) {
+k_ckpt_save(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows,
+            const T *__restrict__ h, uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
+            long long max_rows, DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -161,8 +161,9 @@ k_ckpt_save(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, c
       if (e >= 120)
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = fminf(f[j], 240.f);
-      *reinterpret_cast<uint2 *>(dst + c) = make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16,
-                                                       e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
+      *reinterpret_cast<uint2 *>(dst + c) =
+          make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16,
+                     e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
     }
     if (bad) record_error(st, MOE_ERR_NONFINITE, row * cols + c);
   }
@@ -172,8 +173,9 @@ k_ckpt_save(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, c
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_load(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
-            const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
+k_ckpt_load(int cols, const FixedDiv by_seg, const int32_t *__restrict__ rows,
+            const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, T *__restrict__ h,
+            long long max_rows) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -219,9 +221,9 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // Any width: a warp per block of 32 columns, one column per lane.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_save_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows, const T *__restrict__ h,
-                uint8_t *__restrict__ q, uint8_t *__restrict__ scale, long long max_rows,
-                DeviceStatus *st) {
+k_ckpt_save_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows,
+                const T *__restrict__ h, uint8_t *__restrict__ q, uint8_t *__restrict__ scale,
+                long long max_rows, DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -246,8 +248,9 @@ k_ckpt_save_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ r
 
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
-k_ckpt_load_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows, const uint8_t *__restrict__ q,
-                const uint8_t *__restrict__ scale, T *__restrict__ h, long long max_rows) {
+k_ckpt_load_any(int cols, const FixedDiv by_block, const int32_t *__restrict__ rows,
+                const uint8_t *__restrict__ q, const uint8_t *__restrict__ scale, T *__restrict__ h,
+                long long max_rows) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -278,35 +281,30 @@ __global__ void k_ckpt_choices(int n, int E, const int32_t *__restrict__ idx,
   out[i] = ok ? e : 0;
 }
 
-// Blocks of kWarps warps for max_rows * per_row warps; false past 2^32 warps
-// (rows that no device holds).
-bool grid_of(long long max_rows, int per_row, dim3 &g) {
-  const long long units = max_rows * per_row;
-  if (units >= (1ll << 32) - kWarps) return false;
-  g = dim3((unsigned)((units + kWarps - 1) / kWarps));
-  return true;
+// Blocks of kWarps warps for max_rows * per_row warps (below 2^32, checked by
+// the caller).
+dim3 grid_of(long long max_rows, int per_row) {
+  return dim3((unsigned)((max_rows * per_row + kWarps - 1) / kWarps));
 }
 
 template <typename T>
 cudaError_t run_save(long long max_rows, int cols, const int32_t *rows, const void *h, uint8_t *q,
                      uint8_t *scale, DeviceStatus *st, cudaStream_t s) {
   const T *src = static_cast<const T *>(h);
-  const int per_row = cols % 8 == 0 ? (cols + kSeg - 1) / kSeg : (cols + kCkptBlock - 1) / kCkptBlock;
-  dim3 g;
-  if (!grid_of(max_rows, per_row, g)) return cudaErrorInvalidValue;
-  return launch_pdl(cols % 8 == 0 ? k_ckpt_save<T> : k_ckpt_save_any<T>, g, kWarps * 32, 0, s, cols,
-                    FixedDiv((unsigned)per_row), rows, src, q, scale, max_rows, st);
+  const int unit = cols % 8 == 0 ? kSeg : kCkptBlock, per_row = (cols + unit - 1) / unit;
+  const dim3 g = grid_of(max_rows, per_row);
+  return launch_pdl(cols % 8 == 0 ? k_ckpt_save<T> : k_ckpt_save_any<T>, g, kWarps * 32, 0, s,
+                    cols, FixedDiv((unsigned)per_row), rows, src, q, scale, max_rows, st);
 }
 
 template <typename T>
 cudaError_t run_load(long long max_rows, int cols, const int32_t *rows, const uint8_t *q,
                      const uint8_t *scale, void *h, cudaStream_t s) {
   T *dst = static_cast<T *>(h);
-  const int per_row = cols % 8 == 0 ? (cols + kSeg - 1) / kSeg : (cols + kCkptBlock - 1) / kCkptBlock;
-  dim3 g;
-  if (!grid_of(max_rows, per_row, g)) return cudaErrorInvalidValue;
-  return launch_pdl(cols % 8 == 0 ? k_ckpt_load<T> : k_ckpt_load_any<T>, g, kWarps * 32, 0, s, cols,
-                    FixedDiv((unsigned)per_row), rows, q, scale, dst, max_rows);
+  const int unit = cols % 8 == 0 ? kSeg : kCkptBlock, per_row = (cols + unit - 1) / unit;
+  const dim3 g = grid_of(max_rows, per_row);
+  return launch_pdl(cols % 8 == 0 ? k_ckpt_load<T> : k_ckpt_load_any<T>, g, kWarps * 32, 0, s,
+                    cols, FixedDiv((unsigned)per_row), rows, q, scale, dst, max_rows);
 }
 
 }  // namespace

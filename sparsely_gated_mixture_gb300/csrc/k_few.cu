@@ -25,8 +25,8 @@ struct FewChunk {
 
 constexpr int kSlices = 8;
 
-// The slices of K, up to kSlices: as many as make the fewest rows of K for the busiest block,
-// a unit's own cost (staging, joining) counted as 64 rows.
+// The slices of K, up to kSlices: as many as make the fewest rows of K for the
+// busiest block, a unit's own cost (staging, joining) counted as 64 rows.
 struct FewUnits {
   int blocks, slices, per;  // column blocks, slices of K, rows of K per slice
   int total;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
 template <typename T, int VEC>
 cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
   const size_t smem = kSimtSmemFloats * 4 + few_rows_bytes(p.E, p.T * p.k);
-  int grid = 2 * sm_count();  // two blocks fit an SM (launch bounds, 62 KB at most)
+  int grid = 2 * sm_count();  // two blocks fit an SM (launch bounds, 72 KB at most)
   if (grid > kFewMaxGrid) grid = kFewMaxGrid;
   FewArgs a = p;
   a.rt = few_router(p.T, p.d, p.E, p.Wn != nullptr, grid);

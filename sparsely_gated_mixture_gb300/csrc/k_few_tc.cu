@@ -93,8 +93,9 @@ __device__ __forceinline__ bool epi_all(bool v) {
 // get any (every one of them at least two units, unless there is but one: with
 // one unit each, the smallest layers gain less from the wider load than the
 // doubled partial sums cost, 34.2 against 31.7 us for the noisy top-4 layer's
-// token). total * G stays below 2^32: 2^32 / 512 units of 32 KB would not fit
-// the device.
+// token). total * G stays below 2^32: MOE_FEW_MAX_WIDTH bounds the units of few
+// columns, and 2^32 / 152 units of half their 32 KB or more would not fit the
+// device.
 struct FewLine {
   int N, KC, NT;
   unsigned total, G, lo, hi;

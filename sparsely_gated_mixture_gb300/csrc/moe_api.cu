@@ -312,9 +312,12 @@ static moe_config thr_layer(const moe_config &c) {
 }
 
 // ----------------------------------------------------------------------------- few tokens
+// The widths' bound keeps the kernels' unit counts (and those times the blocks)
+// within 32 bits for every weight that a device holds.
 static int check_few(const moe_config *c) {
   const int r = check_cfg(c);
   if (r != MOE_OK) return r;
+  if (c->d > MOE_FEW_MAX_WIDTH || c->d_ff > MOE_FEW_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
   return c->T <= MOE_FEW_MAX_TOKENS ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
@@ -329,6 +332,16 @@ struct BwdLayout {
 static long long checkpoint_rows(const moe_config &c) {
   const long long A = (long long)c.T * c.k, full = (long long)c.E * host_capacity(c);
   return A < full ? A : full;
+}
+
+// The checkpoint kernels count warps in 32 bits.
+static int check_ckpt(const moe_config *c) {
+  const int r = check_cfg(c);
+  if (r != MOE_OK) return r;
+  const long long blocks = ((long long)c->d_ff + kCkptBlock - 1) / kCkptBlock;
+  return c->d_ff <= 1 << 30 && checkpoint_rows(*c) * blocks < (1ll << 32) - 64
+             ? MOE_OK
+             : MOE_ERR_UNSUPPORTED;
 }
 
 // The expert backward runs on the tensor cores for bf16 layers whose widths
@@ -1218,7 +1231,7 @@ int moe_backward(const moe_config *cfg, const void *x, const float *Wg, const fl
 
 int moe_checkpoint_size(const moe_config *cfg, int64_t *rows, size_t *h8_bytes,
                         size_t *hscale_bytes) {
-  const int r = check_cfg(cfg);
+  const int r = check_ckpt(cfg);
   if (r != MOE_OK) return r;
   if (!rows || !h8_bytes || !hscale_bytes) return MOE_ERR_ARG;
   const long long n = checkpoint_rows(*cfg);
@@ -1230,7 +1243,7 @@ int moe_checkpoint_size(const moe_config *cfg, int64_t *rows, size_t *h8_bytes,
 
 int moe_checkpoint_save(const moe_config *cfg, const void *hbuf, const int32_t *expert_offset,
                         uint8_t *h8, uint8_t *hscale, void *ws, moe_stream_t stream) {
-  const int r = check_cfg(cfg);
+  const int r = check_ckpt(cfg);
   if (r != MOE_OK) return r;
   MOE_OPT(hbuf); MOE_OPT(expert_offset); MOE_REQ(h8); MOE_REQ(hscale);
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
@@ -1248,7 +1261,7 @@ int moe_checkpoint_save(const moe_config *cfg, const void *hbuf, const int32_t *
 int moe_checkpoint_load(const moe_config *cfg, const uint8_t *h8, const uint8_t *hscale,
                         const int32_t *expert_offset, void *hbuf, void *ws,
                         moe_stream_t stream) {
-  const int r = check_cfg(cfg);
+  const int r = check_ckpt(cfg);
   if (r != MOE_OK) return r;
   MOE_REQ(h8); MOE_REQ(hscale); MOE_OPT(expert_offset); MOE_OPT(hbuf);
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
@@ -1270,7 +1283,7 @@ int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *W
                             float w_load, float w_aux, void *dx, float *dWg, float *dWnoise,
                             float *dlogit_bias, void *dW1, void *db1, void *dW2, void *db2,
                             float *dgate, void *ws, void *bws, moe_stream_t stream) {
-  int r = check_cfg(cfg);
+  int r = check_ckpt(cfg);
   if (r != MOE_OK) return r;
   MOE_REQ(x); MOE_REQ(Wg); MOE_OPT(Wnoise); MOE_OPT(noise); MOE_OPT(logit_bias); MOE_REQ(W1);
   MOE_REQ(W2); MOE_OPT(b2); MOE_REQ(expert_idx); MOE_REQ(gate); MOE_REQ(h8); MOE_REQ(hscale);

@@ -89,6 +89,21 @@ def test_sizes(lib):
         B.moe_checkpoint_size(B.config(64, 64, 8, 0, 2, 0.5))
 
 
+def test_sizes_past_the_kernels_counts_refused(lib):
+    n = ctypes.c_int64()
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    rows = 1 << 26  # of 64 blocks of 32
+    for cfg, status in ((B.config(1, 8, 1, (1 << 30) + 8, 1, 1.0), 2),
+                        (B.config(rows, 8, 1, 2048, 1, 1.0), 2),
+                        (B.config(rows - 2, 8, 1, 2048, 1, 1.0), 0),
+                        (B.config(rows, 8, 1, 2016, 1, 1.0), 0)):
+        assert lib.moe_checkpoint_size(ctypes.byref(cfg), ctypes.byref(n), ctypes.byref(a),
+                                       ctypes.byref(b)) == status
+    cfg = B.config(rows, 8, 1, 2048, 1, 1.0)
+    assert lib.moe_checkpoint_save(ctypes.byref(cfg), F, F, F, F, F, None) == 2
+    assert lib.moe_checkpoint_load(ctypes.byref(cfg), F, F, F, F, F, None) == 2
+
+
 @pytest.mark.parametrize("bad", [{0: None}, {1: None}, {2: None}, {3: None}, {4: None},
                                  {4: F + 16}, {0: F + 4}, {2: F + 1}])
 def test_save_pointers_rejected(lib, bad):

@@ -21,7 +21,10 @@ def test_workspace_sizes(lib):
     assert 0 < small < B.moe_few_workspace_size(B.config(64, 64, 8, 128, 2, 1.0))
     n = ctypes.c_size_t()
     for cfg, status in ((B.config(65, 64, 8, 128, 2, 1.0), 2), (B.config(0, 64, 8, 128, 2, 1.0), 1),
-                        (B.config(4, 64, 8, 128, 9, 1.0), 1), (B.config(4, 64, 32, 128, 17, 1.0), 2)):
+                        (B.config(4, 64, 8, 128, 9, 1.0), 1),
+                        (B.config(4, 64, 32, 128, 17, 1.0), 2),
+                        (B.config(4, 64, 8, 524288 + 8, 2, 1.0), 2),
+                        (B.config(4, 524288 + 8, 8, 64, 2, 1.0), 2)):
         assert lib.moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)) == status
     assert lib.moe_few_workspace_size(ctypes.byref(B.config(1, 64, 8, 128, 2, 1.0)), None) == 1
 

@@ -104,6 +104,9 @@ CASES = {
     "k16": _w(64, 128, 40, 64, 16, cf=1.0),
     "largest": _w(64, 72, 1024, 24, 16, cf=1024.0, noisy=True),
     "largest_odd": _w(64, 67, 1024, 23, 16, cf=1024.0, noisy=True),
+    "widest": _w(2, 8, 2, 524288, 1),
+    "widest_back": _w(2, 524288, 2, 8, 1),
+    "widest_f32": _w(2, 5, 2, 524287, 1, dtype="f32"),
     "largest_f32": _w(64, 68, 1024, 24, 16, cf=1024.0, dtype="f32"),
 }
 
@@ -169,6 +172,23 @@ def test_few_optional_outputs_and_same_bits_twice():
                       d["b2"], y, ws)
     assert B.moe_last_device_status(ws)[0] == 0
     assert torch.equal(y, a["y"])
+
+
+@pytest.mark.parametrize("T", [1, 3, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_few_in_place(T, dtype):
+    """y may be x: the same bits as into another buffer."""
+    w = _w(T, 264, 6, 520, 2, cf=2.0, dtype=dtype)
+    d = to_device(w, wl.generate(w, seed=31))
+    apart = run_few(w, d)
+    cfg = B.config_for(w)
+    o = outputs(w, cfg)
+    o["y"] = d["x"] = d["x"].clone()
+    ws = workspace(cfg)
+    call(cfg, d, o, ws)
+    assert B.moe_last_device_status(ws)[0] == 0
+    for name, v in o.items():
+        assert torch.equal(apart[name], v), name
 
 
 def test_few_agrees_with_the_whole_layer():
