@@ -698,14 +698,40 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem, const FewAlone &alone)
   R.token = reinterpret_cast<uint8_t *>(R.place + p.E);
   __shared__ int scan[8][2], total[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (p.T == 1) {
+    // A single token: each pick is kept, in a row of its own; sorted by every
+    // warp's lanes, without the sums over the experts (1.5 -> 0.4 us).
+    const int e = lane < A ? alone.idx[lane] : p.E;
+    const uint32_t some = __ballot_sync(0xffffffffu, e < p.E);
+    int at = 0;
+    for (int a = 0; a < A; ++a) at += __shfl_sync(0xffffffffu, e, a) < e;
+    R.n = R.rows = __popc(some);
+    if (warp == 0 && lane < A) {
+      const bool kept = e < p.E;
+      R.gate[lane] = alone.gate[lane];
+      R.row[lane] = kept ? (int16_t)at : (int16_t)-1;
+      if (kept) {
+        R.expert[at] = e;
+        R.owner[at] = (uint16_t)at;
+        R.token[at] = 0;
+      }
+      if (blockIdx.x == 0) {
+        if (p.pos) p.pos[lane] = kept ? 0 : -1;
+        if (p.keep) p.keep[lane] = kept;
+      }
+    }
+    if (tid <= A) R.first[tid] = min(tid, R.n);
+    __syncthreads();
+    return R;
+  }
   int choice[kFewRows / kFewThreads];
 #pragma unroll
   for (int i = 0; i < kFewRows / kFewThreads; ++i) {
     const int a = i * kFewThreads + tid;
     choice[i] = -1;
     if (a < A) {
-      choice[i] = p.T == 1 ? alone.idx[a] : p.idx[a];
-      R.gate[a] = p.T == 1 ? alone.gate[a] : p.gate[a];
+      choice[i] = p.idx[a];
+      R.gate[a] = p.gate[a];
     }
   }
   for (int e = tid; e < p.E; e += kFewThreads) R.tokens[e] = 0;

@@ -156,6 +156,81 @@ struct FewTc {
   int stages, tok_bytes;  // ring stages; bytes of a stage's token operand
 };
 
+// Layer 2's token operand where the layer has a single token (one row for each
+// expert in use), by one warp, past barrier 2: two columns a lane of a unit's 64,
+// H = ReLU(sum of layer 1's parts + b1) rounded to bf16, as the join of a tile's
+// parts would make it, without that join before the barrier. The loads of eight
+// units are in flight together. Returns the ring position after the last unit.
+__device__ __forceinline__ uint32_t few_tokens(const FewArgs &p, const FewTc &q, const FewRows &R,
+                                               const FewLine *line, uint8_t *ring,
+                                               uint64_t *full_t, uint64_t *empty, uint32_t it,
+                                               volatile int *abort_flag) {
+  constexpr int B = 4, Z = 4;
+  const FewLine &l = line[1];
+  const int lane = threadIdx.x & 31, stage = kWBytes + q.tok_bytes;
+  const __nv_bfloat162 *b1 = static_cast<const __nv_bfloat162 *>(p.b1);
+  const size_t step = (size_t)R.rows * p.F;
+  int j = l.j, nt = l.nt, kb = l.kb;
+  for (unsigned u = l.lo; u < l.hi; u += B) {
+    float2 v[B];
+    const float *src[B];
+    int np[B], most = 0;
+    __nv_bfloat162 bias[B];
+#pragma unroll
+    for (int m = 0; m < B; ++m) {
+      const int k = kb * kChunk + 2 * lane;
+      const bool in = u + m < l.hi && k < p.F;
+      v[m] = make_float2(0.f, 0.f);
+      bias[m] = __floats2bfloat162_rn(0.f, 0.f);
+      np[m] = in ? line[0].pieces(j, k) : 0;
+      src[m] = p.hpart + (size_t)j * p.F + k;
+      if (in && b1) bias[m] = b1[((size_t)R.expert[j] * p.F + k) / 2];
+      most = max(most, np[m]);
+      if (++kb == l.KC) {
+        kb = 0;
+        if (++nt == l.NT) {
+          nt = 0;
+          ++j;
+        }
+      }
+    }
+    for (int z0 = 0; z0 < most; z0 += Z) {
+      float2 w[Z][B];
+#pragma unroll
+      for (int z = 0; z < Z; ++z)
+#pragma unroll
+        for (int m = 0; m < B; ++m)
+          w[z][m] = z0 + z < np[m] ? __ldcg(reinterpret_cast<const float2 *>(src[m] + (z0 + z) * step))
+                                   : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int z = 0; z < Z; ++z)
+#pragma unroll
+        for (int m = 0; m < B; ++m) {
+          v[m].x += w[z][m].x;
+          v[m].y += w[z][m].y;
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < B; ++m) {
+      if (u + m >= l.hi) break;
+      const int st = it % q.stages;
+      const bool free =
+          mbar_wait(&empty[st], ((it / q.stages) & 1u) ^ 1u, abort_flag, p.st, 117, p.wait_ns);
+      if (!__all_sync(0xffffffffu, free)) return it;
+      const __nv_bfloat162 h =
+          __floats2bfloat162_rn(fmaxf(v[m].x + __low2float(bias[m]), 0.f),
+                                fmaxf(v[m].y + __high2float(bias[m]), 0.f));
+      // Row 0 of the operand: the swizzle leaves it in place.
+      *reinterpret_cast<__nv_bfloat162 *>(ring + (size_t)st * stage + kWBytes + lane * 4) = h;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full_t[st]);
+      ++it;
+    }
+  }
+  return it;
+}
+
 // tmX: x [T, d], box [roundup(T, 16), 64]; tmH: H [T k, d_ff], box [16, 64];
 // tm1, tm2: W1 [E, d, d_ff], W2 [E, d_ff, d], box [1, 64, 64]. All bf16 in the
 // 128-byte swizzle; out-of-range rows and columns read as zero.
@@ -179,6 +254,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   const int stage = kWBytes + q.tok_bytes, S = q.stages;
   uint8_t *rows_mem = ring + (size_t)S * stage;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool direct = p.T == 1;  // layer 2's tokens straight from layer 1's partial sums
 
   few_start(p);
   if (threadIdx.x == 0) {
@@ -308,7 +384,13 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
             *abort_flag = 1;
             break;
           }
+          __syncwarp();
           asm volatile("fence.proxy.async.global;" ::: "memory");
+          if (direct) {
+            it = few_tokens(p, q, R, line, ring, full_t, empty, __shfl_sync(0xffffffffu, it, 0),
+                            abort_flag);
+            break;
+          }
         }
         for (FewSeg s(l); s.more() && go; s.next(l)) {
           if (lane == 0) {
@@ -356,7 +438,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           float *out = part + ((size_t)s.piece * R.rows + r0) * l.N;
           // A whole tile of layer 1 becomes H here; a part of one leaves as a
           // partial sum, and whoever writes a tile's last part joins them.
-          const bool whole = layer == 0 && s.kb0 == 0 && s.kb1 == l.KC;
+          const bool whole = layer == 0 && !direct && s.kb0 == 0 && s.kb1 == l.KC;
           const int e = R.expert[s.j];
           for (int h = 0; h < 2; ++h) {
             if (n0 + h * 128 >= l.N) break;
@@ -389,7 +471,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&acc_empty[buf]);
-          if (layer == 0 && !whole) {
+          if (layer == 0 && !whole && !direct) {
             const int np = l.pieces(s.j, n0);
             epi_all(true);  // the part is written
             if (et == 0) {
