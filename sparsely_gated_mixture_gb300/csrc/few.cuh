@@ -91,8 +91,10 @@ __device__ __forceinline__ unsigned long long *few_flag(const FewArgs &p, int b,
 }
 
 __device__ __forceinline__ void few_start(const FewArgs &p) {
-  if (threadIdx.x > 0 && threadIdx.x < kFewBarriers) *few_flag(p, threadIdx.x, blockIdx.x) = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.st = DeviceStatus{};
+  if (blockIdx.x == 0) {
+    if (threadIdx.x > 0 && threadIdx.x < kFewBarriers) *few_flag(p, threadIdx.x, 0) = 0;
+    if (threadIdx.x == 0) *p.st = DeviceStatus{};
+  }
   for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_tiles;
        i += gridDim.x * kFewThreads)
     p.tiles[i] = 0;
@@ -101,7 +103,10 @@ __device__ __forceinline__ void few_start(const FewArgs &p) {
 // Arrive at barrier b (one thread, after a barrier of the block's threads that
 // wrote): what they wrote before is visible to a block that has waited.
 __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
-  few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);  // a release, cumulative over the barrier
+  if (b == 0)
+    few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);  // a release, cumulative over the barrier
+  else
+    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(few_flag(p, b, 0)) : "memory");
 }
 
 // Wait for barrier b (threads tid of n_threads of the block); false: leave the
@@ -109,6 +114,20 @@ __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
 __device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n_threads,
                                          volatile int *abort_flag = nullptr) {
   unsigned long long t0 = 0;
+  if (b > 0) {
+    if (tid == 0)
+      while (few_flag_get(few_flag(p, b, 0)) != gridDim.x) {
+        const unsigned long long now = globaltimer();
+        if (t0 == 0) t0 = now;
+        if (abort_flag && *abort_flag) return false;
+        if (now - t0 >= p.wait_ns) {
+          record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
+          return false;
+        }
+      }
+    __threadfence();
+    return true;
+  }
   for (int i0 = tid; i0 < (int)gridDim.x; i0 += 8 * n_threads) {
     for (;;) {
       // Up to eight flags a thread, looked at together.
