@@ -25,7 +25,7 @@ constexpr int kFewRows = 1024;     // T * k at most (k <= 16)
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxGrid = 320;   // blocks at most (sizes the flags and partial sums)
 constexpr int kFewBarriers = 4;
-constexpr int kFewFlag = 16;       // 64-bit words from one flag to the next: a 128-byte line
+constexpr int kFewFlag = 16;       // 64-bit words from one flag or count to the next: a 128-byte line
 constexpr int kFewTile = 256;      // weight columns of a unit on the tensor cores
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
@@ -52,7 +52,8 @@ struct FewArgs {
   uint32_t *mask;  // [T, ceil(E/32)] or null (threshold)
   // Workspace.
   DeviceStatus *st;
-  unsigned long long *flags;  // [kFewBarriers][kFewMaxGrid][kFewFlag], the first word of each
+  // The first word of each kFewFlag: the first barrier's flags [kFewMaxGrid], the others' counts.
+  unsigned long long *flags;
   uint32_t *tiles;            // pieces of layer 1's tiles that are written (tensor-core form)
   int n_tiles;
   float *rpart;               // router partials [slices][T][columns]
@@ -64,16 +65,17 @@ struct FewArgs {
 namespace {
 
 // ----------------------------------------------------------------------------- grid barrier
-// Every block has one flag per barrier; it arrives by storing the launch's
-// nonce there and waits until all blocks' flags hold it: one hop, where a
-// shared counter would take one atomic per block in turn, and each flag has a
-// 128-byte line of its own (152 blocks polling 152 flags on ten lines took 2
-// to 5 us a barrier: every poll went to the same few L2 slices). The workspace need
-// not be zeroed: flags of an earlier call hold another nonce, and for a
-// replayed graph, whose nonce is the same each time, the flags are cleared:
-// a block clears its flags of the barriers after the first before it arrives
-// at the first (no block looks at them earlier), and its flag of the first
-// once it has passed the last (every block has passed the first by then).
+// The first barrier: every block stores the launch's nonce to a flag of its
+// own, on a 128-byte line of its own (152 blocks polling 152 flags on ten lines
+// took 2 to 5 us: every poll went to the same few L2 slices), and all wait for
+// all flags. So the workspace need not be zeroed: flags of an earlier call hold
+// another nonce. A replayed graph has the same nonce each time; a block clears
+// its flag once it has passed the last barrier, or leaves early. The later
+// barriers count arrivals on one word each, which block 0 clears before it
+// arrives at the first: one poll a block instead of 152 (one token 22.2 -> 21.1
+// us for the noisy top-4 layer). For the first barrier, a tagged count that
+// whoever arrives first sets up costs 304 blocks more than the flags do (13
+// tokens, fp32: 36.9 against 40.2 us) and gains 152 blocks little.
 // Waits are bounded: past the limit the block records MOE_ERR_TIMEOUT and
 // leaves, and so does, within the limit, every block that waits for it.
 __device__ __forceinline__ void few_flag_set(unsigned long long *f, unsigned long long v) {
@@ -86,13 +88,16 @@ __device__ __forceinline__ unsigned long long few_flag_get(const unsigned long l
   return v;
 }
 
-__device__ __forceinline__ unsigned long long *few_flag(const FewArgs &p, int b, int block) {
-  return p.flags + ((size_t)b * kFewMaxGrid + block) * kFewFlag;
+__device__ __forceinline__ unsigned long long *few_flag(const FewArgs &p, int block) {
+  return p.flags + (size_t)block * kFewFlag;
+}
+__device__ __forceinline__ unsigned long long *few_count(const FewArgs &p, int b) {  // b > 0
+  return few_flag(p, kFewMaxGrid + b - 1);
 }
 
 __device__ __forceinline__ void few_start(const FewArgs &p) {
   if (blockIdx.x == 0) {
-    if (threadIdx.x > 0 && threadIdx.x < kFewBarriers) *few_flag(p, threadIdx.x, 0) = 0;
+    if (threadIdx.x > 0 && threadIdx.x < kFewBarriers) *few_count(p, threadIdx.x) = 0;
     if (threadIdx.x == 0) *p.st = DeviceStatus{};
   }
   for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_tiles;
@@ -101,62 +106,63 @@ __device__ __forceinline__ void few_start(const FewArgs &p) {
 }
 
 // Arrive at barrier b (one thread, after a barrier of the block's threads that
-// wrote): what they wrote before is visible to a block that has waited.
+// wrote): what they wrote before is visible to a block that has waited (a
+// release, cumulative over the barrier).
 __device__ __forceinline__ void few_arrive(const FewArgs &p, int b) {
   if (b == 0)
-    few_flag_set(few_flag(p, b, blockIdx.x), p.nonce);  // a release, cumulative over the barrier
+    few_flag_set(few_flag(p, blockIdx.x), p.nonce);
   else
-    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(few_flag(p, b, 0)) : "memory");
+    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(few_count(p, b)) : "memory");
 }
 
-// Wait for barrier b (threads tid of n_threads of the block); false: leave the
-// kernel. With an abort flag, a set one ends the wait too.
-__device__ __forceinline__ bool few_wait(const FewArgs &p, int b, int tid, int n_threads,
-                                         volatile int *abort_flag = nullptr) {
+// Wait until `done()`; false: leave the kernel. With an abort flag, a set one
+// ends the wait too.
+template <typename F>
+__device__ __forceinline__ bool few_poll(const FewArgs &p, int b, volatile int *abort_flag,
+                                         const F &done) {
   unsigned long long t0 = 0;
-  if (b > 0) {
-    if (tid == 0)
-      while (few_flag_get(few_flag(p, b, 0)) != gridDim.x) {
-        const unsigned long long now = globaltimer();
-        if (t0 == 0) t0 = now;
-        if (abort_flag && *abort_flag) return false;
-        if (now - t0 >= p.wait_ns) {
-          record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
-          return false;
-        }
-      }
-    __threadfence();
-    return true;
-  }
-  for (int i0 = tid; i0 < (int)gridDim.x; i0 += 8 * n_threads) {
-    for (;;) {
-      // Up to eight flags a thread, looked at together.
-      bool all = true;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int i = i0 + j * n_threads;
-        if (i < (int)gridDim.x) all &= few_flag_get(few_flag(p, b, i)) == p.nonce;
-      }
-      if (all) break;
-      const unsigned long long now = globaltimer();
-      if (t0 == 0) t0 = now;
-      if (abort_flag && *abort_flag) return false;
-      if (now - t0 >= p.wait_ns) {
-        record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
-        return false;
-      }
+  while (!done()) {
+    const unsigned long long now = globaltimer();
+    if (t0 == 0) t0 = now;
+    if (abort_flag && *abort_flag) return false;
+    if (now - t0 >= p.wait_ns) {
+      record_error(p.st, MOE_ERR_TIMEOUT, 100 + b);
+      return false;
     }
   }
-  __threadfence();  // the flags' acquire
   return true;
 }
+
+// The first barrier, by all threads of the block: up to two flags each.
+__device__ __forceinline__ bool few_wait_first(const FewArgs &p) {
+  static_assert(kFewMaxGrid <= 2 * kFewThreads);
+  const int i = threadIdx.x, j = i + kFewThreads, n = gridDim.x;
+  const bool ok = few_poll(p, 0, nullptr, [&] {
+    return (i >= n || few_flag_get(few_flag(p, i)) == p.nonce) &
+           (j >= n || few_flag_get(few_flag(p, j)) == p.nonce);
+  });
+  __threadfence();  // the flags' acquire
+  return ok;
+}
+// A later one, by one thread.
+__device__ __forceinline__ bool few_wait(const FewArgs &p, int b,
+                                         volatile int *abort_flag = nullptr) {
+  const bool ok =
+      few_poll(p, b, abort_flag, [&] { return few_flag_get(few_count(p, b)) == gridDim.x; });
+  __threadfence();  // the count's acquire
+  return ok;
+}
+
+// A block that leaves the kernel, or has passed the last barrier (then every
+// block has passed the first).
+__device__ __forceinline__ void few_leave(const FewArgs &p) { *few_flag(p, blockIdx.x) = 0; }
 
 __device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
   __syncthreads();
   if (threadIdx.x == 0) few_arrive(p, b);
-  const bool ok = few_wait(p, b, threadIdx.x, blockDim.x);
+  const bool ok = b == 0 ? few_wait_first(p) : threadIdx.x == 0 ? few_wait(p, b) : true;
   const bool fail = __syncthreads_or(!ok);
-  if (threadIdx.x == 0 && (b == kFewBarriers - 1 || fail)) *few_flag(p, 0, blockIdx.x) = 0;
+  if (threadIdx.x == 0 && (b == kFewBarriers - 1 || fail)) few_leave(p);
   return !fail;
 }
 
@@ -834,21 +840,30 @@ __device__ FewRows few_rows(const FewArgs &p, char *smem, const FewAlone &alone)
 }
 
 // ----------------------------------------------------------------------------- combine
-// V floats at p (aligned to V floats), written by other blocks: from L2.
+// V floats at p (aligned to V floats), written by other blocks, from L2; zero
+// unless `some`. Predicated: behind a branch each would be waited for before the
+// next is asked for.
 template <int V>
-__device__ __forceinline__ void few_add(const float *p, float (&v)[V]) {
+__device__ __forceinline__ void few_get(const float *p, bool some, float (&v)[V]) {
   if constexpr (V == 4) {
-    const float4 f = __ldcg(reinterpret_cast<const float4 *>(p));
-    v[0] += f.x;
-    v[1] += f.y;
-    v[2] += f.z;
-    v[3] += f.w;
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.f32 %0, 0f00000000;\n"
+        " mov.f32 %1, 0f00000000;\n mov.f32 %2, 0f00000000;\n mov.f32 %3, 0f00000000;\n"
+        " @p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n}\n"
+        : "=&f"(v[0]), "=&f"(v[1]), "=&f"(v[2]), "=&f"(v[3])
+        : "l"(p), "r"((uint32_t)some));
   } else if constexpr (V == 2) {
-    const float2 f = __ldcg(reinterpret_cast<const float2 *>(p));
-    v[0] += f.x;
-    v[1] += f.y;
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %3, 0;\n mov.f32 %0, 0f00000000;\n"
+        " mov.f32 %1, 0f00000000;\n @p ld.global.cg.v2.f32 {%0, %1}, [%2];\n}\n"
+        : "=&f"(v[0]), "=&f"(v[1])
+        : "l"(p), "r"((uint32_t)some));
   } else {
-    v[0] += __ldcg(p);
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.f32 %0, 0f00000000;\n"
+        " @p ld.global.cg.f32 %0, [%1];\n}\n"
+        : "=&f"(v[0])
+        : "l"(p), "r"((uint32_t)some));
   }
 }
 template <typename T, int V>
@@ -866,11 +881,15 @@ __device__ __forceinline__ void few_st(T *p, const float (&v)[V]) {
   *reinterpret_cast<Pack *>(p) = o;
 }
 
+template <int Q_, int S_>
+struct FewRound {
+  static constexpr int Q = Q_, S = S_;
+};
+
 // y[t] = x[t] + sum over the kept choices, in order, of gate * (sum of the
 // partial sums + b2), in fp32, rounded once. V columns a thread; where that
-// leaves most threads idle (few tokens, whose partials are many), 8 lanes
-// share the partials of the same columns, each adding every 8th, joined in a
-// fixed order.
+// leaves most threads idle (few tokens, whose partials are many), 8 lanes share
+// the same columns' choices and their partials, joined in a fixed order.
 template <typename T, int V, typename PF>
 __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
                                             const PF &pieces) {
@@ -879,59 +898,85 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
   const unsigned cols = p.d / V, total = p.T * cols;
   const size_t step = (size_t)R.rows * p.d;
   const FixedDiv by = V == 4 ? p.by_d4 : FixedDiv(cols);
-  const unsigned lshare = total * 8 <= gridDim.x * kFewThreads ? 3 : 0, share = 1u << lshare;
-  const unsigned sub = threadIdx.x & (share - 1), lane = threadIdx.x & 31;
-  for (unsigned w = blockIdx.x * kFewThreads + threadIdx.x; w - lane < total * share;
-       w += gridDim.x * kFewThreads) {  // whole warps go round together
-    const unsigned i = w >> lshare;
-    const bool live = i < total;
-    const unsigned t = live ? by(i) : 0, c = live ? (i - t * cols) * V : 0;
-    float acc[V] = {};
-    if (live) few_ld<T, V>(x + (size_t)t * p.d + c, acc);
-    // Four choices side by side, so that their loads overlap; each choice's
-    // partials are added in order, then the choices in order.
-    for (int q0 = 0; q0 < p.k; q0 += 4) {
-      float v[4][V] = {};
-      int row[4], np[4], most = 0;
+  const int K = p.T == 1 ? R.n : p.k;  // a single token's picks are its first choices
+  // Token t's columns c .. c + V - 1: every dq-th choice from q0 on, Q at a time,
+  // of its partials every ds-th from s0 on, S at a time.
+  const auto add = [&](auto rounds, unsigned t, unsigned c, int q0, int dq, int s0, int ds,
+                       bool live, float (&acc)[V]) {
+    constexpr int Q = decltype(rounds)::Q, S = decltype(rounds)::S;
+    for (int qb = q0; qb < K; qb += Q * dq) {
+      float v[Q][V] = {};
+      int row[Q], np[Q], most = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        row[q] = live && q0 + q < p.k ? R.row[t * p.k + q0 + q] : -1;
-        np[q] = row[q] >= 0 ? pieces(R.owner[row[q]], (int)c) : 0;
-        most = max(most, np[q]);
+      for (int i = 0; i < Q; ++i) {
+        const int q = qb + i * dq;
+        row[i] = live && q < K ? R.row[t * p.k + q] : -1;
+        np[i] = row[i] >= 0 ? pieces(R.owner[row[i]], (int)c) : 0;
+        most = max(most, np[i]);
       }
-      if (!__any_sync(0xffffffffu, most > 0)) continue;  // places past the last pick
-#pragma unroll 4
-      for (int s = (int)sub; s < most; s += (int)share)
+      for (int sb = s0; sb < most; sb += S * ds) {
+        float w[S][Q][V];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (s < np[q]) few_add<V>(p.zpart + s * step + (size_t)row[q] * p.d + c, v[q]);
-      if (share == 8)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+          for (int i = 0; i < Q; ++i)
+            few_get<V>(p.zpart + (sb + s * ds) * step + (size_t)row[i] * p.d + c,
+                       sb + s * ds < np[i], w[s][i]);
 #pragma unroll
-          for (int z = 0; z < V; ++z)
+        for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1) v[q][z] += __shfl_xor_sync(0xffffffffu, v[q][z], o);
+          for (int i = 0; i < Q; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (row[q] < 0) continue;
-        if (b2) {
+            for (int z = 0; z < V; ++z) v[i][z] += w[s][i][z];
+      }
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        if (row[i] < 0) continue;
+        if (b2 && s0 == 0) {
           float b[V];
-          few_ld<T, V>(b2 + (size_t)R.expert[R.owner[row[q]]] * p.d + c, b);
+          few_ld<T, V>(b2 + (size_t)R.expert[R.owner[row[i]]] * p.d + c, b);
 #pragma unroll
-          for (int z = 0; z < V; ++z) v[q][z] += b[z];
+          for (int z = 0; z < V; ++z) v[i][z] += b[z];
         }
-        const float g = R.gate[t * p.k + q0 + q];
+        const float g = R.gate[t * p.k + qb + i * dq];
 #pragma unroll
-        for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[q][z], acc[z]);
+        for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[i][z], acc[z]);
       }
     }
-    if (!live || sub) continue;
+  };
+  const auto store = [&](unsigned t, unsigned c, const float (&acc)[V]) {
     bool bad = false;
 #pragma unroll
     for (int z = 0; z < V; ++z) bad |= !isfinite(acc[z]);
     if (bad) record_error(p.st, MOE_ERR_NONFINITE, t);
     few_st<T, V>(y + (size_t)t * p.d + c, acc);
+  };
+  const unsigned first = blockIdx.x * kFewThreads + threadIdx.x, stride = gridDim.x * kFewThreads;
+  if (total * 8 <= stride) {
+    const unsigned i = first >> 3, sub = first & 7;
+    if (first - (threadIdx.x & 31) >= total * 8) return;  // whole warps leave
+    const bool live = i < total;
+    const unsigned t = live ? by(i) : 0, c = live ? (i - t * cols) * V : 0;
+    // Lanes over the choices that a token keeps on average, the rest over their
+    // partials.
+    const int lk = R.rows > 4 * p.T ? 3 : R.rows > 2 * p.T ? 2 : R.rows > p.T ? 1 : 0;
+    float acc[V] = {};
+    if (live && sub == 0) few_ld<T, V>(x + (size_t)t * p.d + c, acc);
+    add(FewRound<1, 4>{}, t, c, sub & ((1 << lk) - 1), 1 << lk, (int)sub >> lk,
+        8 >> lk, live, acc);
+#pragma unroll
+    for (int z = 0; z < V; ++z)
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) acc[z] += __shfl_xor_sync(0xffffffffu, acc[z], o);
+    if (live && sub == 0) store(t, c, acc);
+    return;
+  }
+  for (unsigned i = first; i < total; i += stride) {
+    const unsigned t = by(i), c = (i - t * cols) * V;
+    float acc[V];
+    few_ld<T, V>(x + (size_t)t * p.d + c, acc);
+    add(FewRound<4, 2>{}, t, c, 0, 1, 0, 1, true, acc);
+    store(t, c, acc);
   }
 }
 

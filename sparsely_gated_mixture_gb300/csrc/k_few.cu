@@ -282,7 +282,7 @@ FewLayout few_layout(const moe_config &c) {
     return o;
   };
   L.status = take(sizeof(DeviceStatus));
-  L.flags = take((size_t)kFewBarriers * kFewMaxGrid * kFewFlag * 8);
+  L.flags = take((size_t)(kFewMaxGrid + kFewBarriers - 1) * kFewFlag * 8);
   L.n_tiles = few_on_tc(c) ? few_tc_tiles(c) : 0;
   L.tiles = take((size_t)L.n_tiles * 4);
   L.idx = take(A * 4);

@@ -195,19 +195,18 @@ __device__ __forceinline__ uint32_t few_tokens(const FewArgs &p, const FewTc &q,
       }
     }
     for (int z0 = 0; z0 < most; z0 += Z) {
-      float2 w[Z][B];
+      float w[Z][B][2];
 #pragma unroll
       for (int z = 0; z < Z; ++z)
 #pragma unroll
         for (int m = 0; m < B; ++m)
-          w[z][m] = z0 + z < np[m] ? __ldcg(reinterpret_cast<const float2 *>(src[m] + (z0 + z) * step))
-                                   : make_float2(0.f, 0.f);
+          few_get<2>(src[m] + (z0 + z) * step, z0 + z < np[m], w[z][m]);
 #pragma unroll
       for (int z = 0; z < Z; ++z)
 #pragma unroll
         for (int m = 0; m < B; ++m) {
-          v[m].x += w[z][m].x;
-          v[m].y += w[z][m].y;
+          v[m].x += w[z][m][0];
+          v[m].y += w[z][m][1];
         }
     }
 #pragma unroll
@@ -379,7 +378,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
         const FewLine &l = line[layer];
         if (layer) {
           // H is complete when every block has arrived at barrier 2.
-          const bool done = few_wait(p, 2, lane, 32, abort_flag);
+          const bool done = lane == 0 ? few_wait(p, 2, abort_flag) : true;
           if (!__all_sync(0xffffffffu, done)) {
             *abort_flag = 1;
             break;
@@ -495,10 +494,16 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                   c[m] = (i - r[m] * cols) * 4;
                 }
 #pragma unroll 2
-                for (int z = 0; z < np; ++z)
+                for (int z = 0; z < np; ++z) {
+                  float w[4][4];
 #pragma unroll
                   for (int m = 0; m < 4; ++m)
-                    if (r[m] >= 0) few_add<4>(src + z * step + (size_t)r[m] * l.N + c[m], v[m]);
+                    few_get<4>(src + z * step + (size_t)r[m] * l.N + c[m], r[m] >= 0, w[m]);
+#pragma unroll
+                  for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) v[m][x] += w[m][x];
+                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                   if (r[m] < 0) continue;
@@ -536,7 +541,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                  : "memory");
   }
   if (!ok || *abort_flag) {
-    if (threadIdx.x == 0) *few_flag(p, 0, blockIdx.x) = 0;
+    if (threadIdx.x == 0) few_leave(p);
     return;
   }
   if (!few_barrier(p, 3)) return;
