@@ -518,12 +518,13 @@ struct FewAlone {
 //   Switch:    the largest, its gate from the softmax over all experts;
 //   threshold: the experts with Softmax(H) > thr, in order, renormalised.
 // A NaN logit ranks last; a non-finite one is recorded.
-// smem: H [E] floats, red [8], taken words [32], sums [2][256].
+// smem: H [E] floats, red [8], taken words [32], sums [2][256], in whose place
+// then the candidates [128] (64 bits each) and the chosen [16].
 template <typename T>
 __device__ __forceinline__ void few_select(const FewArgs &p, float *smem, FewAlone &alone) {
   const FewRouter &r = p.rt;
   float *H = smem;
-  float *red = smem + p.E;
+  float *red = smem + (p.E + 1) / 2 * 2;  // what follows is 8-byte aligned
   uint32_t *words = reinterpret_cast<uint32_t *>(red + 8);
   float *sums = red + 40;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -536,7 +537,7 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem, FewAlo
     __syncthreads();
     // Up to four experts a thread, four slices at a time, all the loads of a
     // round in flight together (places past the end read the first one).
-    float c[4] = {}, z[4] = {}, add[4] = {}, noise[4] = {};
+    float c[4] = {}, z[4] = {}, add[4] = {}, noise[4] = {}, thr[4] = {};
     const int e0 = tid & (pe - 1);
     const float *q = p.rpart + (size_t)t * r.NC;
     const size_t step = (size_t)p.T * r.NC;
@@ -547,6 +548,8 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem, FewAlo
         if (p.bias) add[i] = p.bias[e];
         if (p.Wn) noise[i] = p.noise[(size_t)t * p.E + e];
       }
+      if (p.mode == kFewThreshold && i * kFewThreads + tid < p.E)
+        thr[i] = p.thr[i * kFewThreads + tid];
     }
     for (int s0 = sl; s0 < r.slices; s0 += 4 * nl) {
       float vc[4][4], vz[4][4];
@@ -610,16 +613,23 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem, FewAlo
     float se = 0.f;
     if (p.mode != kFewTopk) {
       mx = few_block<true>(mx, red);
-      for (int e = tid; e < p.E; e += kFewThreads) se += expf(H[e] - mx);
+      for (int e = tid; e < p.E; e += kFewThreads) {
+        const float v = expf(H[e] - mx);
+        if (p.mode == kFewThreshold) H[e] = v;
+        se += v;
+      }
       se = few_block<false>(se, red);
     }
     __syncthreads();
     if (p.mode == kFewThreshold) {
       const int nw = (p.E + 31) / 32;
-      for (int w = warp; w < nw; w += 8) {
-        const int e = w * 32 + lane;
-        const bool take = e < p.E && expf(H[e] - mx) / se > p.thr[e];
-        const uint32_t b = __ballot_sync(0xffffffffu, take);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int w = i * 8 + warp, e = i * kFewThreads + tid;
+        if (w >= nw) break;
+        const float P = e < p.E ? H[e] / se : 0.f;
+        const uint32_t b = __ballot_sync(0xffffffffu, e < p.E && P > thr[i]);
+        if (e < p.E) H[e] = P;
         if (lane == 0) {
           words[w] = b;
           if (p.mask && tell) p.mask[(size_t)t * nw + w] = b;
@@ -639,51 +649,84 @@ __device__ __forceinline__ void few_select(const FewArgs &p, float *smem, FewAlo
         int at = incl - __popc(mine);
         float sum = 0.f;
         for (uint32_t b = mine; b; b &= b - 1)
-          sum += expf(H[lane * 32 + __ffs(b) - 1] - mx) / se;
+          sum += H[lane * 32 + __ffs(b) - 1];
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         for (uint32_t b = mine; b; b &= b - 1, ++at) {
           if (at >= p.k) break;
           const int e = lane * 32 + __ffs(b) - 1;
-          put(at, e, expf(H[e] - mx) / se / sum);
+          put(at, e, H[e] / sum);
         }
         for (int j = total + lane; j < p.k; j += 32) put(j, p.E, 0.f);
         if (total > p.k && lane == 0) record_error(p.st, MOE_ERR_BOUNDS, t);
       }
-    } else if (warp == 0) {
-      // Lane l ranks experts l, l + 32, ...; `done` marks the chosen ones. A
-      // lane looks its experts through again only after it gave one away. The
-      // warp's choice is two integer reductions: the largest key, then the
-      // lowest index that has it.
-      uint32_t done = 0, lk = 0;
-      int le = 0x7fffffff, mine = 0;
-      bool look = true;
-      for (int j = 0; j < p.k; ++j) {
-        if (look) {
-          lk = 0;
-          le = 0x7fffffff;
-#pragma unroll 4
-          for (int e = lane, q = 0; e < p.E; e += 32, ++q) {
-            const uint32_t key = few_key(H[e]);
-            if (!((done >> q) & 1u) && (le == 0x7fffffff || key > lk)) {
-              lk = key;
-              le = e;
-            }
-          }
-        }
-        const uint32_t best = __reduce_max_sync(0xffffffffu, lk);
-        const int e = (int)__reduce_min_sync(0xffffffffu, lk == best ? (uint32_t)le : 0x7fffffffu);
-        look = (e & 31) == lane;
-        if (look) done |= 1u << (e >> 5);
-        if (lane == j) mine = e;
+    } else if (p.mode == kFewSwitch) {
+      if (warp == 0) {
+        int e = 0x7fffffff;
+        for (int i = lane; i < p.E && e >= p.E; i += 32)
+          if (H[i] == mx) e = i;
+        e = __reduce_min_sync(0xffffffffu, e);
+        if (lane == 0) put(0, e < p.E ? e : 0, 1.f / se);
       }
+    } else {
+      // Candidates, each ranked by one thread that counts those before it (a
+      // larger key, or the same and a lower index). Up to 128 experts are all
+      // candidates (three instructions each, where a pick below is some 300
+      // cycles); of more, every warp picks the k best of its own by two integer
+      // reductions a pick: the largest key, then the lowest index that has it.
+      unsigned long long *cand = reinterpret_cast<unsigned long long *>(sums);
+      int *chosen = reinterpret_cast<int *>(cand + 128), nc = p.E;
+      const auto rank = [](uint32_t key, int e) {  // one number to compare
+        return (unsigned long long)key << 32 | (uint32_t)~e;
+      };
+      if (p.E <= min(128, 64 * p.k)) {
+        if (tid < p.E) cand[tid] = rank(few_key(H[tid]), tid);
+      } else {
+        constexpr int kNone = 0x7fffffff;
+        uint32_t key[4];
+        int left = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = i * kFewThreads + tid;
+          key[i] = e < p.E ? few_key(H[e]) : 0u;
+          left |= (e < p.E) << i;
+        }
+        nc = 8 * p.k;
+        for (int j = 0; j < p.k; ++j) {
+          uint32_t lk = 0;
+          int li = kNone;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((left >> i & 1) && (li == kNone || key[i] > lk)) {
+              lk = key[i];
+              li = i * kFewThreads + tid;
+            }
+          const uint32_t best = __reduce_max_sync(0xffffffffu, lk);
+          const int e = __reduce_min_sync(0xffffffffu, lk == best ? li : kNone);
+          if (e == li && e != kNone) left &= ~(1 << (e / kFewThreads));
+          if (lane == 0) cand[warp * p.k + j] = rank(best, e);  // kNone: behind every expert
+        }
+      }
+      __syncthreads();
+      if (tid < nc) {
+        const unsigned long long mine = cand[tid];
+        int before = 0;
+        for (int c0 = 0; c0 < nc; c0 += 8) {  // past nc: other words of sums, not counted
+#pragma unroll
+          for (int c = 0; c < 8; ++c) before += (cand[c0 + c] > mine) & (c0 + c < nc);
+        }
+        if (before < p.k) chosen[before] = (int)~(uint32_t)mine;
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+      const int mine = lane < p.k ? chosen[lane] : 0;
       const float v = lane < p.k ? H[mine] : -INFINITY;
       const float top = __shfl_sync(0xffffffffu, v, 0);  // every lane takes part
       const float w = lane < p.k ? expf(v - top) : 0.f;
       float sum = w;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane < p.k) put(lane, mine, p.mode == kFewSwitch ? 1.f / se : w / sum);
+      if (lane < p.k) put(lane, mine, w / sum);
     }
   }
 }
