@@ -933,6 +933,7 @@ struct FewRound {
 // partial sums + b2), in fp32, rounded once. V columns a thread; where that
 // leaves most threads idle (few tokens, whose partials are many), 8 lanes share
 // the same columns' choices and their partials, joined in a fixed order.
+// The last barrier is inside, after what does not depend on it.
 template <typename T, int V, typename PF>
 __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
                                             const PF &pieces) {
@@ -956,6 +957,8 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
         row[i] = live && q < K ? R.row[t * p.k + q] : -1;
         np[i] = row[i] >= 0 ? pieces(R.owner[row[i]], (int)c) : 0;
         most = max(most, np[i]);
+        if (b2 && s0 == 0 && row[i] >= 0)
+          few_ld<T, V>(b2 + (size_t)R.expert[R.owner[row[i]]] * p.d + c, v[i]);
       }
       for (int sb = s0; sb < most; sb += S * ds) {
         float w[S][Q][V];
@@ -975,12 +978,6 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
         if (row[i] < 0) continue;
-        if (b2 && s0 == 0) {
-          float b[V];
-          few_ld<T, V>(b2 + (size_t)R.expert[R.owner[row[i]]] * p.d + c, b);
-#pragma unroll
-          for (int z = 0; z < V; ++z) v[i][z] += b[z];
-        }
         const float g = R.gate[t * p.k + qb + i * dq];
 #pragma unroll
         for (int z = 0; z < V; ++z) acc[z] = fmaf(g, v[i][z], acc[z]);
@@ -997,7 +994,6 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
   const unsigned first = blockIdx.x * kFewThreads + threadIdx.x, stride = gridDim.x * kFewThreads;
   if (total * 8 <= stride) {
     const unsigned i = first >> 3, sub = first & 7;
-    if (first - (threadIdx.x & 31) >= total * 8) return;  // whole warps leave
     const bool live = i < total;
     const unsigned t = live ? by(i) : 0, c = live ? (i - t * cols) * V : 0;
     // Lanes over the choices that a token keeps on average, the rest over their
@@ -1005,6 +1001,8 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
     const int lk = R.rows > 4 * p.T ? 3 : R.rows > 2 * p.T ? 2 : R.rows > p.T ? 1 : 0;
     float acc[V] = {};
     if (live && sub == 0) few_ld<T, V>(x + (size_t)t * p.d + c, acc);
+    if (!few_barrier(p, kFewBarriers - 1)) return;
+    if (first - (threadIdx.x & 31) >= total * 8) return;  // whole warps leave
     add(FewRound<1, 4>{}, t, c, sub & ((1 << lk) - 1), 1 << lk, (int)sub >> lk,
         8 >> lk, live, acc);
 #pragma unroll
@@ -1014,6 +1012,7 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
     if (live && sub == 0) store(t, c, acc);
     return;
   }
+  if (!few_barrier(p, kFewBarriers - 1)) return;
   for (unsigned i = first; i < total; i += stride) {
     const unsigned t = by(i), c = (i - t * cols) * V;
     float acc[V];

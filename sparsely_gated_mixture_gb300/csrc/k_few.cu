@@ -234,9 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
   if (!few_barrier(p, 2)) return;
   const FewH<T> h{p.hpart, (size_t)R.rows * p.F, static_cast<const T *>(p.b1), p.F, u[0].slices};
   few_product<T, VEC>(R, u[1], h, static_cast<const T *>(p.W2), p.F, p.d, p.zpart, work);
-  if (!few_barrier(p, 3)) return;
-  constexpr int V = VEC;
-  few_combine<T, V>(p, R, [&](int, int) { return u[1].slices; });
+  few_combine<T, VEC>(p, R, [&](int, int) { return u[1].slices; });
 }
 
 template <typename T, int VEC>

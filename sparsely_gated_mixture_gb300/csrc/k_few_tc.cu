@@ -156,8 +156,18 @@ struct FewTc {
   int stages, tok_bytes;  // ring stages; bytes of a stage's token operand
 };
 
+// Layer 1's results are complete when every block has arrived at barrier 2 (one
+// warp waits).
+__device__ __forceinline__ bool few_wait_warp(const FewArgs &p, volatile int *abort_flag) {
+  const bool done = (threadIdx.x & 31) == 0 ? few_wait(p, 2, abort_flag) : true;
+  const bool all = __all_sync(0xffffffffu, done);
+  if (!all) *abort_flag = 1;
+  __syncwarp();
+  return all;
+}
+
 // Layer 2's token operand where the layer has a single token (one row for each
-// expert in use), by one warp, past barrier 2: two columns a lane of a unit's 64,
+// expert in use), by one warp, which waits for barrier 2 first: two columns a lane of a unit's 64,
 // H = ReLU(sum of layer 1's parts + b1) rounded to bf16, as the join of a tile's
 // parts would make it, without that join before the barrier. The loads of eight
 // units are in flight together. Returns the ring position after the last unit.
@@ -194,6 +204,7 @@ __device__ __forceinline__ uint32_t few_tokens(const FewArgs &p, const FewTc &q,
         }
       }
     }
+    if (u == l.lo && !few_wait_warp(p, abort_flag)) return it;
     for (int z0 = 0; z0 < most; z0 += Z) {
       float w[Z][B][2];
 #pragma unroll
@@ -376,20 +387,14 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
       bool go = true;
       for (int layer = 0; layer < 2 && go; ++layer) {
         const FewLine &l = line[layer];
+        if (layer && direct) {
+          it = few_tokens(p, q, R, line, ring, full_t, empty, __shfl_sync(0xffffffffu, it, 0),
+                          abort_flag);
+          break;
+        }
         if (layer) {
-          // H is complete when every block has arrived at barrier 2.
-          const bool done = lane == 0 ? few_wait(p, 2, abort_flag) : true;
-          if (!__all_sync(0xffffffffu, done)) {
-            *abort_flag = 1;
-            break;
-          }
-          __syncwarp();
+          if (!few_wait_warp(p, abort_flag)) break;
           asm volatile("fence.proxy.async.global;" ::: "memory");
-          if (direct) {
-            it = few_tokens(p, q, R, line, ring, full_t, empty, __shfl_sync(0xffffffffu, it, 0),
-                            abort_flag);
-            break;
-          }
         }
         for (FewSeg s(l); s.more() && go; s.next(l)) {
           if (lane == 0) {
@@ -544,7 +549,6 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     if (threadIdx.x == 0) few_leave(p);
     return;
   }
-  if (!few_barrier(p, 3)) return;
   few_combine<__nv_bfloat16, 4>(p, R, [&](int j, int c) { return line[1].pieces(j, c); });
 }
 
