@@ -157,13 +157,21 @@ __device__ __forceinline__ bool few_wait(const FewArgs &p, int b,
 // block has passed the first).
 __device__ __forceinline__ void few_leave(const FewArgs &p) { *few_flag(p, blockIdx.x) = 0; }
 
-__device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
+// A barrier in two steps, by all threads; between them the block may do what
+// neither the others nor it itself waits for.
+__device__ __forceinline__ void few_barrier_arrive(const FewArgs &p, int b) {
   __syncthreads();
   if (threadIdx.x == 0) few_arrive(p, b);
+}
+__device__ __forceinline__ bool few_barrier_wait(const FewArgs &p, int b) {
   const bool ok = b == 0 ? few_wait_first(p) : threadIdx.x == 0 ? few_wait(p, b) : true;
   const bool fail = __syncthreads_or(!ok);
   if (threadIdx.x == 0 && (b == kFewBarriers - 1 || fail)) few_leave(p);
   return !fail;
+}
+__device__ __forceinline__ bool few_barrier(const FewArgs &p, int b) {
+  few_barrier_arrive(p, b);
+  return few_barrier_wait(p, b);
 }
 
 // ----------------------------------------------------------------------------- element types

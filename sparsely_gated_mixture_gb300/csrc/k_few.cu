@@ -334,7 +334,7 @@ cudaError_t launch_few(const FewCall &q, cudaStream_t s) {
   p.st = ws_at<DeviceStatus>(q.ws, L.status);
   p.flags = ws_at<unsigned long long>(q.ws, L.flags);
   p.tiles = ws_at<uint32_t>(q.ws, L.tiles);
-  p.n_tiles = L.n_tiles;
+  p.n_tiles = c.T > 1 ? L.n_tiles : 0;  // a single token's tiles are not joined
   p.rpart = ws_at<float>(q.ws, L.rpart);
   p.hpart = ws_at<float>(q.ws, L.hpart);
   p.zpart = ws_at<float>(q.ws, L.zpart);

@@ -267,6 +267,10 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
   const bool direct = p.T == 1;  // layer 2's tokens straight from layer 1's partial sums
 
   few_start(p);
+  // The ring's memory serves the router and the selection first.
+  float *work = reinterpret_cast<float *>(ring);
+  few_route<__nv_bfloat16>(p, work);
+  few_barrier_arrive(p, 0);
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full_w[s], 1);
@@ -294,10 +298,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  // The ring's memory serves the router and the selection first.
-  float *work = reinterpret_cast<float *>(ring);
-  few_route<__nv_bfloat16>(p, work);
-  bool ok = few_barrier(p, 0);
+  bool ok = few_barrier_wait(p, 0);
   if (ok) {
     few_select<__nv_bfloat16>(p, work, alone);
     if (p.T > 1) ok = few_barrier(p, 1);
