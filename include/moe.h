@@ -409,9 +409,10 @@ int moe_forward_threshold(const moe_config *cfg, const void *x, const float *Wg,
  * token-order slots (pos, keep) and output, with the expert terms summed in
  * fp32 (moe_forward rounds them to bf16 where it may), so the two agree to
  * rounding, not bit for bit. y may be x. A larger T, or a d or d_ff over
- * MOE_FEW_MAX_WIDTH, returns MOE_ERR_UNSUPPORTED (use moe_forward). ws holds moe_few_workspace_size bytes and needs no
- * initialisation; the status word at its start is cleared first. The launch
- * takes every SM while it runs; calls on other streams wait for one another.
+ * MOE_FEW_MAX_WIDTH, returns MOE_ERR_UNSUPPORTED (use moe_forward). ws holds
+ * moe_few_workspace_size bytes and needs no initialisation; the status word at
+ * its start is cleared first. The launch takes every SM while it runs; calls on
+ * other streams wait for one another.
  */
 #define MOE_FEW_MAX_TOKENS 64
 #define MOE_FEW_MAX_WIDTH 524288

@@ -25,7 +25,7 @@ constexpr int kFewRows = 1024;     // T * k at most (k <= 16)
 constexpr int kFewThreads = 256;
 constexpr int kFewMaxGrid = 320;   // blocks at most (sizes the flags and partial sums)
 constexpr int kFewBarriers = 4;
-constexpr int kFewFlag = 16;       // 64-bit words from one flag or count to the next: a 128-byte line
+constexpr int kFewFlag = 16;       // 64-bit words from one flag or count to the next (128 bytes)
 constexpr int kFewTile = 256;      // weight columns of a unit on the tensor cores
 enum FewMode { kFewTopk = 0, kFewSwitch = 1, kFewThreshold = 2 };
 
@@ -417,10 +417,12 @@ __device__ __forceinline__ void few_route_bf16(const FewArgs &p, float *smem) {
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(xv[i][2 * j], xv[i][2 * j + 1]);  // exact
+            // Exact: x is bf16.
+            const __nv_bfloat162 h = __floats2bfloat162_rn(xv[i][2 * j], xv[i][2 * j + 1]);
             o[j] = *reinterpret_cast<const uint32_t *>(&h);
           }
-          *reinterpret_cast<uint4 *>(xs + xt[i] * P + xo[i] / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4 *>(xs + xt[i] * P + xo[i] / 2) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
       __syncthreads();
       if (kb + kRtRows < k1) fetch(kb + kRtRows);
