@@ -42,12 +42,6 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // v / 2^e (v >= 0) for e4m3, at least 2^-9 where v is over zero. Saturates in
 // the conversion; where 448 * 2^e passes the largest float (e >= 120) it stops
 // at 240, whose value is finite.

@@ -112,7 +112,7 @@ struct FewH {
 #pragma unroll 4
     for (int s = 0; s < slices; ++s) v += __ldcg(p + s * step);
     if (b1) v += few_f(b1[(size_t)e * K + k]);
-    return few_f(few_t<T>(fmaxf(v, 0.f)));
+    return few_f(few_t<T>(max_nan(v, 0.f)));
   }
 };
 

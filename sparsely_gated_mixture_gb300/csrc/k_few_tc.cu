@@ -231,8 +231,8 @@ __device__ __forceinline__ uint32_t few_tokens(const FewArgs &p, const FewTc &q,
           mbar_wait(&empty[st], ((it / q.stages) & 1u) ^ 1u, abort_flag, p.st, 117, p.wait_ns);
       if (!__all_sync(0xffffffffu, free)) return it;
       const __nv_bfloat162 h =
-          __floats2bfloat162_rn(fmaxf(v[m].x + __low2float(bias[m]), 0.f),
-                                fmaxf(v[m].y + __high2float(bias[m]), 0.f));
+          __floats2bfloat162_rn(max_nan(v[m].x + __low2float(bias[m]), 0.f),
+                                max_nan(v[m].y + __high2float(bias[m]), 0.f));
       // Row 0 of the operand: the swizzle leaves it in place.
       *reinterpret_cast<__nv_bfloat162 *>(ring + (size_t)st * stage + kWBytes + lane * 4) = h;
       fence_proxy_async_smem();
@@ -467,7 +467,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                   for (int i = 0; i < 8; ++i)
                     if (r + i < rows)
                       hout[(size_t)(r0 + r + i) * l.N + n] =
-                          __float2bfloat16_rn(fmaxf(__uint_as_float(v[i]) + bias, 0.f));
+                          __float2bfloat16_rn(max_nan(__uint_as_float(v[i]) + bias, 0.f));
                 } else {
 #pragma unroll
                   for (int i = 0; i < 8; ++i)
@@ -523,7 +523,7 @@ k_few_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtens
                     for (int z = 0; z < 4; ++z) v[m][z] += b[z];
                   }
 #pragma unroll
-                  for (int z = 0; z < 4; ++z) v[m][z] = fmaxf(v[m][z], 0.f);
+                  for (int z = 0; z < 4; ++z) v[m][z] = max_nan(v[m][z], 0.f);
                   few_st<__nv_bfloat16, 4>(hout + (size_t)(r0 + r[m]) * l.N + n0 + c[m], v[m]);
                 }
               }

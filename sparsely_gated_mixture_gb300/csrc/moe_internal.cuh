@@ -123,6 +123,14 @@ struct FixedDiv {
   }
 };
 
+// The larger of two numbers, NaN if either is. The ReLU takes it with 0: fmaxf
+// would turn a NaN into 0 and hide it from the checks of the outputs.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // ----------------------------------------------------------------------------- launchers
 // Each returns a cudaError_t from the launch (cudaSuccess if nothing failed).
 
