@@ -41,11 +41,8 @@ L2_FLUSH_BYTES = 256 << 20
 NOMINAL_HBM_GBS = 8000.0  # the part's nominal HBM3e rate, reported beside the measured one
 # DRAM bytes (read + write) of the expert FFN stage per step, from one ncu
 # capture (profiles/expert_ffn_tc_pair_top2_large_experts.md), valid only for
-# the kernel source it was taken on (hash of k_ffn_tc.cu + tc_ptx.cuh). The
-# hash was re-keyed once, when the cluster PTX wrappers moved unchanged from
-# k_ffn_tc.cu into tc_ptx.cuh (ptxas reports the same registers, spills and
-# shared memory for every FFN kernel before and after the move).
-FFN_TRAFFIC = {"top2_large_experts": {"bytes": 3855409664, "source": "166bb4bd3ef617ae"}}
+# the kernel source it was taken on (hash of k_ffn_tc.cu + tc_ptx.cuh).
+FFN_TRAFFIC = {"top2_large_experts": {"bytes": 3862775296, "source": "15e857bb505912ee"}}
 
 
 class nvtx:

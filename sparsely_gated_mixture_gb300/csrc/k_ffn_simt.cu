@@ -80,7 +80,7 @@ k_ffn_simt(int K, int N, const T *__restrict__ Ain, const int32_t *__restrict__ 
       if (n >= N) continue;
       float v = acc[i][j] + (bias ? ld(bias, (size_t)e * N + n) : 0.f);
       if (LAYER == 1) {
-        v = fmaxf(v, 0.f);
+        v = max_nan(v, 0.f);
         T *o = static_cast<T *>(out);
         if constexpr (sizeof(T) == 2) o[r * N + n] = __float2bfloat16_rn(v);
         else o[r * N + n] = v;

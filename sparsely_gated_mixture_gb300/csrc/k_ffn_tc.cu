@@ -288,7 +288,8 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           uint32_t packed[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            __nv_bfloat162 h2 = __floats2bfloat162_rn(fmaxf(f[2 * j], 0.f), fmaxf(f[2 * j + 1], 0.f));
+            __nv_bfloat162 h2 =
+                __floats2bfloat162_rn(max_nan(f[2 * j], 0.f), max_nan(f[2 * j + 1], 0.f));
             packed[j] = *reinterpret_cast<uint32_t *>(&h2);
           }
           if (tma_rows) {
@@ -709,7 +710,7 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             __nv_bfloat162 h2 =
-                __floats2bfloat162_rn(fmaxf(f[2 * j], 0.f), fmaxf(f[2 * j + 1], 0.f));
+                __floats2bfloat162_rn(max_nan(f[2 * j], 0.f), max_nan(f[2 * j + 1], 0.f));
             packed[j] = *reinterpret_cast<uint32_t *>(&h2);
           }
           if (tma_rows) {

@@ -106,3 +106,78 @@ def test_few_logit_errors_name_their_token_and_expert():
         assert res["status"] == NONFINITE
         # The logits are recorded behind a grid barrier before the combine.
         assert 4 * w.E <= res["detail"] < 5 * w.E
+
+
+# ----------------------------------------------------------------------------- the whole layer
+LAYERS = {
+    "single": (96, 128, 192, "bf16"),
+    "pair": (96, 128, 192, "bf16"),
+    "odd_bf16": (40, 66, 130, "bf16"),
+    "f32": (40, 64, 128, "f32"),
+}
+
+
+def run_layer(w, d):
+    cfg = B.config_for(w)
+    act = torch.bfloat16 if w.dtype == "bf16" else torch.float32
+    y = torch.empty((w.T, w.d), dtype=act, device="cuda")
+    idx = torch.empty((w.T, w.k), dtype=torch.int32, device="cuda")
+    gate = torch.empty((w.T, w.k), device="cuda")
+    ws = torch.zeros(B.moe_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    B.moe_forward(cfg, d["x"], d["Wg"], None, None, None, d["W1"], d["b1"], d["W2"], d["b2"], y,
+                  None, ws, idx, gate)
+    st, det = B.moe_last_device_status(ws)
+    return dict(y=y, idx=idx, gate=gate, ws=ws, status=st, detail=det)
+
+
+@pytest.mark.parametrize("name,value", PLACES)
+@pytest.mark.parametrize("layer", sorted(LAYERS))
+def test_layer_reports_what_the_experts_bring_in(monkeypatch, layer, name, value):
+    if layer in ("single", "pair"):
+        monkeypatch.setenv("MOE_FFN_TC_VARIANT", layer)
+    T, d, d_ff, dtype = LAYERS[layer]
+    w = _w(T, d, 6, d_ff, 2, cf=6.0, dtype=dtype)
+    inp = wl.generate(w, seed=19, biases=True)
+    good = run_layer(w, to_device(w, inp))
+    assert good["status"] == 0
+    e = int(good["idx"][0, 0])
+    check(w, good, run_layer(w, to_device(w, planted(w, inp, name, value, e))), e, name)
+
+
+@pytest.mark.parametrize("layer", sorted(LAYERS))
+def test_a_checkpoint_and_its_backward_report_a_nan_of_layer_1(monkeypatch, layer):
+    """The NaN that moe_forward's layer 1 makes reaches the checkpoint, whose
+    save reports it, and the gradients."""
+    if layer in ("single", "pair"):
+        monkeypatch.setenv("MOE_FFN_TC_VARIANT", layer)
+    T, d, d_ff, dtype = LAYERS[layer]
+    w = _w(T, d, 6, d_ff, 2, cf=6.0, dtype=dtype)
+    inp = wl.generate(w, seed=20, biases=True)
+    cfg = B.config_for(w)
+    e = int(run_layer(w, to_device(w, inp))["idx"][0, 0])
+    dev = to_device(w, planted(w, inp, "b1", "nan", e))
+    f = run_layer(w, dev)
+    _, n8, ns = B.moe_checkpoint_size(cfg)
+    h8 = torch.empty(n8, dtype=torch.uint8, device="cuda")
+    hs = torch.empty(ns, dtype=torch.uint8, device="cuda")
+    B.moe_checkpoint_save(cfg, None, None, h8, hs, f["ws"])
+    status, detail = B.moe_last_device_status(f["ws"])
+    assert status == NONFINITE and (detail % d_ff) // 32 == d_ff // 2 // 32
+    # One block of 32 in each of the expert's rows.
+    rows = torch.bincount(f["idx"].flatten(), minlength=w.E).cpu()
+    marks = (hs.reshape(-1, (d_ff + 31) // 32) == 255).cpu()
+    first = int(rows[:e].sum())
+    assert int(marks.sum()) == int(rows[e])
+    assert bool(marks[first:first + int(rows[e]), d_ff // 2 // 32].all())
+    act = f["y"].dtype
+
+    def n(*s, dtype=act):
+        return torch.zeros(s, dtype=dtype, device="cuda")
+    dW2 = n(w.E, d_ff, d)
+    bws = n(B.moe_backward_workspace_size(cfg), dtype=torch.uint8)
+    B.moe_backward_checkpoint(cfg, dev["x"], dev["Wg"], None, None, None, dev["W1"], dev["W2"],
+                              dev["b2"], f["idx"], f["gate"], h8, hs, torch.ones_like(f["y"]),
+                              0.0, 0.0, 0.0, n(T, d), n(d, w.E, dtype=torch.float32), None, None,
+                              n(w.E, d, d_ff), None, dW2, None, None, f["ws"], bws)
+    assert B.moe_last_device_status(f["ws"])[0] == NONFINITE
+    assert not bool(torch.isfinite(dW2[e].float()).all())
