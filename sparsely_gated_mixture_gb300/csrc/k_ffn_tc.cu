@@ -790,6 +790,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
       return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
     return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
   }();
+  // The encoder is a driver call: it wants a current context, which a host
+  // thread has from its first runtime call on only.
+  int dev = 0;
+  if (fn && !current_context() &&
+      (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)) {
+    cudaGetLastError();
+    return nullptr;
+  }
   return fn;
 }
 
