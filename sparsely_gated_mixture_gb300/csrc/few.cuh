@@ -1034,8 +1034,9 @@ __device__ __forceinline__ void few_combine(const FewArgs &p, const FewRows &R,
 
 }  // namespace
 
-// Launches a kernel of one cooperative grid of kFewThreads-thread blocks.
-cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
+// Launches a kernel of one cooperative grid of kFewThreads-thread blocks; no
+// launch of it takes more than `most` of dynamic shared memory.
+cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem, size_t most,
                             cudaStream_t s);
 // k_few_tc.cu: bf16 layers whose widths are multiples of 8, experts on tcgen05.
 inline bool few_on_tc(const moe_config &c) {

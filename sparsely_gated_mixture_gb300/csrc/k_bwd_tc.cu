@@ -908,8 +908,7 @@ int pair_clusters_bwd(size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(k_bwd_tc_pair<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess ||
+  if (allow_smem(k_bwd_tc_pair<MODE>) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, k_bwd_tc_pair<MODE>, &cfg) != cudaSuccess) {
     n = 0;
     cudaGetLastError();
@@ -926,8 +925,7 @@ template <int MODE, bool OB = false>
 cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
                              const BParams &p, int clusters, cudaStream_t s) {
   const size_t smem = bwd_smem_bytes_pair(p.E, MODE);
-  cudaError_t err = cudaFuncSetAttribute(
-      k_bwd_tc_pair<MODE, OB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = allow_smem(k_bwd_tc_pair<MODE, OB>);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
@@ -946,8 +944,7 @@ template <int MODE, bool OB = false>
 cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p,
                         cudaStream_t s) {
   const size_t smem = bwd_smem_bytes(p.E);
-  cudaError_t err = cudaFuncSetAttribute(k_bwd_tc<MODE, OB>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = allow_smem(k_bwd_tc<MODE, OB>);
   if (err != cudaSuccess) return err;
   launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB>, sm_count(), kThreads, smem, s, a, b, p);
   return cudaGetLastError();

@@ -243,20 +243,21 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_few_simt(const FewArgs p) {
 template <typename T, int VEC>
 cudaError_t run_simt(const FewArgs &p, cudaStream_t s) {
   const size_t smem = kSimtSmemFloats * 4 + few_rows_bytes(p.E, p.T * p.k);
+  constexpr size_t most = kSimtSmemFloats * 4 + few_rows_bytes(1024, kFewRows);
   int grid = 2 * sm_count();  // two blocks fit an SM (launch bounds, 72 KB at most)
   if (grid > kFewMaxGrid) grid = kFewMaxGrid;
   FewArgs a = p;
   a.rt = few_router(p.T, p.d, p.E, p.Wn != nullptr, grid);
   void *args[1] = {&a};
-  return launch_few_grid(reinterpret_cast<const void *>(k_few_simt<T, VEC>), args, grid, smem, s);
+  return launch_few_grid(reinterpret_cast<const void *>(k_few_simt<T, VEC>), args, grid, smem,
+                         most, s);
 }
 
 }  // namespace
 
-cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem,
+cudaError_t launch_few_grid(const void *kernel, void **args, int grid, size_t smem, size_t most,
                             cudaStream_t s) {
-  cudaError_t err =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = allow_smem(kernel, most);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -570,7 +570,7 @@ bool make_weight_map(CUtensorMap *m, const void *base, int E, int K, int N) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSmemMax = 227 * 1024 - 1024;  // less the static part
+constexpr size_t kSmemMax = kSmemMost - 1024;  // less the static part
 
 }  // namespace
 
@@ -598,7 +598,7 @@ cudaError_t launch_few_tc(const FewArgs &p, cudaStream_t s) {
   a.rt = few_router(p.T, p.d, p.E, p.Wn != nullptr, grid);
   void *args[6] = {&tx, &th, &t1, &t2, &a, &q};
   return launch_few_grid(reinterpret_cast<const void *>(k_few_tc), args, grid,
-                         1024 + q.stages * stage + rows, s);
+                         1024 + q.stages * stage + rows, kSmemMax, s);
 }
 
 }  // namespace moe

@@ -871,8 +871,7 @@ template <int LAYER>
 cudaError_t launch_layer(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
                          const Params &p, cudaStream_t s) {
   const size_t smem = smem_bytes(p.E);
-  cudaError_t err = cudaFuncSetAttribute(k_ffn_tc<LAYER>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = allow_smem(k_ffn_tc<LAYER>);
   if (err != cudaSuccess) return err;
   launch_pdl_c(kPdlGemm, k_ffn_tc<LAYER>, sm_count(), kThreads, smem, s, a, b, o, p);
   return cudaGetLastError();
@@ -913,8 +912,7 @@ int pair_clusters(size_t smem) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(k_ffn_tc_pair<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess ||
+  if (allow_smem(k_ffn_tc_pair<1>) != cudaSuccess ||
       cudaOccupancyMaxActiveClusters(&n, k_ffn_tc_pair<1>, &cfg) != cudaSuccess)
     n = 0;
   if (used < kSlots) {
@@ -929,8 +927,7 @@ template <int LAYER>
 cudaError_t launch_layer_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
                               const Params &p, int clusters, cudaStream_t s) {
   const size_t smem = smem_bytes_pair(p.E);
-  cudaError_t err = cudaFuncSetAttribute(
-      k_ffn_tc_pair<LAYER>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t err = allow_smem(k_ffn_tc_pair<LAYER>);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);

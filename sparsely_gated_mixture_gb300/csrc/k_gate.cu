@@ -948,6 +948,7 @@ constexpr int kHierMaxKp = 8;    // largest primary k
 // Tokens per block: 64, or 32 when the block's P buffer ([tokens][kp][b]
 // floats, kp*b <= a*b <= 1024) would pass 128 KB at 64.
 __host__ __device__ inline int hier_tokens(int kp, int b) { return kp * b <= 512 ? 64 : 32; }
+constexpr size_t kHierSmemMost = 128 * 1024;
 
 template <int VPL, int KMS>  // b <= 32 * VPL, ks <= KMS
 __global__ void __launch_bounds__(kHierWarps * 32)
@@ -1266,9 +1267,7 @@ cudaError_t launch_hier_select(int T, int a, int b, int kp, int ks, bool noisy,
   const int vpl = (b + 31) / 32;
 #define MOE_HIER_K(V, KM)                                                                     \
   do {                                                                                         \
-    cudaError_t e_ = cudaFuncSetAttribute(k_hier_select<V, KM>,                               \
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,         \
-                                          (int)dsm);                                           \
+    cudaError_t e_ = allow_smem(k_hier_select<V, KM>, kHierSmemMost);                          \
     if (e_ != cudaSuccess) return e_;                                                          \
     launch_pdl(k_hier_select<V, KM>, grid, kHierWarps * 32, dsm, s, T, a, b, kp, ks,          \
                noisy ? 1 : 0, idx_p, g_p, cs, ss, Hs, poff, pos_p, idx, gate, partials, st);  \

@@ -1494,8 +1494,7 @@ cudaError_t run_grp(const GroupedRouter &r, DeviceStatus *st, cudaStream_t s) {
   GParams g{r.a, ncg / BNR, r.kp, r.a * r.b, r.goff, r.grow, r.poff};
   const size_t smem = RCfg<BNR>::SMEM + (size_t)8 * (r.a + 1);
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
-  err = cudaFuncSetAttribute(k_router_grp<BNR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+  err = allow_smem(k_router_grp<BNR>);
   if (err != cudaSuccess) return err;
   const long max_tiles = ((long)r.T * r.kp / RBM + r.a) * (ncg / BNR);
   const int grid = max_tiles < sm_count() ? (int)max_tiles : sm_count();

@@ -131,6 +131,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// The dynamic shared memory that launches of a kernel may ask for. The setting
+// is the kernel's, one for all threads of the process: a call that set its own
+// size could lower it between another call's setting and its launch, which was
+// then refused. So every call sets the same `most`, which covers all sizes.
+constexpr size_t kSmemMost = 227 * 1024;  // what a block can have, static part included
+template <typename K>
+inline cudaError_t allow_smem(K *kernel, size_t most = kSmemMost) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // ----------------------------------------------------------------------------- launchers
 // Each returns a cudaError_t from the launch (cudaSuccess if nothing failed).
 
