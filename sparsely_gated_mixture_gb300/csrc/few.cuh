@@ -344,11 +344,11 @@ __device__ __forceinline__ void few_mma16816(float (&c)[4], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// bf16 x: a weight is the exact sum of three bf16 numbers, so three bf16
-// products with fp32 accumulation give the fp32 product. The CUDA-core form
-// above is bound by its shared-memory reads (9 for 8 multiply-adds: 8 us for 40
-// tokens and 1024 columns); here a 16-row step takes 28 for the whole block's
-// 64 tokens x 16 columns. The products are too small and the weights too few
+// bf16 x: a weight is the sum of three bf16 numbers (exact from 2^-110 on, below
+// that within 2^-134), so three bf16 products with fp32 accumulation give the
+// fp32 product. The CUDA-core form above is bound by its shared-memory reads (9
+// for 8 multiply-adds: 8 us for 40 tokens and 1024 columns); here a 16-row step
+// takes 28 for the whole block's 64 tokens x 16 columns. The products are too small and the weights too few
 // for tcgen05's operands (they would first have to be split into memory).
 // Warps: 4 steps of 16 rows x 2 halves of the columns; joined in shared memory.
 // smem: xs bf16 [tokens][72], w bf16 [3][cw][72] (rows of 64 with a pad that
@@ -406,9 +406,10 @@ __device__ __forceinline__ void few_route_bf16(const FewArgs &p, float *smem) {
 #pragma unroll
         for (int z = 0; z < 3; ++z) {
           const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          dst[z * cw * P] = *reinterpret_cast<const uint32_t *>(&h);
-          a -= __low2float(h);
-          b -= __high2float(h);
+          const uint32_t u = z ? *reinterpret_cast<const uint32_t *>(&h) : bf16x2_finite(a, b);
+          dst[z * cw * P] = u;
+          a -= __uint_as_float(u << 16);
+          b -= __uint_as_float(u & 0xffff0000u);
         }
       }
 #pragma unroll

@@ -4,7 +4,8 @@
 // x is bf16, so every product x_i * W[i,e] is exact once W is written as the
 // sum of three bf16 pieces: hi = bf16(W), mid = bf16(W - hi), lo = bf16(W -
 // hi - mid), with W = hi + mid + lo exactly (each piece carries 8 of fp32's
-// 24 significand bits; the differences are exact in fp32). The router is then
+// 24 significand bits; the differences are exact in fp32) for finite W of
+// 2^-110 or more and within 2^-134 below. The router is then
 // three bf16 GEMMs, x * hi + x * mid + x * lo, accumulated in fp32 in TMEM:
 // the fp32 router's arithmetic at the tensor cores' rate.
 //
@@ -127,7 +128,7 @@ __global__ void k_router_split(int d, int E, int noisy, int NC, int NCP, int BNR
     const int n = n0 + r, k = k0 + threadIdx.x;
     if (n >= NCP || k >= d) continue;
     const float w = tile[threadIdx.x][r];
-    const __nv_bfloat16 hi = __float2bfloat16_rn(w);
+    const __nv_bfloat16 hi = __ushort_as_bfloat16((unsigned short)bf16x2_finite(w, 0.f));
     const float r1 = w - __bfloat162float(hi);
     const __nv_bfloat16 mid = __float2bfloat16_rn(r1);
     const float r2 = r1 - __bfloat162float(mid);

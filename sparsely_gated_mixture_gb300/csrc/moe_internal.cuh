@@ -131,6 +131,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// Two floats to the nearest bf16 numbers (a in the low half), an Inf to the
+// largest one. The first of the three terms that the routers write a weight as:
+// a finite weight over 3.396e38 would round to Inf there, and what is left of it
+// to -Inf. (What is left of an Inf is Inf, so that one stays non-finite.)
+__device__ __forceinline__ uint32_t bf16x2_finite(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 // The dynamic shared memory that launches of a kernel may ask for. The setting
 // is the kernel's, one for all threads of the process: a call that set its own
 // size could lower it between another call's setting and its launch, which was
