@@ -142,9 +142,12 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
-        # The handle without a Stream object around it (3 us a call less).
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        device = torch.cuda.current_device()
+        # The handle without a Stream object around it takes 3 us a call less; a
+        # torch that does not offer it has the object.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
