@@ -58,7 +58,7 @@ struct FewArgs {
   int n_tiles;
   float *rpart;               // router partials [slices][T][columns]
   float *hpart, *zpart;       // partials of the layers [slices][rows][N]
-  void *h;                    // [rows, F], the layer's type
+  void *h;                    // [rows, F] in bf16 (tensor-core form)
   unsigned long long nonce, wait_ns;
 };
 

@@ -301,7 +301,7 @@ FewLayout few_layout(const moe_config &c) {
   };
   L.hpart = take(partials(F) * 4);
   L.zpart = take(partials(d) * 4);
-  L.h = take(A * F * elem_bytes(c.act_dtype));
+  L.h = take(few_on_tc(c) ? A * F * 2 : 0);
   L.total = off;
   return L;
 }

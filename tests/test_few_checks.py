@@ -37,6 +37,15 @@ def test_workspace_holds_the_cuda_cores_partial_sums(lib):
         assert B.moe_few_workspace_size(cfg) >= 8 * 64 * 16 * (d + d_ff) * 4
 
 
+def test_workspace_of_the_cuda_cores_holds_no_hidden_rows(lib):
+    """They make the hidden rows of layer 1's partial sums where they read them:
+    what grows with d_ff are the 8 partial sums of each of its values alone."""
+    for act, d, d_ff, step in ((B.MOE_BF16, 66, 130, 4098), (B.MOE_F32, 64, 128, 4096)):
+        size = [B.moe_few_workspace_size(B.config(64, d, 16, n, 16, 1.0, act_dtype=act))
+                for n in (d_ff, d_ff + step)]
+        assert size[1] - size[0] <= 8 * 64 * 16 * step * 4 + 256
+
+
 @pytest.mark.parametrize("bad", [
     {0: None}, {0: F + 8}, {1: None}, {2: F}, {3: F}, {4: F + 4}, {5: None}, {6: F + 2}, {7: None},
     {9: None}, {10: F + 4}, {11: F + 4}, {12: F + 4}, {13: F + 1}, {14: None}, {14: F + 16}])
