@@ -375,15 +375,20 @@ static BwdLayout bwd_layout(const moe_config &cfg) {
   L.dU = take(P * d * rb);
   L.dP = take(P * dff * rb);
   L.dX = take(P * d * 4);
-  L.dgpart = take(P * L.n_blocks2 * 4);
   L.dg = take(T * k * 4);
   L.coef = take(3 * E * 4);
+  L.dxr = take(T * d * 4);
+  L.dgpart = take(P * L.n_blocks2 * 4);
   L.dc = take(T * E * 4);
   L.dz = take(T * E * 4);
-  L.dxr = take(T * d * 4);
   L.rpart = take(rp * d * 4);
   L.bpart = take(rp * 4);
-  L.cpart = take((size_t)L.chunks * E * (d + dff) * 4);
+  // The bias gradients' partials take the place of dL/dgate's and what the router
+  // gradients are made of: their kernels run after the last ones that read these,
+  // on the same stream.
+  L.cpart = L.dgpart;
+  const size_t cend = align_up(L.cpart + (size_t)L.chunks * E * (d + dff) * 4, 256);
+  if (cend > off) off = cend;
   L.st2 = take(sizeof(DeviceStatus));  // a router run beside the rest
   L.total = off;
   return L;
