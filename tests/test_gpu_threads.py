@@ -69,6 +69,107 @@ def test_expert_ffn_as_a_threads_first_call():
         assert torch.equal(a, b)
 
 
+def entry_points():
+    """Every other entry point that enqueues work, as (call, outputs, workspace):
+    the call takes a stream."""
+    z = dict(device="cuda")
+    w = wl.Workload("t", T=96, d=64, E=6, d_ff=128, k=2, cf=1.0, mode=wl.TOPK, dtype="bf16",
+                    noisy=True)
+    cfg, d = B.config_for(w), to_device(w, wl.generate(w, seed=3, biases=True))
+    A = w.T * w.k
+
+    def new(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype, **z)
+
+    def space(n):
+        return new(n, dtype=torch.uint8)
+    bf, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    router = (d["x"], d["Wg"], d["Wn"], d["noise"], None)
+    experts = (d["W1"], d["b1"], d["W2"], d["b2"])
+    # A forward's state, which some of them start from.
+    base, bws = space(B.moe_workspace_size(cfg)), space(B.moe_backward_workspace_size(cfg))
+    y0, out0 = new(w.T, w.d, dtype=bf), new(3)
+    idx, gate = new(w.T, w.k, dtype=i32), new(w.T, w.k)
+    B.moe_forward(cfg, *router, *experts, y0, out0, base, idx, gate)
+    _, n8, ns = B.moe_checkpoint_size(cfg)
+    h8, hs = space(n8), space(ns)
+    B.moe_checkpoint_save(cfg, None, None, h8, hs, base)
+    dy = torch.ones_like(y0)
+    ep = {}
+
+    def add(name, make, outs, ws):
+        ep[name] = (make, outs, ws)
+
+    o, ws = [new(w.T, w.k, dtype=i32), new(w.T, w.k), new(w.T, 2)], base.clone()
+    add("moe_gate", lambda s, o=o, ws=ws: B.moe_gate(cfg, *router, *o, ws, stream=s), o, ws)
+    o, ws = [new(w.T, w.d, dtype=bf), new(3)], base.clone()
+    add("moe_forward", lambda s, o=o, ws=ws: B.moe_forward(cfg, *router, *experts, *o, ws,
+                                                           stream=s), o, ws)
+    o = [new(w.T, w.k, dtype=i32), new(w.T, w.k, dtype=u8), new(w.E, dtype=i32),
+         new(w.E + 1, dtype=i32), new(A, w.d, dtype=bf), new(A, dtype=i32), new(A)]
+    ws = base.clone()
+    add("moe_dispatch", lambda s, o=o, ws=ws: B.moe_dispatch(cfg, idx, gate, d["x"], *o, ws,
+                                                             stream=s), o, ws)
+    o = [torch.zeros_like(v) for v in o]
+    add("moe_dispatch_noalloc", lambda s, o=o: B.moe_dispatch_noalloc(cfg, idx, gate, d["x"], *o,
+                                                                      stream=s), o, ws)
+
+    def grads(dtype):
+        return [new(w.T, w.d, dtype=bf), new(w.d, w.E), new(w.d, w.E), new(w.E),
+                new(w.E, w.d, w.d_ff, dtype=dtype), new(w.E, w.d_ff, dtype=dtype),
+                new(w.E, w.d_ff, w.d, dtype=dtype), new(w.E, w.d, dtype=dtype), new(w.T, w.k)]
+    o, ws = grads(torch.float32), base.clone()
+    add("moe_backward", lambda s, o=o, ws=ws: B.moe_backward(
+        cfg, *router[:4], d["W1"], d["W2"], d["b2"], idx, gate, None, None, dy, 0.1, 0.2, 0.3, *o,
+        ws, bws, stream=s), o, ws)
+    o, ws = grads(bf), base.clone()
+    add("moe_backward_checkpoint", lambda s, o=o, ws=ws: B.moe_backward_checkpoint(
+        cfg, *router, d["W1"], d["W2"], d["b2"], idx, gate, h8, hs, dy, 0.1, 0.2, 0.3, *o, ws,
+        bws, stream=s), o, ws)
+    o, ws = [space(n8), space(ns)], base.clone()
+    add("moe_checkpoint_save", lambda s, o=o, ws=ws: B.moe_checkpoint_save(
+        cfg, None, None, *o, ws, stream=s), o, ws)
+    ws = base.clone()
+    add("moe_checkpoint_load", lambda s, ws=ws: B.moe_checkpoint_load(
+        cfg, h8, hs, None, None, ws, stream=s), [ws], ws)
+    thr, thr2 = (torch.full((w.E,), v, **z) for v in (0.2, 0.4))
+    o, ws = [new(w.T, w.d, dtype=bf)], space(B.moe_threshold_workspace_size(cfg))
+    add("moe_forward_threshold", lambda s, o=o, ws=ws: B.moe_forward_threshold(
+        cfg, d["x"], d["Wg"], None, thr2, *experts, *o, ws, stream=s), o, ws)
+    few = B.config(32, w.d, w.E, w.d_ff, w.E, 1.0)
+    o, ws = [new(32, w.d, dtype=bf)], space(B.moe_few_workspace_size(few))
+    add("moe_forward_threshold_few", lambda s, o=o, ws=ws: B.moe_forward_threshold_few(
+        few, d["x"], d["Wg"], None, thr, *experts, *o, ws, stream=s), o, ws)
+    o, ws = [new(w.T, w.d, dtype=bf), new(1)], space(B.moe_balanced_workspace_size(cfg))
+    add("moe_forward_balanced", lambda s, o=o, ws=ws: B.moe_forward_balanced(
+        cfg, d["x"], d["Wg"], None, thr, *experts, *o, None, ws, stream=s), o, ws)
+    h = wl.HierWorkload("t", T=64, d=64, a=4, b=8, kp=2, ks=2, d_ff=64, cf=4.0, dtype="bf16",
+                        noisy=False)
+    hd = hier_to_device(h, wl.generate_hier(h, seed=4))
+    o = [torch.zeros_like(hd["x"]), new(2)]
+    ws = space(B.moe_hier_workspace_size(B.hier_config_for(h)))
+    add("moe_forward_hier", lambda s, o=o, ws=ws: B.moe_forward_hier(
+        B.hier_config_for(h), hd["x"], hd["Wp"], None, None, hd["Ws"], None, None, hd["W1"], None,
+        hd["W2"], None, *o, ws, stream=s), o, ws)
+    return ep
+
+
+def test_every_entry_point_as_a_threads_first_call():
+    stream = torch.cuda.Stream().cuda_stream
+    for name, (run, outs, ws) in entry_points().items():
+        run(None)
+        assert B.moe_last_device_status(ws)[0] == 0, name
+        want = [o.clone() for o in outs]
+        for o in outs:
+            if o is not ws:
+                o.zero_()
+        torch.cuda.synchronize()
+        on_new_thread(lambda run=run: run(stream))
+        assert B.moe_last_device_status(ws)[0] == 0, name
+        for a, b in zip(outs, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+
+
 # ----------------------------------------------------------------------------- at once
 # What launches of a kernel may take of shared memory is one setting for all
 # threads, and the two sizes of each test ask for different amounts: no call may
