@@ -35,7 +35,9 @@
  *   a side stream. When none fits (the pool is not made yet and `stream` is
  *   capturing; 8 other caller streams hold them; a side stream in another
  *   capture) the call runs everything on `stream`, with the same results.
- *   After cudaDeviceReset the next call makes a new pool.
+ *   After cudaDeviceReset the next call makes a new pool. Calls on several
+ *   host threads at once need a stream and workspaces of their own each, and
+ *   any call may be the first CUDA call of its thread.
  * Element types.  cfg->act_dtype (MOE_F32 or MOE_BF16) is the type of x, W1,
  *   b1, W2, b2, y, xbuf and hbuf. The router weights, router bias, noise,
  *   gates and zbuf are always fp32.
@@ -406,9 +408,10 @@ int moe_forward_threshold(const moe_config *cfg, const void *x, const float *Wg,
  * moe_forward's chain, bound by reading the weights of the experts in use
  * once. Arguments, outputs and definition are moe_forward's without the
  * balancing losses, which belong to training: the same gate, capacity,
- * token-order slots (pos, keep) and output, with the expert terms summed in
- * fp32 (moe_forward rounds them to bf16 where it may), so the two agree to
- * rounding, not bit for bit. y may be x. A larger T, or a d or d_ff over
+ * token-order slots (pos, keep) and output, with the hidden rows rounded to
+ * act_dtype (as moe_expert_ffn's hbuf) and the expert terms summed in fp32
+ * (moe_forward rounds them to bf16 where it may), so the two agree to rounding,
+ * not bit for bit. y may be x. A larger T, or a d or d_ff over
  * MOE_FEW_MAX_WIDTH, returns MOE_ERR_UNSUPPORTED (use moe_forward). ws holds
  * moe_few_workspace_size bytes and needs no initialisation; the status word at
  * its start is cleared first. The launch takes every SM while it runs; calls on
@@ -459,7 +462,11 @@ int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float 
  * results unchanged, so it may be repeated with another dy.
  * Every configuration moe_forward takes: bf16 layers with d and d_ff
  * multiples of 64 run the expert GEMMs on the tensor cores, the others
- * (fp32 layers, other widths) on the CUDA cores with fp32 row buffers.
+ * (fp32 layers, other widths) on the CUDA cores with fp32 row buffers. On the
+ * tensor cores the operands gate * dy and dpre are bf16 rows, and sums are
+ * theirs in fp32, which cut instead of rounding: dL/dgate and the router
+ * gradients that follow it are off by some 5e-6 of their size at d = 4096 (5e-7
+ * at 512), where a plain fp32 product is off by 6e-7 (2e-7).
  * Inputs: dy [T,d] act_dtype. Outputs (fp32 unless stated): dx [T,d]
  * act_dtype; dWg
  * [d,E]; dWnoise [d,E] (required iff Wnoise is given); dlogit_bias [E] (may

@@ -348,8 +348,9 @@ __device__ __forceinline__ void few_mma16816(float (&c)[4], const uint32_t (&a)[
 // that within 2^-134), so three bf16 products with fp32 accumulation give the
 // fp32 product. The CUDA-core form above is bound by its shared-memory reads (9
 // for 8 multiply-adds: 8 us for 40 tokens and 1024 columns); here a 16-row step
-// takes 28 for the whole block's 64 tokens x 16 columns. The products are too small and the weights too few
-// for tcgen05's operands (they would first have to be split into memory).
+// takes 28 for the whole block's 64 tokens x 16 columns. The products are too
+// small and the weights too few for tcgen05's operands (they would first have to
+// be split into memory).
 // Warps: 4 steps of 16 rows x 2 halves of the columns; joined in shared memory.
 // smem: xs bf16 [tokens][72], w bf16 [3][cw][72] (rows of 64 with a pad that
 // spreads the fragments' reads over the banks); then red [4][tokens][cw] floats.

@@ -18,10 +18,10 @@
 // every 16-byte (fp32: 32-byte) load issued before the first is used; 4 lanes
 // of 8 columns make a block. Widths that are not a multiple of 8 go one
 // column per lane. Saving and loading the 16384 rows of 14336 of the large-expert
-// layer take 215 us for 1.42 GB, 6.6 TB/s. Saving was bound by its instructions
-// first (some 10 a value, 227 us for both): the ReLU and the largest value now
-// take one packed instruction for two bf16 values, the lift over zero two a
-// value, and a warp's row no 64-bit division.
+// layer take 215 to 223 us for 1.42 GB, 6.4 to 6.6 TB/s. Saving was bound by its
+// instructions first (some 10 a value, 227 us for both): the ReLU and the
+// largest value now take one packed instruction for two bf16 values, the lift
+// over zero two a value, and a warp's row no 64-bit division.
 #include "checkpoint.cuh"
 #include "moe_internal.cuh"
 
@@ -215,7 +215,7 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bf
 // Any width: one column of a block per lane, kAny consecutive blocks (over the
 // rows' ends) a warp, all their loads in flight. A block's largest value is one
 // integer reduction: bits of floats that are not below zero order as they do,
-// NaN last. Saving and loading 8192 rows of 10001 bf16 columns take 262 us, bound
+// NaN last. Saving and loading 8192 rows of 10001 bf16 columns take 260 us, bound
 // by instructions (75 us is their bytes at the copy rate; one block a warp took
 // 645).
 constexpr int kAny = 8;

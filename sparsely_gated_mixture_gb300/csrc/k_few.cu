@@ -1,7 +1,13 @@
 // The few-token layer on the CUDA cores: fp32 layers, and bf16 layers of
 // widths that are not multiples of 8. The weights of the experts in use are
-// read once, in 16-byte vectors where the widths allow it, and multiplied
-// with up to 8 rows at a time from registers.
+// read in vectors of 2, 4, 8 or 16 bytes, as the widths allow, and multiplied
+// with up to 8 rows at a time from registers; more rows read them again, from
+// L2 or HBM. A warp asks for nothing while it multiplies a chunk, which is what
+// bounds the form: in fp32 one token of the large-expert layer takes 164 us (141
+// us at the copy rate), 64 tokens 1.92 ms (0.56). The 128 registers that two
+// blocks an SM leave a thread are all in use; fp32 with vectors of four and of
+// one and bf16 with vectors of one spill 28 to 36 bytes. moe_forward takes 4.5
+// and 6.9 ms there.
 #include "few.cuh"
 
 #include <atomic>
@@ -90,7 +96,8 @@ constexpr int kSimtSmemFloats = 256 * 8 + 8 * 8 * 32 * 4;
 
 // The rows of a product's left operand: layer 1's are tokens' x; layer 2's the
 // hidden ones, made of layer 1's partial sums where they are staged (ReLU of
-// their sum and b1, rounded once to the layer's type).
+// their sum and b1, rounded once to the layer's type: the layer's hidden rows are
+// of that type, in moe_expert_ffn and on the tensor cores too).
 template <typename T>
 struct FewX {
   const FewRows &rows;

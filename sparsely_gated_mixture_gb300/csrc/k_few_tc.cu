@@ -172,7 +172,7 @@ __device__ __forceinline__ bool few_wait_warp(const FewArgs &p, volatile int *ab
 // Layer 2's token operand where the layer has a single token (one row for each
 // expert in use), by one warp, which waits for barrier 2 first: two columns a lane of a unit's 64,
 // H = ReLU(sum of layer 1's parts + b1) rounded to bf16, as the join of a tile's
-// parts would make it, without that join before the barrier. The loads of eight
+// parts would make it, without that join before the barrier. The loads of four
 // units are in flight together. Returns the ring position after the last unit.
 __device__ __forceinline__ uint32_t few_tokens(const FewArgs &p, const FewTc &q, const FewRows &R,
                                                const FewLine *line, uint8_t *ring,
