@@ -475,7 +475,10 @@ int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float 
  * gate value (<dy_t, U_e(x_t)> for a kept choice plus the Importance term).
  * bws is the backward's own workspace, moe_backward_workspace_size bytes,
  * 256-byte aligned. Device-side errors (a non-finite gradient, a bounded wait
- * that ran out) go to the status word of `ws`.
+ * that ran out) go to the status word of `ws`. After MOE_ERR_NONFINITE no
+ * expert's gradients are to be used: on the tensor cores a non-finite x or hidden
+ * row meets the zero padding of the experts up to 63 rows before it, and makes
+ * their dW1 or dW2 non-finite too.
  */
 int moe_backward_workspace_size(const moe_config *cfg, size_t *bytes);
 int moe_backward(const moe_config *cfg, const void *x, const float *Wg, const float *Wnoise,
