@@ -1,8 +1,9 @@
 /*
  * moe.h -- C ABI of libmoe.so: the forward path of the sparsely-gated
  * Mixture-of-Experts layer on one NVIDIA GB300 (sm_103a), its hierarchical
- * and strictly balanced variants, its form for a few tokens, and the flat
- * layer's backward, also from 8-bit activation checkpoints.
+ * and strictly balanced variants, its form for a few tokens, the flat
+ * layer's backward, also from 8-bit activation checkpoints, and experts that
+ * are gated feed-forward blocks, with their backward and an 8-bit form.
  *
  * The layer, as the pages state it ("Outrageously Large Neural Networks: The
  * Sparsely-Gated Mixture-of-Experts Layer", section 3.4; "Switch Transformer",
@@ -50,7 +51,8 @@
  *   (the Switch page raises on each), an index out of range, or a bounded wait
  *   that ran out -- are recorded in a status word inside `ws`;
  *   moe_last_device_status() reads it. moe_gate(), moe_forward(), the few-token
- *   calls and moe_backward_checkpoint() clear it when they start,
+ *   calls, moe_backward_checkpoint(), the gated experts' calls and
+ *   moe_weights_fp8() clear it when they start,
  *   moe_last_device_status() after reading it; a caller whose first call on a
  *   fresh workspace is another stage zero-fills the workspace (or calls
  *   moe_last_device_status) first. Each bounded wait inside the
@@ -568,6 +570,107 @@ int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *W
                             float w_load, float w_aux, void *dx, float *dWg, float *dWnoise,
                             float *dlogit_bias, void *dW1, void *db1, void *dW2, void *db2,
                             float *dgate, void *ws, void *bws, moe_stream_t stream);
+
+/*
+ * Gated experts, from given choices. Expert e is a gated feed-forward block,
+ *   U_e(x) = (act(x W1[e] + b1[e]) * (x W3[e] + b3[e])) W2[e] + b2[e]
+ * (* elementwise; "Switch Transformer", step 6, with a product of two
+ * projections in place of the ReLU), act one of moe_activation, and
+ *   y[t] = x[t] + sum over the kept choices j of gate[t,j] * U_{expert_idx[t,j]}(x[t])
+ * with moe_dispatch's capacity and token-order slots (pos, keep). The choices
+ * and their gate values are the caller's: moe_gate's, or any router's; an
+ * expert may stand twice in a token's choices. Uses T, d, E, d_ff, k,
+ * capacity_factor, min_capacity and act_dtype of cfg; E <= 1024, k <= 16, d and
+ * d_ff at most MOE_GATED_MAX_WIDTH, and rows * ceil(max(d, d_ff) / 128) under
+ * 2^32, else MOE_ERR_UNSUPPORTED.
+ *
+ * x [T,d], W1, W3 [E,d,d_ff], b1, b3 [E,d_ff] (NULL = 0), W2 [E,d_ff,d], b2
+ * [E,d] (NULL = 0), y [T,d] in act_dtype (y may be x); expert_idx [T,k] int32,
+ * gate [T,k] fp32; pos [T,k] int32 and keep [T,k] uint8 may be NULL. pre1, pre3
+ * [T*k,d_ff] act_dtype, both given or both NULL: the pre-activations x W1 + b1
+ * and x W3 + b3 of the kept rows, packed as moe_dispatch packs them, for
+ * moe_experts_gated_backward; rows past the last kept one are left as they were.
+ * Products and the activation are fp32; hidden rows are rounded to act_dtype,
+ * as moe_expert_ffn's. ws: moe_gated_workspace_size bytes, no initialisation
+ * needed; the status word at its start is cleared first. An expert_idx outside
+ * [0, E) is recorded as MOE_ERR_BOUNDS (pos -1, keep 0), a non-finite output
+ * as MOE_ERR_NONFINITE.
+ */
+typedef enum {
+  MOE_ACT_SILU = 0, /* v / (1 + exp(-v)) */
+  MOE_ACT_GELU = 1, /* v * Phi(v), Phi the normal distribution function */
+  MOE_ACT_RELU = 2
+} moe_activation;
+#define MOE_GATED_MAX_WIDTH 524288
+int moe_gated_workspace_size(const moe_config *cfg, size_t *bytes);
+int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
+                      const int32_t *expert_idx, const float *gate, const void *W1,
+                      const void *b1, const void *W3, const void *b3, const void *W2,
+                      const void *b2, void *y, void *pre1, void *pre3, int32_t *pos,
+                      uint8_t *keep, void *ws, moe_stream_t stream);
+
+/*
+ * Its backward: the gradients of L = sum_t <dy_t, y_t> with the choices held
+ * fixed. With D = dy W2^T, g the gate and p1, p3 the pre-activations of a row:
+ *   dgate = <D, act(p1) * p3> + <dy, b2>      (0 for a dropped choice)
+ *   dP1 = g * D * p3 * act'(p1)     dP3 = g * D * act(p1)
+ *   dx = dy + sum over the kept rows of (dP1 W1^T + dP3 W3^T)
+ *   dW1 = x^T dP1   dW3 = x^T dP3   dW2 = h^T (g dy)   (h = act(p1) * p3)
+ *   db1, db3, db2 = the column sums of dP1, dP3, g dy
+ * (ReLU: act'(0) = 0.) dx lacks the router's share, which moe_gate_backward
+ * gives from this dgate. x, expert_idx, gate, the weights and b2 as the
+ * forward had them, pre1 and pre3 as it wrote them (the hidden rows are made
+ * again from these, so nothing else is kept), dy [T,d] act_dtype. Outputs: dx
+ * [T,d], dW1, dW3 [E,d,d_ff], dW2 [E,d_ff,d], db1, db3 [E,d_ff], db2 [E,d] in
+ * act_dtype (fp32 sums rounded once; an expert without rows gets zeros), dgate
+ * [T,k] fp32; db1, db3 and db2 may each be NULL. In bf16 layers dP1, dP3, g dy
+ * and h are bf16 operands of the products. No output may overlap an input. ws:
+ * moe_gated_backward_workspace_size bytes, scratch, its status word cleared
+ * first; after MOE_ERR_NONFINITE no expert's gradients are to be used.
+ */
+int moe_gated_backward_workspace_size(const moe_config *cfg, size_t *bytes);
+int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const void *x,
+                               const int32_t *expert_idx, const float *gate, const void *pre1,
+                               const void *pre3, const void *W1, const void *W3, const void *W2,
+                               const void *b2, const void *dy, void *dx, float *dgate, void *dW1,
+                               void *db1, void *dW3, void *db3, void *dW2, void *db2, void *ws,
+                               moe_stream_t stream);
+
+/*
+ * Expert weights in 8 bits, for moe_experts_gated_fp8: W [E,K,N] (dtype MOE_F32
+ * or MOE_BF16) as e4m3 values with one power-of-two scale for each block of 128
+ * rows and 128 columns, laid out with K contiguous.
+ *   w8 [E,N,Kp]: e4m3 bytes of W transposed, Kp = K rounded up to 128, zero past K;
+ *   wscale [E, ceil(N/128), Kp/128]: byte e + 127; the value is e4m3(w8) * 2^e, e
+ *   the smallest exponent, at least -124, with 448 * 2^e >= the block's largest
+ *   magnitude; values round to nearest, ties to even.
+ * A block with an Inf or a NaN gets the byte 255 (its products are NaN) and is
+ * recorded as MOE_ERR_NONFINITE (detail = its place in wscale). E <= 1024, K and
+ * N at most MOE_GATED_MAX_WIDTH. ws: the status word only (256 bytes), cleared
+ * first. moe_weights_fp8_size gives the arrays' bytes.
+ */
+int moe_weights_fp8_size(int32_t E, int32_t K, int32_t N, size_t *w8_bytes,
+                         size_t *wscale_bytes);
+int moe_weights_fp8(int32_t E, int32_t K, int32_t N, int32_t dtype, const void *W, uint8_t *w8,
+                    uint8_t *wscale, void *ws, moe_stream_t stream);
+
+/*
+ * moe_experts_gated for serving, with both matrix products in e4m3. Weights and
+ * scales are moe_weights_fp8's: W1, s1 and W3, s3 of [E,d,d_ff], W2, s2 of
+ * [E,d_ff,d]. A token's row is put in 8 bits with one scale for each 128
+ * columns, by the same rule, and so is a hidden row, after it was rounded to
+ * bf16; products are summed in fp32 with the scales applied. cfg->act_dtype is
+ * MOE_BF16 (else MOE_ERR_UNSUPPORTED): x, y, b1, b3, b2. Everything else as
+ * moe_experts_gated; a row with an Inf or a NaN makes its outputs NaN. ws:
+ * moe_gated_fp8_workspace_size bytes.
+ */
+int moe_gated_fp8_workspace_size(const moe_config *cfg, size_t *bytes);
+int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void *x,
+                          const int32_t *expert_idx, const float *gate, const uint8_t *W1,
+                          const uint8_t *s1, const void *b1, const uint8_t *W3,
+                          const uint8_t *s3, const void *b3, const uint8_t *W2,
+                          const uint8_t *s2, const void *b2, void *y, int32_t *pos,
+                          uint8_t *keep, void *ws, moe_stream_t stream);
 
 /*
  * Diagnostic: out[i] = Phi(u[i]) for i < n, the standard normal CDF exactly as

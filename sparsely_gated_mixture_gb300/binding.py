@@ -18,6 +18,9 @@ MOE_GATE_TOPK_SOFTMAX = 0
 MOE_GATE_SWITCH = 1
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_ACT_SILU = 0
+MOE_ACT_GELU = 1
+MOE_ACT_RELU = 2
 
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_CUDA",
                 4: "MOE_ERR_NONFINITE", 5: "MOE_ERR_TIMEOUT", 6: "MOE_ERR_BOUNDS"}
@@ -32,7 +35,10 @@ EXPORTS = ("moe_status_string", "moe_capacity", "moe_workspace_size", "moe_gate"
            "moe_forward_threshold", "moe_expert_counts", "moe_dispatch_ranked",
            "moe_aux_totals", "moe_aux_from_totals", "moe_few_workspace_size",
            "moe_forward_few", "moe_forward_threshold_few", "moe_checkpoint_size",
-           "moe_checkpoint_save", "moe_checkpoint_load", "moe_backward_checkpoint")
+           "moe_checkpoint_save", "moe_checkpoint_load", "moe_backward_checkpoint",
+           "moe_gated_workspace_size", "moe_experts_gated", "moe_gated_backward_workspace_size",
+           "moe_experts_gated_backward", "moe_weights_fp8_size", "moe_weights_fp8",
+           "moe_gated_fp8_workspace_size", "moe_experts_gated_fp8")
 
 
 class MoEError(RuntimeError):
@@ -126,6 +132,15 @@ def lib():
             L.moe_checkpoint_save.argtypes = [CP] + [P] * 6
             L.moe_checkpoint_load.argtypes = [CP] + [P] * 6
             L.moe_backward_checkpoint.argtypes = [CP] + [P] * 13 + [F, F, F] + [P] * 12
+            SP = ctypes.POINTER(ctypes.c_size_t)
+            L.moe_gated_workspace_size.argtypes = [CP, SP]
+            L.moe_experts_gated.argtypes = [CP, I32] + [P] * 16
+            L.moe_gated_backward_workspace_size.argtypes = [CP, SP]
+            L.moe_experts_gated_backward.argtypes = [CP, I32] + [P] * 20
+            L.moe_weights_fp8_size.argtypes = [I32, I32, I32, SP, SP]
+            L.moe_weights_fp8.argtypes = [I32] * 4 + [P] * 5
+            L.moe_gated_fp8_workspace_size.argtypes = [CP, SP]
+            L.moe_experts_gated_fp8.argtypes = [CP, I32] + [P] * 17
             for name in EXPORTS[1:]:
                 getattr(L, name).restype = I
             _lib = L
@@ -405,6 +420,68 @@ def moe_aux_totals(cfg, ws, totals, stream=None):
 def moe_aux_from_totals(cfg, T_total, totals, out3, ws, stream=None):
     _check(lib().moe_aux_from_totals(ctypes.byref(cfg), int(T_total), _p(totals), _p(out3),
                                      _p(ws), _stream(stream)), "moe_aux_from_totals")
+
+
+def moe_gated_workspace_size(cfg) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_gated_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_gated_workspace_size")
+    return n.value
+
+
+def moe_experts_gated(cfg, activation, x, expert_idx, gate, W1, b1, W3, b3, W2, b2, y, ws,
+                      pre1=None, pre3=None, pos=None, keep=None, stream=None):
+    """Gated experts from given choices, y = x + the kept choices' gate * U(x)."""
+    _check(lib().moe_experts_gated(ctypes.byref(cfg), int(activation), _p(x), _p(expert_idx),
+                                   _p(gate), _p(W1), _p(b1), _p(W3), _p(b3), _p(W2), _p(b2),
+                                   _p(y), _p(pre1), _p(pre3), _p(pos), _p(keep), _p(ws),
+                                   _stream(stream)), "moe_experts_gated")
+
+
+def moe_gated_backward_workspace_size(cfg) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_gated_backward_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_gated_backward_workspace_size")
+    return n.value
+
+
+def moe_experts_gated_backward(cfg, activation, x, expert_idx, gate, pre1, pre3, W1, W3, W2, b2,
+                               dy, dx, dgate, dW1, db1, dW3, db3, dW2, db2, ws, stream=None):
+    """The gradients of moe_experts_gated from the pre-activations it kept."""
+    _check(lib().moe_experts_gated_backward(
+        ctypes.byref(cfg), int(activation), _p(x), _p(expert_idx), _p(gate), _p(pre1), _p(pre3),
+        _p(W1), _p(W3), _p(W2), _p(b2), _p(dy), _p(dx), _p(dgate), _p(dW1), _p(db1), _p(dW3),
+        _p(db3), _p(dW2), _p(db2), _p(ws), _stream(stream)), "moe_experts_gated_backward")
+
+
+def moe_weights_fp8_size(E, K, N):
+    """(bytes of w8, bytes of wscale) of expert weights [E, K, N] in 8 bits."""
+    w8, ws = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().moe_weights_fp8_size(int(E), int(K), int(N), ctypes.byref(w8),
+                                      ctypes.byref(ws)), "moe_weights_fp8_size")
+    return w8.value, ws.value
+
+
+def moe_weights_fp8(E, K, N, dtype, W, w8, wscale, ws, stream=None):
+    """Expert weights W [E, K, N] to e4m3 [E, N, Kp] with 128 x 128 scales."""
+    _check(lib().moe_weights_fp8(int(E), int(K), int(N), int(dtype), _p(W), _p(w8), _p(wscale),
+                                 _p(ws), _stream(stream)), "moe_weights_fp8")
+
+
+def moe_gated_fp8_workspace_size(cfg) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_gated_fp8_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_gated_fp8_workspace_size")
+    return n.value
+
+
+def moe_experts_gated_fp8(cfg, activation, x, expert_idx, gate, W1, s1, b1, W3, s3, b3, W2, s2, b2,
+                          y, ws, pos=None, keep=None, stream=None):
+    """moe_experts_gated with weights of moe_weights_fp8 and 8-bit products."""
+    _check(lib().moe_experts_gated_fp8(ctypes.byref(cfg), int(activation), _p(x), _p(expert_idx),
+                                       _p(gate), _p(W1), _p(s1), _p(b1), _p(W3), _p(s3), _p(b3),
+                                       _p(W2), _p(s2), _p(b2), _p(y), _p(pos), _p(keep), _p(ws),
+                                       _stream(stream)), "moe_experts_gated_fp8")
 
 
 def moe_eval_normal_cdf(u, out, stream=None):

@@ -1,0 +1,396 @@
+// Gated experts on the CUDA cores: fp32 layers (the tensor cores have no fp32
+// input kind) and bf16 widths that the tensor-core kernels do not take. With
+// the packed rows r of expert e (token t, gate g):
+//   forward 1:  p1 = x W1 + b1, p3 = x W3 + b3, h = act(p1) * p3
+//   forward 2:  z = g * (h W2 + b2)
+//   backward 1: D = dy W2^T; dgate's <D, h>; dP1 = g D p3 act'(p1), dP3 = g D act(p1)
+//   backward 2: dX = dP1 W1^T + dP3 W3^T
+//   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
+//   8 bits:     forward 1 and 2 with e4m3 operands and their blocks' scales
+// One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
+// block of 256 threads, TM x TN a thread, K in chunks of 16 whose next one is
+// fetched while this one is multiplied, packed fp32 multiply-adds (two a lane
+// and instruction). Both projections of forward 1 share a block's columns, so
+// that a thread holds p1 and p3 of the same places. Sums run over K in order.
+#include "gated.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int BK = 16, kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float ld(const T *p, size_t i) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(p[i]);
+  else return p[i];
+}
+template <typename T>
+__device__ __forceinline__ void put(T *p, size_t i, float v) {
+  if constexpr (sizeof(T) == 2) p[i] = __float2bfloat16_rn(v);
+  else p[i] = v;
+}
+
+enum Op { kF1, kF2, kB1, kB2, kW1, kW3, kW2, kQ1, kQ2 };
+
+__device__ __forceinline__ float from8(uint8_t v) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(v, __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half *>(&h));
+}
+__device__ __forceinline__ float scale_of(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte << 23);
+}
+
+// a * b + c on two floats at once.
+__device__ __forceinline__ void fma2(unsigned long long &c, unsigned long long a,
+                                     unsigned long long b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+template <int OP, typename T, int ACT, int TM, int TN>
+__global__ void __launch_bounds__(kThreads)
+k_gated_simt(const GatedSimt p) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int BM = 16 * TM, BN = 16 * TN;
+  constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;  // a weight gradient
+  constexpr int LA = BM * BK / kThreads, LB = BN * BK / kThreads;
+  __shared__ __align__(16) float As[BK][BM + 4];
+  __shared__ __align__(16) float Bs[BK][BN + 4];
+  const int E = p.c.E, d = p.c.d, F = p.c.d_ff, k = p.c.k;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+
+  // The block's expert, first row and row count.
+  int e, m0;
+  if (kWeight) {
+    e = blockIdx.z;
+    m0 = blockIdx.x * BM;
+  } else {
+    constexpr int kSplit = kTcBM / BM;  // blocks for each 128-row tile
+    const int tile = blockIdx.x / kSplit;
+    if (tile >= p.rows.mtiles[E]) return;
+    int lo = 0, hi = E;  // largest e with mtiles[e] <= tile
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.rows.mtiles[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    e = lo;
+    m0 = (tile - p.rows.mtiles[e]) * kTcBM + (blockIdx.x % kSplit) * BM;
+  }
+  const int r0 = p.rows.offset[e], rows = p.rows.offset[e + 1] - r0;
+  if (!kWeight && m0 >= rows) return;
+  constexpr bool kPair = OP == kF1 || OP == kQ1;
+  constexpr int BNu = kPair ? BN / 2 : BN;  // columns of the output a block covers
+  const int n0 = blockIdx.y * BNu;
+  const int M = kWeight ? (OP == kW2 ? F : d) : rows;
+  const int N = kPair || OP == kB1 || OP == kW1 || OP == kW3 ? F : d;
+  const int K = kWeight ? rows : kPair || OP == kB1 ? d : OP == kF2 || OP == kQ2 ? F : 2 * F;
+  const int KB = (K + kFp8Block - 1) / kFp8Block;  // 8 bits: blocks of K
+  const size_t we = (size_t)e * d * F;  // this expert's place in each weight
+
+  // A: rows (K contiguous; K in lanes) or, for a weight gradient, columns of
+  // the rows (M contiguous). Rows of x and dy are read through their token.
+  size_t arow[kWeight ? 1 : LA];
+  if (!kWeight) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      const int m = m0 + (tid >> 4) + 16 * i;
+      const int r = r0 + min(m, rows - 1);
+      if (OP == kF1 || OP == kB1) arow[i] = (size_t)(p.rows.row_token[r] / k) * d;
+      else if (OP == kQ1 || OP == kQ2) arow[i] = r;
+      else arow[i] = (size_t)r * F;
+    }
+  }
+  const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
+  const T *W1 = static_cast<const T *>(p.W1) + we, *W3 = static_cast<const T *>(p.W3) + we;
+  const T *W2 = static_cast<const T *>(p.W2) + we;
+
+  float ra[LA], rb[LB];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      float v = 0.f;
+      if constexpr (kWeight) {
+        const int mm = tid % BM, kk = k0 + tid / BM + i * (kThreads / BM), m = m0 + mm;
+        if (m < M && kk < K) {
+          const int r = r0 + kk;
+          v = OP == kW2 ? p.hf[(size_t)r * F + m]
+                        : ld(x, (size_t)(p.rows.row_token[r] / k) * d + m);
+        }
+      } else {
+        const int kk = k0 + (tid & 15), m = m0 + (tid >> 4) + 16 * i;
+        if (m < M && kk < K) {
+          if (OP == kF1) v = ld(x, arow[i] + kk);
+          else if (OP == kF2) v = ld(static_cast<const T *>(p.h), arow[i] + kk);
+          else if (OP == kQ1 || OP == kQ2)
+            v = from8(p.a8[arow[i] * KB * kFp8Block + kk]) *
+                scale_of(p.sa[(size_t)(kk / kFp8Block) * p.max_rows + arow[i]]);
+          else if (OP == kB1) v = ld(dy, arow[i] + kk);
+          else v = kk < F ? p.dP1[arow[i] + kk] : p.dP3[arow[i] + kk - F];
+        }
+      }
+      ra[i] = v;
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      float v = 0.f;
+      if constexpr (OP == kQ1 || OP == kQ2) {
+        const int kk = k0 + (tid & 15), nn = (tid >> 4) + 16 * i;
+        const bool second = OP == kQ1 && nn >= BNu;
+        const int n = n0 + (second ? nn - BNu : nn);
+        if (n < N && kk < K) {
+          const size_t w = (size_t)e * N + n;
+          const size_t sc = ((size_t)e * ((N + 127) / 128) + n / 128) * KB + kk / 128;
+          const void *q = OP == kQ2 ? p.W2 : second ? p.W3 : p.W1;
+          const uint8_t *qs = OP == kQ2 ? p.s2 : second ? p.s3 : p.s1;
+          v = from8(static_cast<const uint8_t *>(q)[w * KB * kFp8Block + kk]) * scale_of(qs[sc]);
+        }
+      } else if constexpr (OP == kB1 || OP == kB2) {  // the weight's rows are the output's columns
+        const int kk = k0 + (tid & 15), n = n0 + (tid >> 4) + 16 * i;
+        if (n < N && kk < K) {
+          if (OP == kB1) v = ld(W2, (size_t)n * d + kk);
+          else v = kk < F ? ld(W1, (size_t)n * F + kk) : ld(W3, (size_t)n * F + kk - F);
+        }
+      } else {
+        const int nn = tid % BN, kk = k0 + tid / BN + i * (kThreads / BN);
+        const bool second = OP == kF1 && nn >= BNu;
+        const int n = n0 + (second ? nn - BNu : nn);
+        if (n < N && kk < K) {
+          if (OP == kF1) v = ld(second ? W3 : W1, (size_t)kk * F + n);
+          else if (OP == kF2) v = ld(W2, (size_t)kk * d + n);
+          else if (OP == kW2) v = p.dU[(size_t)(r0 + kk) * d + n];
+          else v = (OP == kW1 ? p.dP1 : p.dP3)[(size_t)(r0 + kk) * F + n];
+        }
+      }
+      rb[i] = v;
+    }
+  };
+  auto stage = [&] {
+#pragma unroll
+    for (int i = 0; i < LA; ++i) {
+      if (kWeight) As[tid / BM + i * (kThreads / BM)][tid % BM] = ra[i];
+      else As[tid & 15][(tid >> 4) + 16 * i] = ra[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LB; ++i) {
+      if (OP == kB1 || OP == kB2 || OP == kQ1 || OP == kQ2) Bs[tid & 15][(tid >> 4) + 16 * i] = rb[i];
+      else Bs[tid / BN + i * (kThreads / BN)][tid % BN] = rb[i];
+    }
+  };
+
+  // Thread (ty, tx) holds rows {0, BM/2} + ty TM/2 + .. and columns {0, BN/2} +
+  // tx TN/2 + .., so that its operands are short vectors and, in forward 1, the
+  // second half of its columns is W3's.
+  constexpr int HM = TM / 2, HN = TN / 2;
+  unsigned long long acc[TM][TN / 2] = {};
+  if (K > 0) fetch(0);
+  for (int k0 = 0; k0 < K; k0 += BK) {
+    stage();
+    __syncthreads();
+    if (k0 + BK < K) fetch(k0 + BK);
+#pragma unroll
+    for (int kk = 0; kk < BK; ++kk) {
+      float a[TM];
+      unsigned long long b[TN / 2];
+      if constexpr (HM == 4) {
+        *reinterpret_cast<float4 *>(&a[0]) = *reinterpret_cast<const float4 *>(&As[kk][ty * 4]);
+        *reinterpret_cast<float4 *>(&a[4]) =
+            *reinterpret_cast<const float4 *>(&As[kk][BM / 2 + ty * 4]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) a[i] = As[kk][(i / HM) * (BM / 2) + ty * HM + i % HM];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float *row = &Bs[kk][h * (BN / 2) + tx * HN];
+        if constexpr (HN == 4) {
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
+          b[2 * h] = u.x;
+          b[2 * h + 1] = u.y;
+        } else {
+          b[h] = *reinterpret_cast<const unsigned long long *>(row);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const unsigned long long aa = pack2(a[i], a[i]);
+#pragma unroll
+        for (int j = 0; j < TN / 2; ++j) fma2(acc[i][j], aa, b[j]);
+      }
+    }
+    __syncthreads();
+  }
+
+  const T *b1 = static_cast<const T *>(p.b1), *b3 = static_cast<const T *>(p.b3);
+  const T *b2 = static_cast<const T *>(p.b2);
+  constexpr bool kPrecise = sizeof(T) == 4;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + (i / HM) * (BM / 2) + ty * HM + i % HM;
+    float v[TN];
+#pragma unroll
+    for (int j = 0; j < TN / 2; ++j)
+      asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[i][j]));
+    const bool live = m < M;
+    const size_t r = (size_t)r0 + m;
+    bool bad = false;
+    if constexpr (kPair) {
+      if (!live) continue;
+#pragma unroll
+      for (int j = 0; j < HN; ++j) {
+        const int n = n0 + tx * HN + j;
+        if (n >= N) continue;
+        float p1 = v[j], p3 = v[HN + j];
+        if (b1) p1 += ld(b1, (size_t)e * F + n);
+        if (b3) p3 += ld(b3, (size_t)e * F + n);
+        if (p.pre1) put(static_cast<T *>(p.pre1), r * F + n, p1);
+        if (p.pre3) put(static_cast<T *>(p.pre3), r * F + n, p3);
+        put(static_cast<T *>(p.h), r * F + n, gated_act<kPrecise, ACT>(p1) * p3);
+      }
+    } else if constexpr (OP == kB1) {
+      const float g = live ? p.rows.row_gate[r] : 0.f;
+      float part = 0.f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = n0 + (j / HN) * (BN / 2) + tx * HN + j % HN;
+        if (!live || n >= N) continue;
+        const float p1 = ld(static_cast<const T *>(p.pre1), r * F + n);
+        const float p3 = ld(static_cast<const T *>(p.pre3), r * F + n);
+        float a, sl;
+        gated_act_slope<kPrecise, ACT>(p1, a, sl);
+        const float h = a * p3, D = v[j];
+        part = fmaf(D, h, part);
+        p.hf[r * F + n] = h;
+        p.dP1[r * F + n] = g * D * p3 * sl;
+        p.dP3[r * F + n] = g * D * a;
+      }
+      // Over the 16 lanes that share the row.
+#pragma unroll
+      for (int o = 8; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (live && tx == 0) p.dgpart[r * gridDim.y + blockIdx.y] = part;
+    } else {
+      if (!live) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = n0 + (j / HN) * (BN / 2) + tx * HN + j % HN;
+        if (n >= N) continue;
+        float u = v[j];
+        if constexpr (OP == kF2 || OP == kQ2) {
+          if (b2) u += ld(b2, (size_t)e * d + n);
+          u *= p.rows.row_gate[r];
+          p.z[r * d + n] = u;
+        } else if constexpr (OP == kB2) {
+          p.dX[r * d + n] = u;
+        } else {
+          void *out = OP == kW1 ? p.dW1 : OP == kW3 ? p.dW3 : p.dW2;
+          put(static_cast<T *>(out), we + (size_t)m * N + n, u);
+        }
+        bad |= !isfinite(u);
+      }
+    }
+    if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)(kWeight ? m : r));
+  }
+}
+
+// dU[r] = g * dy of the row's token, in fp32; one warp per packed row.
+template <typename T>
+__global__ void __launch_bounds__(256) k_gated_dy_rows(const GatedSimt p) {
+  pdl_wait();
+  pdl_trigger();
+  const long long r = (blockIdx.x * 256ll + threadIdx.x) >> 5;
+  if (r >= p.max_rows || r >= p.rows.offset[p.c.E]) return;
+  const size_t src = (size_t)(p.rows.row_token[r] / p.c.k) * p.c.d;
+  const float g = p.rows.row_gate[r];
+  for (int i = threadIdx.x & 31; i < p.c.d; i += 32)
+    p.dU[r * p.c.d + i] = g * ld(static_cast<const T *>(p.dy), src + i);
+}
+
+// Rows in 128-row tiles at most: every expert's last one may be short.
+long long max_tiles(const GatedSimt &p) {
+  return ((long long)p.max_rows + kTcBM - 1) / kTcBM + (p.c.E < p.max_rows ? p.c.E : p.max_rows);
+}
+
+template <int OP, typename T, int ACT, int TM, int TN>
+cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
+  constexpr int BM = 16 * TM, BN = 16 * TN;
+  constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;
+  constexpr bool kPair = OP == kF1 || OP == kQ1;
+  const int N = kPair || OP == kB1 || OP == kW1 || OP == kW3 ? p.c.d_ff : p.c.d;
+  const int BNu = kPair ? BN / 2 : BN;
+  dim3 grid(1, (N + BNu - 1) / BNu, 1);  // row blocks fastest: they share the weight's columns
+  if (kWeight) {
+    grid.x = ((OP == kW2 ? p.c.d_ff : p.c.d) + BM - 1) / BM;
+    grid.z = p.c.E;
+  } else {
+    grid.x = (unsigned)(max_tiles(p) * (kTcBM / BM));
+  }
+  return launch_pdl_c(kPdlGemm, k_gated_simt<OP, T, ACT, TM, TN>, grid, kThreads, 0, s, p);
+}
+
+// 128 x 128 tiles where they give every SM a block and rows to fill them, else
+// 32 x 64.
+bool wide_tiles(const moe_config &c, int max_rows, int op) {
+  const bool weight = op == kW1 || op == kW3 || op == kW2;
+  const bool to_d = op == kF2 || op == kB2 || op == kW2 || op == kQ2;
+  const int N = (op == kF1 || op == kQ1 ? 2 : 1) * (to_d ? c.d : c.d_ff);
+  const int M = op == kW2 ? c.d_ff : c.d;
+  const long long row_blocks = weight ? (long long)c.E * ((M + 127) / 128)
+                                      : ((long long)max_rows + 127) / 128;
+  return row_blocks * ((N + 127) / 128) >= sm_count() && (weight || max_rows >= 64 * c.E);
+}
+
+template <int OP, typename T, int ACT>
+cudaError_t run_op(const GatedSimt &p, cudaStream_t s) {
+  return wide_tiles(p.c, p.max_rows, OP) ? run_one<OP, T, ACT, 8, 8>(p, s)
+                                         : run_one<OP, T, ACT, 2, 4>(p, s);
+}
+
+template <typename T>
+cudaError_t forward(const GatedSimt &p, cudaStream_t s) {
+  const cudaError_t err = gated_dispatch(p.activation, [&](auto act) {
+    return run_op<kF1, T, decltype(act)::value>(p, s);
+  });
+  return err != cudaSuccess ? err : run_op<kF2, T, MOE_ACT_RELU>(p, s);
+}
+
+template <typename T>
+cudaError_t backward(const GatedSimt &p, cudaStream_t s) {
+  cudaError_t err = launch_pdl(k_gated_dy_rows<T>, (unsigned)((p.max_rows + 7) / 8), 256, 0, s, p);
+  if (err == cudaSuccess)
+    err = gated_dispatch(p.activation, [&](auto act) {
+      return run_op<kB1, T, decltype(act)::value>(p, s);
+    });
+  if (err == cudaSuccess) err = run_op<kB2, T, MOE_ACT_RELU>(p, s);
+  if (err == cudaSuccess) err = run_op<kW1, T, MOE_ACT_RELU>(p, s);
+  if (err == cudaSuccess) err = run_op<kW3, T, MOE_ACT_RELU>(p, s);
+  return err != cudaSuccess ? err : run_op<kW2, T, MOE_ACT_RELU>(p, s);
+}
+
+}  // namespace
+
+int gated_simt_dg_blocks(const moe_config &c, int max_rows) {
+  const int cols = wide_tiles(c, max_rows, kB1) ? 128 : 64;
+  return (c.d_ff + cols - 1) / cols;
+}
+
+cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s) {
+  return p.c.act_dtype == MOE_BF16 ? forward<__nv_bfloat16>(p, s) : forward<float>(p, s);
+}
+
+cudaError_t launch_gated_simt_fp8(const GatedSimt &p, int layer, cudaStream_t s) {
+  if (layer == 2) return run_op<kQ2, __nv_bfloat16, MOE_ACT_RELU>(p, s);
+  return gated_dispatch(p.activation, [&](auto act) {
+    return run_op<kQ1, __nv_bfloat16, decltype(act)::value>(p, s);
+  });
+}
+
+cudaError_t launch_gated_simt_backward(const GatedSimt &p, cudaStream_t s) {
+  return p.c.act_dtype == MOE_BF16 ? backward<__nv_bfloat16>(p, s) : backward<float>(p, s);
+}
+
+}  // namespace moe

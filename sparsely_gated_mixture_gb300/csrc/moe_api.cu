@@ -1,17 +1,14 @@
 // C ABI of libmoe.so (declared in include/moe.h): argument checks, the
 // workspace layout and the order of launches. No computation happens here;
 // every stage runs in the kernels of the other translation units.
-#include "moe_internal.cuh"
+#include "api.cuh"
 
 #include <mutex>
 
-#include <math.h>
 #include <stdlib.h>
 #include <string.h>
 
 namespace moe {
-
-static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 void *current_context() {
   using GetCurrent = int (*)(void **);  // CUresult cuCtxGetCurrent(CUcontext *)
@@ -79,44 +76,6 @@ WsLayout ws_layout(const moe_config &cfg) {
   L.total = off;
   return L;
 }
-
-static int host_capacity(const moe_config &c) {
-  double raw = floor((double)c.k * (double)c.T * (double)c.capacity_factor / (double)c.E);
-  long v = (long)raw;
-  if (v > c.T) v = c.T;
-  if (v < c.min_capacity) v = c.min_capacity;
-  return (int)v;
-}
-
-static int check_cfg(const moe_config *c) {
-  if (!c) return MOE_ERR_ARG;
-  if (c->T < 1 || c->d < 1 || c->E < 1 || c->d_ff < 1 || c->k < 1 || c->k > c->E) return MOE_ERR_ARG;
-  if (!(c->capacity_factor > 0.f) || !isfinite(c->capacity_factor)) return MOE_ERR_ARG;
-  if (c->min_capacity < 1) return MOE_ERR_ARG;
-  if (c->gate_mode != MOE_GATE_TOPK_SOFTMAX && c->gate_mode != MOE_GATE_SWITCH) return MOE_ERR_ARG;
-  if (c->gate_mode == MOE_GATE_SWITCH && c->k != 1) return MOE_ERR_ARG;
-  if (c->act_dtype != MOE_F32 && c->act_dtype != MOE_BF16) return MOE_ERR_ARG;
-  if ((long long)c->T * c->k > 0x7fffffffLL || (long long)c->T * c->E > 0x7fffffffLL)
-    return MOE_ERR_UNSUPPORTED;
-  if (c->E > 1024 || c->k > 16) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-static bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-// Required pointers must be non-null; every given pointer 16-byte aligned.
-#define MOE_REQ(p)                                      \
-  do {                                                  \
-    if (!(p) || !aligned((p), 16)) return MOE_ERR_ARG;  \
-  } while (0)
-#define MOE_OPT(p)                                      \
-  do {                                                  \
-    if ((p) && !aligned((p), 16)) return MOE_ERR_ARG;   \
-  } while (0)
-#define MOE_CUDA(call)                                  \
-  do {                                                  \
-    if ((call) != cudaSuccess) return MOE_ERR_CUDA;     \
-  } while (0)
 
 static int gate_impl(const moe_config &c, const void *x, const float *Wg, const float *Wn,
                      const float *noise, const float *bias, int32_t *idx, float *gate, float *thr,
