@@ -7,6 +7,8 @@
 
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 namespace moe {
 
 // ----------------------------------------------------------------------------- activations
@@ -100,24 +102,48 @@ struct GatedSimt {
   float *hf, *dU, *dP1, *dP3, *dX, *dgpart;  // backward: fp32 rows
   void *dW1, *dW3, *dW2;                     // act_dtype
   DeviceStatus *st;
-  const uint8_t *a8 = nullptr, *sa = nullptr;  // 8 bits: rows and their scales [K / 128][max_rows]
-  const uint8_t *s1 = nullptr, *s3 = nullptr, *s2 = nullptr;  // the weights' scales
 };
-cudaError_t launch_gated_simt_fp8(const GatedSimt &p, int layer, cudaStream_t s);
 cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s);
 cudaError_t launch_gated_simt_backward(const GatedSimt &p, cudaStream_t s);
 int gated_simt_dg_blocks(const moe_config &c, int max_rows);  // columns of dgpart [rows, ..]
+
+// k_ffn_tc.cu: the gated first layer on the tensor cores (ffn_tc_supported
+// layers; the second is launch_ffn_layer2). Buffers of max_rows packed rows;
+// pre1 and pre3 may be null.
+cudaError_t launch_gated_tc_layer1(const moe_config &c, int C, int activation, long long max_rows,
+                                   const void *xbuf, const int32_t *offset, const void *W1,
+                                   const void *b1, const void *W3, const void *b3, void *hbuf,
+                                   void *pre1, void *pre3, DeviceStatus *st, cudaStream_t s);
 
 // k_fp8.cu: to 8 bits.
 // Weights [E, K, N] (bf16 or fp32) to q [E, N, Kp] (Kp = K rounded up to 128,
 // zeros past K) and scale [E, ceil(N/128), Kp/128].
 cudaError_t launch_fp8_weights(bool bf16, int E, int K, int N, const void *W, uint8_t *q,
                                uint8_t *scale, DeviceStatus *st, cudaStream_t s);
-// Packed rows r < *count to q [max_rows, Kp] and scale [Kp/128][max_rows]. With
-// row_token, row r is that of token row_token[r] / k of src, else row r.
+// Packed rows r < *count to q [max_rows, Kp] and scale [Kp/128][max_rows]; row r
+// is that of token row_token[r] / k of src.
 cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,
                             const int32_t *row_token, const void *src, uint8_t *q,
                             uint8_t *scale, cudaStream_t s);
+
+// k_fp8_tc.cu: one of the 8-bit layer's products on the tensor cores, any
+// widths. Layer 1: a8 = x rows, W and W3 -> h8 [max_rows, d_ff rounded up to
+// 128], sh [ceil(d_ff/128)][max_rows]; layer 2: a8 = h8, W -> z [max_rows, d] in
+// fp32, or bf16 (d a multiple of 8). sa: the rows' scales [K / 128][max_rows].
+struct Fp8Layer {
+  moe_config c;
+  int layer, activation, max_rows;
+  const int32_t *offset;
+  const float *row_gate;
+  const uint8_t *a8, *sa, *W, *sb, *W3, *sb3;
+  const void *bias, *bias3;
+  uint8_t *h8, *sh;
+  void *z;
+  bool z_bf16;
+  DeviceStatus *st;
+};
+bool fp8_tc_supported();
+cudaError_t launch_fp8_tc(const Fp8Layer &q, cudaStream_t s);
 
 // k_gated.cu: what surrounds the products of the backward.
 // dgate [T,k] = sum of a kept choice's dgpart row plus <dy, b2>; 0 for the others.

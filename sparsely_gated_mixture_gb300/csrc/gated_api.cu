@@ -52,24 +52,37 @@ static GatedRoute gated_route(const moe_config &c, GatedTake &take) {
   return L;
 }
 
+// The products run on the tensor cores for bf16 layers whose widths are
+// multiples of 64, else on the CUDA cores.
+static bool gated_tc_shape(const moe_config &c) {
+  return c.act_dtype == MOE_BF16 && c.d % 64 == 0 && c.d_ff % 64 == 0;
+}
+// The experts' outputs in bf16 before the combine, where that reads 16 bytes
+// at a time: half the bytes of moe_expert_ffn's fp32 rows, one more rounding a
+// term, as in moe_forward.
+static bool gated_z_bf16(const moe_config &c) { return gated_tc_shape(c) && c.k <= 4; }
+
 struct GatedLayout {
   GatedRoute r;
-  size_t h, z, total;
+  size_t xbuf, h, z, total;
 };
 static GatedLayout gated_layout(const moe_config &c) {
   GatedLayout L{};
   GatedTake take;
   const size_t R = (size_t)gated_max_rows(c);
   L.r = gated_route(c, take);
+  L.xbuf = take(gated_tc_shape(c) ? R * c.d * 2 : 0);
   L.h = take(R * c.d_ff * elem_bytes(c.act_dtype));
-  L.z = take(R * c.d * 4);
+  L.z = take(R * c.d * (gated_z_bf16(c) ? 2 : 4));
   L.total = take.off;
   return L;
 }
 
+static bool gated_fp8_z_bf16(const moe_config &c) { return c.d % 8 == 0 && c.k <= 4; }
+
 struct GatedFp8Layout {
   GatedRoute r;
-  size_t x8, sx, h, h8, sh, z, total;
+  size_t x8, sx, h8, sh, z, total;
 };
 static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
   GatedFp8Layout L{};
@@ -79,32 +92,41 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
   L.r = gated_route(c, take);
   L.x8 = take(R * db * kFp8Block);
   L.sx = take(R * db);
-  L.h = take(R * c.d_ff * 2);
   L.h8 = take(R * fb * kFp8Block);
   L.sh = take(R * fb);
-  L.z = take(R * c.d * 4);
+  L.z = take(R * c.d * (gated_fp8_z_bf16(c) ? 2 : 4));
   L.total = take.off;
   return L;
 }
 
+// Tensor cores: xbuf and h are packed rows (64 more than there can be, for the
+// zeroed tail that the weight gradients read), dY, dU, dP1, dP3 and dX rows of
+// padded blocks (offsets poff). CUDA cores: fp32 packed rows, no xbuf and dY.
 struct GatedBwdLayout {
   GatedRoute r;
-  size_t h, dU, dP1, dP3, dX, dgpart, cpart, total;
+  size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, cpart, total;
+  long long P_max;
   int dg_blocks, chunks;
 };
 static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   GatedBwdLayout L{};
   GatedTake take;
+  const bool tc = gated_tc_shape(c);
   const size_t R = (size_t)gated_max_rows(c), d = c.d, F = c.d_ff;
+  L.P_max = (long long)R + (tc ? (long long)kBwdRowPad * c.E : 0);
+  const size_t P = (size_t)L.P_max, eb = tc ? 2 : 4;
   L.r = gated_route(c, take);
-  L.dg_blocks = gated_simt_dg_blocks(c, (int)R);
+  L.dg_blocks = tc ? 2 * ((c.d_ff + 255) / 256) : gated_simt_dg_blocks(c, (int)R);
   L.chunks = colsum_chunks(host_capacity(c));
-  L.h = take(R * F * 4);
-  L.dU = take(R * d * 4);
-  L.dP1 = take(R * F * 4);
-  L.dP3 = take(R * F * 4);
-  L.dX = take(R * d * 4);
-  L.dgpart = take(R * L.dg_blocks * 4);
+  L.poff = take(((size_t)c.E + 1) * 4);
+  L.xbuf = take(tc ? (R + kBwdRowPad) * d * 2 : 0);
+  L.h = take((R + (tc ? kBwdRowPad : 0)) * F * eb);
+  L.dY = take(tc ? P * d * 2 : 0);
+  L.dU = take(P * d * eb);
+  L.dP1 = take(P * F * eb);
+  L.dP3 = take(P * F * eb);
+  L.dX = take(P * d * 4);
+  L.dgpart = take(P * L.dg_blocks * 4);
   L.cpart = take((size_t)L.chunks * c.E * (d + F) * 4);
   L.total = take.off;
   return L;
@@ -127,6 +149,66 @@ static int gated_slots(const moe_config &c, const GatedRoute &L, const int32_t *
 static GatedRows gated_rows(const GatedRoute &L, void *ws) {
   return {ws_at<int32_t>(ws, L.offset), ws_at<int32_t>(ws, L.mtiles),
           ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate)};
+}
+
+// The backward's products on the tensor cores, dx included.
+struct GatedBwdCall {
+  int activation;
+  const void *x;
+  const int32_t *idx;
+  const void *pre1, *pre3, *W1, *W3, *W2, *b2, *dy;
+  void *dx;
+  float *dgate;
+  void *dW1, *db1, *dW3, *db3, *dW2, *db2;
+};
+static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const GatedBwdCall &q,
+                             void *ws, cudaStream_t s) {
+  DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
+  const GatedRows rows = gated_rows(L.r, ws);
+  const int32_t *pos = ws_at<int32_t>(ws, L.r.pos);
+  const uint8_t *keep = ws_at<uint8_t>(ws, L.r.keep);
+  int32_t *poff = ws_at<int32_t>(ws, L.poff);
+  void *xbuf = ws_at<char>(ws, L.xbuf), *h = ws_at<char>(ws, L.h);
+  void *dY = ws_at<char>(ws, L.dY), *dU = ws_at<char>(ws, L.dU);
+  void *dP1 = ws_at<char>(ws, L.dP1), *dP3 = ws_at<char>(ws, L.dP3);
+  float *dX = ws_at<float>(ws, L.dX), *dgpart = ws_at<float>(ws, L.dgpart);
+  float *cpart = ws_at<float>(ws, L.cpart);
+  const long long R = gated_max_rows(c), cap = host_capacity(c);
+  MOE_CUDA(launch_bwd_offsets(c.E, rows.offset, poff, s));
+  MOE_CUDA(launch_gather(c, q.x, rows.offset, rows.row_token, xbuf, st, s));
+  MOE_CUDA(launch_bwd_tail_zero(c, rows.offset, xbuf, h, s));
+  MOE_CUDA(launch_bwd_gather(c, L.P_max, rows.offset, poff, rows.row_token, rows.row_gate, q.dy,
+                             dY, dU, s));
+  BwdGemm g{3, c.d, c.d_ff, 0, c.E, L.P_max, 0, 0, dY, q.W2, rows.offset, poff, rows.row_gate,
+            nullptr, dP1, dgpart, false};
+  g.activation = q.activation;
+  g.pre1 = q.pre1;
+  g.pre3 = q.pre3;
+  g.out3 = dP3;
+  g.h = h;
+  g.h_rows = R;
+  MOE_CUDA(launch_bwd_gemm(g, st, s));
+  MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
+                              s));
+  MOE_CUDA(launch_bwd_colsum(c, L.chunks, rows.offset, poff, nullptr, dU, dP1, false, cpart, q.db2,
+                             q.db1, true, s));
+  MOE_CUDA(launch_bwd_colsum(c, L.chunks, rows.offset, poff, nullptr, dU, dP3, false, cpart,
+                             nullptr, q.db3, true, s));
+  BwdGemm gx{4, c.d_ff, c.d, 0, c.E, L.P_max, 0, 0, dP1, q.W1, rows.offset, poff, nullptr, nullptr,
+             dX, nullptr, false};
+  gx.A3 = dP3;
+  gx.B3 = q.W3;
+  MOE_CUDA(launch_bwd_gemm(gx, st, s));
+  const auto wgrad = [&](const void *A, int M, const void *B, int N, void *out) {
+    const BwdGemm w{2, 0, N, M, c.E, R, L.P_max, cap, A, B, rows.offset, poff, nullptr, nullptr,
+                    out, nullptr, true};
+    return launch_bwd_gemm(w, st, s);
+  };
+  MOE_CUDA(wgrad(h, c.d_ff, dU, c.d, q.dW2));
+  MOE_CUDA(wgrad(xbuf, c.d, dP1, c.d_ff, q.dW1));
+  MOE_CUDA(wgrad(xbuf, c.d, dP3, c.d_ff, q.dW3));
+  MOE_CUDA(launch_bwd_dx(c, q.idx, pos, keep, poff, dX, nullptr, q.dy, q.dx, s));
+  return MOE_OK;
 }
 
 static bool known_activation(int a) {
@@ -168,6 +250,7 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
   if ((pre1 == nullptr) != (pre3 == nullptr)) return MOE_ERR_ARG;
   const moe_config &c = *cfg;
+  if (gated_tc_shape(c) && !ffn_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
   const GatedLayout L = gated_layout(c);
   cudaStream_t s = (cudaStream_t)stream;
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
@@ -175,17 +258,31 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
   r = gated_slots(c, L.r, expert_idx, gate, ps, kp, ws, s);
   if (r != MOE_OK) return r;
+  const long long R = gated_max_rows(c);
+  void *z = ws_at<char>(ws, L.z);
+  if (gated_tc_shape(c)) {
+    const GatedRows rows = gated_rows(L.r, ws);
+    void *xbuf = ws_at<char>(ws, L.xbuf), *h = ws_at<char>(ws, L.h);
+    const int C = host_capacity(c);
+    const bool zb = gated_z_bf16(c);
+    MOE_CUDA(launch_gather(c, x, rows.offset, rows.row_token, xbuf, st, s));
+    MOE_CUDA(launch_gated_tc_layer1(c, C, activation, R, xbuf, rows.offset, W1, b1, W3, b3, h,
+                                    pre1, pre3, st, s));
+    MOE_CUDA(launch_ffn_layer2(c, C, R, h, rows.offset, rows.row_gate, W2, b2, z, zb, st, s));
+    MOE_CUDA(launch_combine(c, x, z, zb, ps, kp, expert_idx, rows.offset, y, st, s));
+    return MOE_OK;
+  }
   GatedSimt p{};
   p.c = c;
   p.activation = activation;
-  p.max_rows = (int)gated_max_rows(c);
+  p.max_rows = (int)R;
   p.rows = gated_rows(L.r, ws);
   p.x = x;
   p.W1 = W1; p.b1 = b1; p.W3 = W3; p.b3 = b3; p.W2 = W2; p.b2 = b2;
   p.h = ws_at<char>(ws, L.h);
   p.pre1 = pre1;
   p.pre3 = pre3;
-  p.z = ws_at<float>(ws, L.z);
+  p.z = static_cast<float *>(z);
   p.st = st;
   MOE_CUDA(launch_gated_simt_forward(p, s));
   MOE_CUDA(launch_combine(c, x, p.z, false, ps, kp, expert_idx, p.rows.offset, y, st, s));
@@ -214,12 +311,18 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   MOE_REQ(dW1); MOE_OPT(db1); MOE_REQ(dW3); MOE_OPT(db3); MOE_REQ(dW2); MOE_OPT(db2);
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
   const moe_config &c = *cfg;
+  if (gated_tc_shape(c) && !bwd_tc_supported(c)) return MOE_ERR_UNSUPPORTED;
   const GatedBwdLayout L = gated_bwd_layout(c);
   cudaStream_t s = (cudaStream_t)stream;
   int32_t *pos = ws_at<int32_t>(ws, L.r.pos);
   uint8_t *keep = ws_at<uint8_t>(ws, L.r.keep);
   r = gated_slots(c, L.r, expert_idx, gate, pos, keep, ws, s);
   if (r != MOE_OK) return r;
+  if (gated_tc_shape(c)) {
+    const GatedBwdCall q{activation, x, expert_idx, pre1, pre3, W1, W3, W2, b2, dy, dx,
+                         dgate, dW1, db1, dW3, db3, dW2, db2};
+    return gated_backward_tc(c, L, q, ws, s);
+  }
   GatedSimt p{};
   p.c = c;
   p.activation = activation;
@@ -301,6 +404,7 @@ int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void 
   MOE_OPT(pos); MOE_OPT(keep);
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
   const moe_config &c = *cfg;
+  if (!fp8_tc_supported()) return MOE_ERR_UNSUPPORTED;
   const GatedFp8Layout L = gated_fp8_layout(c);
   cudaStream_t s = (cudaStream_t)stream;
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
@@ -308,27 +412,18 @@ int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void 
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
   r = gated_slots(c, L.r, expert_idx, gate, ps, kp, ws, s);
   if (r != MOE_OK) return r;
-  GatedSimt p{};
-  p.c = c;
-  p.activation = activation;
-  p.max_rows = (int)gated_max_rows(c);
-  p.rows = gated_rows(L.r, ws);
-  p.x = x;
-  p.W1 = W1; p.b1 = b1; p.W3 = W3; p.b3 = b3; p.W2 = W2; p.b2 = b2;
-  p.s1 = s1; p.s3 = s3; p.s2 = s2;
-  p.h = ws_at<char>(ws, L.h);
-  p.z = ws_at<float>(ws, L.z);
-  p.st = st;
+  const GatedRows rows = gated_rows(L.r, ws);
+  const int R = (int)gated_max_rows(c);
   uint8_t *x8 = ws_at<uint8_t>(ws, L.x8), *sx = ws_at<uint8_t>(ws, L.sx);
   uint8_t *h8 = ws_at<uint8_t>(ws, L.h8), *sh = ws_at<uint8_t>(ws, L.sh);
-  const int32_t *count = p.rows.offset + c.E;
-  MOE_CUDA(launch_fp8_rows(p.max_rows, c.d, c.k, count, p.rows.row_token, x, x8, sx, s));
-  p.a8 = x8; p.sa = sx;
-  MOE_CUDA(launch_gated_simt_fp8(p, 1, s));
-  MOE_CUDA(launch_fp8_rows(p.max_rows, c.d_ff, c.k, count, nullptr, p.h, h8, sh, s));
-  p.a8 = h8; p.sa = sh;
-  MOE_CUDA(launch_gated_simt_fp8(p, 2, s));
-  MOE_CUDA(launch_combine(c, x, p.z, false, ps, kp, expert_idx, p.rows.offset, y, st, s));
+  void *z = ws_at<char>(ws, L.z);
+  const bool zb = gated_fp8_z_bf16(c);
+  MOE_CUDA(launch_fp8_rows(R, c.d, c.k, rows.offset + c.E, rows.row_token, x, x8, sx, s));
+  MOE_CUDA(launch_fp8_tc({c, 1, activation, R, rows.offset, nullptr, x8, sx, W1, s1, W3, s3, b1,
+                          b3, h8, sh, nullptr, false, st}, s));
+  MOE_CUDA(launch_fp8_tc({c, 2, activation, R, rows.offset, rows.row_gate, h8, sh, W2, s2, nullptr,
+                          nullptr, b2, nullptr, nullptr, nullptr, z, zb, st}, s));
+  MOE_CUDA(launch_combine(c, x, z, zb, ps, kp, expert_idx, rows.offset, y, st, s));
   return MOE_OK;
 }
 

@@ -10,6 +10,12 @@
 //   dgrad through W1 (mode 1):  dX_rows = dpre_rows W1[e]^T   [rows, d]   (fp32)
 //   weight gradient  (mode 2):  dW[e] = A_rows^T B_rows       [M, N]      (fp32)
 //       dW2: A = h rows, B = g * dY rows;  dW1: A = x rows, B = dpre rows
+//   gated dgrad through W2 (mode 3): D as in mode 0; with the kept
+//       pre-activations p1, p3 of the row, a = act(p1), h = a * p3:
+//       dP1 = g D p3 act'(p1), dP3 = g D a (bf16, padded rows), h (bf16, packed
+//       rows: the weight gradient's operand) and the dgate partial <D, h>
+//   gated dgrad (mode 4): dX_rows = dP1 W1[e]^T + dP3 W3[e]^T, as mode 1 with a
+//       reduction that runs over both pairs
 //
 // The backward's own row buffers (dY, g*dY, dpre, dX) give each expert a
 // block of rows padded to a multiple of 64 (at least 64), pad rows zero, at
@@ -31,6 +37,7 @@
 #include "moe_internal.cuh"
 #include "tc_ptx.cuh"
 #include "checkpoint.cuh"
+#include "gated.cuh"
 
 #include <stdlib.h>
 
@@ -42,8 +49,6 @@ namespace {
 constexpr int BM = kTcBM;  // 128 rows (TMEM lanes)
 constexpr int BN = 256;    // accumulator columns per tile
 constexpr int BK = 64;     // K per stage
-constexpr int STAGES = 4;
-constexpr int kThreads = 192;
 constexpr int A_BYTES = BM * BK * 2;  // 16 KB
 constexpr int B_BYTES = BK * BN * 2;  // 32 KB
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
@@ -70,6 +75,34 @@ struct BParams {
   int tma_out;      // CTA-pair kernel, modes 0 and 1: 32-row groups leave by TMA store
   int snake;        // CTA-pair kernel: 1 = odd waves of tiles run K backwards, 2 = all do
 };
+
+// The gated modes' further operands.
+template <int MODE>
+struct BExtra {};
+template <>
+struct BExtra<3> {
+  CUtensorMap o3, oh;  // dP3 [padded rows, N], h [packed rows, N]: box [32, 32]
+  const __nv_bfloat16 *pre1, *pre3;  // [packed rows, N]
+  __nv_bfloat16 *dP3, *h;
+};
+template <>
+struct BExtra<4> {
+  CUtensorMap a, b;  // dP3, W3
+};
+
+// Mode 3 has the heaviest epilogue (two operands read, three written, an
+// exponential and a reciprocal an element): eight warps instead of four, each
+// with four staging tiles of 2 KB, at the price of one or two stages of the ring.
+template <int MODE>
+__host__ __device__ constexpr int epi_warps() { return MODE == 3 ? 8 : 4; }
+template <int MODE>
+__host__ __device__ constexpr int threads_of() { return 64 + 32 * epi_warps<MODE>(); }
+template <int MODE>
+__host__ __device__ constexpr int stages_of(bool pair) {
+  return pair ? (MODE == 3 ? 4 : 6) : (MODE == 3 ? 3 : 4);
+}
+constexpr int G_TILE = 32 * 32 / 2;             // a staging tile of bf16, counted in floats
+constexpr int G_STG_BYTES = 8 * 4 * G_TILE * 4;  // mode 3
 
 // The CTA-pair kernel's tile ring, as in the forward expert GEMM: tile
 // indices from the even CTA's producer to the MMA issuer, both CTAs'
@@ -141,7 +174,7 @@ __device__ __forceinline__ BTile locate(const BParams &p, const int *start, int 
     const int local = tile - start[t.e];
     t.nb = local / mt;
     t.mb = local - t.nb * mt;
-    t.num_kb = p.K / BK;
+    t.num_kb = (MODE == 4 ? 2 : 1) * (p.K / BK);
   } else {
     t.num_kb = t.prows / BK;
   }
@@ -175,7 +208,7 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
   // as zero), mode 1 the real rows (every padded row through TMA), mode 2 the
   // output rows m < M.
   const bool valid = MODE == 0 ? m < t.prows
-                     : MODE == 1 ? (tma || m < t.rows)
+                     : MODE != 2 ? (tma || m < t.rows)
                                  : m < p.M;
   const bool real = m < t.rows;
   const size_t pr = (size_t)t.prow0 + m;
@@ -268,7 +301,7 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
           o[w] = make_uint4(packed[4 * w], packed[4 * w + 1], packed[4 * w + 2],
                             packed[4 * w + 3]);
       } else {
-        float *o = MODE == 1
+        float *o = MODE != 2
                        ? static_cast<float *>(p.out) + pr * p.N + n
                        : static_cast<float *>(p.out) + ((size_t)t.e * p.M + m) * p.N + n;
 #pragma unroll
@@ -282,19 +315,127 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
   if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)(MODE == 2 ? m : (long long)pr));
 }
 
+// Mode 3's epilogue for one warp: its 32 rows and half of the tile's columns
+// (half 0 or 1), 32 at a time. The pre-activations of the next 32 columns are
+// fetched while these are worked on, four lanes to a row (a lane to a row would
+// touch 32 lines an instruction), and change to a lane's own row through the
+// warp's staging tiles 0 and 1; the outputs leave through tiles 2 and 3.
+// Warp-collective.
+template <int ACT>
+__device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3> &ex,
+                                               const BTile &t, int m0, int half,
+                                               uint32_t lane_addr, float *stg,
+                                               const CUtensorMap *tmO, uint32_t &cnt) {
+  const int lane = threadIdx.x & 31;
+  const int m = m0 + lane;
+  if (m0 >= t.prows) return;  // padded rows come in 64s: all of the warp's or none
+  const bool real = m < t.rows, tma = p.tma_out, whole = tma && m0 + 32 <= t.rows;
+  const size_t pr = (size_t)t.prow0 + m;
+  const int q0 = p.offset[t.e] + m0;  // packed row of the warp's first
+  const float g = real ? p.row_gate[q0 + lane] : 0.f;
+  float part = 0.f;
+  bool bad = false;
+  const int sub = lane >> 2, quarter = lane & 3;
+  uint4 pre[2][4];
+  const auto fetch = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = sub + 8 * i;
+      const bool ok = m0 + row < t.rows && n < p.N;
+      const size_t at = (size_t)(q0 + row) * p.N + n + quarter * 8;
+      pre[0][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre1 + at) : make_uint4(0, 0, 0, 0);
+      pre[1][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre3 + at) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const int c0 = half * (BN / 64);
+  fetch(t.nb * BN + c0 * 32);
+  const int x = (lane >> 1) & 3;
+#pragma unroll 1
+  for (int c = c0; c < c0 + BN / 64; ++c) {
+    const int n = t.nb * BN + c * 32;
+    if (n >= p.N) break;
+    __syncwarp();  // the last columns' rows have been read
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = sub + 8 * i;
+        reinterpret_cast<uint4 *>(stg + w * G_TILE)[row * 4 + (quarter ^ ((row >> 1) & 3))] =
+            pre[w][i];
+      }
+    __syncwarp();
+    if (c + 1 < c0 + BN / 64) fetch(n + 32);
+    uint32_t v[32];
+    tmem_ld32(lane_addr + (uint32_t)(c * 32), v);
+    uint32_t out[3][16];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint4 u1 = reinterpret_cast<const uint4 *>(stg)[lane * 4 + (w ^ x)];
+      const uint4 u3 = reinterpret_cast<const uint4 *>(stg + G_TILE)[lane * 4 + (w ^ x)];
+      const uint32_t a1[4] = {u1.x, u1.y, u1.z, u1.w}, a3[4] = {u3.x, u3.y, u3.z, u3.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float d1[2], d3[2], h[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p1 = __uint_as_float(i ? a1[j] & 0xffff0000u : a1[j] << 16);
+          const float p3 = __uint_as_float(i ? a3[j] & 0xffff0000u : a3[j] << 16);
+          const float D = __uint_as_float(v[8 * w + 2 * j + i]), gD = g * D;
+          float a, s;
+          gated_act_slope<false, ACT>(p1, a, s);
+          h[i] = a * p3;
+          part = fmaf(D, h[i], part);
+          d1[i] = real ? gD * (p3 * s) : 0.f;
+          d3[i] = real ? gD * a : 0.f;
+          bad |= !isfinite(d1[i] + d3[i]);
+        }
+        __nv_bfloat162 b = __floats2bfloat162_rn(d1[0], d1[1]);
+        out[0][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
+        b = __floats2bfloat162_rn(d3[0], d3[1]);
+        out[1][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
+        b = __floats2bfloat162_rn(h[0], h[1]);
+        out[2][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
+      }
+    }
+    __nv_bfloat16 *const to[3] = {static_cast<__nv_bfloat16 *>(p.out) + pr * p.N + n,
+                                  ex.dP3 + pr * p.N + n,
+                                  ex.h + (size_t)(q0 + lane) * p.N + n};
+    const CUtensorMap *const maps[3] = {tmO, &ex.o3, &ex.oh};
+#pragma unroll
+    for (int o = 0; o < 3; ++o) {
+      if (o < 2 ? tma : whole) {
+        stage_store_bf16(maps[o], stg + (2 + (cnt & 1u)) * G_TILE, out[o], n,
+                         o < 2 ? t.prow0 + m0 : q0);
+        ++cnt;
+      } else if (o < 2 || real) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          reinterpret_cast<uint4 *>(to[o])[w] = make_uint4(out[o][4 * w], out[o][4 * w + 1],
+                                                           out[o][4 * w + 2], out[o][4 * w + 3]);
+      }
+    }
+  }
+  p.dgpart[(pr * p.n_blocks + t.nb) * 2 + half] = real ? part : 0.f;
+  if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)pr);
+}
+
 // OB: in mode 2 the weight gradient is written in bf16, in mode 0 the hidden
-// rows are read in 8 bits (a checkpoint's).
-template <int MODE, bool OB = false>
-__global__ void __launch_bounds__(kThreads, 1)
+// rows are read in 8 bits (a checkpoint's). ACT: mode 3's activation.
+template <int MODE, bool OB = false, int ACT = 0>
+__global__ void __launch_bounds__(threads_of<MODE>(), 1)
 k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+         const __grid_constant__ CUtensorMap tmO, const __grid_constant__ BExtra<MODE> ex,
          const BParams p) {
+  constexpr int STAGES = stages_of<MODE>(false);
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   uint8_t *sA = smem;
   uint8_t *sB = smem + STAGES * A_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + STAGES * B_BYTES);
+  float *stg_all = reinterpret_cast<float *>(sB + STAGES * B_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + STAGES * B_BYTES +
+                                                (MODE == 3 ? G_STG_BYTES : 0));
   uint64_t *full = bars, *empty = bars + STAGES;
   uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -310,7 +451,7 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);
+      mbar_init(&acc_empty[b], epi_warps<MODE>());
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -365,8 +506,17 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           }
           mbar_expect_tx(&full[s], STAGE_BYTES);
           if (MODE != 2) {
-            tma_load_2d(sA + s * A_BYTES, &tmA, &full[s], kb * BK, t.prow0 + t.mb * BM);
-            tma_load_2d(sB + s * B_BYTES, &tmB, &full[s], kb * BK, t.e * p.N + t.nb * BN);
+            const CUtensorMap *ta = &tmA, *tb = &tmB;
+            int kx = kb * BK;
+            if constexpr (MODE == 4) {
+              if (kx >= p.K) {  // the second pair
+                ta = &ex.a;
+                tb = &ex.b;
+                kx -= p.K;
+              }
+            }
+            tma_load_2d(sA + s * A_BYTES, ta, &full[s], kx, t.prow0 + t.mb * BM);
+            tma_load_2d(sB + s * B_BYTES, tb, &full[s], kx, t.e * p.N + t.nb * BN);
           } else {
             const int arow = p.offset[t.e] + kb * BK, brow = t.prow0 + kb * BK;
 #pragma unroll
@@ -434,6 +584,7 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     // ----------------------------------------------------------------- epilogue
     const int quad = warp & 3;
     const int r_in_tile = quad * 32 + lane;
+    [[maybe_unused]] uint32_t stg_cnt = 0;
     int local = 0;
     for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x, ++local) {
       const BTile t = locate<MODE>(p, tile_start, tile);
@@ -444,12 +595,18 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
       if (!ready) break;
       tc_fence_after();
       const int m = t.mb * BM + r_in_tile;
-      epilogue_rows<MODE, OB>(p, t, m, tmem_base + ((uint32_t)(quad * 32) << 16) +
-                                           (uint32_t)(buf * BN));
+      const uint32_t lane_addr =
+          tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
+      if constexpr (MODE == 3)
+        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr,
+                            stg_all + (warp - 2) * 4 * G_TILE, &tmO, stg_cnt);
+      else
+        epilogue_rows<MODE, OB>(p, t, m, lane_addr);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
     }
+    if (MODE == 3 && lane == 0) bulk_wait_all();  // this warp's TMA stores are complete
     pdl_trigger();
   }
   tc_fence_before();
@@ -472,7 +629,6 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
 // barriers, commits arrive on both CTAs' barriers, and both CTAs' epilogues
 // arrive on the even CTA's "accumulator empty" barriers (the forward's pair
 // kernel, same protocol).
-constexpr int P_STAGES = 6;
 constexpr int P_A_BYTES = BM * BK * 2;          // 16 KB
 constexpr int P_B_BYTES = BK * (BN / 2) * 2;    // 16 KB
 constexpr int P_STAGE_BYTES = P_A_BYTES + P_B_BYTES;
@@ -527,7 +683,7 @@ __device__ __forceinline__ BTile locate_pair(const BParams &p, const int *start,
     const int local = tile - start[t.e];
     t.nb = local / mt;
     t.mb = local - t.nb * mt;
-    t.num_kb = p.K / BK;
+    t.num_kb = (MODE == 4 ? 2 : 1) * (p.K / BK);
   } else {
     t.num_kb = t.prows / BK;
   }
@@ -598,10 +754,13 @@ __device__ __forceinline__ void epilogue_wgrad_tma(const BParams &p, const BTile
 // tmO: mode 2's output dW as [E, M, N] fp32, box [1, 32, 32], 128-byte
 // swizzle; modes 0 and 1: the output [padded rows, N] (bf16 / fp32), box [32,
 // 32], when p.tma_out is set.
-template <int MODE, bool OB = false>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int MODE, bool OB = false, int ACT = 0>
+__global__ void __launch_bounds__(threads_of<MODE>(), 1)
 k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmO, const BParams p) {
+              const __grid_constant__ CUtensorMap tmO, const __grid_constant__ BExtra<MODE> ex,
+              const BParams p) {
+  constexpr int P_STAGES = stages_of<MODE>(true);
+  constexpr int kStgBytes = MODE == 3 ? G_STG_BYTES : P_STG_BYTES;
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -609,7 +768,7 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   uint8_t *sA = smem;
   uint8_t *sB = smem + P_STAGES * P_A_BYTES;
   float *stg_all = reinterpret_cast<float *>(sB + P_STAGES * P_B_BYTES);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + P_STAGES * P_B_BYTES + P_STG_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + P_STAGES * P_B_BYTES + kStgBytes);
   uint64_t *full = bars, *empty = bars + P_STAGES;
   uint64_t *acc_full = bars + 2 * P_STAGES, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
   uint64_t *tfull = drain + 1, *tempty = tfull + kRing;
@@ -630,11 +789,11 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);
+      mbar_init(&acc_empty[b], 2 * epi_warps<MODE>());
     }
     for (int r = 0; r < kRing; ++r) {
       mbar_init(&tfull[r], 1);
-      mbar_init(&tempty[r], kRingConsumers);
+      mbar_init(&tempty[r], kRingConsumers + 2 * (epi_warps<MODE>() - 4));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -732,9 +891,18 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           const uint32_t full_leader = mapa(smem_u32(&full[s]), 0);
           if (leader) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
           if (MODE != 2) {
-            tma_load_2d_pair(sA + s * P_A_BYTES, &tmA, full_leader, kx,
+            const CUtensorMap *ta = &tmA, *tb = &tmB;
+            int kk = kx;
+            if constexpr (MODE == 4) {
+              if (kx >= p.K) {  // the second pair
+                ta = &ex.a;
+                tb = &ex.b;
+                kk -= p.K;
+              }
+            }
+            tma_load_2d_pair(sA + s * P_A_BYTES, ta, full_leader, kk,
                              t.prow0 + t.mb * 2 * BM + (int)rank * BM);
-            tma_load_2d_pair(sB + s * P_B_BYTES, &tmB, full_leader, kx,
+            tma_load_2d_pair(sB + s * P_B_BYTES, tb, full_leader, kk,
                              t.e * p.N + t.nb * BN + (int)rank * (BN / 2));
           } else {
             const int arow = p.offset[t.e] + kx, brow = t.prow0 + kx;
@@ -821,7 +989,8 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int r_in_tile = quad * 32 + lane;
     const uint32_t acc_empty_leader0 = mapa(smem_u32(&acc_empty[0]), 0);
     const uint32_t acc_empty_leader1 = mapa(smem_u32(&acc_empty[1]), 0);
-    float *stg = stg_all + (size_t)(warp - 2) * 2 * P_STG_TILE;  // this warp's two tiles
+    // This warp's two tiles (mode 3: four smaller ones).
+    float *stg = stg_all + (size_t)(warp - 2) * (MODE == 3 ? 4 * G_TILE : 2 * P_STG_TILE);
     uint32_t stg_cnt = 0;
     for (int local = 0;; ++local) {
       const int slot = local % kRing;
@@ -850,6 +1019,8 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
       if constexpr (MODE == 2)
         epilogue_wgrad_tma<OB>(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
+      else if constexpr (MODE == 3)
+        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr, stg, &tmO, stg_cnt);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
       tc_fence_before();
@@ -869,14 +1040,18 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
   }
 }
 
-constexpr size_t bwd_smem_bytes_pair(int E, int mode) {
-  (void)mode;
-  return 1024 + (size_t)P_STAGES * P_STAGE_BYTES + P_STG_BYTES +
-         (2 * P_STAGES + 5 + 2 * kRing) * 8 + 8 + (size_t)kRing * 4 + (size_t)(E + 1) * 4;
+template <int MODE>
+constexpr size_t bwd_smem_bytes_pair(int E) {
+  constexpr int st = stages_of<MODE>(true);
+  return 1024 + (size_t)st * P_STAGE_BYTES + (MODE == 3 ? G_STG_BYTES : P_STG_BYTES) +
+         (2 * st + 5 + 2 * kRing) * 8 + 8 + (size_t)kRing * 4 + (size_t)(E + 1) * 4;
 }
 
+template <int MODE>
 constexpr size_t bwd_smem_bytes(int E) {
-  return 1024 + (size_t)STAGES * STAGE_BYTES + (2 * STAGES + 5) * 8 + 8 + (size_t)(E + 1) * 4;
+  constexpr int st = stages_of<MODE>(false);
+  return 1024 + (size_t)st * STAGE_BYTES + (MODE == 3 ? G_STG_BYTES : 0) + (2 * st + 5) * 8 + 8 +
+         (size_t)(E + 1) * 4;
 }
 
 cudaLaunchAttribute cluster2_attr() {
@@ -902,7 +1077,7 @@ int pair_clusters_bwd(size_t smem) {
     if (keys[i] == smem) return vals[i];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (sm_count() / 2));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of<MODE>());
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1] = {cluster2_attr()};
   cfg.attrs = attr;
@@ -921,15 +1096,16 @@ int pair_clusters_bwd(size_t smem) {
   return n;
 }
 
-template <int MODE, bool OB = false>
+template <int MODE, bool OB = false, int ACT = 0>
 cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
-                             const BParams &p, int clusters, cudaStream_t s) {
-  const size_t smem = bwd_smem_bytes_pair(p.E, MODE);
-  cudaError_t err = allow_smem(k_bwd_tc_pair<MODE, OB>);
+                             const BParams &p, int clusters, cudaStream_t s,
+                             const BExtra<MODE> &ex = {}) {
+  const size_t smem = bwd_smem_bytes_pair<MODE>(p.E);
+  cudaError_t err = allow_smem(k_bwd_tc_pair<MODE, OB, ACT>);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of<MODE>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {cluster2_attr(), {}};
@@ -937,16 +1113,18 @@ cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const C
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled(kPdlGemm) ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_bwd_tc_pair<MODE, OB>, a, b, o, p);
+  return cudaLaunchKernelEx(&cfg, k_bwd_tc_pair<MODE, OB, ACT>, a, b, o, ex, p);
 }
 
-template <int MODE, bool OB = false>
-cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p,
-                        cudaStream_t s) {
-  const size_t smem = bwd_smem_bytes(p.E);
-  cudaError_t err = allow_smem(k_bwd_tc<MODE, OB>);
+// o: mode 3's output map (unused otherwise).
+template <int MODE, bool OB = false, int ACT = 0>
+cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
+                        const BParams &p, cudaStream_t s, const BExtra<MODE> &ex = {}) {
+  const size_t smem = bwd_smem_bytes<MODE>(p.E);
+  cudaError_t err = allow_smem(k_bwd_tc<MODE, OB, ACT>);
   if (err != cudaSuccess) return err;
-  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB>, sm_count(), kThreads, smem, s, a, b, p);
+  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB, ACT>, sm_count(), threads_of<MODE>(), smem, s, a, b, o,
+               ex, p);
   return cudaGetLastError();
 }
 
@@ -973,7 +1151,7 @@ bool make_out_map3(CUtensorMap *m, void *base, int E, int M, int N, bool bf16) {
 
 bool bwd_tc_supported(const moe_config &c) {
   return c.act_dtype == MOE_BF16 && c.d % 64 == 0 && c.d_ff % 64 == 0 &&
-         bwd_smem_bytes(c.E) <= 227 * 1024 && encode_fn() != nullptr;
+         bwd_smem_bytes<0>(c.E) <= 227 * 1024 && encode_fn() != nullptr;
 }
 
 // MOE_BWD_TC_VARIANT=single or =pair forces one kernel (read at each call);
@@ -989,8 +1167,8 @@ static int bwd_variant() {
 template <int MODE>
 static int pick_pair(const BwdGemm &g, long long k_len, long long tiles) {
   const int force = bwd_variant();
-  if (force == 1 || bwd_smem_bytes_pair(g.E, MODE) > 227 * 1024) return 0;
-  const int clusters = pair_clusters_bwd<MODE>(bwd_smem_bytes_pair(g.E, MODE));
+  if (force == 1 || bwd_smem_bytes_pair<MODE>(g.E) > 227 * 1024) return 0;
+  const int clusters = pair_clusters_bwd<MODE>(bwd_smem_bytes_pair<MODE>(g.E));
   if (clusters <= 0) return 0;
   if (force == 2) return clusters;
   return (k_len >= 1024 && tiles >= 4LL * clusters) ? clusters : 0;
@@ -1036,24 +1214,50 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
         make_out_map3(&to, g.out, g.E, g.M, g.N, g.out_bf16))
       return g.out_bf16 ? launch_mode_pair<2, true>(ta, tb, to, p, cl, s)
                         : launch_mode_pair<2>(ta, tb, to, p, cl, s);
-    return g.out_bf16 ? launch_mode<2, true>(ta, tb, p, s) : launch_mode<2>(ta, tb, p, s);
+    return g.out_bf16 ? launch_mode<2, true>(ta, tb, ta, p, s) : launch_mode<2>(ta, tb, ta, p, s);
   }
   // A: padded rows [a_rows, K]; B: the weight as [E*N rows, K] (the pair
   // kernel loads half of a tile's 256 B rows per CTA).
   const long long tiles = (g.a_rows + 255) / 256 * nb;
-  const int cl = g.mode == 0 ? pick_pair<0>(g, g.K, tiles) : pick_pair<1>(g, g.K, tiles);
-  if (!make_map(&ta, g.A, (uint64_t)g.a_rows, (uint64_t)g.K, BM) ||
-      !make_map(&tb, g.B, (uint64_t)g.E * g.N, (uint64_t)g.K, cl > 0 ? BN / 2 : BN))
+  const int cl = g.mode == 0   ? pick_pair<0>(g, g.K, tiles)
+                 : g.mode == 1 ? pick_pair<1>(g, g.K, tiles)
+                 : g.mode == 3 ? pick_pair<3>(g, g.K, tiles)
+                               : pick_pair<4>(g, 2ll * g.K, tiles);
+  const uint64_t rows = (uint64_t)g.a_rows, wrows = (uint64_t)g.E * g.N;
+  const uint32_t box_b = cl > 0 ? BN / 2 : BN;
+  if (!make_map(&ta, g.A, rows, (uint64_t)g.K, BM) || !make_map(&tb, g.B, wrows, (uint64_t)g.K, box_b))
+    return cudaErrorInvalidValue;
+  CUtensorMap to = ta;  // unused unless p.tma_out
+  if (g.mode == 3) {
+    BExtra<3> ex{};
+    ex.pre1 = static_cast<const __nv_bfloat16 *>(g.pre1);
+    ex.pre3 = static_cast<const __nv_bfloat16 *>(g.pre3);
+    ex.dP3 = static_cast<__nv_bfloat16 *>(g.out3);
+    ex.h = static_cast<__nv_bfloat16 *>(g.h);
+    ex.o3 = ex.oh = ta;
+    p.tma_out = make_rows_map(&to, g.out, rows, (uint64_t)g.N, false) &&
+                make_rows_map(&ex.o3, g.out3, rows, (uint64_t)g.N, false) &&
+                make_rows_map(&ex.oh, g.h, (uint64_t)g.h_rows, (uint64_t)g.N, false);
+    return gated_dispatch(g.activation, [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
+      return cl > 0 ? launch_mode_pair<3, false, ACT>(ta, tb, to, p, cl, s, ex)
+                    : launch_mode<3, false, ACT>(ta, tb, to, p, s, ex);
+    });
+  }
+  BExtra<4> ex4{};
+  if (g.mode == 4 && (!make_map(&ex4.a, g.A3, rows, (uint64_t)g.K, BM) ||
+                      !make_map(&ex4.b, g.B3, wrows, (uint64_t)g.K, box_b)))
     return cudaErrorInvalidValue;
   if (cl > 0) {
-    CUtensorMap to = ta;  // unused unless p.tma_out
-    p.tma_out = make_rows_map(&to, g.out, (uint64_t)g.a_rows, (uint64_t)g.N, g.mode == 1) ? 1 : 0;
+    p.tma_out = make_rows_map(&to, g.out, rows, (uint64_t)g.N, g.mode != 0) ? 1 : 0;
+    if (g.mode == 4) return launch_mode_pair<4>(ta, tb, to, p, cl, s, ex4);
     if (g.mode == 0 && g.h8) return launch_mode_pair<0, true>(ta, tb, to, p, cl, s);
     return g.mode == 0 ? launch_mode_pair<0>(ta, tb, to, p, cl, s)
                        : launch_mode_pair<1>(ta, tb, to, p, cl, s);
   }
-  if (g.mode == 0 && g.h8) return launch_mode<0, true>(ta, tb, p, s);
-  return g.mode == 0 ? launch_mode<0>(ta, tb, p, s) : launch_mode<1>(ta, tb, p, s);
+  if (g.mode == 4) return launch_mode<4>(ta, tb, to, p, s, ex4);
+  if (g.mode == 0 && g.h8) return launch_mode<0, true>(ta, tb, to, p, s);
+  return g.mode == 0 ? launch_mode<0>(ta, tb, to, p, s) : launch_mode<1>(ta, tb, to, p, s);
 }
 
 }  // namespace moe

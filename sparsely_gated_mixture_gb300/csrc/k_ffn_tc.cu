@@ -3,6 +3,10 @@
 // Large", the expert networks E_i). Grouped GEMM over the packed rows:
 //   layer 1: hbuf[r] = ReLU(xbuf[r] W1[e] + b1[e])            (bf16 out)
 //   layer 2: zbuf[r] = row_gate[r] * (hbuf[r] W2[e] + b2[e])  (fp32 out)
+//   gated:   hbuf[r] = act(p1) * p3, p1 = xbuf[r] W1[e] + b1[e], p3 = xbuf[r] W3[e] + b3[e]
+// The gated layer's tiles are 128 columns of W1 beside the same 128 of W3, so
+// one accumulator holds p1 and p3 of the same places and its epilogue needs no
+// other tile; p1 and p3 leave as well where the caller keeps them.
 //
 // Design (one persistent CTA per SM, 6 warps):
 //   warp 0     TMA producer: A tile [128 rows x 64 K] (K-major, 128B swizzle)
@@ -21,6 +25,7 @@
 // the same time share the same weight columns in L2. Every wait is bounded:
 // past the limit the CTA records MOE_ERR_TIMEOUT, stops issuing, waits
 // (bounded) for its copies and MMAs in flight, frees TMEM and returns.
+#include "gated.cuh"
 #include "moe_internal.cuh"
 #include "tc_ptx.cuh"
 
@@ -45,6 +50,21 @@ constexpr int TMEM_COLS = 2 * BN;     // two accumulators
 // 64-byte swizzle).
 constexpr int STG_TILE = 32 * 32 / 2;  // 2 KB, counted in floats
 constexpr int STG_BYTES = 4 * 2 * STG_TILE * 4;
+
+// The kernel's LAYER.
+constexpr int kGated = 3;
+constexpr int kGatedBN = BN / 2;  // output columns of a gated tile
+
+// What the gated layer has beside the others' operands: W3, and the outputs p1
+// and p3 [rows, N] where they are kept.
+template <int LAYER>
+struct Extra {};
+template <>
+struct Extra<kGated> {
+  CUtensorMap b, o1, o3;
+  const __nv_bfloat16 *bias3;  // [E, N] or null
+  __nv_bfloat16 *pre1, *pre3;  // or null
+};
 
 struct Params {
   int K, N, E, n_blocks;
@@ -97,13 +117,66 @@ struct TileMap {
   }
 };
 
+// A gated tile's outputs of one warp's rows: 32 columns at a time of both
+// halves of the accumulator at lane_addr. Warp-collective.
+template <int ACT>
+__device__ __forceinline__ void gated_rows(const Params &p, const Extra<kGated> &ex,
+                                           const CUtensorMap &tmO, uint32_t lane_addr, int e,
+                                           int n0, size_t r, bool valid, bool tma_rows, int r0,
+                                           float *stg, int tile_floats, uint32_t &cnt) {
+  __nv_bfloat16 *const outs[3] = {ex.pre1, ex.pre3, static_cast<__nv_bfloat16 *>(p.out)};
+  const CUtensorMap *const maps[3] = {&ex.o1, &ex.o3, &tmO};
+#pragma unroll 1
+  for (int c = 0; c < kGatedBN / 32; ++c) {
+    const int n = n0 + c * 32;
+    uint32_t v1[32], v3[32];
+    tmem_ld32(lane_addr + (uint32_t)(c * 32), v1);
+    tmem_ld32(lane_addr + (uint32_t)(kGatedBN + c * 32), v3);
+    if (!valid || n >= p.N) continue;
+    uint32_t packed[3][16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      float p1[2], p3[2], h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p1[i] = __uint_as_float(v1[2 * j + i]);
+        p3[i] = __uint_as_float(v3[2 * j + i]);
+        if (p.bias) p1[i] += __bfloat162float(p.bias[(size_t)e * p.N + n + 2 * j + i]);
+        if (ex.bias3) p3[i] += __bfloat162float(ex.bias3[(size_t)e * p.N + n + 2 * j + i]);
+        h[i] = gated_act<false, ACT>(p1[i]) * p3[i];
+      }
+      __nv_bfloat162 b = __floats2bfloat162_rn(p1[0], p1[1]);
+      packed[0][j] = *reinterpret_cast<uint32_t *>(&b);
+      b = __floats2bfloat162_rn(p3[0], p3[1]);
+      packed[1][j] = *reinterpret_cast<uint32_t *>(&b);
+      b = __floats2bfloat162_rn(h[0], h[1]);
+      packed[2][j] = *reinterpret_cast<uint32_t *>(&b);
+    }
+#pragma unroll
+    for (int o = 0; o < 3; ++o) {
+      if (!outs[o]) continue;
+      if (tma_rows) {
+        stage_store_bf16(maps[o], stg + (cnt & 1u) * tile_floats, packed[o], n, r0);
+        ++cnt;
+      } else {
+        uint4 *w = reinterpret_cast<uint4 *>(outs[o] + r * p.N + n);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          w[q] = make_uint4(packed[o][4 * q], packed[o][4 * q + 1], packed[o][4 * q + 2],
+                            packed[o][4 * q + 3]);
+      }
+    }
+  }
+}
+
 // tmO: the output [rows, N] when p.tma_out is set: bf16 with a [32 rows, 32
 // columns] box, or fp32 (layer 2's Z) with a [32 rows, 16 columns] box, both
 // in the 64-byte swizzle.
-template <int LAYER>
+template <int LAYER, int ACT = 0>
 __global__ void __launch_bounds__(kThreads, 1)
 k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-         const __grid_constant__ CUtensorMap tmO, const Params p) {
+         const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Extra<LAYER> ex,
+         const Params p) {
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // 1024-byte alignment for the 128B-swizzle atoms.
@@ -181,7 +254,7 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
         int e, mb, nb, row0, rows;
         map.locate(tile, e, mb, nb, row0, rows);
         const int arow = row0 + mb * BM;
-        const int n0 = nb * BN;
+        const int n0 = nb * (LAYER == kGated ? kGatedBN : BN);
         const int brow = e * p.K;
         for (int kb = 0; kb < num_kb; ++kb, ++it) {
           const int s = it % STAGES;
@@ -193,9 +266,17 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           mbar_expect_tx(&full[s], STAGE_BYTES);
           tma_load_2d(sA + s * A_BYTES, &tmA, &full[s], kb * BK, arow);
 #pragma unroll
-          for (int j = 0; j < BN / 64; ++j)
-            tma_load_2d(sB + s * B_BYTES + j * (BK * 128), &tmB, &full[s], n0 + j * 64,
-                        brow + kb * BK);
+          for (int j = 0; j < BN / 64; ++j) {
+            const CUtensorMap *tm = &tmB;
+            int n = n0 + j * 64;
+            if constexpr (LAYER == kGated) {
+              if (j >= kGatedBN / 64) {
+                tm = &ex.b;
+                n -= kGatedBN;
+              }
+            }
+            tma_load_2d(sB + s * B_BYTES + j * (BK * 128), tm, &full[s], n, brow + kb * BK);
+          }
         }
       }
       // Copies in flight complete before the CTA leaves (bounded).
@@ -269,6 +350,11 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
       const bool tma_rows = p.tma_out && m - lane + 32 <= rows;
       const int r0 = row0 + m - lane;
       bool bad = false;
+      if constexpr (LAYER == kGated)
+        gated_rows<ACT>(p, ex, tmO,
+                        tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN), e,
+                        nb * kGatedBN, r, valid, tma_rows, r0, stg, STG_TILE, stg_cnt);
+      else
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
         const int n = nb * BN + c * 32;
@@ -406,10 +492,11 @@ __device__ __forceinline__ void umma_pair(uint32_t tmem_d, uint64_t a, uint64_t 
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-template <int LAYER>
+template <int LAYER, int ACT = 0>
 __global__ void __launch_bounds__(kThreads, 1)
 k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-              const __grid_constant__ CUtensorMap tmO, const Params p) {
+              const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Extra<LAYER> ex,
+              const Params p) {
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -553,7 +640,13 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
         locate(tile, e, pm, nb, row0, rows, half);
         // A half tile's CTA uses the first 64 of the 128 rows its box brings.
         const int arow = row0 + pm * 2 * BM + (int)rank * (half ? BM / 2 : BM);
-        const int ncol = nb * BN + (int)rank * P_BN_HALF;
+        // The gated layer's even CTA holds columns of W1, the odd one the same of W3.
+        int ncol = nb * BN + (int)rank * P_BN_HALF;
+        const CUtensorMap *tmb = &tmB;
+        if constexpr (LAYER == kGated) {
+          ncol = nb * kGatedBN;
+          if (rank) tmb = &ex.b;
+        }
         const int brow = e * p.K;
         const int take_at = num_kb > 4 ? num_kb - 4 : 0;
         // Tiles of odd waves (tile / pairs) walk K from the end: their first
@@ -576,7 +669,7 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           tma_load_2d_pair(sA + s * P_A_BYTES, &tmA, full_leader, kx, arow);
 #pragma unroll
           for (int q = 0; q < P_BN_HALF / 64; ++q)
-            tma_load_2d_pair(sB + s * P_B_BYTES + q * (BK * 128), &tmB, full_leader,
+            tma_load_2d_pair(sB + s * P_B_BYTES + q * (BK * 128), tmb, full_leader,
                              ncol + q * 64, brow + kx);
         }
       }
@@ -690,6 +783,11 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       const bool tma_rows = p.tma_out && m - lane + 32 <= rows;
       const int r0 = row0 + m - lane;
       bool bad = false;
+      if constexpr (LAYER == kGated)
+        gated_rows<ACT>(p, ex, tmO,
+                        tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN), e,
+                        nb * kGatedBN, r, valid, tma_rows, r0, stg, P_STG_TILE, stg_cnt);
+      else
 #pragma unroll 1
       for (int c = 0; c < nchunks; ++c) {
         const int n = ncol0 + c * 32;
@@ -867,13 +965,13 @@ constexpr size_t smem_bytes(int E) {
          (size_t)(E + 1) * 4;
 }
 
-template <int LAYER>
+template <int LAYER, int ACT = 0>
 cudaError_t launch_layer(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
-                         const Params &p, cudaStream_t s) {
+                         const Params &p, cudaStream_t s, const Extra<LAYER> &ex = {}) {
   const size_t smem = smem_bytes(p.E);
-  cudaError_t err = allow_smem(k_ffn_tc<LAYER>);
+  cudaError_t err = allow_smem(k_ffn_tc<LAYER, ACT>);
   if (err != cudaSuccess) return err;
-  launch_pdl_c(kPdlGemm, k_ffn_tc<LAYER>, sm_count(), kThreads, smem, s, a, b, o, p);
+  launch_pdl_c(kPdlGemm, k_ffn_tc<LAYER, ACT>, sm_count(), kThreads, smem, s, a, b, o, ex, p);
   return cudaGetLastError();
 }
 
@@ -923,11 +1021,12 @@ int pair_clusters(size_t smem) {
   return n;
 }
 
-template <int LAYER>
+template <int LAYER, int ACT = 0>
 cudaError_t launch_layer_pair(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
-                              const Params &p, int clusters, cudaStream_t s) {
+                              const Params &p, int clusters, cudaStream_t s,
+                              const Extra<LAYER> &ex = {}) {
   const size_t smem = smem_bytes_pair(p.E);
-  cudaError_t err = allow_smem(k_ffn_tc_pair<LAYER>);
+  cudaError_t err = allow_smem(k_ffn_tc_pair<LAYER, ACT>);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
@@ -939,7 +1038,7 @@ cudaError_t launch_layer_pair(const CUtensorMap &a, const CUtensorMap &b, const 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled(kPdlGemm) ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_ffn_tc_pair<LAYER>, a, b, o, p);
+  return cudaLaunchKernelEx(&cfg, k_ffn_tc_pair<LAYER, ACT>, a, b, o, ex, p);
 }
 
 // MOE_FFN_SCHED=static makes the CTA-pair kernel take its tiles round robin
@@ -980,55 +1079,107 @@ bool ffn_tc_supported(const moe_config &c) {
          smem_bytes(c.E) <= 227 * 1024 && encode_fn() != nullptr;
 }
 
+// Whether a layer of reduction length K and `tiles` column blocks runs on the
+// CTA-pair kernel (its clusters, else 0): it pays off for long K and enough
+// 256-row tiles to fill several waves; otherwise the one-CTA kernel's finer
+// tiles win.
+static int pair_for(const moe_config &c, int C, int K, int n_blocks) {
+  const int clusters = pair_clusters_for(c.E);
+  if (clusters <= 0) return 0;
+  const long rows = (long)c.T * c.k < (long)c.E * C ? (long)c.T * c.k : (long)c.E * C;
+  return ffn_variant() == 2 || (K >= 2048 && (rows / 256) * n_blocks >= 4L * clusters) ? clusters
+                                                                                      : 0;
+}
+
+// What both layers' parameters share.
+static Params layer_params(int K, int N, int n_blocks, int E, const int32_t *offset,
+                           const float *row_gate, const void *bias, void *out, DeviceStatus *st) {
+  // MOE_FFN_HALF=0 runs every row tile at M = 256 (read at each call; for comparisons).
+  const char *hv = getenv("MOE_FFN_HALF");
+  Params p{K, N, E, n_blocks, &st->gemm_next, ffn_dynamic(), hv && hv[0] == '0' ? 0 : 1, offset,
+           row_gate, static_cast<const __nv_bfloat16 *>(bias), out, st, wait_limit_ns()};
+  p.snake = ffn_snake();
+  return p;
+}
+
+static cudaError_t launch_ffn_layer1(const moe_config &c, int C, const void *xbuf,
+                                     const int32_t *offset, const float *row_gate, const void *W1,
+                                     const void *b1, void *hbuf, DeviceStatus *st,
+                                     cudaStream_t s) {
+  const uint64_t A = (uint64_t)c.T * c.k;
+  CUtensorMap ta, tb, to;
+  if (!make_map(&ta, xbuf, A, c.d, BM) || !make_map(&tb, W1, (uint64_t)c.E * c.d, c.d_ff, BK))
+    return cudaErrorInvalidValue;
+  const int n_blocks = (c.d_ff + BN - 1) / BN;
+  Params p = layer_params(c.d, c.d_ff, n_blocks, c.E, offset, row_gate, b1, hbuf, st);
+  p.tma_out = make_rows_map(&to, hbuf, A, c.d_ff, false) ? 1 : 0;
+  if (!p.tma_out) to = ta;  // unused
+  const int clusters = pair_for(c, C, c.d, n_blocks);
+  return clusters ? launch_layer_pair<1>(ta, tb, to, p, clusters, s)
+                  : launch_layer<1>(ta, tb, to, p, s);
+}
+
+cudaError_t launch_ffn_layer2(const moe_config &c, int C, long long max_rows, const void *hbuf,
+                              const int32_t *offset, const float *row_gate, const void *W2,
+                              const void *b2, void *zbuf, bool z_bf16, DeviceStatus *st,
+                              cudaStream_t s) {
+  const uint64_t A = (uint64_t)max_rows;
+  CUtensorMap ta, tb, to;
+  if (!make_map(&ta, hbuf, A, c.d_ff, BM) || !make_map(&tb, W2, (uint64_t)c.E * c.d_ff, c.d, BK))
+    return cudaErrorInvalidValue;
+  const int n_blocks = (c.d + BN - 1) / BN;
+  Params p = layer_params(c.d_ff, c.d, n_blocks, c.E, offset, row_gate, b2, zbuf, st);
+  p.z_bf16 = z_bf16 ? 1 : 0;
+  const int clusters = pair_for(c, C, c.d_ff, n_blocks);
+  // The CTA-pair kernel's output box is [32 rows, 32 columns]; the one-CTA
+  // kernel stores fp32 Z in 16-column boxes (its staging tiles are 2 KB).
+  p.tma_out = (clusters || z_bf16 ? make_rows_map(&to, zbuf, A, c.d, !z_bf16)
+                                  : make_rows_map16(&to, zbuf, A, c.d))
+                  ? 1
+                  : 0;
+  if (!p.tma_out) to = ta;  // unused
+  return clusters ? launch_layer_pair<2>(ta, tb, to, p, clusters, s)
+                  : launch_layer<2>(ta, tb, to, p, s);
+}
+
 cudaError_t launch_ffn_tc(const moe_config &c, int C, const void *xbuf, const int32_t *offset,
                           const int32_t *mtiles, const float *row_gate, const void *W1,
                           const void *b1, const void *W2, const void *b2, void *hbuf, void *zbuf,
                           bool z_bf16, DeviceStatus *st, cudaStream_t s) {
   (void)mtiles;
-  const uint64_t A = (uint64_t)c.T * c.k;
-  CUtensorMap ta1, tb1, ta2, tb2;
-  if (!make_map(&ta1, xbuf, A, c.d, BM) || !make_map(&tb1, W1, (uint64_t)c.E * c.d, c.d_ff, BK) ||
-      !make_map(&ta2, hbuf, A, c.d_ff, BM) || !make_map(&tb2, W2, (uint64_t)c.E * c.d_ff, c.d, BK))
+  const cudaError_t err =
+      launch_ffn_layer1(c, C, xbuf, offset, row_gate, W1, b1, hbuf, st, s);
+  return err != cudaSuccess ? err
+                            : launch_ffn_layer2(c, C, (long long)c.T * c.k, hbuf, offset, row_gate,
+                                                W2, b2, zbuf, z_bf16, st, s);
+}
+
+cudaError_t launch_gated_tc_layer1(const moe_config &c, int C, int activation, long long max_rows,
+                                   const void *xbuf, const int32_t *offset, const void *W1,
+                                   const void *b1, const void *W3, const void *b3, void *hbuf,
+                                   void *pre1, void *pre3, DeviceStatus *st, cudaStream_t s) {
+  const uint64_t A = (uint64_t)max_rows, wrows = (uint64_t)c.E * c.d;
+  CUtensorMap ta, tb, to;
+  Extra<kGated> ex{};
+  if (!make_map(&ta, xbuf, A, c.d, BM) || !make_map(&tb, W1, wrows, c.d_ff, BK) ||
+      !make_map(&ex.b, W3, wrows, c.d_ff, BK))
     return cudaErrorInvalidValue;
-  uint32_t *sched = &st->gemm_next;  // gemm_next, gemm_done: adjacent words
-  const int dyn = ffn_dynamic();
-  // MOE_FFN_HALF=0 runs every row tile at M = 256 (read at each call; for comparisons).
-  const char *hv = getenv("MOE_FFN_HALF");
-  const int half = hv && hv[0] == '0' ? 0 : 1;
-  Params p1{c.d, c.d_ff, c.E, (c.d_ff + BN - 1) / BN, sched, dyn, half, offset, row_gate,
-            static_cast<const __nv_bfloat16 *>(b1), hbuf, st, wait_limit_ns()};
-  Params p2{c.d_ff, c.d, c.E, (c.d + BN - 1) / BN, sched, dyn, half, offset, row_gate,
-            static_cast<const __nv_bfloat16 *>(b2), zbuf, st, wait_limit_ns(), z_bf16 ? 1 : 0};
-  // Per layer: the CTA pair pays off for long K and enough 256-row tiles to
-  // fill several waves; otherwise the one-CTA kernel's finer tiles win.
-  const long rows = (long)c.T * c.k < (long)c.E * C ? (long)c.T * c.k : (long)c.E * C;
-  const int clusters = pair_clusters_for(c.E);
-  const bool force_pair = ffn_variant() == 2;
-  auto pair_for = [&](int K, int N) {
-    return clusters > 0 &&
-           (force_pair || (K >= 2048 && (rows / 256) * ((N + BN - 1) / BN) >= 4L * clusters));
-  };
-  // The CTA-pair kernel's output maps (H, then Z): box [32 rows, 32 columns].
-  // The one-CTA kernel stores fp32 Z in 16-column boxes (its staging tiles
-  // are 2 KB).
-  CUtensorMap to1, to2, to2s;
-  p1.tma_out = make_rows_map(&to1, hbuf, A, c.d_ff, false) ? 1 : 0;
-  p2.tma_out = make_rows_map(&to2, zbuf, A, c.d, !z_bf16) ? 1 : 0;
-  if (!p1.tma_out) to1 = ta1;  // unused
-  if (!p2.tma_out) to2 = ta2;
-  p1.snake = p2.snake = ffn_snake();
-  Params p2s = p2;
-  if (z_bf16) {
-    to2s = to2;
-  } else {
-    p2s.tma_out = make_rows_map16(&to2s, zbuf, A, c.d) ? 1 : 0;
-    if (!p2s.tma_out) to2s = ta2;
-  }
-  cudaError_t err = pair_for(c.d, c.d_ff) ? launch_layer_pair<1>(ta1, tb1, to1, p1, clusters, s)
-                                          : launch_layer<1>(ta1, tb1, to1, p1, s);
-  if (err != cudaSuccess) return err;
-  return pair_for(c.d_ff, c.d) ? launch_layer_pair<2>(ta2, tb2, to2, p2, clusters, s)
-                               : launch_layer<2>(ta2, tb2, to2s, p2s, s);
+  const int n_blocks = (c.d_ff + kGatedBN - 1) / kGatedBN;
+  Params p = layer_params(c.d, c.d_ff, n_blocks, c.E, offset, nullptr, b1, hbuf, st);
+  p.half_tiles = 0;  // a half tile's p1 and p3 would lie in different warps' lanes
+  ex.bias3 = static_cast<const __nv_bfloat16 *>(b3);
+  ex.pre1 = static_cast<__nv_bfloat16 *>(pre1);
+  ex.pre3 = static_cast<__nv_bfloat16 *>(pre3);
+  ex.o1 = ex.o3 = to = ta;  // unused unless made
+  p.tma_out = make_rows_map(&to, hbuf, A, c.d_ff, false) &&
+              (!pre1 || (make_rows_map(&ex.o1, pre1, A, c.d_ff, false) &&
+                         make_rows_map(&ex.o3, pre3, A, c.d_ff, false)));
+  const int clusters = pair_for(c, C, c.d, n_blocks);
+  return gated_dispatch(activation, [&](auto act) {
+    constexpr int ACT = decltype(act)::value;
+    return clusters ? launch_layer_pair<kGated, ACT>(ta, tb, to, p, clusters, s, ex)
+                    : launch_layer<kGated, ACT>(ta, tb, to, p, s, ex);
+  });
 }
 
 }  // namespace moe

@@ -70,7 +70,7 @@ k_fp8_rows(int max_rows, int K, int KB, int k, const int32_t *__restrict__ count
   const long long r = w / KB;
   const int kb = (int)(w - r * KB);
   if (r >= max_rows || r >= *count) return;
-  const size_t row = row_token ? (size_t)(row_token[r] / k) : (size_t)r;
+  const size_t row = (size_t)(row_token[r] / k);
   float v[4], top = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

@@ -6,7 +6,6 @@
 //   backward 1: D = dy W2^T; dgate's <D, h>; dP1 = g D p3 act'(p1), dP3 = g D act(p1)
 //   backward 2: dX = dP1 W1^T + dP3 W3^T
 //   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
-//   8 bits:     forward 1 and 2 with e4m3 operands and their blocks' scales
 // One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
 // block of 256 threads, TM x TN a thread, K in chunks of 16 whose next one is
 // fetched while this one is multiplied, packed fp32 multiply-adds (two a lane
@@ -30,15 +29,7 @@ __device__ __forceinline__ void put(T *p, size_t i, float v) {
   else p[i] = v;
 }
 
-enum Op { kF1, kF2, kB1, kB2, kW1, kW3, kW2, kQ1, kQ2 };
-
-__device__ __forceinline__ float from8(uint8_t v) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(v, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half *>(&h));
-}
-__device__ __forceinline__ float scale_of(uint32_t byte) {
-  return __uint_as_float(byte == 255u ? 0x7fc00000u : byte << 23);
-}
+enum Op { kF1, kF2, kB1, kB2, kW1, kW3, kW2 };
 
 // a * b + c on two floats at once.
 __device__ __forceinline__ void fma2(unsigned long long &c, unsigned long long a,
@@ -84,13 +75,11 @@ k_gated_simt(const GatedSimt p) {
   }
   const int r0 = p.rows.offset[e], rows = p.rows.offset[e + 1] - r0;
   if (!kWeight && m0 >= rows) return;
-  constexpr bool kPair = OP == kF1 || OP == kQ1;
-  constexpr int BNu = kPair ? BN / 2 : BN;  // columns of the output a block covers
+  constexpr int BNu = OP == kF1 ? BN / 2 : BN;  // columns of the output a block covers
   const int n0 = blockIdx.y * BNu;
   const int M = kWeight ? (OP == kW2 ? F : d) : rows;
-  const int N = kPair || OP == kB1 || OP == kW1 || OP == kW3 ? F : d;
-  const int K = kWeight ? rows : kPair || OP == kB1 ? d : OP == kF2 || OP == kQ2 ? F : 2 * F;
-  const int KB = (K + kFp8Block - 1) / kFp8Block;  // 8 bits: blocks of K
+  const int N = OP == kF1 || OP == kB1 || OP == kW1 || OP == kW3 ? F : d;
+  const int K = kWeight ? rows : OP == kF1 || OP == kB1 ? d : OP == kF2 ? F : 2 * F;
   const size_t we = (size_t)e * d * F;  // this expert's place in each weight
 
   // A: rows (K contiguous; K in lanes) or, for a weight gradient, columns of
@@ -102,7 +91,6 @@ k_gated_simt(const GatedSimt p) {
       const int m = m0 + (tid >> 4) + 16 * i;
       const int r = r0 + min(m, rows - 1);
       if (OP == kF1 || OP == kB1) arow[i] = (size_t)(p.rows.row_token[r] / k) * d;
-      else if (OP == kQ1 || OP == kQ2) arow[i] = r;
       else arow[i] = (size_t)r * F;
     }
   }
@@ -127,9 +115,6 @@ k_gated_simt(const GatedSimt p) {
         if (m < M && kk < K) {
           if (OP == kF1) v = ld(x, arow[i] + kk);
           else if (OP == kF2) v = ld(static_cast<const T *>(p.h), arow[i] + kk);
-          else if (OP == kQ1 || OP == kQ2)
-            v = from8(p.a8[arow[i] * KB * kFp8Block + kk]) *
-                scale_of(p.sa[(size_t)(kk / kFp8Block) * p.max_rows + arow[i]]);
           else if (OP == kB1) v = ld(dy, arow[i] + kk);
           else v = kk < F ? p.dP1[arow[i] + kk] : p.dP3[arow[i] + kk - F];
         }
@@ -139,18 +124,7 @@ k_gated_simt(const GatedSimt p) {
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
       float v = 0.f;
-      if constexpr (OP == kQ1 || OP == kQ2) {
-        const int kk = k0 + (tid & 15), nn = (tid >> 4) + 16 * i;
-        const bool second = OP == kQ1 && nn >= BNu;
-        const int n = n0 + (second ? nn - BNu : nn);
-        if (n < N && kk < K) {
-          const size_t w = (size_t)e * N + n;
-          const size_t sc = ((size_t)e * ((N + 127) / 128) + n / 128) * KB + kk / 128;
-          const void *q = OP == kQ2 ? p.W2 : second ? p.W3 : p.W1;
-          const uint8_t *qs = OP == kQ2 ? p.s2 : second ? p.s3 : p.s1;
-          v = from8(static_cast<const uint8_t *>(q)[w * KB * kFp8Block + kk]) * scale_of(qs[sc]);
-        }
-      } else if constexpr (OP == kB1 || OP == kB2) {  // the weight's rows are the output's columns
+      if constexpr (OP == kB1 || OP == kB2) {  // the weight's rows are the output's columns
         const int kk = k0 + (tid & 15), n = n0 + (tid >> 4) + 16 * i;
         if (n < N && kk < K) {
           if (OP == kB1) v = ld(W2, (size_t)n * d + kk);
@@ -178,7 +152,7 @@ k_gated_simt(const GatedSimt p) {
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      if (OP == kB1 || OP == kB2 || OP == kQ1 || OP == kQ2) Bs[tid & 15][(tid >> 4) + 16 * i] = rb[i];
+      if (OP == kB1 || OP == kB2) Bs[tid & 15][(tid >> 4) + 16 * i] = rb[i];
       else Bs[tid / BN + i * (kThreads / BN)][tid % BN] = rb[i];
     }
   };
@@ -239,7 +213,7 @@ k_gated_simt(const GatedSimt p) {
     const bool live = m < M;
     const size_t r = (size_t)r0 + m;
     bool bad = false;
-    if constexpr (kPair) {
+    if constexpr (OP == kF1) {
       if (!live) continue;
 #pragma unroll
       for (int j = 0; j < HN; ++j) {
@@ -280,7 +254,7 @@ k_gated_simt(const GatedSimt p) {
         const int n = n0 + (j / HN) * (BN / 2) + tx * HN + j % HN;
         if (n >= N) continue;
         float u = v[j];
-        if constexpr (OP == kF2 || OP == kQ2) {
+        if constexpr (OP == kF2) {
           if (b2) u += ld(b2, (size_t)e * d + n);
           u *= p.rows.row_gate[r];
           p.z[r * d + n] = u;
@@ -319,9 +293,8 @@ template <int OP, typename T, int ACT, int TM, int TN>
 cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
   constexpr int BM = 16 * TM, BN = 16 * TN;
   constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;
-  constexpr bool kPair = OP == kF1 || OP == kQ1;
-  const int N = kPair || OP == kB1 || OP == kW1 || OP == kW3 ? p.c.d_ff : p.c.d;
-  const int BNu = kPair ? BN / 2 : BN;
+  const int N = OP == kF1 || OP == kB1 || OP == kW1 || OP == kW3 ? p.c.d_ff : p.c.d;
+  const int BNu = OP == kF1 ? BN / 2 : BN;
   dim3 grid(1, (N + BNu - 1) / BNu, 1);  // row blocks fastest: they share the weight's columns
   if (kWeight) {
     grid.x = ((OP == kW2 ? p.c.d_ff : p.c.d) + BM - 1) / BM;
@@ -336,8 +309,8 @@ cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
 // 32 x 64.
 bool wide_tiles(const moe_config &c, int max_rows, int op) {
   const bool weight = op == kW1 || op == kW3 || op == kW2;
-  const bool to_d = op == kF2 || op == kB2 || op == kW2 || op == kQ2;
-  const int N = (op == kF1 || op == kQ1 ? 2 : 1) * (to_d ? c.d : c.d_ff);
+  const bool to_d = op == kF2 || op == kB2 || op == kW2;
+  const int N = (op == kF1 ? 2 : 1) * (to_d ? c.d : c.d_ff);
   const int M = op == kW2 ? c.d_ff : c.d;
   const long long row_blocks = weight ? (long long)c.E * ((M + 127) / 128)
                                       : ((long long)max_rows + 127) / 128;
@@ -380,13 +353,6 @@ int gated_simt_dg_blocks(const moe_config &c, int max_rows) {
 
 cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s) {
   return p.c.act_dtype == MOE_BF16 ? forward<__nv_bfloat16>(p, s) : forward<float>(p, s);
-}
-
-cudaError_t launch_gated_simt_fp8(const GatedSimt &p, int layer, cudaStream_t s) {
-  if (layer == 2) return run_op<kQ2, __nv_bfloat16, MOE_ACT_RELU>(p, s);
-  return gated_dispatch(p.activation, [&](auto act) {
-    return run_op<kQ1, __nv_bfloat16, decltype(act)::value>(p, s);
-  });
 }
 
 cudaError_t launch_gated_simt_backward(const GatedSimt &p, cudaStream_t s) {

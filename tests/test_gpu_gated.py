@@ -147,6 +147,31 @@ def test_forward_and_backward(shape, kind):
     check_backward(cfg, kind, s, o["p1"], o["p3"], run_backward(cfg, kind, g, o["p1"], o["p3"]))
 
 
+# Row counts around the tiles of 128 (a CTA) and 256 (a pair of CTAs).
+VARIANT_SHAPES = [(300, 128, 3, 320, 1, 3.0), (1100, 192, 4, 256, 1, 4.0), (700, 256, 2, 576, 2, 2.0)]
+
+
+@pytest.mark.parametrize("variant", ["single", "pair"])
+@pytest.mark.parametrize("shape", VARIANT_SHAPES, ids=lambda v: "-".join(map(str, v)))
+def test_tensor_core_variants(shape, variant, monkeypatch):
+    """The one-CTA and the CTA-pair kernels, each forced; the pairs also with
+    every tile's K backwards."""
+    T, d, E, F, k, cf = shape
+    monkeypatch.setenv("MOE_FFN_TC_VARIANT", variant)
+    monkeypatch.setenv("MOE_BWD_TC_VARIANT", variant)
+    s = inputs(T, d, E, F, k, BF16, seed=T)
+    cfg, g = config(s, cf), dev(s)
+    ref = reference(cfg, R.SILU, s)
+    w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+    for snake in ("1", "all") if variant == "pair" else ("1",):
+        monkeypatch.setenv("MOE_FFN_SNAKE", snake)
+        o = run_forward(cfg, R.SILU, g)
+        check_forward(cfg, R.SILU, s, o, ref)
+        check_backward(cfg, R.SILU, s, o["p1"], o["p3"],
+                       run_backward(cfg, R.SILU, g, o["p1"], o["p3"]))
+    check_forward(cfg, R.SILU, s, run_fp8(cfg, R.SILU, g, w8), reference8(cfg, R.SILU, s, w8))
+
+
 @pytest.mark.parametrize("T", [1, 40, 300])
 @pytest.mark.parametrize("dt,d,F", [(BF16, 128, 192), (F32, 66, 70)])
 def test_empty_experts_repeats_and_bad_indexes(T, dt, d, F):
