@@ -120,7 +120,8 @@ cudaError_t launch_gated_tc_layer1(const moe_config &c, int C, int activation, l
 // zeros past K) and scale [E, ceil(N/128), Kp/128].
 cudaError_t launch_fp8_weights(bool bf16, int E, int K, int N, const void *W, uint8_t *q,
                                uint8_t *scale, DeviceStatus *st, cudaStream_t s);
-// Packed rows r < *count to q [max_rows, Kp] and scale [Kp/128][max_rows]; row r
+// Packed rows r < *count to q [max_rows, Kp] and scale [Kp/512 rounded
+// up][max_rows][4], the bytes of four blocks of a row together; row r
 // is that of token row_token[r] / k of src.
 cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,
                             const int32_t *row_token, const void *src, uint8_t *q,
@@ -128,8 +129,8 @@ cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,
 
 // k_fp8_tc.cu: one of the 8-bit layer's products on the tensor cores, any
 // widths. Layer 1: a8 = x rows, W and W3 -> h8 [max_rows, d_ff rounded up to
-// 128], sh [ceil(d_ff/128)][max_rows]; layer 2: a8 = h8, W -> z [max_rows, d] in
-// fp32, or bf16 (d a multiple of 8). sa: the rows' scales [K / 128][max_rows].
+// 128], sh; layer 2: a8 = h8, W -> z [max_rows, d] in fp32, or bf16 (d a multiple
+// of 8). sa, sh: the rows' scales, as launch_fp8_rows writes them.
 struct Fp8Layer {
   moe_config c;
   int layer, activation, max_rows;

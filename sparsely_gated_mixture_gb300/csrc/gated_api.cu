@@ -91,9 +91,9 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
   const size_t db = (size_t)fp8_blocks(c.d), fb = (size_t)fp8_blocks(c.d_ff);
   L.r = gated_route(c, take);
   L.x8 = take(R * db * kFp8Block);
-  L.sx = take(R * db);
+  L.sx = take(R * ((db + 3) / 4 * 4));
   L.h8 = take(R * fb * kFp8Block);
-  L.sh = take(R * fb);
+  L.sh = take(R * ((fb + 3) / 4 * 4));
   L.z = take(R * c.d * (gated_fp8_z_bf16(c) ? 2 : 4));
   L.total = take.off;
   return L;

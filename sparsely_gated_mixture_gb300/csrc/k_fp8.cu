@@ -84,7 +84,7 @@ k_fp8_rows(int max_rows, int K, int KB, int k, const int32_t *__restrict__ count
   const float inv = fp8_inverse(byte);
   *reinterpret_cast<uint32_t *>(q + (size_t)r * KB * B + kb * B + lane * 4) =
       fp8_pack2(v[0] * inv, v[1] * inv) | fp8_pack2(v[2] * inv, v[3] * inv) << 16;
-  if (lane == 0) scale[(size_t)kb * max_rows + r] = (uint8_t)byte;
+  if (lane == 0) scale[((size_t)(kb >> 2) * max_rows + r) * 4 + (kb & 3)] = (uint8_t)byte;
 }
 
 }  // namespace

@@ -3,17 +3,18 @@
 //            and put in 8 bits with a scale for each 128 columns
 //   layer 2: z = gate * (h W2 + b2)
 // tcgen05.mma kind::mxf8f6f4 takes e4m3 operands and applies a power-of-two
-// scale to each row and 32 values of K as it multiplies, so blocks of 128 cost
-// nothing: their scale stands there four times. Operands are K-major, 128 bytes
+// scale to each row and 32 values of K as it multiplies: a byte of a TMEM word
+// for each row, which of the four is in the instruction. The four MMAs of a block
+// of 128 take the same byte, so a word serves four blocks of K. Operands are K-major, 128 bytes
 // of K a stage, as the bf16 kernels' 64 values; so are the tiles, 128 rows (a
 // CTA) or 256 (a pair of CTAs) by 256 columns, in layer 1 128 of W1 and the
 // same 128 of W3: one accumulator holds p1 and p3 of the same places, and a
 // thread all 128 of its row's hidden values that share a scale.
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner, 2 scales, 4-7 epilogue.
-// The scale warp reads the bytes of eight K blocks ahead and writes a stage's
-// in the form that tcgen05.cp takes to TMEM: 16 bytes for a lane's rows l, l +
-// 32, l + 64, l + 96, each row's byte four times (K in steps of 32).
+// The scale warp has a ring of its own, a slot for four K blocks, in the form
+// that tcgen05.cp takes to TMEM: 16 bytes for a lane's rows l, l + 32, l + 64, l
+// + 96. It reads the next four blocks' bytes before it waits for a slot.
 //
 // TMEM: two accumulators of 256 columns and 2 x 12 columns of scales are more
 // than its 512, so the accumulators lie at columns 0 and 224. The epilogue takes
@@ -34,7 +35,7 @@ constexpr int kThreads = 256;
 constexpr int A_BYTES = BM * BK;           // 16 KB
 constexpr int S_BYTES = 512 + 1024;        // scales of 128 rows and 256 columns
 constexpr int TMEM_COLS = 512, ACC1 = 224, SF_COL = 480;
-constexpr int kAhead = 8;                  // K blocks whose scales are read at once
+constexpr int SF_SLOTS = 4;                // of four K blocks' scales each
 constexpr int STG_TILE = 32 * 32 / 2;      // floats: [32 x 32] bf16 or [32 x 16] fp32
 template <int CG>
 __host__ __device__ constexpr int stages_of() { return CG == 2 ? 6 : 4; }
@@ -46,10 +47,10 @@ struct Params {
   int K, N, E, KB, NB, n_blocks, max_rows;  // KB, NB: scale blocks of K and of a weight's N
   const int32_t *offset;
   const float *row_gate;
-  const uint8_t *sa;           // [KB][max_rows]
+  const uint32_t *sa;          // [KB / 4][max_rows]: bytes of four K blocks
   const uint8_t *sb, *sb3;     // [E][NB][KB]
   const __nv_bfloat16 *bias, *bias3;
-  uint8_t *h8, *sh;            // layer 1: [max_rows][128 NB], [NB][max_rows]
+  uint8_t *h8, *sh;            // layer 1: [max_rows][128 NB], [NB / 4][max_rows][4]
   void *z;                     // layer 2: [max_rows][N] fp32 or bf16
   int z_bf16, tma_out;
   DeviceStatus *st;
@@ -57,27 +58,28 @@ struct Params {
 };
 
 // kind::mxf8f6f4: e4m3 both, both K-major, fp32 accumulate, scales UE8M0 (bit
-// 23), scale byte 0 of its word (all four are alike).
-constexpr uint32_t idesc_of(int cg) {
-  return ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM * cg >> 4) << 24);
+// 23), byte `id` of the scales' words (bits 4 and 29).
+__device__ __forceinline__ uint32_t idesc_of(int cg, uint32_t id) {
+  return ((uint32_t)(BN >> 3) << 17) | (1u << 23) | ((uint32_t)(BM * cg >> 4) << 24) | id << 4 |
+         id << 29;
 }
 
 template <int CG>
 __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t sfa, uint32_t sfb,
-                                     uint32_t acc) {
+                                     uint32_t idesc, uint32_t acc) {
   if constexpr (CG == 2)
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
         " tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
         " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc_of(2)), "r"(sfa), "r"(sfb), "r"(acc)
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");
   else
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
         " tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
         " [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc_of(1)), "r"(sfa), "r"(sfb), "r"(acc)
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");
 }
 
@@ -145,10 +147,10 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
   uint8_t *sB = sA + STAGES * A_BYTES;
   float *stg_all = reinterpret_cast<float *>(sB + STAGES * B_BYTES);
   uint8_t *sS = reinterpret_cast<uint8_t *>(stg_all) + STG_BYTES;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sS + STAGES * S_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sS + SF_SLOTS * S_BYTES);
   uint64_t *full = bars, *empty = full + STAGES;
   uint64_t *acc_full = empty + STAGES, *acc_empty = acc_full + 2, *ovl = acc_empty + 2;
-  uint64_t *drain = ovl + 2;
+  uint64_t *sf_full = ovl + 2, *sf_empty = sf_full + SF_SLOTS, *drain = sf_empty + SF_SLOTS;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *tile_start = reinterpret_cast<int *>(tmem_slot + 2);
@@ -160,8 +162,12 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1 + CG);  // the bytes expected, and each CTA's scales
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < SF_SLOTS; ++s) {
+      mbar_init(&sf_full[s], CG);  // each CTA's scale warp
+      mbar_init(&sf_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -261,56 +267,57 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     pdl_trigger();
   } else if (warp == 2) {
     // --------------------------------------------------------------- scales (both CTAs)
-    uint32_t it = 0;
-    bool ok = true;
-    for (int tile = unit; ok && tile < total; tile += n_units) {
-      const Tile t = locate(tile);
+    // Lane l < 8 reads column block l / 4's byte of K block l % 4 of a group.
+    const int half = (lane >> 2) & 1;
+    int tile = unit, k0 = 0;  // the next group to read
+    Tile t{};
+    uint32_t a[4], b = 0;
+    const auto read = [&] {
+      if (k0 == 0) t = locate(tile);
       const int arow = t.row0 + (t.mb * CG + (int)rank) * BM;
-      // Lanes 0-15: column block lane / 8, K block lane % 8 of a group.
-      const int half = (lane >> 3) & 1;
-      const int nb = LAYER == 1 ? t.nb : min(2 * t.nb + half, p.NB - 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = arow + lane + 32 * j;
+        a[j] = row < p.max_rows ? p.sa[(size_t)(k0 >> 2) * p.max_rows + row] : 0x7f7f7f7fu;
+      }
+      const int nb = LAYER == 1 ? t.nb : min(2 * t.nb + half, p.NB - 1), kb = k0 + (lane & 3);
       const uint8_t *sb = (LAYER == 1 && half ? p.sb3 : p.sb) + ((size_t)t.e * p.NB + nb) * p.KB;
-      for (int k0 = 0; ok && k0 < p.KB; k0 += kAhead) {
-        uint32_t a[kAhead][4], b;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = arow + lane + 32 * j;
-            a[i][j] = k0 + i < p.KB && row < p.max_rows
-                          ? p.sa[(size_t)(k0 + i) * p.max_rows + row]
-                          : 127u;
-          }
-        b = k0 + (lane & 7) < p.KB ? sb[k0 + (lane & 7)] : 127u;
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (k0 + i >= p.KB || !ok) break;
-          const int s = it % STAGES;
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / STAGES) & 1u) ^ 1u, abort_flag,
-                                                 p.st, 122, p.wait_ns));
-          if (!ok) break;
-          uint4 *out = reinterpret_cast<uint4 *>(sS + s * S_BYTES) + lane;
-          out[0] = make_uint4(a[i][0] * 0x01010101u, a[i][1] * 0x01010101u,
-                              a[i][2] * 0x01010101u, a[i][3] * 0x01010101u);
-          const uint32_t b0 = __shfl_sync(0xffffffffu, b, i) * 0x01010101u;
-          const uint32_t b1 = __shfl_sync(0xffffffffu, b, 8 + i) * 0x01010101u;
-          out[32] = make_uint4(b0, b0, b0, b0);
-          out[64] = make_uint4(b1, b1, b1, b1);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_cluster(mapa(smem_u32(&full[s]), 0));
-            else mbar_arrive(&full[s]);
-          }
-          ++it;
-        }
+      b = lane < 8 && kb < p.KB ? (uint32_t)sb[kb] << 8 * (lane & 3) : 0u;
+      k0 += 4;
+      if (k0 >= p.KB) {
+        k0 = 0;
+        tile += n_units;
+      }
+    };
+    bool more = tile < total;
+    if (more) read();
+    for (uint32_t g = 0; more; ++g) {
+      const uint4 av = make_uint4(a[0], a[1], a[2], a[3]);
+      uint32_t w = b | __shfl_xor_sync(0xffffffffu, b, 1);
+      w |= __shfl_xor_sync(0xffffffffu, w, 2);
+      const uint32_t b0 = __shfl_sync(0xffffffffu, w, 0), b1 = __shfl_sync(0xffffffffu, w, 4);
+      more = tile < total;
+      if (more) read();  // the next group's, in flight over the wait
+      const int s = g % SF_SLOTS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sf_empty[s], ((g / SF_SLOTS) & 1u) ^ 1u, abort_flag,
+                                             p.st, 122, p.wait_ns)))
+        break;
+      uint4 *out = reinterpret_cast<uint4 *>(sS + s * S_BYTES) + lane;
+      out[0] = av;
+      out[32] = make_uint4(b0, b0, b0, b0);
+      out[64] = make_uint4(b1, b1, b1, b1);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster(mapa(smem_u32(&sf_full[s]), 0));
+        else mbar_arrive(&sf_full[s]);
       }
     }
     pdl_trigger();
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------- MMA issuer
-      uint32_t it = 0;
+      uint32_t it = 0, g = 0;  // K blocks, groups of four
       int local = 0;
       bool ok = true;
       for (int tile = unit; ok && tile < total; tile += n_units, ++local) {
@@ -323,24 +330,38 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           break;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(buf ? ACC1 : 0);
+        uint32_t sf = 0;
         for (int kb = 0; kb < p.KB; ++kb, ++it) {
+          if ((kb & 3) == 0) {
+            const int q = g % SF_SLOTS;
+            const uint32_t ph = (g / SF_SLOTS) & 1u;
+            if (!(CG == 2 ? mbar_wait_cl(&sf_full[q], ph, abort_flag, p.st, 127, p.wait_ns)
+                          : mbar_wait(&sf_full[q], ph, abort_flag, p.st, 127, p.wait_ns))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            // Copies and MMAs run in order, so this slot's last readers are done.
+            sf = tmem + SF_COL + (g & 1u) * 16;
+            const uint32_t ss = smem_u32(sS + q * S_BYTES);
+            copy_scales<CG>(sf, ss);
+            copy_scales<CG>(sf + 4, ss + 512);
+            copy_scales<CG>(sf + 8, ss + 1024);
+            commit8<CG>(&sf_empty[q]);
+            ++g;
+          }
           const int s = it % STAGES;
-          const uint32_t ph = (it / STAGES) & 1u;
-          if (!(CG == 2 ? mbar_wait_cl(&full[s], ph, abort_flag, p.st, 125, p.wait_ns)
-                        : mbar_wait(&full[s], ph, abort_flag, p.st, 125, p.wait_ns))) {
+          if (!mbar_wait(&full[s], (it / STAGES) & 1u, abort_flag, p.st, 125, p.wait_ns)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sf = tmem + SF_COL + (it & 1u) * 16, ss = smem_u32(sS + s * S_BYTES);
-          copy_scales<CG>(sf, ss);
-          copy_scales<CG>(sf + 4, ss + 512);
-          copy_scales<CG>(sf + 8, ss + 1024);
           const uint32_t a0 = smem_u32(sA + s * A_BYTES), b0 = smem_u32(sB + s * B_BYTES);
+          const uint32_t idesc = idesc_of(CG, (uint32_t)kb & 3u);
 #pragma unroll
           for (int kk = 0; kk < BK / 32; ++kk)
             mma8<CG>(d, sdesc(a0 + kk * 32, 16, 1024), sdesc(b0 + kk * 32, 16, 1024), sf, sf + 4,
-                     (kb | kk) ? 1u : 0u);
+                     idesc, (kb | kk) ? 1u : 0u);
           commit8<CG>(&empty[s]);
         }
         if (ok) commit8<CG>(&acc_full[buf]);
@@ -408,7 +429,7 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
         if (valid) {
           const uint32_t byte = fp8_scale_byte(top);
           const float inv = fp8_inverse(byte);
-          p.sh[(size_t)t.nb * p.max_rows + r] = (uint8_t)byte;
+          p.sh[((size_t)(t.nb >> 2) * p.max_rows + r) * 4 + (t.nb & 3)] = (uint8_t)byte;
           uint4 *out = reinterpret_cast<uint4 *>(p.h8 + (r * p.NB + t.nb) * 128);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -501,8 +522,8 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
 
 template <int CG>
 constexpr size_t smem_bytes(int E) {
-  return 1024 + (size_t)stages_of<CG>() * (A_BYTES + b_bytes<CG>() + S_BYTES) + STG_BYTES +
-         (2 * stages_of<CG>() + 7) * 8 + 8 + (size_t)(E + 1) * 4;
+  return 1024 + (size_t)stages_of<CG>() * (A_BYTES + b_bytes<CG>()) + SF_SLOTS * S_BYTES +
+         STG_BYTES + (2 * stages_of<CG>() + 2 * SF_SLOTS + 7) * 8 + 8 + (size_t)(E + 1) * 4;
 }
 static_assert(smem_bytes<1>(1024) <= 227 * 1024 && smem_bytes<2>(1024) <= 227 * 1024, "");
 
@@ -600,7 +621,7 @@ cudaError_t launch_fp8_tc(const Fp8Layer &q, cudaStream_t s) {
   p.max_rows = q.max_rows;
   p.offset = q.offset;
   p.row_gate = q.row_gate;
-  p.sa = q.sa;
+  p.sa = reinterpret_cast<const uint32_t *>(q.sa);
   p.sb = q.sb;
   p.sb3 = q.layer == 1 ? q.sb3 : q.sb;
   p.bias = static_cast<const __nv_bfloat16 *>(q.bias);
