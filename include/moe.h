@@ -51,8 +51,8 @@
  *   (the Switch page raises on each), an index out of range, or a bounded wait
  *   that ran out -- are recorded in a status word inside `ws`;
  *   moe_last_device_status() reads it. moe_gate(), moe_forward(), the few-token
- *   calls, moe_backward_checkpoint(), the gated experts' calls and
- *   moe_weights_fp8() clear it when they start,
+ *   calls, moe_backward_checkpoint() and the gated experts' calls clear it when they
+ *   start,
  *   moe_last_device_status() after reading it; a caller whose first call on a
  *   fresh workspace is another stage zero-fills the workspace (or calls
  *   moe_last_device_status) first. Each bounded wait inside the
@@ -646,8 +646,8 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
  *   magnitude; values round to nearest, ties to even.
  * A block with an Inf or a NaN gets the byte 255 (its products are NaN) and is
  * recorded as MOE_ERR_NONFINITE (detail = its place in wscale). E <= 1024, K and
- * N at most MOE_GATED_MAX_WIDTH. ws: the status word only (256 bytes), cleared
- * first. moe_weights_fp8_size gives the arrays' bytes.
+ * N at most MOE_GATED_MAX_WIDTH. ws: the status word only (256 bytes); it is not
+ * cleared. moe_weights_fp8_size gives the arrays' bytes.
  */
 int moe_weights_fp8_size(int32_t E, int32_t K, int32_t N, size_t *w8_bytes,
                          size_t *wscale_bytes);

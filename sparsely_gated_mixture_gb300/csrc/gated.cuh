@@ -3,6 +3,7 @@
 //   U(x) = (act(x W1 + b1) * (x W3 + b3)) W2 + b2
 #pragma once
 
+#include "gate_math.cuh"
 #include "moe_internal.cuh"
 
 #include <cuda_fp8.h>
@@ -14,7 +15,9 @@ namespace moe {
 // ----------------------------------------------------------------------------- activations
 // act(v) and, for the backward, act'(v) with act(v). PRECISE is for fp32
 // layers; bf16 layers take the fast exponential (2 ulp and 1.2 ulp for each
-// unit of |v|, some 1e-6 where the result is not negligible) and division.
+// unit of |v|, some 1e-6 where the result is not negligible) and division, and
+// the routers' normal distribution function (1e-6 relative; erff's two branches
+// take half as long again).
 template <bool PRECISE>
 __device__ __forceinline__ float gated_sigmoid(float v) {
   if constexpr (PRECISE) return 1.f / (1.f + expf(-v));
@@ -23,7 +26,8 @@ __device__ __forceinline__ float gated_sigmoid(float v) {
 template <bool PRECISE>
 __device__ __forceinline__ float gated_phi(float v) {  // the normal distribution function
   if constexpr (PRECISE) return normcdff(v);
-  return fmaf(0.5f, erff(v * 0.70710678118654752f), 0.5f);
+  // Past 30 it is 0 or 1; the fit would square a larger one to infinity.
+  return normal_cdf(fminf(fmaxf(v, -30.f), 30.f));
 }
 template <bool PRECISE, int ACT>
 __device__ __forceinline__ float gated_act(float v) {
@@ -157,6 +161,21 @@ cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t 
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                             const uint8_t *keep, const int32_t *base, const float *dX,
                             const void *dy, void *dx, cudaStream_t s);
+// The status word cleared, then the choices' slots, row maps, offsets and tile
+// prefix (launch_slots' outputs), in one launch. poff [E+1], or null: the
+// backward's padded offsets. Up to kRouteMost assignments.
+constexpr int kRouteMost = 32768;
+struct GatedRouteArgs {
+  int A, E, C;
+  const int32_t *idx;
+  const float *gate;
+  int32_t *pos;
+  uint8_t *keep;
+  int32_t *offset, *mtiles, *poff, *row_token;
+  float *row_gate;
+  DeviceStatus *st;
+};
+cudaError_t launch_gated_route(const GatedRouteArgs &a, cudaStream_t s);
 // Clears the status word: a kernel, for its place in the chain of dependent launches.
 cudaError_t launch_gated_begin(DeviceStatus *st, cudaStream_t s);
 

@@ -133,16 +133,25 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
 }
 
 // The status cleared and the choices' slots; pos and keep go to the caller's
-// arrays where given.
+// arrays where given. poff: the backward's padded offsets, or null.
 static int gated_slots(const moe_config &c, const GatedRoute &L, const int32_t *idx,
-                       const float *gate, int32_t *pos, uint8_t *keep, void *ws, cudaStream_t s) {
+                       const float *gate, int32_t *pos, uint8_t *keep, int32_t *poff, void *ws,
+                       cudaStream_t s) {
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.status);
+  if ((long long)c.T * c.k <= kRouteMost) {
+    MOE_CUDA(launch_gated_route({c.T * c.k, c.E, host_capacity(c), idx, gate, pos, keep,
+                                 ws_at<int32_t>(ws, L.offset), ws_at<int32_t>(ws, L.mtiles), poff,
+                                 ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate),
+                                 st}, s));
+    return MOE_OK;
+  }
   MOE_CUDA(launch_gated_begin(st, s));
   MOE_CUDA(launch_slots(c, host_capacity(c), idx, gate, ws_at<int32_t>(ws, L.hist),
                         ws_at<int32_t>(ws, L.chunk_base), ws_at<int32_t>(ws, L.count),
                         ws_at<int32_t>(ws, L.offset), ws_at<int32_t>(ws, L.mtiles), pos, keep,
                         ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate), L.n_chunks,
                         st, s));
+  if (poff) MOE_CUDA(launch_bwd_offsets(c.E, ws_at<int32_t>(ws, L.offset), poff, s));
   return MOE_OK;
 }
 
@@ -167,14 +176,13 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   const GatedRows rows = gated_rows(L.r, ws);
   const int32_t *pos = ws_at<int32_t>(ws, L.r.pos);
   const uint8_t *keep = ws_at<uint8_t>(ws, L.r.keep);
-  int32_t *poff = ws_at<int32_t>(ws, L.poff);
+  const int32_t *poff = ws_at<int32_t>(ws, L.poff);
   void *xbuf = ws_at<char>(ws, L.xbuf), *h = ws_at<char>(ws, L.h);
   void *dY = ws_at<char>(ws, L.dY), *dU = ws_at<char>(ws, L.dU);
   void *dP1 = ws_at<char>(ws, L.dP1), *dP3 = ws_at<char>(ws, L.dP3);
   float *dX = ws_at<float>(ws, L.dX), *dgpart = ws_at<float>(ws, L.dgpart);
   float *cpart = ws_at<float>(ws, L.cpart);
   const long long R = gated_max_rows(c), cap = host_capacity(c);
-  MOE_CUDA(launch_bwd_offsets(c.E, rows.offset, poff, s));
   MOE_CUDA(launch_gather(c, q.x, rows.offset, rows.row_token, xbuf, st, s));
   MOE_CUDA(launch_bwd_tail_zero(c, rows.offset, xbuf, h, s));
   MOE_CUDA(launch_bwd_gather(c, L.P_max, rows.offset, poff, rows.row_token, rows.row_gate, q.dy,
@@ -256,7 +264,7 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
   int32_t *ps = pos ? pos : ws_at<int32_t>(ws, L.r.pos);
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
-  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, ws, s);
+  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
   if (r != MOE_OK) return r;
   const long long R = gated_max_rows(c);
   void *z = ws_at<char>(ws, L.z);
@@ -316,7 +324,8 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   cudaStream_t s = (cudaStream_t)stream;
   int32_t *pos = ws_at<int32_t>(ws, L.r.pos);
   uint8_t *keep = ws_at<uint8_t>(ws, L.r.keep);
-  r = gated_slots(c, L.r, expert_idx, gate, pos, keep, ws, s);
+  r = gated_slots(c, L.r, expert_idx, gate, pos, keep,
+                  gated_tc_shape(c) ? ws_at<int32_t>(ws, L.poff) : nullptr, ws, s);
   if (r != MOE_OK) return r;
   if (gated_tc_shape(c)) {
     const GatedBwdCall q{activation, x, expert_idx, pre1, pre3, W1, W3, W2, b2, dy, dx,
@@ -374,9 +383,8 @@ int moe_weights_fp8(int32_t E, int32_t K, int32_t N, int32_t dtype, const void *
   MOE_REQ(W); MOE_REQ(w8); MOE_REQ(wscale);
   if (!ws || !aligned(ws, 256)) return MOE_ERR_ARG;
   cudaStream_t s = (cudaStream_t)stream;
-  DeviceStatus *st = ws_at<DeviceStatus>(ws, 0);
-  MOE_CUDA(launch_gated_begin(st, s));
-  MOE_CUDA(launch_fp8_weights(dtype == MOE_BF16, E, K, N, W, w8, wscale, st, s));
+  MOE_CUDA(launch_fp8_weights(dtype == MOE_BF16, E, K, N, W, w8, wscale,
+                              ws_at<DeviceStatus>(ws, 0), s));
   return MOE_OK;
 }
 
@@ -410,7 +418,7 @@ int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void 
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
   int32_t *ps = pos ? pos : ws_at<int32_t>(ws, L.r.pos);
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
-  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, ws, s);
+  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
   if (r != MOE_OK) return r;
   const GatedRows rows = gated_rows(L.r, ws);
   const int R = (int)gated_max_rows(c);

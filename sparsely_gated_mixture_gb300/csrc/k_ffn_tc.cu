@@ -54,6 +54,13 @@ constexpr int STG_BYTES = 4 * 2 * STG_TILE * 4;
 // The kernel's LAYER.
 constexpr int kGated = 3;
 constexpr int kGatedBN = BN / 2;  // output columns of a gated tile
+// The gated epilogue's exponential, reciprocal and up to three outputs an
+// element take eight warps, each with half of the tile's columns (with four,
+// short reductions wait for it: d = 512, 40 us a layer 1 against MEASURE).
+template <int LAYER>
+__host__ __device__ constexpr int epi_warps() { return LAYER == kGated ? 8 : 4; }
+template <int LAYER>
+__host__ __device__ constexpr int threads_of() { return 64 + 32 * epi_warps<LAYER>(); }
 
 // What the gated layer has beside the others' operands: W3, and the outputs p1
 // and p3 [rows, N] where they are kept.
@@ -64,6 +71,7 @@ struct Extra<kGated> {
   CUtensorMap b, o1, o3;
   const __nv_bfloat16 *bias3;  // [E, N] or null
   __nv_bfloat16 *pre1, *pre3;  // or null
+  int stg_tiles;               // one-CTA kernel: staging tiles of a warp, 1 or 2
 };
 
 struct Params {
@@ -117,32 +125,49 @@ struct TileMap {
   }
 };
 
-// A gated tile's outputs of one warp's rows: 32 columns at a time of both
-// halves of the accumulator at lane_addr. Warp-collective.
+// 32 values of a bias (a multiple of 64 columns, so 16-byte loads), or zeros.
+__device__ __forceinline__ void load_bias(const __nv_bfloat16 *b, size_t at, uint32_t (&w)[16]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint4 u = b ? *reinterpret_cast<const uint4 *>(b + at + 8 * q) : make_uint4(0, 0, 0, 0);
+    w[4 * q] = u.x;
+    w[4 * q + 1] = u.y;
+    w[4 * q + 2] = u.z;
+    w[4 * q + 3] = u.w;
+  }
+}
+__device__ __forceinline__ float bf16_of(uint32_t pair, int i) {
+  return __uint_as_float(i ? pair & 0xffff0000u : pair << 16);
+}
+
+// A gated tile's outputs of one warp's rows and half of its columns: 32 at a
+// time of both halves of the accumulator at lane_addr. stg: the warp's staging
+// tiles of 2 KB, `tiles` of them. Warp-collective.
 template <int ACT>
 __device__ __forceinline__ void gated_rows(const Params &p, const Extra<kGated> &ex,
                                            const CUtensorMap &tmO, uint32_t lane_addr, int e,
-                                           int n0, size_t r, bool valid, bool tma_rows, int r0,
-                                           float *stg, int tile_floats, uint32_t &cnt) {
+                                           int n0, int half, size_t r, bool valid, bool tma_rows,
+                                           int r0, float *stg, int tiles, uint32_t &cnt) {
   __nv_bfloat16 *const outs[3] = {ex.pre1, ex.pre3, static_cast<__nv_bfloat16 *>(p.out)};
   const CUtensorMap *const maps[3] = {&ex.o1, &ex.o3, &tmO};
+  constexpr int kChunks = kGatedBN / 64;
 #pragma unroll 1
-  for (int c = 0; c < kGatedBN / 32; ++c) {
+  for (int c = half * kChunks; c < (half + 1) * kChunks; ++c) {
     const int n = n0 + c * 32;
     uint32_t v1[32], v3[32];
     tmem_ld32(lane_addr + (uint32_t)(c * 32), v1);
     tmem_ld32(lane_addr + (uint32_t)(kGatedBN + c * 32), v3);
     if (!valid || n >= p.N) continue;
-    uint32_t packed[3][16];
+    uint32_t b1[16], b3[16], packed[3][16];
+    load_bias(p.bias, (size_t)e * p.N + n, b1);
+    load_bias(ex.bias3, (size_t)e * p.N + n, b3);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       float p1[2], p3[2], h[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        p1[i] = __uint_as_float(v1[2 * j + i]);
-        p3[i] = __uint_as_float(v3[2 * j + i]);
-        if (p.bias) p1[i] += __bfloat162float(p.bias[(size_t)e * p.N + n + 2 * j + i]);
-        if (ex.bias3) p3[i] += __bfloat162float(ex.bias3[(size_t)e * p.N + n + 2 * j + i]);
+        p1[i] = __uint_as_float(v1[2 * j + i]) + bf16_of(b1[j], i);
+        p3[i] = __uint_as_float(v3[2 * j + i]) + bf16_of(b3[j], i);
         h[i] = gated_act<false, ACT>(p1[i]) * p3[i];
       }
       __nv_bfloat162 b = __floats2bfloat162_rn(p1[0], p1[1]);
@@ -156,7 +181,8 @@ __device__ __forceinline__ void gated_rows(const Params &p, const Extra<kGated> 
     for (int o = 0; o < 3; ++o) {
       if (!outs[o]) continue;
       if (tma_rows) {
-        stage_store_bf16(maps[o], stg + (cnt & 1u) * tile_floats, packed[o], n, r0);
+        if (tiles == 1 && (threadIdx.x & 31) == 0) bulk_wait_read_all();
+        stage_store_bf16(maps[o], stg + (cnt & (uint32_t)(tiles - 1)) * STG_TILE, packed[o], n, r0);
         ++cnt;
       } else {
         uint4 *w = reinterpret_cast<uint4 *>(outs[o] + r * p.N + n);
@@ -173,7 +199,7 @@ __device__ __forceinline__ void gated_rows(const Params &p, const Extra<kGated> 
 // columns] box, or fp32 (layer 2's Z) with a [32 rows, 16 columns] box, both
 // in the 64-byte swizzle.
 template <int LAYER, int ACT = 0>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of<LAYER>(), 1)
 k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
          const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Extra<LAYER> ex,
          const Params p) {
@@ -185,7 +211,12 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
   uint8_t *sA = smem;
   uint8_t *sB = smem + STAGES * A_BYTES;
   float *stg_all = reinterpret_cast<float *>(sB + STAGES * B_BYTES);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + STAGES * B_BYTES + STG_BYTES);
+  int stg_bytes = STG_BYTES, stg_warp = 2 * STG_TILE;  // bytes in all, floats a warp
+  if constexpr (LAYER == kGated) {
+    stg_warp = ex.stg_tiles * STG_TILE;
+    stg_bytes = epi_warps<LAYER>() * stg_warp * 4;
+  }
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sB + STAGES * B_BYTES + stg_bytes);
   uint64_t *full = bars, *empty = bars + STAGES;
   uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = acc_full + 2, *drain = acc_empty + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
@@ -201,7 +232,7 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4);  // one arrival per epilogue warp
+      mbar_init(&acc_empty[b], epi_warps<LAYER>());  // one arrival per epilogue warp
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -328,7 +359,7 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     // ----------------------------------------------------------------- epilogue
     const int quad = warp & 3;  // TMEM lanes 32*quad .. 32*quad+31
     const int r_in_tile = quad * 32 + lane;
-    float *stg = stg_all + (size_t)(warp - 2) * 2 * STG_TILE;  // this warp's two tiles
+    float *stg = stg_all + (size_t)(warp - 2) * stg_warp;  // this warp's two tiles
     uint32_t stg_cnt = 0;
     int local = 0;
     for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x, ++local) {
@@ -353,7 +384,8 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
       if constexpr (LAYER == kGated)
         gated_rows<ACT>(p, ex, tmO,
                         tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN), e,
-                        nb * kGatedBN, r, valid, tma_rows, r0, stg, STG_TILE, stg_cnt);
+                        nb * kGatedBN, (warp - 2) >> 2, r, valid, tma_rows, r0, stg, ex.stg_tiles,
+                        stg_cnt);
       else
 #pragma unroll 1
       for (int c = 0; c < BN / 32; ++c) {
@@ -493,7 +525,7 @@ __device__ __forceinline__ void umma_pair(uint32_t tmem_d, uint64_t a, uint64_t 
       : "memory");
 }
 template <int LAYER, int ACT = 0>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of<LAYER>(), 1)
 k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
               const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Extra<LAYER> ex,
               const Params p) {
@@ -525,11 +557,11 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 8);  // four epilogue warps in each CTA
+      mbar_init(&acc_empty[b], 2 * epi_warps<LAYER>());  // the epilogue warps of both CTAs
     }
     for (int r = 0; r < kRing; ++r) {
       mbar_init(&tfull[r], 1);                // the even CTA's producer publishes
-      mbar_init(&tempty[r], kRingConsumers);  // used in the even CTA only
+      mbar_init(&tempty[r], kRingConsumers + 2 * (epi_warps<LAYER>() - 4));  // even CTA only
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -742,7 +774,8 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int r_in_tile = quad * 32 + lane;
     const uint32_t acc_empty_leader0 = mapa(smem_u32(&acc_empty[0]), 0);
     const uint32_t acc_empty_leader1 = mapa(smem_u32(&acc_empty[1]), 0);
-    float *stg = stg_all + (size_t)(warp - 2) * 2 * P_STG_TILE;  // this warp's two tiles
+    // This warp's two tiles (the gated layer's eight warps: of 2 KB).
+    float *stg = stg_all + (size_t)(warp - 2) * 2 * (LAYER == kGated ? STG_TILE : P_STG_TILE);
     uint32_t stg_cnt = 0;                                         // chunks staged so far
     for (int local = 0;; ++local) {
       const int slot = local % kRing;
@@ -786,7 +819,7 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       if constexpr (LAYER == kGated)
         gated_rows<ACT>(p, ex, tmO,
                         tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN), e,
-                        nb * kGatedBN, r, valid, tma_rows, r0, stg, P_STG_TILE, stg_cnt);
+                        nb * kGatedBN, (warp - 2) >> 2, r, valid, tma_rows, r0, stg, 2, stg_cnt);
       else
 #pragma unroll 1
       for (int c = 0; c < nchunks; ++c) {
@@ -960,18 +993,23 @@ int sm_count() {
 
 namespace {
 
-constexpr size_t smem_bytes(int E) {
-  return 1024 + (size_t)STAGES * STAGE_BYTES + STG_BYTES + (2 * STAGES + 5) * 8 + 8 +
+constexpr size_t smem_bytes(int E, int stg = STG_BYTES) {
+  return 1024 + (size_t)STAGES * STAGE_BYTES + stg + (2 * STAGES + 5) * 8 + 8 +
          (size_t)(E + 1) * 4;
+}
+// The gated layer's staging: a second tile a warp where many experts leave room.
+constexpr int gated_stg_tiles(int E) {
+  return smem_bytes(E, 2 * STG_BYTES) <= kSmemMost ? 2 : 1;
 }
 
 template <int LAYER, int ACT = 0>
 cudaError_t launch_layer(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
                          const Params &p, cudaStream_t s, const Extra<LAYER> &ex = {}) {
-  const size_t smem = smem_bytes(p.E);
+  const size_t smem =
+      smem_bytes(p.E, LAYER == kGated ? gated_stg_tiles(p.E) * STG_BYTES : STG_BYTES);
   cudaError_t err = allow_smem(k_ffn_tc<LAYER, ACT>);
   if (err != cudaSuccess) return err;
-  launch_pdl_c(kPdlGemm, k_ffn_tc<LAYER, ACT>, sm_count(), kThreads, smem, s, a, b, o, ex, p);
+  launch_pdl_c(kPdlGemm, k_ffn_tc<LAYER, ACT>, sm_count(), threads_of<LAYER>(), smem, s, a, b, o, ex, p);
   return cudaGetLastError();
 }
 
@@ -1030,7 +1068,7 @@ cudaError_t launch_layer_pair(const CUtensorMap &a, const CUtensorMap &b, const 
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads_of<LAYER>());
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2] = {pair_cluster_attr(), {}};
@@ -1170,6 +1208,7 @@ cudaError_t launch_gated_tc_layer1(const moe_config &c, int C, int activation, l
   ex.bias3 = static_cast<const __nv_bfloat16 *>(b3);
   ex.pre1 = static_cast<__nv_bfloat16 *>(pre1);
   ex.pre3 = static_cast<__nv_bfloat16 *>(pre3);
+  ex.stg_tiles = gated_stg_tiles(c.E);
   ex.o1 = ex.o3 = to = ta;  // unused unless made
   p.tma_out = make_rows_map(&to, hbuf, A, c.d_ff, false) &&
               (!pre1 || (make_rows_map(&ex.o1, pre1, A, c.d_ff, false) &&

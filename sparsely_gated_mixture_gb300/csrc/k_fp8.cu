@@ -8,32 +8,65 @@ namespace {
 
 constexpr int B = kFp8Block;
 
-template <typename T>
-__device__ __forceinline__ float ld(const T *p, size_t i) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(p[i]);
-  else return p[i];
-}
+// Eight values along N of one row, as floats; VEC: 16-byte loads (the row
+// starts on 16 bytes and N is a multiple of 8, or 4 for fp32).
+template <typename T, bool VEC>
+struct Eight {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T *row, int n, int N) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+        u[i] = n + i * 4 < N ? *reinterpret_cast<const uint4 *>(row + n + i * 4)
+                             : make_uint4(0, 0, 0, 0);
+    } else {
+      T t[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = n + j < N ? row[n + j] : T(0.f);
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(t)[i];
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(u);
+    if constexpr (sizeof(T) == 2)
+      return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    return __uint_as_float(w[j]);
+  }
+};
 
-// One block of 256 threads for a 128 x 128 block of one expert's weight: read
-// along N, written along K.
-template <typename T>
+// One block of 256 threads for a 128 x 128 block of one expert's weight, read
+// along N and written along K. A thread holds 8 rows of 8 columns (v = tid % 16
+// its eighth of columns, q = tid / 16 of rows), all of its loads in flight at
+// once; its bytes change places through shared memory, where the 8-byte piece q
+// of column n stands at q ^ v, so that neither side meets bank conflicts.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
-k_fp8_weights(int K, int N, int KB, const T *__restrict__ W, uint8_t *__restrict__ q,
+k_fp8_weights(int K, int N, int KB, const T *__restrict__ W, uint8_t *__restrict__ out,
               uint8_t *__restrict__ scale, DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float tile[];  // [128 k][129]
+  __shared__ uint2 tile[B * 16];
   __shared__ float tops[8];
-  const int kb = blockIdx.x, nb = blockIdx.y, e = blockIdx.z;
-  const int tid = threadIdx.x, n = tid & 127;
+  const int nb = blockIdx.x, kb = blockIdx.y, e = blockIdx.z;
+  const int tid = threadIdx.x, v = tid & 15, q = tid >> 4;
+  const int n = nb * B + v * 8, k0 = kb * B + q * 8;
   const T *src = W + (size_t)e * K * N;
-  float top = 0.f;
-  for (int i = tid >> 7; i < B; i += 2) {
-    const int kk = kb * B + i, nn = nb * B + n;
-    const float v = kk < K && nn < N ? ld(src, (size_t)kk * N + nn) : 0.f;
-    tile[i * 129 + n] = v;
-    top = max_nan(top, fabsf(v));
+  Eight<T, VEC> r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (k0 + i < K) r[i].load(src + (size_t)(k0 + i) * N, n, N);
+    else r[i].zero();
   }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(r[i].get(j)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((tid & 31) == 0) tops[tid >> 5] = top;
@@ -42,19 +75,29 @@ k_fp8_weights(int K, int N, int KB, const T *__restrict__ W, uint8_t *__restrict
   for (int w = 0; w < 8; ++w) top = max_nan(top, tops[w]);
   const uint32_t byte = fp8_scale_byte(top);
   const float inv = fp8_inverse(byte);
-  const size_t at = ((size_t)e * gridDim.y + nb) * KB + kb;
   if (tid == 0) {
+    const size_t at = ((size_t)e * gridDim.x + nb) * KB + kb;
     scale[at] = (uint8_t)byte;
     if (byte == 255u) record_error(st, MOE_ERR_NONFINITE, (long long)at);
   }
-  // Each warp a column, 4 values a lane.
-  const int lane = tid & 31;
-  for (int c = tid >> 5; c < B && nb * B + c < N; c += 8) {
-    float v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = tile[(lane * 4 + j) * 129 + c] * inv;
-    const uint32_t u = fp8_pack2(v[0], v[1]) | fp8_pack2(v[2], v[3]) << 16;
-    *reinterpret_cast<uint32_t *>(q + ((size_t)e * N + nb * B + c) * KB * B + kb * B + lane * 4) = u;
+  for (int j = 0; j < 8; ++j) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = fp8_pack2(r[4 * h].get(j) * inv, r[4 * h + 1].get(j) * inv) |
+             fp8_pack2(r[4 * h + 2].get(j) * inv, r[4 * h + 3].get(j) * inv) << 16;
+    tile[(v * 8 + j) * 16 + (q ^ v)] = make_uint2(w[0], w[1]);
+  }
+  __syncthreads();
+  // Eight lanes write a column's 128 bytes.
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = i * 32 + (tid >> 3), piece = tid & 7, vc = c >> 3;
+    uint4 u = reinterpret_cast<const uint4 *>(tile)[c * 8 + (piece ^ (vc >> 1))];
+    if (vc & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+    if (nb * B + c < N)
+      reinterpret_cast<uint4 *>(out + ((size_t)e * N + nb * B + c) * KB * B + kb * B)[piece] = u;
   }
 }
 
@@ -92,18 +135,17 @@ k_fp8_rows(int max_rows, int K, int KB, int k, const int32_t *__restrict__ count
 cudaError_t launch_fp8_weights(bool bf16, int E, int K, int N, const void *W, uint8_t *q,
                                uint8_t *scale, DeviceStatus *st, cudaStream_t s) {
   const int KB = (int)fp8_blocks(K);
-  const dim3 grid(KB, (unsigned)fp8_blocks(N), E);
-  constexpr size_t smem = 128 * 129 * 4;
+  const dim3 grid((unsigned)fp8_blocks(N), KB, E);  // blocks side by side read on along a row
+  const auto run = [&](auto kernel, auto *w) {
+    return launch_pdl(kernel, grid, 256, 0, s, K, N, KB, w, q, scale, st);
+  };
   if (bf16) {
-    const cudaError_t err = allow_smem(k_fp8_weights<__nv_bfloat16>, smem);
-    if (err != cudaSuccess) return err;
-    return launch_pdl(k_fp8_weights<__nv_bfloat16>, grid, 256, smem, s, K, N, KB,
-                      (const __nv_bfloat16 *)W, q, scale, st);
+    const auto *w = static_cast<const __nv_bfloat16 *>(W);
+    return N % 8 == 0 ? run(k_fp8_weights<__nv_bfloat16, true>, w)
+                      : run(k_fp8_weights<__nv_bfloat16, false>, w);
   }
-  const cudaError_t err = allow_smem(k_fp8_weights<float>, smem);
-  if (err != cudaSuccess) return err;
-  return launch_pdl(k_fp8_weights<float>, grid, 256, smem, s, K, N, KB, (const float *)W, q, scale,
-                    st);
+  const auto *w = static_cast<const float *>(W);
+  return N % 4 == 0 ? run(k_fp8_weights<float, true>, w) : run(k_fp8_weights<float, false>, w);
 }
 
 cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,

@@ -1,5 +1,5 @@
-// What surrounds the products of the gated experts' backward: dL/dgate of each
-// choice from the products' partial sums, and the gradient of x.
+// What surrounds the gated experts' products: the choices' slots in one launch,
+// dL/dgate of each choice from the products' partial sums, the gradient of x.
 #include "gated.cuh"
 
 namespace moe {
@@ -14,6 +14,124 @@ __device__ __forceinline__ float ld(const T *p, size_t i) {
 __global__ void k_gated_begin(DeviceStatus *st) {
   pdl_wait();
   if (threadIdx.x < sizeof(DeviceStatus) / 4) reinterpret_cast<uint32_t *>(st)[threadIdx.x] = 0;
+}
+
+// Exclusive sum of v over the block's 256 threads; *total gets the whole.
+__device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();  // the last call's reads of warps are done
+  if (lane == 31) warps[warp] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) before += warps[w];
+    all += warps[w];
+  }
+  *total = all;
+  return before + incl - v;
+}
+
+// Slots without a pass over the grid between: a block ranks 256 assignments
+// and counts, for itself, all of them before its own and all after. A batch of
+// kRouteMost choices is 128 KB that every block reads from L2; the histogram,
+// scan and rank passes for long batches and a separate clearing of the status
+// word take four launches (4096 tokens of top 4: 17 us against 6).
+constexpr int kRouteChunk = 256;
+__global__ void __launch_bounds__(kRouteChunk) k_gated_route(const GatedRouteArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int route_mem[];
+  int *before = route_mem, *total = before + p.E, *off = total + p.E;  // [E], [E], [E + 1]
+  __shared__ int own[kRouteChunk];
+  __shared__ int warps[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int a0 = (int)blockIdx.x * kRouteChunk, a = a0 + tid;
+  const bool first = blockIdx.x == 0;
+  if (first && tid < (int)(sizeof(DeviceStatus) / 4)) reinterpret_cast<uint32_t *>(p.st)[tid] = 0;
+  for (int e = tid; e < 2 * p.E; e += kRouteChunk) route_mem[e] = 0;
+  int mine = a < p.A ? p.idx[a] : -1;
+  if (mine >= p.E) mine = -1;
+  own[tid] = mine;
+  __syncthreads();
+  // Sixteen loads in flight a thread.
+  for (int i0 = tid; i0 < p.A; i0 += 16 * kRouteChunk) {
+    int e[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int i = i0 + j * kRouteChunk;
+      e[j] = i < p.A ? p.idx[i] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int i = i0 + j * kRouteChunk;
+      if (e[j] >= 0 && e[j] < p.E)
+        atomicAdd(i < a0 ? &before[e[j]] : &total[e[j]], 1);
+      else if (first && i < p.A)
+        record_error(p.st, MOE_ERR_BOUNDS, (long long)i);  // after block 0's clearing
+    }
+  }
+  __syncthreads();
+  // Kept rows, their offsets and the tiles of 128 rows, four experts a thread.
+  int rows[4], n = 0, tiles = 0, pads = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = 4 * tid + j;
+    rows[j] = 0;
+    if (e < p.E) {
+      rows[j] = min(before[e] + total[e], p.C);
+      tiles += (rows[j] + kTcBM - 1) / kTcBM;
+      pads += max(kBwdRowPad, (rows[j] + kBwdRowPad - 1) / kBwdRowPad * kBwdRowPad);
+    }
+    n += rows[j];
+  }
+  int all;
+  int at = block_scan(n, warps, &all);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (4 * tid + j < p.E) {
+      off[4 * tid + j] = at;
+      if (first) p.offset[4 * tid + j] = at;
+    }
+    at += rows[j];
+  }
+  if (first) {
+    if (tid == 0) p.offset[p.E] = all;
+    int tile = block_scan(tiles, warps, &all);
+    if (tid == 0) p.mtiles[p.E] = all;
+    int pad = block_scan(pads, warps, &all);
+    if (tid == 0 && p.poff) p.poff[p.E] = all;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = 4 * tid + j;
+      if (e >= p.E) break;
+      p.mtiles[e] = tile;
+      tile += (rows[j] + kTcBM - 1) / kTcBM;
+      if (p.poff) p.poff[e] = pad;
+      pad += max(kBwdRowPad, (rows[j] + kBwdRowPad - 1) / kBwdRowPad * kBwdRowPad);
+    }
+  }
+  __syncthreads();
+  // The rank among the block's own: equal lanes before this one, and the warps
+  // before.
+  const unsigned peers = __match_any_sync(0xffffffffu, mine);
+  int rank = __popc(peers & ((1u << lane) - 1u));
+  for (int i = 0; i < warp * 32; ++i) rank += own[i] == mine;
+  if (a >= p.A) return;
+  const int ps = mine < 0 ? -1 : before[mine] + rank;
+  const bool kept = mine >= 0 && ps < p.C;
+  p.pos[a] = ps;
+  p.keep[a] = kept ? 1 : 0;
+  if (kept) {
+    p.row_token[off[mine] + ps] = a;
+    p.row_gate[off[mine] + ps] = p.gate[a];
+  }
 }
 
 // The row of assignment a = t*k + j, or -1 (dropped, or not an expert).
@@ -79,6 +197,11 @@ k_gated_dx(int T_, int E, int k, int d, const int32_t *__restrict__ idx,
 }
 
 }  // namespace
+
+cudaError_t launch_gated_route(const GatedRouteArgs &a, cudaStream_t s) {
+  return launch_pdl(k_gated_route, (a.A + kRouteChunk - 1) / kRouteChunk, kRouteChunk,
+                    (3 * (size_t)a.E + 1) * 4, s, a);
+}
 
 cudaError_t launch_gated_begin(DeviceStatus *st, cudaStream_t s) {
   return launch_pdl(k_gated_begin, 1, 32, 0, s, st);

@@ -328,7 +328,7 @@ def quantise(g, name, dt):
     W = g[name]
     E, K, N = W.shape
     n8, ns = B.moe_weights_fp8_size(E, K, N)
-    q, sc, ws = buf(n8), buf(ns), buf(256)
+    q, sc, ws = buf(n8), buf(ns), buf(256, 0)
     B.moe_weights_fp8(E, K, N, B.MOE_BF16 if dt == BF16 else B.MOE_F32, W, q, sc, ws)
     assert B.moe_last_device_status(ws)[0] == 0
     return q.view(E, N, -1), sc.view(E, R.blocks(N), R.blocks(K))
@@ -370,7 +370,7 @@ def test_weights_fp8_borders():
         W = torch.ones((2, 130, 5), device="cuda")
         W[1, 129, 3] = bad
         n8, ns = B.moe_weights_fp8_size(2, 130, 5)
-        q, sc, ws = buf(n8), buf(ns), buf(256)
+        q, sc, ws = buf(n8), buf(ns), buf(256, 0)
         B.moe_weights_fp8(2, 130, 5, B.MOE_F32, W, q, sc, ws)
         assert B.moe_last_device_status(ws) == (4, 3)
         assert sc.tolist() == [119, 119, 119, 255]
