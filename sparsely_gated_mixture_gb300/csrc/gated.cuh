@@ -3,7 +3,6 @@
 //   U(x) = (act(x W1 + b1) * (x W3 + b3)) W2 + b2
 #pragma once
 
-#include "gate_math.cuh"
 #include "moe_internal.cuh"
 
 #include <cuda_fp8.h>
@@ -13,43 +12,115 @@
 namespace moe {
 
 // ----------------------------------------------------------------------------- activations
-// act(v) and, for the backward, act'(v) with act(v). PRECISE is for fp32
-// layers; bf16 layers take the fast exponential (2 ulp and 1.2 ulp for each
-// unit of |v|, some 1e-6 where the result is not negligible) and division, and
-// the routers' normal distribution function (1e-6 relative; erff's two branches
-// take half as long again).
-template <bool PRECISE>
-__device__ __forceinline__ float gated_sigmoid(float v) {
-  if constexpr (PRECISE) return 1.f / (1.f + expf(-v));
-  return __fdividef(1.f, 1.f + fminf(__expf(-v), 1e30f));  // the fast division wants < 2^126
-}
-template <bool PRECISE>
-__device__ __forceinline__ float gated_phi(float v) {  // the normal distribution function
-  if constexpr (PRECISE) return normcdff(v);
-  // Past 30 it is 0 or 1; the fit would square a larger one to infinity.
-  return normal_cdf(fminf(fmaxf(v, -30.f), 30.f));
-}
-template <bool PRECISE, int ACT>
-__device__ __forceinline__ float gated_act(float v) {
-  if constexpr (ACT == MOE_ACT_SILU) return v * gated_sigmoid<PRECISE>(v);
-  if constexpr (ACT == MOE_ACT_GELU) return v * gated_phi<PRECISE>(v);
-  return max_nan(v, 0.f);
-}
-template <bool PRECISE, int ACT>
+// act(v) and, for the backward, act'(v) with act(v): for the CUDA cores' kernels
+// one value, for fp32 layers by CUDA's own functions.
+template <int ACT>
 __device__ __forceinline__ void gated_act_slope(float v, float &a, float &s) {
   if constexpr (ACT == MOE_ACT_SILU) {
-    const float t = gated_sigmoid<PRECISE>(v);
+    const float t = 1.f / (1.f + expf(-v));
     a = v * t;
     s = t * fmaf(v, 1.f - t, 1.f);
   } else if constexpr (ACT == MOE_ACT_GELU) {
-    const float t = gated_phi<PRECISE>(v);
-    const float e = PRECISE ? expf(-0.5f * v * v) : __expf(-0.5f * v * v);
+    const float t = normcdff(v);
     a = v * t;
-    s = fmaf(v * 0.3989422804014327f, e, t);
+    s = fmaf(v * 0.3989422804014327f, expf(-0.5f * v * v), t);
   } else {
     a = max_nan(v, 0.f);
     s = v > 0.f ? 1.f : 0.f;
   }
+}
+
+// Two floats at once: packed fp32 arithmetic takes one instruction for both.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mov.b64 z, {%6, %7};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// act(v) and, with SLOPE, act'(v) of two values, for the tensor-core kernels'
+// epilogues, whose instructions are what bounds short reductions. The
+// exponential and the reciprocal are the hardware's (2^-22 and 2^-23 relative;
+// an exponential that overflows ends in a zero). The normal distribution
+// function is normal_cdf's fit (gate_math.cuh) without the compensation of z^2:
+// some 1e-6 relative where it is over 1e-7. No branches, so values of either
+// sign cost the same.
+template <int ACT, bool SLOPE>
+__device__ __forceinline__ float2 gated_act2(float2 v, float2 *slope) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  if constexpr (ACT == MOE_ACT_SILU) {
+    const float2 z = mul2(v, both(-kLog2e));
+    const float2 d = add2(make_float2(exp2_fast(z.x), exp2_fast(z.y)), both(1.f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    const float2 a = mul2(v, t);
+    if constexpr (SLOPE) *slope = fma2(a, fma2(t, both(-1.f), both(1.f)), t);
+    return a;
+  } else if constexpr (ACT == MOE_ACT_GELU) {
+    const float2 m = make_float2(fabsf(v.x), fabsf(v.y));
+    const float2 d = fma2(m, both(0.35355339059327376f), both(1.f));  // 1 + z / 2, z = |v| / sqrt 2
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    float2 q = both(0.17087277f);
+    q = fma2(t, q, both(-0.82215223f));
+    q = fma2(t, q, both(1.48851587f));
+    q = fma2(t, q, both(-1.13520398f));
+    q = fma2(t, q, both(0.27886807f));
+    q = fma2(t, q, both(-0.18628806f));
+    q = fma2(t, q, both(0.09678418f));
+    q = fma2(t, q, both(0.37409196f));
+    q = fma2(t, q, both(1.00002368f));
+    q = fma2(t, q, both(-1.26551223f - 0.69314718f));  // with the half of erfc / 2
+    const float2 zz = mul2(mul2(m, m), both(-0.5f * kLog2e));
+    const float2 x = fma2(q, both(kLog2e), zz);
+    const float2 tail = mul2(t, make_float2(exp2_fast(x.x), exp2_fast(x.y)));  // Phi(-|v|)
+    if constexpr (SLOPE) {
+      const float2 g = mul2(v, both(0.3989422804014327f));
+      const float2 phi = make_float2(v.x < 0.f ? tail.x : 1.f - tail.x,
+                                     v.y < 0.f ? tail.y : 1.f - tail.y);
+      *slope = fma2(g, make_float2(exp2_fast(zz.x), exp2_fast(zz.y)), phi);
+    }
+    // v Phi(v) = max(v, 0) - |v| Phi(-|v|)
+    return fma2(make_float2(-m.x, -m.y), tail, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+  } else {
+    if constexpr (SLOPE) *slope = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
+    return make_float2(max_nan(v.x, 0.f), max_nan(v.y, 0.f));
+  }
+}
+// A bf16 pair as floats, and two floats as one.
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t *>(&b);
 }
 
 // Calls f with the activation as a compile-time constant.
@@ -157,6 +228,12 @@ cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t 
                                const int32_t *pos, const uint8_t *keep, const int32_t *base,
                                const float *dgpart, const void *dy, const void *b2, float *dgate,
                                cudaStream_t s);
+// The bias gradients (each may be null) db2 = the column sums of dU [rows, d],
+// db1 and db3 of dP1 and dP3 [rows, d_ff], over each expert's rows from base[e]
+// on; rows in act_dtype, or fp32 (src_f32), sums in act_dtype.
+cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t *offset,
+                                const int32_t *base, const void *dU, void *db2, const void *dP1,
+                                void *db1, const void *dP3, void *db3, cudaStream_t s);
 // dx = dy + the kept choices' rows base[e] + pos of dX.
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                             const uint8_t *keep, const int32_t *base, const float *dX,

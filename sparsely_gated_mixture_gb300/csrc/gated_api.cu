@@ -104,9 +104,9 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
 // padded blocks (offsets poff). CUDA cores: fp32 packed rows, no xbuf and dY.
 struct GatedBwdLayout {
   GatedRoute r;
-  size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, cpart, total;
+  size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, total;
   long long P_max;
-  int dg_blocks, chunks;
+  int dg_blocks;
 };
 static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   GatedBwdLayout L{};
@@ -117,7 +117,6 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   const size_t P = (size_t)L.P_max, eb = tc ? 2 : 4;
   L.r = gated_route(c, take);
   L.dg_blocks = tc ? 2 * ((c.d_ff + 255) / 256) : gated_simt_dg_blocks(c, (int)R);
-  L.chunks = colsum_chunks(host_capacity(c));
   L.poff = take(((size_t)c.E + 1) * 4);
   L.xbuf = take(tc ? (R + kBwdRowPad) * d * 2 : 0);
   L.h = take((R + (tc ? kBwdRowPad : 0)) * F * eb);
@@ -127,7 +126,6 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   L.dP3 = take(P * F * eb);
   L.dX = take(P * d * 4);
   L.dgpart = take(P * L.dg_blocks * 4);
-  L.cpart = take((size_t)L.chunks * c.E * (d + F) * 4);
   L.total = take.off;
   return L;
 }
@@ -181,7 +179,6 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   void *dY = ws_at<char>(ws, L.dY), *dU = ws_at<char>(ws, L.dU);
   void *dP1 = ws_at<char>(ws, L.dP1), *dP3 = ws_at<char>(ws, L.dP3);
   float *dX = ws_at<float>(ws, L.dX), *dgpart = ws_at<float>(ws, L.dgpart);
-  float *cpart = ws_at<float>(ws, L.cpart);
   const long long R = gated_max_rows(c), cap = host_capacity(c);
   MOE_CUDA(launch_gather(c, q.x, rows.offset, rows.row_token, xbuf, st, s));
   MOE_CUDA(launch_bwd_tail_zero(c, rows.offset, xbuf, h, s));
@@ -194,14 +191,10 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   g.pre3 = q.pre3;
   g.out3 = dP3;
   g.h = h;
-  g.h_rows = R;
   MOE_CUDA(launch_bwd_gemm(g, st, s));
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
                               s));
-  MOE_CUDA(launch_bwd_colsum(c, L.chunks, rows.offset, poff, nullptr, dU, dP1, false, cpart, q.db2,
-                             q.db1, true, s));
-  MOE_CUDA(launch_bwd_colsum(c, L.chunks, rows.offset, poff, nullptr, dU, dP3, false, cpart,
-                             nullptr, q.db3, true, s));
+  MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dU, q.db2, dP1, q.db1, dP3, q.db3, s));
   BwdGemm gx{4, c.d_ff, c.d, 0, c.E, L.P_max, 0, 0, dP1, q.W1, rows.offset, poff, nullptr, nullptr,
              dX, nullptr, false};
   gx.A3 = dP3;
@@ -354,12 +347,7 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   const int32_t *off = p.rows.offset;
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, expert_idx, pos, keep, off, p.dgpart, dy, b2, dgate,
                               s));
-  float *cpart = ws_at<float>(ws, L.cpart);
-  const bool bf16 = c.act_dtype == MOE_BF16;
-  MOE_CUDA(launch_bwd_colsum(c, L.chunks, off, off, nullptr, p.dU, p.dP1, true, cpart, db2, db1,
-                             bf16, s));
-  MOE_CUDA(launch_bwd_colsum(c, L.chunks, off, off, nullptr, p.dU, p.dP3, true, cpart, nullptr,
-                             db3, bf16, s));
+  MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, db2, p.dP1, db1, p.dP3, db3, s));
   MOE_CUDA(launch_gated_dx(c, expert_idx, pos, keep, off, p.dX, dy, dx, s));
   return MOE_OK;
 }

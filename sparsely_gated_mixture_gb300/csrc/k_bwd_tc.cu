@@ -81,7 +81,6 @@ template <int MODE>
 struct BExtra {};
 template <>
 struct BExtra<3> {
-  CUtensorMap o3, oh;  // dP3 [padded rows, N], h [packed rows, N]: box [32, 32]
   const __nv_bfloat16 *pre1, *pre3;  // [packed rows, N]
   __nv_bfloat16 *dP3, *h;
 };
@@ -92,17 +91,17 @@ struct BExtra<4> {
 
 // Mode 3 has the heaviest epilogue (two operands read, three written, an
 // exponential and a reciprocal an element): eight warps instead of four, each
-// with four staging tiles of 2 KB, at the price of one or two stages of the ring.
+// with three staging tiles of 2 KB, at the price of one or two stages of the ring.
 template <int MODE>
 __host__ __device__ constexpr int epi_warps() { return MODE == 3 ? 8 : 4; }
 template <int MODE>
 __host__ __device__ constexpr int threads_of() { return 64 + 32 * epi_warps<MODE>(); }
 template <int MODE>
 __host__ __device__ constexpr int stages_of(bool pair) {
-  return pair ? (MODE == 3 ? 4 : 6) : (MODE == 3 ? 3 : 4);
+  return pair ? (MODE == 3 ? 5 : 6) : (MODE == 3 ? 3 : 4);
 }
 constexpr int G_TILE = 32 * 32 / 2;             // a staging tile of bf16, counted in floats
-constexpr int G_STG_BYTES = 8 * 4 * G_TILE * 4;  // mode 3
+constexpr int G_STG_BYTES = 8 * 3 * G_TILE * 4;  // mode 3
 
 // The CTA-pair kernel's tile ring, as in the forward expert GEMM: tile
 // indices from the even CTA's producer to the MMA issuer, both CTAs'
@@ -316,25 +315,23 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
 }
 
 // Mode 3's epilogue for one warp: its 32 rows and half of the tile's columns
-// (half 0 or 1), 32 at a time. The pre-activations of the next 32 columns are
-// fetched while these are worked on, four lanes to a row (a lane to a row would
-// touch 32 lines an instruction), and change to a lane's own row through the
-// warp's staging tiles 0 and 1; the outputs leave through tiles 2 and 3.
-// Warp-collective.
+// (half 0 or 1), 32 at a time. Global memory is read and written four lanes to a
+// row (a lane to a row would touch 32 lines an instruction); p1 and p3 of the
+// next 32 columns are fetched while these are worked on. They change to a lane's
+// own row through two of the warp's three staging tiles, where dP1 and dP3 take
+// their places, and h the third's, on the way back. Warp-collective.
 template <int ACT>
 __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3> &ex,
                                                const BTile &t, int m0, int half,
-                                               uint32_t lane_addr, float *stg,
-                                               const CUtensorMap *tmO, uint32_t &cnt) {
+                                               uint32_t lane_addr, float *stg) {
   const int lane = threadIdx.x & 31;
   const int m = m0 + lane;
   if (m0 >= t.prows) return;  // padded rows come in 64s: all of the warp's or none
-  const bool real = m < t.rows, tma = p.tma_out, whole = tma && m0 + 32 <= t.rows;
+  const bool real = m < t.rows;
   const size_t pr = (size_t)t.prow0 + m;
   const int q0 = p.offset[t.e] + m0;  // packed row of the warp's first
   const float g = real ? p.row_gate[q0 + lane] : 0.f;
-  float part = 0.f;
-  bool bad = false;
+  float2 part = both(0.f), odd = both(0.f);
   const int sub = lane >> 2, quarter = lane & 3;
   uint4 pre[2][4];
   const auto fetch = [&](int n) {
@@ -347,76 +344,68 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
       pre[1][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre3 + at) : make_uint4(0, 0, 0, 0);
     }
   };
-  const int c0 = half * (BN / 64);
+  uint4 *const tile = reinterpret_cast<uint4 *>(stg);
+  constexpr int kTile = G_TILE / 4;  // in 16-byte pieces
+  const auto piece = [&](int i) {  // of row sub + 8 i
+    const int row = sub + 8 * i;
+    return row * 4 + (quarter ^ ((row >> 1) & 3));
+  };
+  const int c0 = half * (BN / 64), x = (lane >> 1) & 3;
   fetch(t.nb * BN + c0 * 32);
-  const int x = (lane >> 1) & 3;
 #pragma unroll 1
   for (int c = c0; c < c0 + BN / 64; ++c) {
     const int n = t.nb * BN + c * 32;
     if (n >= p.N) break;
-    __syncwarp();  // the last columns' rows have been read
+    uint32_t v[32];
+    tmem_ld32(lane_addr + (uint32_t)(c * 32), v);
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = sub + 8 * i;
-        reinterpret_cast<uint4 *>(stg + w * G_TILE)[row * 4 + (quarter ^ ((row >> 1) & 3))] =
-            pre[w][i];
-      }
+      for (int i = 0; i < 4; ++i) tile[w * kTile + piece(i)] = pre[w][i];
     __syncwarp();
     if (c + 1 < c0 + BN / 64) fetch(n + 32);
-    uint32_t v[32];
-    tmem_ld32(lane_addr + (uint32_t)(c * 32), v);
-    uint32_t out[3][16];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const uint4 u1 = reinterpret_cast<const uint4 *>(stg)[lane * 4 + (w ^ x)];
-      const uint4 u3 = reinterpret_cast<const uint4 *>(stg + G_TILE)[lane * 4 + (w ^ x)];
+      uint4 *const at = tile + lane * 4 + (w ^ x);
+      const uint4 u1 = at[0], u3 = at[kTile];
       const uint32_t a1[4] = {u1.x, u1.y, u1.z, u1.w}, a3[4] = {u3.x, u3.y, u3.z, u3.w};
+      uint32_t o[3][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float d1[2], d3[2], h[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float p1 = __uint_as_float(i ? a1[j] & 0xffff0000u : a1[j] << 16);
-          const float p3 = __uint_as_float(i ? a3[j] & 0xffff0000u : a3[j] << 16);
-          const float D = __uint_as_float(v[8 * w + 2 * j + i]), gD = g * D;
-          float a, s;
-          gated_act_slope<false, ACT>(p1, a, s);
-          h[i] = a * p3;
-          part = fmaf(D, h[i], part);
-          d1[i] = real ? gD * (p3 * s) : 0.f;
-          d3[i] = real ? gD * a : 0.f;
-          bad |= !isfinite(d1[i] + d3[i]);
-        }
-        __nv_bfloat162 b = __floats2bfloat162_rn(d1[0], d1[1]);
-        out[0][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
-        b = __floats2bfloat162_rn(d3[0], d3[1]);
-        out[1][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
-        b = __floats2bfloat162_rn(h[0], h[1]);
-        out[2][4 * w + j] = *reinterpret_cast<uint32_t *>(&b);
+        const float2 p3 = unpack2(a3[j]);
+        float2 s;
+        const float2 a = gated_act2<ACT, true>(unpack2(a1[j]), &s);
+        const float2 D = make_float2(__uint_as_float(v[8 * w + 2 * j]),
+                                     __uint_as_float(v[8 * w + 2 * j + 1]));
+        const float2 gD = mul2(D, both(g)), h = mul2(a, p3);
+        part = fma2(D, h, part);
+        const float2 d1 = mul2(gD, mul2(p3, s)), d3 = mul2(gD, a);
+        // 0 * d is 0, or a NaN that stays, for any number of places.
+        odd = fma2(d1, both(0.f), fma2(d3, both(0.f), odd));
+        o[0][j] = pack_bf16x2(d1);
+        o[1][j] = pack_bf16x2(d3);
+        o[2][j] = pack_bf16x2(h);
       }
-    }
-    __nv_bfloat16 *const to[3] = {static_cast<__nv_bfloat16 *>(p.out) + pr * p.N + n,
-                                  ex.dP3 + pr * p.N + n,
-                                  ex.h + (size_t)(q0 + lane) * p.N + n};
-    const CUtensorMap *const maps[3] = {tmO, &ex.o3, &ex.oh};
+      if (!real) o[0][0] = o[0][1] = o[0][2] = o[0][3] = o[1][0] = o[1][1] = o[1][2] = o[1][3] = 0;
 #pragma unroll
-    for (int o = 0; o < 3; ++o) {
-      if (o < 2 ? tma : whole) {
-        stage_store_bf16(maps[o], stg + (2 + (cnt & 1u)) * G_TILE, out[o], n,
-                         o < 2 ? t.prow0 + m0 : q0);
-        ++cnt;
-      } else if (o < 2 || real) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          reinterpret_cast<uint4 *>(to[o])[w] = make_uint4(out[o][4 * w], out[o][4 * w + 1],
-                                                           out[o][4 * w + 2], out[o][4 * w + 3]);
-      }
+      for (int q = 0; q < 3; ++q)
+        at[q * kTile] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = sub + 8 * i;
+      const size_t at = (pr - lane + row) * p.N + n + quarter * 8;
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = tile[piece(i)];
+      *reinterpret_cast<uint4 *>(ex.dP3 + at) = tile[kTile + piece(i)];
+      if (m0 + row < t.rows)
+        *reinterpret_cast<uint4 *>(ex.h + (size_t)(q0 + row) * p.N + n + quarter * 8) =
+            tile[2 * kTile + piece(i)];
+    }
+    __syncwarp();  // read before the next columns are written
   }
-  p.dgpart[(pr * p.n_blocks + t.nb) * 2 + half] = real ? part : 0.f;
-  if (bad) record_error(p.st, MOE_ERR_NONFINITE, (long long)pr);
+  p.dgpart[(pr * p.n_blocks + t.nb) * 2 + half] = real ? part.x + part.y : 0.f;
+  if (real && !(odd.x + odd.y == 0.f)) record_error(p.st, MOE_ERR_NONFINITE, (long long)pr);
 }
 
 // OB: in mode 2 the weight gradient is written in bf16, in mode 0 the hidden
@@ -424,8 +413,7 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
 template <int MODE, bool OB = false, int ACT = 0>
 __global__ void __launch_bounds__(threads_of<MODE>(), 1)
 k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-         const __grid_constant__ CUtensorMap tmO, const __grid_constant__ BExtra<MODE> ex,
-         const BParams p) {
+         const __grid_constant__ BExtra<MODE> ex, const BParams p) {
   constexpr int STAGES = stages_of<MODE>(false);
   pdl_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -584,7 +572,6 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
     // ----------------------------------------------------------------- epilogue
     const int quad = warp & 3;
     const int r_in_tile = quad * 32 + lane;
-    [[maybe_unused]] uint32_t stg_cnt = 0;
     int local = 0;
     for (int tile = blockIdx.x; tile < total_tiles; tile += gridDim.x, ++local) {
       const BTile t = locate<MODE>(p, tile_start, tile);
@@ -599,14 +586,13 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
       if constexpr (MODE == 3)
         epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr,
-                            stg_all + (warp - 2) * 4 * G_TILE, &tmO, stg_cnt);
+                            stg_all + (warp - 2) * 3 * G_TILE);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[buf]);
     }
-    if (MODE == 3 && lane == 0) bulk_wait_all();  // this warp's TMA stores are complete
     pdl_trigger();
   }
   tc_fence_before();
@@ -989,8 +975,8 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int r_in_tile = quad * 32 + lane;
     const uint32_t acc_empty_leader0 = mapa(smem_u32(&acc_empty[0]), 0);
     const uint32_t acc_empty_leader1 = mapa(smem_u32(&acc_empty[1]), 0);
-    // This warp's two tiles (mode 3: four smaller ones).
-    float *stg = stg_all + (size_t)(warp - 2) * (MODE == 3 ? 4 * G_TILE : 2 * P_STG_TILE);
+    // This warp's two tiles (mode 3: three smaller ones).
+    float *stg = stg_all + (size_t)(warp - 2) * (MODE == 3 ? 3 * G_TILE : 2 * P_STG_TILE);
     uint32_t stg_cnt = 0;
     for (int local = 0;; ++local) {
       const int slot = local % kRing;
@@ -1020,7 +1006,7 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       if constexpr (MODE == 2)
         epilogue_wgrad_tma<OB>(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
       else if constexpr (MODE == 3)
-        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr, stg, &tmO, stg_cnt);
+        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr, stg);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
       tc_fence_before();
@@ -1116,15 +1102,13 @@ cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const C
   return cudaLaunchKernelEx(&cfg, k_bwd_tc_pair<MODE, OB, ACT>, a, b, o, ex, p);
 }
 
-// o: mode 3's output map (unused otherwise).
 template <int MODE, bool OB = false, int ACT = 0>
-cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const CUtensorMap &o,
-                        const BParams &p, cudaStream_t s, const BExtra<MODE> &ex = {}) {
+cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p, cudaStream_t s, const BExtra<MODE> &ex = {}) {
   const size_t smem = bwd_smem_bytes<MODE>(p.E);
   cudaError_t err = allow_smem(k_bwd_tc<MODE, OB, ACT>);
   if (err != cudaSuccess) return err;
-  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB, ACT>, sm_count(), threads_of<MODE>(), smem, s, a, b, o,
-               ex, p);
+  launch_pdl_c(kPdlGemm, k_bwd_tc<MODE, OB, ACT>, sm_count(), threads_of<MODE>(), smem, s, a, b, ex,
+               p);
   return cudaGetLastError();
 }
 
@@ -1214,7 +1198,7 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
         make_out_map3(&to, g.out, g.E, g.M, g.N, g.out_bf16))
       return g.out_bf16 ? launch_mode_pair<2, true>(ta, tb, to, p, cl, s)
                         : launch_mode_pair<2>(ta, tb, to, p, cl, s);
-    return g.out_bf16 ? launch_mode<2, true>(ta, tb, ta, p, s) : launch_mode<2>(ta, tb, ta, p, s);
+    return g.out_bf16 ? launch_mode<2, true>(ta, tb, p, s) : launch_mode<2>(ta, tb, p, s);
   }
   // A: padded rows [a_rows, K]; B: the weight as [E*N rows, K] (the pair
   // kernel loads half of a tile's 256 B rows per CTA).
@@ -1234,14 +1218,10 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
     ex.pre3 = static_cast<const __nv_bfloat16 *>(g.pre3);
     ex.dP3 = static_cast<__nv_bfloat16 *>(g.out3);
     ex.h = static_cast<__nv_bfloat16 *>(g.h);
-    ex.o3 = ex.oh = ta;
-    p.tma_out = make_rows_map(&to, g.out, rows, (uint64_t)g.N, false) &&
-                make_rows_map(&ex.o3, g.out3, rows, (uint64_t)g.N, false) &&
-                make_rows_map(&ex.oh, g.h, (uint64_t)g.h_rows, (uint64_t)g.N, false);
     return gated_dispatch(g.activation, [&](auto act) {
       constexpr int ACT = decltype(act)::value;
       return cl > 0 ? launch_mode_pair<3, false, ACT>(ta, tb, to, p, cl, s, ex)
-                    : launch_mode<3, false, ACT>(ta, tb, to, p, s, ex);
+                    : launch_mode<3, false, ACT>(ta, tb, p, s, ex);
     });
   }
   BExtra<4> ex4{};
@@ -1255,9 +1235,9 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
     return g.mode == 0 ? launch_mode_pair<0>(ta, tb, to, p, cl, s)
                        : launch_mode_pair<1>(ta, tb, to, p, cl, s);
   }
-  if (g.mode == 4) return launch_mode<4>(ta, tb, to, p, s, ex4);
-  if (g.mode == 0 && g.h8) return launch_mode<0, true>(ta, tb, to, p, s);
-  return g.mode == 0 ? launch_mode<0>(ta, tb, to, p, s) : launch_mode<1>(ta, tb, to, p, s);
+  if (g.mode == 4) return launch_mode<4>(ta, tb, p, s, ex4);
+  if (g.mode == 0 && g.h8) return launch_mode<0, true>(ta, tb, p, s);
+  return g.mode == 0 ? launch_mode<0>(ta, tb, p, s) : launch_mode<1>(ta, tb, p, s);
 }
 
 }  // namespace moe

@@ -136,9 +136,6 @@ __device__ __forceinline__ void load_bias(const __nv_bfloat16 *b, size_t at, uin
     w[4 * q + 3] = u.w;
   }
 }
-__device__ __forceinline__ float bf16_of(uint32_t pair, int i) {
-  return __uint_as_float(i ? pair & 0xffff0000u : pair << 16);
-}
 
 // A gated tile's outputs of one warp's rows and half of its columns: 32 at a
 // time of both halves of the accumulator at lane_addr. stg: the warp's staging
@@ -163,19 +160,13 @@ __device__ __forceinline__ void gated_rows(const Params &p, const Extra<kGated> 
     load_bias(ex.bias3, (size_t)e * p.N + n, b3);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      float p1[2], p3[2], h[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        p1[i] = __uint_as_float(v1[2 * j + i]) + bf16_of(b1[j], i);
-        p3[i] = __uint_as_float(v3[2 * j + i]) + bf16_of(b3[j], i);
-        h[i] = gated_act<false, ACT>(p1[i]) * p3[i];
-      }
-      __nv_bfloat162 b = __floats2bfloat162_rn(p1[0], p1[1]);
-      packed[0][j] = *reinterpret_cast<uint32_t *>(&b);
-      b = __floats2bfloat162_rn(p3[0], p3[1]);
-      packed[1][j] = *reinterpret_cast<uint32_t *>(&b);
-      b = __floats2bfloat162_rn(h[0], h[1]);
-      packed[2][j] = *reinterpret_cast<uint32_t *>(&b);
+      float2 p1 = make_float2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
+      float2 p3 = make_float2(__uint_as_float(v3[2 * j]), __uint_as_float(v3[2 * j + 1]));
+      if (p.bias) p1 = add2(p1, unpack2(b1[j]));
+      if (ex.bias3) p3 = add2(p3, unpack2(b3[j]));
+      packed[0][j] = pack_bf16x2(p1);
+      packed[1][j] = pack_bf16x2(p3);
+      packed[2][j] = pack_bf16x2(mul2(gated_act2<ACT, false>(p1, nullptr), p3));
     }
 #pragma unroll
     for (int o = 0; o < 3; ++o) {

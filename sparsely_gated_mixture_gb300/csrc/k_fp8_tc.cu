@@ -126,6 +126,13 @@ __device__ __forceinline__ void load_weight(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Two values of a bias of any width; zero past it.
+__device__ __forceinline__ float2 bias2(const __nv_bfloat16 *b, int e, int n, int N) {
+  const __nv_bfloat16 *at = b + (size_t)e * N + n;
+  return make_float2(n < N ? __bfloat162float(at[0]) : 0.f,
+                     n + 1 < N ? __bfloat162float(at[1]) : 0.f);
+}
+
 struct Tile {
   int e, mb, nb, row0, rows;
 };
@@ -411,18 +418,12 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           if (i == 3) arrive(&acc_empty[buf]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float g[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float p1 = __uint_as_float(v1[2 * j + u]), p3 = __uint_as_float(v3[2 * j + u]);
-              const int nn = n + 2 * j + u;
-              if (p.bias && nn < p.N) p1 += __bfloat162float(p.bias[(size_t)t.e * p.N + nn]);
-              if (p.bias3 && nn < p.N) p3 += __bfloat162float(p.bias3[(size_t)t.e * p.N + nn]);
-              g[u] = gated_act<false, ACT>(p1) * p3;
-            }
-            __nv_bfloat162 b = __floats2bfloat162_rn(g[0], g[1]);
-            h[i][j] = *reinterpret_cast<uint32_t *>(&b);
-            const float2 f = __bfloat1622float2(b);
+            float2 p1 = make_float2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
+            float2 p3 = make_float2(__uint_as_float(v3[2 * j]), __uint_as_float(v3[2 * j + 1]));
+            if (p.bias) p1 = add2(p1, bias2(p.bias, t.e, n + 2 * j, p.N));
+            if (p.bias3) p3 = add2(p3, bias2(p.bias3, t.e, n + 2 * j, p.N));
+            h[i][j] = pack_bf16x2(mul2(gated_act2<ACT, false>(p1, nullptr), p3));
+            const float2 f = unpack2(h[i][j]);
             top = max_nan(top, max_nan(fabsf(f.x), fabsf(f.y)));
           }
         }
@@ -437,13 +438,9 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
             uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              float f[4];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                f[2 * u] = __uint_as_float(h[i][2 * j + u] << 16) * inv;
-                f[2 * u + 1] = __uint_as_float(h[i][2 * j + u] & 0xffff0000u) * inv;
-              }
-              w[j] = fp8_pack2(f[0], f[1]) | fp8_pack2(f[2], f[3]) << 16;
+              const float2 lo = mul2(unpack2(h[i][2 * j]), both(inv));
+              const float2 hi = mul2(unpack2(h[i][2 * j + 1]), both(inv));
+              w[j] = fp8_pack2(lo.x, lo.y) | fp8_pack2(hi.x, hi.y) << 16;
             }
             out[2 * c] = make_uint4(w[0], w[1], w[2], w[3]);
             out[2 * c + 1] = make_uint4(w[4], w[5], w[6], w[7]);

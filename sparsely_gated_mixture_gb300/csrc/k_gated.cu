@@ -5,6 +5,14 @@
 namespace moe {
 namespace {
 
+// Up to three arrays of rows and what their column sums are.
+template <typename S, typename O>
+struct GatedColumns {
+  const S *src[3];
+  O *out[3];
+  int cols[3], blocks[3];
+};
+
 template <typename T>
 __device__ __forceinline__ float ld(const T *p, size_t i) {
   if constexpr (sizeof(T) == 2) return __bfloat162float(p[i]);
@@ -44,40 +52,61 @@ __device__ __forceinline__ int block_scan(int v, int *warps, int *total) {
 // scan and rank passes for long batches and a separate clearing of the status
 // word take four launches (4096 tokens of top 4: 17 us against 6).
 constexpr int kRouteChunk = 256;
+__host__ __device__ constexpr int route_copies(int E) { return E <= 256 ? 8 : 1; }
 __global__ void __launch_bounds__(kRouteChunk) k_gated_route(const GatedRouteArgs p) {
   pdl_wait();
   pdl_trigger();
+  // Counts before and from the block's own on, `copies` of each (lanes take
+  // turns, so that few experts do not mean long queues for one counter), offsets.
   extern __shared__ int route_mem[];
-  int *before = route_mem, *total = before + p.E, *off = total + p.E;  // [E], [E], [E + 1]
+  const int copies = route_copies(p.E);
+  int *before = route_mem, *total = before + p.E, *off = route_mem + 2 * copies * p.E;
   __shared__ int own[kRouteChunk];
   __shared__ int warps[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int a0 = (int)blockIdx.x * kRouteChunk, a = a0 + tid;
   const bool first = blockIdx.x == 0;
   if (first && tid < (int)(sizeof(DeviceStatus) / 4)) reinterpret_cast<uint32_t *>(p.st)[tid] = 0;
-  for (int e = tid; e < 2 * p.E; e += kRouteChunk) route_mem[e] = 0;
+  for (int e = tid; e < 2 * copies * p.E; e += kRouteChunk) route_mem[e] = 0;
   int mine = a < p.A ? p.idx[a] : -1;
   if (mine >= p.E) mine = -1;
   own[tid] = mine;
   __syncthreads();
-  // Sixteen loads in flight a thread.
-  for (int i0 = tid; i0 < p.A; i0 += 16 * kRouteChunk) {
-    int e[16];
+  // Eight loads of four in flight a thread (own chunks begin on a multiple of 4).
+  int *const hist = route_mem + (lane & (copies - 1)) * 2 * p.E;
+  for (int i0 = 4 * tid; i0 < p.A; i0 += 32 * kRouteChunk) {
+    int4 u[8];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int i = i0 + j * kRouteChunk;
-      e[j] = i < p.A ? p.idx[i] : -1;
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * 4 * kRouteChunk;
+      if (i + 3 < p.A) {
+        u[j] = *reinterpret_cast<const int4 *>(p.idx + i);
+      } else {
+        u[j].x = i < p.A ? p.idx[i] : -1;
+        u[j].y = i + 1 < p.A ? p.idx[i + 1] : -1;
+        u[j].z = i + 2 < p.A ? p.idx[i + 2] : -1;
+        u[j].w = -1;
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int i = i0 + j * kRouteChunk;
-      if (e[j] >= 0 && e[j] < p.E)
-        atomicAdd(i < a0 ? &before[e[j]] : &total[e[j]], 1);
-      else if (first && i < p.A)
-        record_error(p.st, MOE_ERR_BOUNDS, (long long)i);  // after block 0's clearing
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * 4 * kRouteChunk, e[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (e[q] >= 0 && e[q] < p.E) atomicAdd(hist + (i < a0 ? 0 : p.E) + e[q], 1);
+        else if (first && i + q < p.A) record_error(p.st, MOE_ERR_BOUNDS, (long long)(i + q));
+      }
     }
   }
   __syncthreads();
+  if (copies > 1) {
+    for (int e = tid; e < 2 * p.E; e += kRouteChunk) {
+      int n = 0;
+      for (int c = 0; c < copies; ++c) n += route_mem[c * 2 * p.E + e];
+      route_mem[e] = n;
+    }
+    __syncthreads();
+  }
   // Kept rows, their offsets and the tiles of 128 rows, four experts a thread.
   int rows[4], n = 0, tiles = 0, pads = 0;
 #pragma unroll
@@ -160,13 +189,94 @@ k_gated_dgate(long long A, int E, int k, int d, int n_blocks, const int32_t *__r
   if (r >= 0) {
     for (int b = lane; b < n_blocks; b += 32) s += dgpart[r * n_blocks + b];
     if (b2) {
-      const size_t t = (size_t)(a / k) * d, e = (size_t)idx[a] * d;
-      for (int i = lane; i < d; i += 32) s = fmaf(ld(dy, t + i), ld(b2, e + i), s);
+      const T *y = dy + (size_t)(a / k) * d, *b = b2 + (size_t)idx[a] * d;
+      constexpr int V = 16 / (int)sizeof(T);
+      if (d % V == 0) {
+        for (int i = lane * V; i < d; i += 32 * V) {
+          const uint4 u = *reinterpret_cast<const uint4 *>(y + i);
+          const uint4 w = *reinterpret_cast<const uint4 *>(b + i);
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            s = fmaf(ld(reinterpret_cast<const T *>(&u), j), ld(reinterpret_cast<const T *>(&w), j), s);
+        }
+      } else {
+        for (int i = lane; i < d; i += 32) s = fmaf(ld(y, i), ld(b, i), s);
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) dgate[a] = s;
+}
+
+// The bias gradients: column sums of each expert's rows, a block for 64 columns
+// and an expert. Eight warps take rows in turn, 16 bytes a lane and eight of
+// them in flight (widths of an odd size: a value a lane); lanes, then warps,
+// add in a fixed order. The pad rows behind an expert's are not read.
+template <typename S, typename O, bool VEC>
+__global__ void __launch_bounds__(256)
+k_gated_colsum(const int32_t *__restrict__ offset, const int32_t *__restrict__ base,
+               const GatedColumns<S, O> p) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = VEC ? 16 / (int)sizeof(S) : 1, LANES = VEC ? 64 / V : 32, PER = 32 / LANES;
+  constexpr int Q = 64 / (LANES * V);  // column groups of a lane
+  __shared__ float sums[8][64];
+  int job = 0, cb = blockIdx.x;
+  while (cb >= p.blocks[job]) cb -= p.blocks[job++];
+  const int e = blockIdx.y, cols = p.cols[job], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = offset[e + 1] - offset[e];
+  const int c0 = cb * 64 + (lane % LANES) * V;
+  const S *src = p.src[job] + (size_t)base[e] * cols;
+  float acc[Q][V] = {};
+  for (int r0 = warp * PER + lane / LANES; r0 < rows; r0 += 64 * PER) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int c = c0 + q * 32;
+      if (c >= cols) continue;
+      if constexpr (VEC) {
+        uint4 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * 8 * PER;
+          u[i] = r < rows ? *reinterpret_cast<const uint4 *>(src + (size_t)r * cols + c)
+                          : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[q][v] += ld(reinterpret_cast<const S *>(&u[i]), v);
+      } else {
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * 8 * PER;
+          u[i] = r < rows ? ld(src, (size_t)r * cols + c) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[q][0] += u[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int o = LANES; o < 32; o <<= 1)
+        acc[q][v] += __shfl_xor_sync(0xffffffffu, acc[q][v], o);
+      if (lane < LANES) sums[warp][lane * V + q * 32 + v] = acc[q][v];
+    }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < 64 && cb * 64 + c < cols) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sums[w][c];
+    O *out = p.out[job] + (size_t)e * cols + cb * 64 + c;
+    if constexpr (sizeof(O) == 2) *out = __float2bfloat16_rn(s);
+    else *out = s;
+  }
 }
 
 // One warp per token; choices in order.
@@ -200,7 +310,7 @@ k_gated_dx(int T_, int E, int k, int d, const int32_t *__restrict__ idx,
 
 cudaError_t launch_gated_route(const GatedRouteArgs &a, cudaStream_t s) {
   return launch_pdl(k_gated_route, (a.A + kRouteChunk - 1) / kRouteChunk, kRouteChunk,
-                    (3 * (size_t)a.E + 1) * 4, s, a);
+                    ((2 * (size_t)route_copies(a.E) + 1) * a.E + 1) * 4, s, a);
 }
 
 cudaError_t launch_gated_begin(DeviceStatus *st, cudaStream_t s) {
@@ -219,6 +329,39 @@ cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t 
                       (const __nv_bfloat16 *)b2, dgate);
   return launch_pdl(k_gated_dgate<float>, grid, 256, 0, s, A, c.E, c.k, c.d, n_blocks, idx, pos,
                     keep, base, dgpart, (const float *)dy, (const float *)b2, dgate);
+}
+
+template <typename S, typename O>
+static cudaError_t run_colsum(int E, const int32_t *offset, const int32_t *base,
+                              const void *const (&src)[3], void *const (&out)[3],
+                              const int (&cols)[3], cudaStream_t s) {
+  GatedColumns<S, O> p{};
+  int n = 0, blocks = 0;
+  bool vec = true;
+  for (int j = 0; j < 3; ++j) {
+    if (!out[j]) continue;
+    p.src[n] = static_cast<const S *>(src[j]);
+    p.out[n] = static_cast<O *>(out[j]);
+    p.cols[n] = cols[j];
+    p.blocks[n] = (cols[j] + 63) / 64;
+    blocks += p.blocks[n++];
+    vec = vec && cols[j] % (16 / (int)sizeof(S)) == 0;
+  }
+  if (!n) return cudaSuccess;
+  const dim3 grid(blocks, E);
+  return vec ? launch_pdl(k_gated_colsum<S, O, true>, grid, 256, 0, s, offset, base, p)
+             : launch_pdl(k_gated_colsum<S, O, false>, grid, 256, 0, s, offset, base, p);
+}
+
+cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t *offset,
+                                const int32_t *base, const void *dU, void *db2, const void *dP1,
+                                void *db1, const void *dP3, void *db3, cudaStream_t s) {
+  const void *const src[3] = {dU, dP1, dP3};
+  void *const out[3] = {db2, db1, db3};
+  const int cols[3] = {c.d, c.d_ff, c.d_ff};
+  if (c.act_dtype == MOE_F32) return run_colsum<float, float>(c.E, offset, base, src, out, cols, s);
+  if (src_f32) return run_colsum<float, __nv_bfloat16>(c.E, offset, base, src, out, cols, s);
+  return run_colsum<__nv_bfloat16, __nv_bfloat16>(c.E, offset, base, src, out, cols, s);
 }
 
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,

@@ -31,8 +31,8 @@ __device__ __forceinline__ void put(T *p, size_t i, float v) {
 
 enum Op { kF1, kF2, kB1, kB2, kW1, kW3, kW2 };
 
-// a * b + c on two floats at once.
-__device__ __forceinline__ void fma2(unsigned long long &c, unsigned long long a,
+// c += a * b on two floats at once, kept as they are in registers.
+__device__ __forceinline__ void fma_pair(unsigned long long &c, unsigned long long a,
                                      unsigned long long b) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
 }
@@ -194,7 +194,7 @@ k_gated_simt(const GatedSimt p) {
       for (int i = 0; i < TM; ++i) {
         const unsigned long long aa = pack2(a[i], a[i]);
 #pragma unroll
-        for (int j = 0; j < TN / 2; ++j) fma2(acc[i][j], aa, b[j]);
+        for (int j = 0; j < TN / 2; ++j) fma_pair(acc[i][j], aa, b[j]);
       }
     }
     __syncthreads();
@@ -202,7 +202,6 @@ k_gated_simt(const GatedSimt p) {
 
   const T *b1 = static_cast<const T *>(p.b1), *b3 = static_cast<const T *>(p.b3);
   const T *b2 = static_cast<const T *>(p.b2);
-  constexpr bool kPrecise = sizeof(T) == 4;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = m0 + (i / HM) * (BM / 2) + ty * HM + i % HM;
@@ -224,7 +223,9 @@ k_gated_simt(const GatedSimt p) {
         if (b3) p3 += ld(b3, (size_t)e * F + n);
         if (p.pre1) put(static_cast<T *>(p.pre1), r * F + n, p1);
         if (p.pre3) put(static_cast<T *>(p.pre3), r * F + n, p3);
-        put(static_cast<T *>(p.h), r * F + n, gated_act<kPrecise, ACT>(p1) * p3);
+        float a, sl;
+        gated_act_slope<ACT>(p1, a, sl);
+        put(static_cast<T *>(p.h), r * F + n, a * p3);
       }
     } else if constexpr (OP == kB1) {
       const float g = live ? p.rows.row_gate[r] : 0.f;
@@ -236,7 +237,7 @@ k_gated_simt(const GatedSimt p) {
         const float p1 = ld(static_cast<const T *>(p.pre1), r * F + n);
         const float p3 = ld(static_cast<const T *>(p.pre3), r * F + n);
         float a, sl;
-        gated_act_slope<kPrecise, ACT>(p1, a, sl);
+        gated_act_slope<ACT>(p1, a, sl);
         const float h = a * p3, D = v[j];
         part = fmaf(D, h, part);
         p.hf[r * F + n] = h;
