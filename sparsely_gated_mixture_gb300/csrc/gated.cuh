@@ -221,6 +221,36 @@ struct Fp8Layer {
 bool fp8_tc_supported();
 cudaError_t launch_fp8_tc(const Fp8Layer &q, cudaStream_t s);
 
+// k_gated_few.cu: routing and both products for up to kGatedFewRows rows an
+// expert and kGatedFewChoices choices, bf16 (widths in steps of 64) or 8 bits.
+constexpr int kGatedFewRows = 64, kGatedFewChoices = 512;
+// Blocks: one an SM, up to what the workspace (sized without a device) holds.
+constexpr int kGatedFewMaxBlocks = 160;
+int gated_few_blocks();
+struct GatedFew {
+  moe_config c;
+  bool fp8;
+  int activation, C, max_rows, toks;  // toks: rows an expert at most, in steps of 16
+  const void *x;
+  const int32_t *idx;
+  const float *gate;
+  const void *W1, *b1, *W3, *b3, *W2, *b2;
+  const uint8_t *s1, *s3, *s2;
+  int32_t *pos;
+  uint8_t *keep;
+  int32_t *offset;
+  float *row_gate;
+  int4 *list;         // [choices]
+  int32_t *counters;  // [1 + 2 blocks]
+  float *part;        // [blocks][2][toks][256]
+  void *xbuf, *h;     // bf16, or e4m3 with scales sx, sh
+  uint8_t *sx, *sh;
+  void *pre1, *pre3, *z;
+  bool z_bf16;
+  DeviceStatus *st;
+};
+cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s);
+
 // k_gated.cu: what surrounds the products of the backward.
 // dgate [T,k] = sum of a kept choice's dgpart row plus <dy, b2>; 0 for the others.
 // dgpart's row of assignment (t, j) is base[e] + pos[t,j].

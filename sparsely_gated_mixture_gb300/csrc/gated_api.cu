@@ -62,8 +62,27 @@ static bool gated_tc_shape(const moe_config &c) {
 // term, as in moe_forward.
 static bool gated_z_bf16(const moe_config &c) { return gated_tc_shape(c) && c.k <= 4; }
 
+// Few rows an expert: the kernels that are bound by reading the weights once.
+static int gated_few_toks(const moe_config &c) {
+  const long long A = (long long)c.T * c.k, C = host_capacity(c), rows = A < C ? A : C;
+  if (A > kGatedFewChoices || rows > kGatedFewRows) return 0;
+  return (int)((rows + 15) / 16 * 16);
+}
+struct GatedFewLayout {
+  size_t list, counters, part;
+};
+static GatedFewLayout gated_few_layout(const moe_config &c, GatedTake &take) {
+  const size_t toks = (size_t)gated_few_toks(c), blocks = kGatedFewMaxBlocks;
+  GatedFewLayout L{};
+  L.list = take(toks ? (size_t)c.T * c.k * sizeof(int4) : 0);
+  L.counters = take(toks ? (1 + 2 * blocks) * 4 : 0);
+  L.part = take(blocks * 2 * toks * 256 * 4);
+  return L;
+}
+
 struct GatedLayout {
   GatedRoute r;
+  GatedFewLayout few;
   size_t xbuf, h, z, total;
 };
 static GatedLayout gated_layout(const moe_config &c) {
@@ -74,6 +93,7 @@ static GatedLayout gated_layout(const moe_config &c) {
   L.xbuf = take(gated_tc_shape(c) ? R * c.d * 2 : 0);
   L.h = take(R * c.d_ff * elem_bytes(c.act_dtype));
   L.z = take(R * c.d * (gated_z_bf16(c) ? 2 : 4));
+  if (gated_tc_shape(c)) L.few = gated_few_layout(c, take);
   L.total = take.off;
   return L;
 }
@@ -82,6 +102,7 @@ static bool gated_fp8_z_bf16(const moe_config &c) { return c.d % 8 == 0 && c.k <
 
 struct GatedFp8Layout {
   GatedRoute r;
+  GatedFewLayout few;
   size_t x8, sx, h8, sh, z, total;
 };
 static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
@@ -95,6 +116,7 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
   L.h8 = take(R * fb * kFp8Block);
   L.sh = take(R * ((fb + 3) / 4 * 4));
   L.z = take(R * c.d * (gated_fp8_z_bf16(c) ? 2 : 4));
+  L.few = gated_few_layout(c, take);
   L.total = take.off;
   return L;
 }
@@ -212,6 +234,30 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   return MOE_OK;
 }
 
+// What the few-row kernels take from the routing part of a workspace.
+static GatedFew gated_few(const moe_config &c, const GatedRoute &L, const GatedFewLayout &F,
+                          int activation, const void *x, const int32_t *idx, const float *gate,
+                          int32_t *pos, uint8_t *keep, void *ws) {
+  GatedFew q{};
+  q.c = c;
+  q.activation = activation;
+  q.C = host_capacity(c);
+  q.max_rows = (int)gated_max_rows(c);
+  q.toks = gated_few_toks(c);
+  q.x = x;
+  q.idx = idx;
+  q.gate = gate;
+  q.pos = pos;
+  q.keep = keep;
+  q.offset = ws_at<int32_t>(ws, L.offset);
+  q.row_gate = ws_at<float>(ws, L.row_gate);
+  q.list = ws_at<int4>(ws, F.list);
+  q.counters = ws_at<int32_t>(ws, F.counters);
+  q.part = ws_at<float>(ws, F.part);
+  q.st = ws_at<DeviceStatus>(ws, L.status);
+  return q;
+}
+
 static bool known_activation(int a) {
   return a == MOE_ACT_SILU || a == MOE_ACT_GELU || a == MOE_ACT_RELU;
 }
@@ -257,10 +303,23 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
   int32_t *ps = pos ? pos : ws_at<int32_t>(ws, L.r.pos);
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
-  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
-  if (r != MOE_OK) return r;
   const long long R = gated_max_rows(c);
   void *z = ws_at<char>(ws, L.z);
+  if (gated_tc_shape(c) && gated_few_toks(c)) {
+    GatedFew q = gated_few(c, L.r, L.few, activation, x, expert_idx, gate, ps, kp, ws);
+    q.W1 = W1; q.b1 = b1; q.W3 = W3; q.b3 = b3; q.W2 = W2; q.b2 = b2;
+    q.xbuf = ws_at<char>(ws, L.xbuf);
+    q.h = ws_at<char>(ws, L.h);
+    q.pre1 = pre1;
+    q.pre3 = pre3;
+    q.z = z;
+    q.z_bf16 = gated_z_bf16(c);
+    MOE_CUDA(launch_gated_few(q, s));
+    MOE_CUDA(launch_combine(c, x, z, q.z_bf16, ps, kp, expert_idx, q.offset, y, st, s));
+    return MOE_OK;
+  }
+  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
+  if (r != MOE_OK) return r;
   if (gated_tc_shape(c)) {
     const GatedRows rows = gated_rows(L.r, ws);
     void *xbuf = ws_at<char>(ws, L.xbuf), *h = ws_at<char>(ws, L.h);
@@ -406,14 +465,29 @@ int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void 
   DeviceStatus *st = ws_at<DeviceStatus>(ws, L.r.status);
   int32_t *ps = pos ? pos : ws_at<int32_t>(ws, L.r.pos);
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
-  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
-  if (r != MOE_OK) return r;
-  const GatedRows rows = gated_rows(L.r, ws);
   const int R = (int)gated_max_rows(c);
   uint8_t *x8 = ws_at<uint8_t>(ws, L.x8), *sx = ws_at<uint8_t>(ws, L.sx);
   uint8_t *h8 = ws_at<uint8_t>(ws, L.h8), *sh = ws_at<uint8_t>(ws, L.sh);
   void *z = ws_at<char>(ws, L.z);
   const bool zb = gated_fp8_z_bf16(c);
+  if (gated_few_toks(c)) {
+    GatedFew q = gated_few(c, L.r, L.few, activation, x, expert_idx, gate, ps, kp, ws);
+    q.fp8 = true;
+    q.W1 = W1; q.s1 = s1; q.b1 = b1; q.W3 = W3; q.s3 = s3; q.b3 = b3;
+    q.W2 = W2; q.s2 = s2; q.b2 = b2;
+    q.xbuf = x8;
+    q.sx = sx;
+    q.h = h8;
+    q.sh = sh;
+    q.z = z;
+    q.z_bf16 = zb;
+    MOE_CUDA(launch_gated_few(q, s));
+    MOE_CUDA(launch_combine(c, x, z, zb, ps, kp, expert_idx, q.offset, y, st, s));
+    return MOE_OK;
+  }
+  r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
+  if (r != MOE_OK) return r;
+  const GatedRows rows = gated_rows(L.r, ws);
   MOE_CUDA(launch_fp8_rows(R, c.d, c.k, rows.offset + c.E, rows.row_token, x, x8, sx, s));
   MOE_CUDA(launch_fp8_tc({c, 1, activation, R, rows.offset, nullptr, x8, sx, W1, s1, W3, s3, b1,
                           b3, h8, sh, nullptr, false, st}, s));
