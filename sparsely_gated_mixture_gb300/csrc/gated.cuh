@@ -221,7 +221,7 @@ struct Fp8Layer {
 bool fp8_tc_supported();
 cudaError_t launch_fp8_tc(const Fp8Layer &q, cudaStream_t s);
 
-// k_gated_few.cu: routing and both products for up to kGatedFewRows rows an
+// k_gated_few.cu: the whole layer for up to kGatedFewRows rows an
 // expert and kGatedFewChoices choices, bf16 (widths in steps of 64) or 8 bits.
 constexpr int kGatedFewRows = 64, kGatedFewChoices = 512;
 // Blocks: one an SM, up to what the workspace (sized without a device) holds.
@@ -245,8 +245,9 @@ struct GatedFew {
   float *part;        // [blocks][2][toks][256]
   void *xbuf, *h;     // bf16, or e4m3 with scales sx, sh
   uint8_t *sx, *sh;
-  void *pre1, *pre3, *z;
+  void *pre1, *pre3, *z;  // z: bf16 (d a multiple of 8) or fp32
   bool z_bf16;
+  void *y;
   DeviceStatus *st;
 };
 cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s);

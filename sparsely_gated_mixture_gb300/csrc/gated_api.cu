@@ -314,8 +314,8 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
     q.pre3 = pre3;
     q.z = z;
     q.z_bf16 = gated_z_bf16(c);
+    q.y = y;
     MOE_CUDA(launch_gated_few(q, s));
-    MOE_CUDA(launch_combine(c, x, z, q.z_bf16, ps, kp, expert_idx, q.offset, y, st, s));
     return MOE_OK;
   }
   r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);
@@ -481,8 +481,8 @@ int moe_experts_gated_fp8(const moe_config *cfg, int32_t activation, const void 
     q.sh = sh;
     q.z = z;
     q.z_bf16 = zb;
+    q.y = y;
     MOE_CUDA(launch_gated_few(q, s));
-    MOE_CUDA(launch_combine(c, x, z, zb, ps, kp, expert_idx, q.offset, y, st, s));
     return MOE_OK;
   }
   r = gated_slots(c, L.r, expert_idx, gate, ps, kp, nullptr, ws, s);

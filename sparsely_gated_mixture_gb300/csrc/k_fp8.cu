@@ -101,33 +101,56 @@ k_fp8_weights(int K, int N, int KB, const T *__restrict__ W, uint8_t *__restrict
   }
 }
 
-// A warp for a block of 128 columns of a row, 4 a lane.
+// A warp a row: blocks of 128 columns, 4 a lane, eight blocks in flight.
+// VEC: 8-byte loads (K a multiple of 4).
+template <bool VEC>
 __global__ void __launch_bounds__(256)
 k_fp8_rows(int max_rows, int K, int KB, int k, const int32_t *__restrict__ count,
            const int32_t *__restrict__ row_token, const __nv_bfloat16 *__restrict__ src,
            uint8_t *__restrict__ q, uint8_t *__restrict__ scale) {
   pdl_wait();
   pdl_trigger();
-  const long long w = (blockIdx.x * 256ll + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const long long r = w / KB;
-  const int kb = (int)(w - r * KB);
+  const int r = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (r >= max_rows || r >= *count) return;
-  const size_t row = (size_t)(row_token[r] / k);
-  float v[4], top = 0.f;
+  const __nv_bfloat16 *row = src + (size_t)(row_token[r] / k) * K;
+  uint32_t *out = reinterpret_cast<uint32_t *>(q + (size_t)r * KB * B) + lane;
+  constexpr int N = 8;
+  for (int kb0 = 0; kb0 < KB; kb0 += N) {
+    uint2 u[N];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = kb * B + lane * 4 + j;
-    v[j] = c < K ? __bfloat162float(src[row * K + c]) : 0.f;
-    top = max_nan(top, fabsf(v[j]));
+    for (int i = 0; i < N; ++i) {
+      const int c = (kb0 + i) * B + lane * 4;
+      if constexpr (VEC) {
+        u[i] = c < K ? *reinterpret_cast<const uint2 *>(row + c) : make_uint2(0, 0);
+      } else {
+        const unsigned short *w = reinterpret_cast<const unsigned short *>(row);
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = c + j < K ? w[c + j] : 0u;
+        u[i] = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+      }
+    }
+    uint32_t bytes[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (kb0 + i >= KB) break;
+      const float2 a = unpack2(u[i].x), b = unpack2(u[i].y);
+      float top = max_nan(max_nan(fabsf(a.x), fabsf(a.y)), max_nan(fabsf(b.x), fabsf(b.y)));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      bytes[i] = fp8_scale_byte(top);
+      const float inv = fp8_inverse(bytes[i]);
+      out[(kb0 + i) * 32] = fp8_pack2(a.x * inv, a.y * inv) | fp8_pack2(b.x * inv, b.y * inv) << 16;
+    }
+    // Four blocks' bytes of a row are a word (those past KB are not read).
+    if (lane < 2 && kb0 + 4 * lane < KB) {
+      uint32_t w = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i / 4 == lane && kb0 + i < KB) w |= bytes[i] << 8 * (i & 3);
+      reinterpret_cast<uint32_t *>(scale)[(size_t)(kb0 / 4 + lane) * max_rows + r] = w;
+    }
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const uint32_t byte = fp8_scale_byte(top);
-  const float inv = fp8_inverse(byte);
-  *reinterpret_cast<uint32_t *>(q + (size_t)r * KB * B + kb * B + lane * 4) =
-      fp8_pack2(v[0] * inv, v[1] * inv) | fp8_pack2(v[2] * inv, v[3] * inv) << 16;
-  if (lane == 0) scale[((size_t)(kb >> 2) * max_rows + r) * 4 + (kb & 3)] = (uint8_t)byte;
 }
 
 }  // namespace
@@ -152,9 +175,11 @@ cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,
                             const int32_t *row_token, const void *src, uint8_t *q,
                             uint8_t *scale, cudaStream_t s) {
   const int KB = (int)fp8_blocks(K);
-  const long long warps = (long long)max_rows * KB;
-  return launch_pdl(k_fp8_rows, (unsigned)((warps + 7) / 8), 256, 0, s, max_rows, K, KB, k, count,
-                    row_token, (const __nv_bfloat16 *)src, q, scale);
+  const auto run = [&](auto kernel) {
+    return launch_pdl(kernel, (unsigned)((max_rows + 7ll) / 8), 256, 0, s, max_rows, K, KB, k, count,
+                      row_token, (const __nv_bfloat16 *)src, q, scale);
+  };
+  return K % 4 == 0 ? run(k_fp8_rows<true>) : run(k_fp8_rows<false>);
 }
 
 }  // namespace moe

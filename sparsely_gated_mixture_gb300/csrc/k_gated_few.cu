@@ -641,6 +641,77 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
   }
 }
 
+// y = x + the kept choices' rows of z, a block for 1024 columns of a token (a
+// warp a token, as for long batches, is 10 us for one token of 4096 columns).
+// VEC: 8 columns a thread (d a multiple of 8).
+template <bool VEC, bool ZB>
+__global__ void __launch_bounds__(128)
+k_few_gated_combine(int E, int k, int d, const __nv_bfloat16 *x, const void *__restrict__ z,
+                    const int32_t *__restrict__ idx, const int32_t *__restrict__ pos,
+                    const uint8_t *__restrict__ keep, const int32_t *__restrict__ offset,
+                    __nv_bfloat16 *y, DeviceStatus *st) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ int rows[16];
+  const int t = blockIdx.y, tid = threadIdx.x;
+  if (tid < k) {
+    const int a = t * k + tid, e = idx[a];
+    rows[tid] = keep[a] && e >= 0 && e < E ? offset[e] + pos[a] : -1;
+  }
+  __syncthreads();
+  constexpr int V = VEC ? 8 : 1;
+  bool bad = false;
+  for (int q = 0; q < 8 / V; ++q) {
+    const int c = blockIdx.x * 1024 + (q * 128 + tid) * V;
+    if (c >= d) break;
+    float f[V];
+    const size_t at = (size_t)t * d + c;
+    if constexpr (VEC) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(x + at);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = unpack2(w[j]);
+        f[2 * j] = v.x;
+        f[2 * j + 1] = v.y;
+      }
+    } else {
+      f[0] = __bfloat162float(x[at]);
+    }
+#pragma unroll 4
+    for (int j = 0; j < k; ++j) {
+      if (rows[j] < 0) continue;
+      const size_t r = (size_t)rows[j] * d + c;
+      if constexpr (VEC && ZB) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(z) + r);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = unpack2(w[i]);
+          f[2 * i] += v.x;
+          f[2 * i + 1] += v.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] += static_cast<const float *>(z)[r + i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) bad |= !isfinite(f[i]);
+    if constexpr (VEC) {
+      uint4 o;
+      o.x = pack_bf16x2(make_float2(f[0], f[1]));
+      o.y = pack_bf16x2(make_float2(f[2], f[3]));
+      o.z = pack_bf16x2(make_float2(f[4], f[5]));
+      o.w = pack_bf16x2(make_float2(f[6], f[7]));
+      *reinterpret_cast<uint4 *>(y + at) = o;
+    } else {
+      y[at] = __float2bfloat16_rn(f[0]);
+    }
+  }
+  if (bad) record_error(st, MOE_ERR_NONFINITE, (long long)t);
+}
+
 // ----------------------------------------------------------------------------- host
 bool map3(CUtensorMap *m, const void *base, uint64_t x, uint64_t y, uint64_t z, uint32_t bx,
           uint32_t by, bool fp8) {
@@ -738,7 +809,16 @@ cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s) {
                           : launch_pdl(k_few_gated_route<false>, r.A, 256, smem, s, r);
   if (err == cudaSuccess) err = q.fp8 ? few_layer<true>(q, 1, s) : few_layer<false>(q, 1, s);
   if (err == cudaSuccess) err = q.fp8 ? few_layer<true>(q, 2, s) : few_layer<false>(q, 2, s);
-  return err;
+  if (err != cudaSuccess) return err;
+  const auto combine = [&](auto kernel) {
+    return launch_pdl_c(kPdlCombine, kernel, dim3((c.d + 1023) / 1024, c.T), 128, 0, s, c.E, c.k,
+                        c.d, static_cast<const __nv_bfloat16 *>(q.x), (const void *)q.z, q.idx,
+                        (const int32_t *)q.pos, (const uint8_t *)q.keep, (const int32_t *)q.offset,
+                        static_cast<__nv_bfloat16 *>(q.y), q.st);
+  };
+  if (q.z_bf16) return combine(k_few_gated_combine<true, true>);
+  return c.d % 8 == 0 ? combine(k_few_gated_combine<true, false>)
+                      : combine(k_few_gated_combine<false, false>);
 }
 
 }  // namespace moe

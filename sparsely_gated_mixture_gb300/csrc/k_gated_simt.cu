@@ -7,16 +7,18 @@
 //   backward 2: dX = dP1 W1^T + dP3 W3^T
 //   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
 // One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
-// block of 256 threads, TM x TN a thread, K in chunks of 16 whose next one is
-// fetched while this one is multiplied, packed fp32 multiply-adds (two a lane
-// and instruction). Both projections of forward 1 share a block's columns, so
+// block of 256 threads, TM x TN a thread, K in chunks whose next one is fetched
+// while this one is multiplied (of 16 for large tiles, of 64 for small ones,
+// whose arithmetic is over long before a fetch: 517 rows of 130, backward 2 of
+// 2 x 234 values of K 61 us with chunks of 16), packed fp32 multiply-adds (two a
+// lane and instruction). Both projections of forward 1 share a block's columns, so
 // that a thread holds p1 and p3 of the same places. Sums run over K in order.
 #include "gated.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int BK = 16, kThreads = 256;
+constexpr int kThreads = 256;
 
 template <typename T>
 __device__ __forceinline__ float ld(const T *p, size_t i) {
@@ -47,7 +49,8 @@ __global__ void __launch_bounds__(kThreads)
 k_gated_simt(const GatedSimt p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int BM = 16 * TM, BN = 16 * TN;
+  constexpr int BM = 16 * TM, BN = 16 * TN, BK = TM == 8 ? 16 : 64;
+  constexpr int KL = BK, KR = kThreads / BK;  // K-contiguous operands: lanes along K, rows a pass
   constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;  // a weight gradient
   constexpr int LA = BM * BK / kThreads, LB = BN * BK / kThreads;
   __shared__ __align__(16) float As[BK][BM + 4];
@@ -88,7 +91,7 @@ k_gated_simt(const GatedSimt p) {
   if (!kWeight) {
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      const int m = m0 + (tid >> 4) + 16 * i;
+      const int m = m0 + tid / KL + KR * i;
       const int r = r0 + min(m, rows - 1);
       if (OP == kF1 || OP == kB1) arow[i] = (size_t)(p.rows.row_token[r] / k) * d;
       else arow[i] = (size_t)r * F;
@@ -111,7 +114,7 @@ k_gated_simt(const GatedSimt p) {
                         : ld(x, (size_t)(p.rows.row_token[r] / k) * d + m);
         }
       } else {
-        const int kk = k0 + (tid & 15), m = m0 + (tid >> 4) + 16 * i;
+        const int kk = k0 + tid % KL, m = m0 + tid / KL + KR * i;
         if (m < M && kk < K) {
           if (OP == kF1) v = ld(x, arow[i] + kk);
           else if (OP == kF2) v = ld(static_cast<const T *>(p.h), arow[i] + kk);
@@ -125,7 +128,7 @@ k_gated_simt(const GatedSimt p) {
     for (int i = 0; i < LB; ++i) {
       float v = 0.f;
       if constexpr (OP == kB1 || OP == kB2) {  // the weight's rows are the output's columns
-        const int kk = k0 + (tid & 15), n = n0 + (tid >> 4) + 16 * i;
+        const int kk = k0 + tid % KL, n = n0 + tid / KL + KR * i;
         if (n < N && kk < K) {
           if (OP == kB1) v = ld(W2, (size_t)n * d + kk);
           else v = kk < F ? ld(W1, (size_t)n * F + kk) : ld(W3, (size_t)n * F + kk - F);
@@ -148,11 +151,11 @@ k_gated_simt(const GatedSimt p) {
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       if (kWeight) As[tid / BM + i * (kThreads / BM)][tid % BM] = ra[i];
-      else As[tid & 15][(tid >> 4) + 16 * i] = ra[i];
+      else As[tid % KL][tid / KL + KR * i] = ra[i];
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      if (OP == kB1 || OP == kB2) Bs[tid & 15][(tid >> 4) + 16 * i] = rb[i];
+      if (OP == kB1 || OP == kB2) Bs[tid % KL][tid / KL + KR * i] = rb[i];
       else Bs[tid / BN + i * (kThreads / BN)][tid % BN] = rb[i];
     }
   };
@@ -167,7 +170,7 @@ k_gated_simt(const GatedSimt p) {
     stage();
     __syncthreads();
     if (k0 + BK < K) fetch(k0 + BK);
-#pragma unroll
+#pragma unroll 16
     for (int kk = 0; kk < BK; ++kk) {
       float a[TM];
       unsigned long long b[TN / 2];
