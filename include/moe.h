@@ -27,7 +27,8 @@
  *   gate and joined back before it returns (so later work on `stream`, and
  *   stream capture, see one ordered forward); moe_backward forks its gate
  *   branch onto the side stream and joins it back before its last kernel, as
- *   moe_backward_checkpoint does that and part of what it rebuilds.
+ *   moe_backward_checkpoint does that and part of what it rebuilds, and
+ *   moe_experts_gated_backward dgate and the bias gradients.
  *   Each device has a pool of 8 side streams, made on the first such call
  *   that is not under stream capture (make one call before capturing if the
  *   captured graph should keep the overlap) and kept; each serves one caller

@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <mutex>
+
 namespace moe {
 
 static inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -47,5 +49,13 @@ static inline bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) 
   do {                                                  \
     if ((call) != cudaSuccess) return MOE_ERR_CUDA;     \
   } while (0)
+
+// The library's side stream for work forked from `caller`, or null (moe_api.cu);
+// the lock is held while the call enqueues on it.
+struct SideStream {
+  cudaStream_t s = nullptr;
+  cudaEvent_t fork = nullptr, join = nullptr;
+};
+SideStream *side_stream(std::unique_lock<std::mutex> &lock, cudaStream_t caller);
 
 }  // namespace moe

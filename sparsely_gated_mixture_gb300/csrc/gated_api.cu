@@ -214,9 +214,19 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   g.out3 = dP3;
   g.h = h;
   MOE_CUDA(launch_bwd_gemm(g, st, s));
+  // Beside the products that follow, on the library's side stream: dL/dgate and
+  // the bias gradients, whose small blocks fit next to the GEMMs' one an SM.
+  std::unique_lock<std::mutex> side_lock;
+  SideStream *side = side_stream(side_lock, s);
+  cudaStream_t fs = s;
+  if (side) {
+    fs = side->s;
+    MOE_CUDA(cudaEventRecord(side->fork, s));
+    MOE_CUDA(cudaStreamWaitEvent(fs, side->fork, 0));
+  }
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
-                              s));
-  MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dU, q.db2, dP1, q.db1, dP3, q.db3, s));
+                              fs));
+  MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dU, q.db2, dP1, q.db1, dP3, q.db3, fs));
   BwdGemm gx{4, c.d_ff, c.d, 0, c.E, L.P_max, 0, 0, dP1, q.W1, rows.offset, poff, nullptr, nullptr,
              dX, nullptr, false};
   gx.A3 = dP3;
@@ -230,6 +240,10 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   MOE_CUDA(wgrad(h, c.d_ff, dU, c.d, q.dW2));
   MOE_CUDA(wgrad(xbuf, c.d, dP1, c.d_ff, q.dW1));
   MOE_CUDA(wgrad(xbuf, c.d, dP3, c.d_ff, q.dW3));
+  if (side) {
+    MOE_CUDA(cudaEventRecord(side->join, side->s));
+    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
+  }
   MOE_CUDA(launch_bwd_dx(c, q.idx, pos, keep, poff, dX, nullptr, q.dy, q.dx, s));
   return MOE_OK;
 }

@@ -315,15 +315,33 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
 }
 
 // Mode 3's epilogue for one warp: its 32 rows and half of the tile's columns
-// (half 0 or 1), 32 at a time. Global memory is read and written four lanes to a
+// (half 0 or 1), 32 at a time; pre holds the first 32's p1 and p3, fetched before
+// the accumulator was waited for. Global memory is read and written four lanes to a
 // row (a lane to a row would touch 32 lines an instruction); p1 and p3 of the
 // next 32 columns are fetched while these are worked on. They change to a lane's
 // own row through two of the warp's three staging tiles, where dP1 and dP3 take
 // their places, and h the third's, on the way back. Warp-collective.
+struct GatedPre {
+  uint4 v[2][4];  // p1, p3: 8 columns of rows lane / 4 + 8 i
+  // Columns n .. n + 31 of the warp's rows from m0 on; zero past the expert's.
+  __device__ __forceinline__ void fetch(const BParams &p, const BExtra<3> &ex, const BTile &t,
+                                        int m0, int n) {
+    const int sub = (threadIdx.x & 31) >> 2, quarter = threadIdx.x & 3;
+    const int q0 = p.offset[t.e] + m0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = sub + 8 * i;
+      const bool ok = m0 + row < t.rows && n < p.N;
+      const size_t at = (size_t)(q0 + row) * p.N + n + quarter * 8;
+      v[0][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre1 + at) : make_uint4(0, 0, 0, 0);
+      v[1][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre3 + at) : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
 template <int ACT>
 __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3> &ex,
                                                const BTile &t, int m0, int half,
-                                               uint32_t lane_addr, float *stg) {
+                                               uint32_t lane_addr, float *stg, GatedPre &pre) {
   const int lane = threadIdx.x & 31;
   const int m = m0 + lane;
   if (m0 >= t.prows) return;  // padded rows come in 64s: all of the warp's or none
@@ -333,17 +351,6 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
   const float g = real ? p.row_gate[q0 + lane] : 0.f;
   float2 part = both(0.f), odd = both(0.f);
   const int sub = lane >> 2, quarter = lane & 3;
-  uint4 pre[2][4];
-  const auto fetch = [&](int n) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = sub + 8 * i;
-      const bool ok = m0 + row < t.rows && n < p.N;
-      const size_t at = (size_t)(q0 + row) * p.N + n + quarter * 8;
-      pre[0][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre1 + at) : make_uint4(0, 0, 0, 0);
-      pre[1][i] = ok ? *reinterpret_cast<const uint4 *>(ex.pre3 + at) : make_uint4(0, 0, 0, 0);
-    }
-  };
   uint4 *const tile = reinterpret_cast<uint4 *>(stg);
   constexpr int kTile = G_TILE / 4;  // in 16-byte pieces
   const auto piece = [&](int i) {  // of row sub + 8 i
@@ -351,7 +358,6 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
     return row * 4 + (quarter ^ ((row >> 1) & 3));
   };
   const int c0 = half * (BN / 64), x = (lane >> 1) & 3;
-  fetch(t.nb * BN + c0 * 32);
 #pragma unroll 1
   for (int c = c0; c < c0 + BN / 64; ++c) {
     const int n = t.nb * BN + c * 32;
@@ -361,9 +367,9 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tile[w * kTile + piece(i)] = pre[w][i];
+      for (int i = 0; i < 4; ++i) tile[w * kTile + piece(i)] = pre.v[w][i];
     __syncwarp();
-    if (c + 1 < c0 + BN / 64) fetch(n + 32);
+    if (c + 1 < c0 + BN / 64) pre.fetch(p, ex, t, m0, n + 32);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint4 *const at = tile + lane * 4 + (w ^ x);
@@ -577,6 +583,9 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
       const BTile t = locate<MODE>(p, tile_start, tile);
       const int buf = local & 1;
       const uint32_t use = (uint32_t)(local >> 1);
+      [[maybe_unused]] GatedPre pre;
+      if constexpr (MODE == 3)
+        pre.fetch(p, ex, t, t.mb * BM + quad * 32, t.nb * BN + ((warp - 2) >> 2) * (BN / 2));
       const bool ready = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], use & 1u, abort_flag,
                                                            p.st, 34, p.wait_ns));
       if (!ready) break;
@@ -586,7 +595,7 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
       if constexpr (MODE == 3)
         epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr,
-                            stg_all + (warp - 2) * 3 * G_TILE);
+                            stg_all + (warp - 2) * 3 * G_TILE, pre);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr);
       tc_fence_before();
@@ -996,6 +1005,10 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       const BTile t = locate_pair<MODE>(p, tile_start, tile);
       const int buf = local & 1;
       const uint32_t use = (uint32_t)(local >> 1);
+      [[maybe_unused]] GatedPre pre;
+      if constexpr (MODE == 3)
+        pre.fetch(p, ex, t, t.mb * 2 * BM + (int)rank * BM + quad * 32,
+                  t.nb * BN + ((warp - 2) >> 2) * (BN / 2));
       const bool ready = __all_sync(0xffffffffu, mbar_wait(&acc_full[buf], use & 1u, abort_flag,
                                                            p.st, 44, p.wait_ns));
       if (!ready) break;
@@ -1006,7 +1019,7 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
       if constexpr (MODE == 2)
         epilogue_wgrad_tma<OB>(p, t, m - lane, lane_addr, stg, &tmO, stg_cnt);
       else if constexpr (MODE == 3)
-        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr, stg);
+        epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr, stg, pre);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr, p.tma_out ? stg : nullptr, &tmO, &stg_cnt);
       tc_fence_before();

@@ -369,10 +369,6 @@ static BwdLayout bwd_layout(const moe_config &cfg) {
 // call from another context (after cudaDeviceReset) makes a new one. The lock
 // is held while a call enqueues on its side stream, so calls from several
 // host threads do not interleave their records.
-struct SideStream {
-  cudaStream_t s = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-};
 constexpr int kSideMaxDevices = 64;
 constexpr int kSidePool = 8;
 struct DeviceSides {
@@ -394,7 +390,7 @@ static size_t side_thread_key(cudaStream_t caller) {
   return caller == cudaStreamPerThread ? reinterpret_cast<size_t>(&tag) : 0;
 }
 
-static SideStream *side_stream(std::unique_lock<std::mutex> &lock, cudaStream_t caller) {
+SideStream *side_stream(std::unique_lock<std::mutex> &lock, cudaStream_t caller) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kSideMaxDevices) {
     cudaGetLastError();
