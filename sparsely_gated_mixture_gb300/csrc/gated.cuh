@@ -174,12 +174,15 @@ struct GatedSimt {
   void *pre1, *pre3;  // forward: written if not null; backward: read
   float *z;           // forward: [rows, d] gate * U
   const void *dy;     // backward
-  float *hf, *dU, *dP1, *dP3, *dX, *dgpart;  // backward: fp32 rows
+  float *xf, *hf, *dU, *dP1, *dP3, *dX, *dgpart;  // backward: fp32 rows
   void *dW1, *dW3, *dW2;                     // act_dtype
   DeviceStatus *st;
 };
 cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s);
-cudaError_t launch_gated_simt_backward(const GatedSimt &p, cudaStream_t s);
+// Backward: x, g dy, dP1, dP3, h and dgpart first; then dX, and the weight gradients.
+cudaError_t launch_gated_simt_front(const GatedSimt &p, cudaStream_t s);
+cudaError_t launch_gated_simt_dx(const GatedSimt &p, cudaStream_t s);
+cudaError_t launch_gated_simt_weights(const GatedSimt &p, cudaStream_t s);
 int gated_simt_dg_blocks(const moe_config &c, int max_rows);  // columns of dgpart [rows, ..]
 
 // k_ffn_tc.cu: the gated first layer on the tensor cores (ffn_tc_supported

@@ -68,6 +68,16 @@ static int gated_few_toks(const moe_config &c) {
   if (A > kGatedFewChoices || rows > kGatedFewRows) return 0;
   return (int)((rows + 15) / 16 * 16);
 }
+// In bf16 the kernels for long batches read the weights as fast (64 tokens
+// through 8 large experts 419 us against 437) once the experts in use, at
+// uniform choices, have tiles of layer 2 for three quarters of the SMs; with
+// fewer they leave most of them idle (one token 227 us against 127). In 8 bits
+// they do not (64 tokens 257 us against 242).
+static bool gated_few_pays(const moe_config &c) {
+  if (!gated_few_toks(c)) return false;
+  const double used = c.E * (1.0 - pow(1.0 - (double)c.k / c.E, (double)c.T));
+  return used * ((c.d + 255) / 256) < 0.75 * gated_few_blocks();
+}
 struct GatedFewLayout {
   size_t list, counters, part;
 };
@@ -123,7 +133,7 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
 
 // Tensor cores: xbuf and h are packed rows (64 more than there can be, for the
 // zeroed tail that the weight gradients read), dY, dU, dP1, dP3 and dX rows of
-// padded blocks (offsets poff). CUDA cores: fp32 packed rows, no xbuf and dY.
+// padded blocks (offsets poff). CUDA cores: fp32 packed rows, no dY.
 struct GatedBwdLayout {
   GatedRoute r;
   size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, total;
@@ -140,7 +150,7 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   L.r = gated_route(c, take);
   L.dg_blocks = tc ? 2 * ((c.d_ff + 255) / 256) : gated_simt_dg_blocks(c, (int)R);
   L.poff = take(((size_t)c.E + 1) * 4);
-  L.xbuf = take(tc ? (R + kBwdRowPad) * d * 2 : 0);
+  L.xbuf = take(tc ? (R + kBwdRowPad) * d * 2 : R * d * 4);
   L.h = take((R + (tc ? kBwdRowPad : 0)) * F * eb);
   L.dY = take(tc ? P * d * 2 : 0);
   L.dU = take(P * d * eb);
@@ -178,6 +188,15 @@ static int gated_slots(const moe_config &c, const GatedRoute &L, const int32_t *
 static GatedRows gated_rows(const GatedRoute &L, void *ws) {
   return {ws_at<int32_t>(ws, L.offset), ws_at<int32_t>(ws, L.mtiles),
           ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate)};
+}
+
+// Work enqueued on fs from here follows that on s (fs: the side stream, or s).
+static int gated_fork(SideStream *side, cudaStream_t s, cudaStream_t &fs) {
+  if (!side) return MOE_OK;
+  MOE_CUDA(cudaEventRecord(side->fork, s));
+  MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
+  fs = side->s;
+  return MOE_OK;
 }
 
 // The backward's products on the tensor cores, dx included.
@@ -219,11 +238,8 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   std::unique_lock<std::mutex> side_lock;
   SideStream *side = side_stream(side_lock, s);
   cudaStream_t fs = s;
-  if (side) {
-    fs = side->s;
-    MOE_CUDA(cudaEventRecord(side->fork, s));
-    MOE_CUDA(cudaStreamWaitEvent(fs, side->fork, 0));
-  }
+  const int r = gated_fork(side, s, fs);
+  if (r != MOE_OK) return r;
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
                               fs));
   MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dU, q.db2, dP1, q.db1, dP3, q.db3, fs));
@@ -319,7 +335,7 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   uint8_t *kp = keep ? keep : ws_at<uint8_t>(ws, L.r.keep);
   const long long R = gated_max_rows(c);
   void *z = ws_at<char>(ws, L.z);
-  if (gated_tc_shape(c) && gated_few_toks(c)) {
+  if (gated_tc_shape(c) && gated_few_pays(c)) {
     GatedFew q = gated_few(c, L.r, L.few, activation, x, expert_idx, gate, ps, kp, ws);
     q.W1 = W1; q.b1 = b1; q.W3 = W3; q.b3 = b3; q.W2 = W2; q.b2 = b2;
     q.xbuf = ws_at<char>(ws, L.xbuf);
@@ -408,6 +424,7 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   p.pre1 = const_cast<void *>(pre1);
   p.pre3 = const_cast<void *>(pre3);
   p.dy = dy;
+  p.xf = ws_at<float>(ws, L.xbuf);
   p.hf = ws_at<float>(ws, L.h);
   p.dU = ws_at<float>(ws, L.dU);
   p.dP1 = ws_at<float>(ws, L.dP1);
@@ -416,12 +433,24 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   p.dgpart = ws_at<float>(ws, L.dgpart);
   p.dW1 = dW1; p.dW3 = dW3; p.dW2 = dW2;
   p.st = ws_at<DeviceStatus>(ws, L.r.status);
-  MOE_CUDA(launch_gated_simt_backward(p, s));
+  MOE_CUDA(launch_gated_simt_front(p, s));
+  // The weight gradients beside all that dx needs, and the small sums.
+  std::unique_lock<std::mutex> side_lock;
+  SideStream *side = side_stream(side_lock, s);
+  cudaStream_t fs = s;
+  r = gated_fork(side, s, fs);
+  if (r != MOE_OK) return r;
   const int32_t *off = p.rows.offset;
+  MOE_CUDA(launch_gated_simt_weights(p, fs));
+  MOE_CUDA(launch_gated_simt_dx(p, s));
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, expert_idx, pos, keep, off, p.dgpart, dy, b2, dgate,
                               s));
-  MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, db2, p.dP1, db1, p.dP3, db3, s));
+  MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, db2, p.dP1, db1, p.dP3, db3, fs));
   MOE_CUDA(launch_gated_dx(c, expert_idx, pos, keep, off, p.dX, dy, dx, s));
+  if (side) {
+    MOE_CUDA(cudaEventRecord(side->join, side->s));
+    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
+  }
   return MOE_OK;
 }
 

@@ -292,16 +292,29 @@ k_gated_dx(int T_, int E, int k, int d, const int32_t *__restrict__ idx,
   const int lane = threadIdx.x & 31;
   if (t >= T_) return;
   const long long mine = lane < k ? gated_row(t * k + lane, E, idx, pos, keep, base) : -1;
-  for (int i0 = 0; i0 < d; i0 += 32) {
-    const int i = i0 + lane;
-    float s = i < d ? ld(dy, (size_t)t * d + i) : 0.f;
+  constexpr int N = 4;  // columns of a lane in flight
+  for (int i0 = lane; i0 - lane < d; i0 += 32 * N) {
+    float s[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int i = i0 + 32 * q;
+      s[q] = i < d ? ld(dy, (size_t)t * d + i) : 0.f;
+    }
     for (int j = 0; j < k; ++j) {
       const long long r = __shfl_sync(0xffffffffu, mine, j);
-      if (r >= 0 && i < d) s += dX[(size_t)r * d + i];
+      if (r < 0) continue;
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        const int i = i0 + 32 * q;
+        if (i < d) s[q] += dX[(size_t)r * d + i];
+      }
     }
-    if (i < d) {
-      if constexpr (sizeof(T) == 2) dx[(size_t)t * d + i] = __float2bfloat16_rn(s);
-      else dx[(size_t)t * d + i] = s;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const int i = i0 + 32 * q;
+      if (i >= d) continue;
+      if constexpr (sizeof(T) == 2) dx[(size_t)t * d + i] = __float2bfloat16_rn(s[q]);
+      else dx[(size_t)t * d + i] = s[q];
     }
   }
 }

@@ -8,11 +8,10 @@
 //   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
 // One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
 // block of 256 threads, TM x TN a thread, K in chunks whose next one is fetched
-// while this one is multiplied (of 16 for large tiles, of 64 for small ones,
-// whose arithmetic is over long before a fetch: 517 rows of 130, backward 2 of
-// 2 x 234 values of K 61 us with chunks of 16), packed fp32 multiply-adds (two a
-// lane and instruction). Both projections of forward 1 share a block's columns, so
-// that a thread holds p1 and p3 of the same places. Sums run over K in order.
+// while this one is multiplied, packed fp32 multiply-adds (two a lane and
+// instruction). Both projections of forward 1 share a block's columns, so that a
+// thread holds p1 and p3 of the same places; the three weight gradients are one
+// launch. Sums run over K in order.
 #include "gated.cuh"
 
 namespace moe {
@@ -31,7 +30,7 @@ __device__ __forceinline__ void put(T *p, size_t i, float v) {
   else p[i] = v;
 }
 
-enum Op { kF1, kF2, kB1, kB2, kW1, kW3, kW2 };
+enum Op { kF1, kF2, kB1, kB2, kW };  // kW: the weight gradients
 
 // c += a * b on two floats at once, kept as they are in registers.
 __device__ __forceinline__ void fma_pair(unsigned long long &c, unsigned long long a,
@@ -49,39 +48,49 @@ __global__ void __launch_bounds__(kThreads)
 k_gated_simt(const GatedSimt p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int BM = 16 * TM, BN = 16 * TN, BK = TM == 8 ? 16 : 64;
+  constexpr int BM = 16 * TM, BN = 16 * TN, BK = TM == 8 ? 16 : 32;
   constexpr int KL = BK, KR = kThreads / BK;  // K-contiguous operands: lanes along K, rows a pass
-  constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;  // a weight gradient
+  constexpr bool kWeight = OP == kW;
   constexpr int LA = BM * BK / kThreads, LB = BN * BK / kThreads;
   __shared__ __align__(16) float As[BK][BM + 4];
   __shared__ __align__(16) float Bs[BK][BN + 4];
   const int E = p.c.E, d = p.c.d, F = p.c.d_ff, k = p.c.k;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
-  // The block's expert, first row and row count.
-  int e, m0;
-  if (kWeight) {
-    e = blockIdx.z;
-    m0 = blockIdx.x * BM;
+  // The block's expert, first row and row count. A weight gradient's blocks are
+  // (weight, row block, column block) along x, experts along y.
+  int e, m0, n0, which = 0;
+  constexpr int BNu = OP == kF1 ? BN / 2 : BN;  // columns of the output a block covers
+  if constexpr (kWeight) {
+    const int db = (d + BM - 1) / BM, fb = (F + BM - 1) / BM;  // BM = BN
+    int i = blockIdx.x;
+    which = i / (db * fb);
+    i -= which * db * fb;
+    const int mb = which == 2 ? fb : db;  // dW1, dW3: [d, F]; dW2: [F, d]
+    e = blockIdx.y;
+    n0 = i / mb * BN;
+    m0 = i % mb * BM;
   } else {
     constexpr int kSplit = kTcBM / BM;  // blocks for each 128-row tile
+    __shared__ int starts[1025];
     const int tile = blockIdx.x / kSplit;
-    if (tile >= p.rows.mtiles[E]) return;
-    int lo = 0, hi = E;  // largest e with mtiles[e] <= tile
+    for (int i = tid; i <= E; i += kThreads) starts[i] = p.rows.mtiles[i];
+    __syncthreads();
+    if (tile >= starts[E]) return;
+    int lo = 0, hi = E;  // largest e with starts[e] <= tile
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.rows.mtiles[mid] <= tile) lo = mid;
+      if (starts[mid] <= tile) lo = mid;
       else hi = mid;
     }
     e = lo;
-    m0 = (tile - p.rows.mtiles[e]) * kTcBM + (blockIdx.x % kSplit) * BM;
+    m0 = (tile - starts[e]) * kTcBM + (blockIdx.x % kSplit) * BM;
+    n0 = blockIdx.y * BNu;
   }
   const int r0 = p.rows.offset[e], rows = p.rows.offset[e + 1] - r0;
   if (!kWeight && m0 >= rows) return;
-  constexpr int BNu = OP == kF1 ? BN / 2 : BN;  // columns of the output a block covers
-  const int n0 = blockIdx.y * BNu;
-  const int M = kWeight ? (OP == kW2 ? F : d) : rows;
-  const int N = OP == kF1 || OP == kB1 || OP == kW1 || OP == kW3 ? F : d;
+  const int M = kWeight ? (which == 2 ? F : d) : rows;
+  const int N = kWeight ? (which == 2 ? d : F) : OP == kF1 || OP == kB1 ? F : d;
   const int K = kWeight ? rows : OP == kF1 || OP == kB1 ? d : OP == kF2 ? F : 2 * F;
   const size_t we = (size_t)e * d * F;  // this expert's place in each weight
 
@@ -100,6 +109,12 @@ k_gated_simt(const GatedSimt p) {
   const T *x = static_cast<const T *>(p.x), *dy = static_cast<const T *>(p.dy);
   const T *W1 = static_cast<const T *>(p.W1) + we, *W3 = static_cast<const T *>(p.W3) + we;
   const T *W2 = static_cast<const T *>(p.W2) + we;
+  // A weight gradient's rows [rows, M] and [rows, N].
+  const float *wa = nullptr, *wb = nullptr;
+  if constexpr (kWeight) {
+    wa = (which == 2 ? p.hf : p.xf) + (size_t)r0 * M;
+    wb = (which == 0 ? p.dP1 : which == 1 ? p.dP3 : p.dU) + (size_t)r0 * N;
+  }
 
   float ra[LA], rb[LB];
   auto fetch = [&](int k0) {
@@ -108,18 +123,14 @@ k_gated_simt(const GatedSimt p) {
       float v = 0.f;
       if constexpr (kWeight) {
         const int mm = tid % BM, kk = k0 + tid / BM + i * (kThreads / BM), m = m0 + mm;
-        if (m < M && kk < K) {
-          const int r = r0 + kk;
-          v = OP == kW2 ? p.hf[(size_t)r * F + m]
-                        : ld(x, (size_t)(p.rows.row_token[r] / k) * d + m);
-        }
+        if (m < M && kk < K) v = wa[(size_t)kk * M + m];
       } else {
         const int kk = k0 + tid % KL, m = m0 + tid / KL + KR * i;
         if (m < M && kk < K) {
           if (OP == kF1) v = ld(x, arow[i] + kk);
           else if (OP == kF2) v = ld(static_cast<const T *>(p.h), arow[i] + kk);
           else if (OP == kB1) v = ld(dy, arow[i] + kk);
-          else v = kk < F ? p.dP1[arow[i] + kk] : p.dP3[arow[i] + kk - F];
+          else v = (kk < F ? p.dP1 + kk : p.dP3 + (kk - F))[arow[i]];
         }
       }
       ra[i] = v;
@@ -131,7 +142,7 @@ k_gated_simt(const GatedSimt p) {
         const int kk = k0 + tid % KL, n = n0 + tid / KL + KR * i;
         if (n < N && kk < K) {
           if (OP == kB1) v = ld(W2, (size_t)n * d + kk);
-          else v = kk < F ? ld(W1, (size_t)n * F + kk) : ld(W3, (size_t)n * F + kk - F);
+          else v = ld(kk < F ? W1 + kk : W3 + (kk - F), (size_t)n * F);
         }
       } else {
         const int nn = tid % BN, kk = k0 + tid / BN + i * (kThreads / BN);
@@ -140,8 +151,7 @@ k_gated_simt(const GatedSimt p) {
         if (n < N && kk < K) {
           if (OP == kF1) v = ld(second ? W3 : W1, (size_t)kk * F + n);
           else if (OP == kF2) v = ld(W2, (size_t)kk * d + n);
-          else if (OP == kW2) v = p.dU[(size_t)(r0 + kk) * d + n];
-          else v = (OP == kW1 ? p.dP1 : p.dP3)[(size_t)(r0 + kk) * F + n];
+          else v = wb[(size_t)kk * N + n];
         }
       }
       rb[i] = v;
@@ -172,15 +182,15 @@ k_gated_simt(const GatedSimt p) {
     if (k0 + BK < K) fetch(k0 + BK);
 #pragma unroll 16
     for (int kk = 0; kk < BK; ++kk) {
-      float a[TM];
+      __align__(16) float a[TM];
       unsigned long long b[TN / 2];
-      if constexpr (HM == 4) {
-        *reinterpret_cast<float4 *>(&a[0]) = *reinterpret_cast<const float4 *>(&As[kk][ty * 4]);
-        *reinterpret_cast<float4 *>(&a[4]) =
-            *reinterpret_cast<const float4 *>(&As[kk][BM / 2 + ty * 4]);
-      } else {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) a[i] = As[kk][(i / HM) * (BM / 2) + ty * HM + i % HM];
+      for (int h = 0; h < 2; ++h) {
+        const float *row = &As[kk][h * (BM / 2) + ty * HM];
+        if constexpr (HM == 4)
+          *reinterpret_cast<float4 *>(&a[4 * h]) = *reinterpret_cast<const float4 *>(row);
+        else
+          *reinterpret_cast<float2 *>(&a[2 * h]) = *reinterpret_cast<const float2 *>(row);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -265,7 +275,7 @@ k_gated_simt(const GatedSimt p) {
         } else if constexpr (OP == kB2) {
           p.dX[r * d + n] = u;
         } else {
-          void *out = OP == kW1 ? p.dW1 : OP == kW3 ? p.dW3 : p.dW2;
+          void *out = which == 0 ? p.dW1 : which == 1 ? p.dW3 : p.dW2;
           put(static_cast<T *>(out), we + (size_t)m * N + n, u);
         }
         bad |= !isfinite(u);
@@ -275,17 +285,21 @@ k_gated_simt(const GatedSimt p) {
   }
 }
 
-// dU[r] = g * dy of the row's token, in fp32; one warp per packed row.
+// dU[r] = g * dy and xf[r] = x of the row's token, in fp32; one warp per packed
+// row.
 template <typename T>
-__global__ void __launch_bounds__(256) k_gated_dy_rows(const GatedSimt p) {
+__global__ void __launch_bounds__(256) k_gated_rows(const GatedSimt p) {
   pdl_wait();
   pdl_trigger();
   const long long r = (blockIdx.x * 256ll + threadIdx.x) >> 5;
   if (r >= p.max_rows || r >= p.rows.offset[p.c.E]) return;
   const size_t src = (size_t)(p.rows.row_token[r] / p.c.k) * p.c.d;
   const float g = p.rows.row_gate[r];
-  for (int i = threadIdx.x & 31; i < p.c.d; i += 32)
+#pragma unroll 4
+  for (int i = threadIdx.x & 31; i < p.c.d; i += 32) {
     p.dU[r * p.c.d + i] = g * ld(static_cast<const T *>(p.dy), src + i);
+    p.xf[r * p.c.d + i] = ld(static_cast<const T *>(p.x), src + i);
+  }
 }
 
 // Rows in 128-row tiles at most: every expert's last one may be short.
@@ -296,35 +310,32 @@ long long max_tiles(const GatedSimt &p) {
 template <int OP, typename T, int ACT, int TM, int TN>
 cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
   constexpr int BM = 16 * TM, BN = 16 * TN;
-  constexpr bool kWeight = OP == kW1 || OP == kW3 || OP == kW2;
-  const int N = OP == kF1 || OP == kB1 || OP == kW1 || OP == kW3 ? p.c.d_ff : p.c.d;
+  const int N = OP == kF1 || OP == kB1 ? p.c.d_ff : p.c.d;
   const int BNu = OP == kF1 ? BN / 2 : BN;
-  dim3 grid(1, (N + BNu - 1) / BNu, 1);  // row blocks fastest: they share the weight's columns
-  if (kWeight) {
-    grid.x = ((OP == kW2 ? p.c.d_ff : p.c.d) + BM - 1) / BM;
-    grid.z = p.c.E;
-  } else {
-    grid.x = (unsigned)(max_tiles(p) * (kTcBM / BM));
-  }
+  dim3 grid;
+  if (OP == kW)
+    grid = dim3(3 * ((p.c.d + BM - 1) / BM) * ((p.c.d_ff + BM - 1) / BM), p.c.E);
+  else  // row blocks fastest: they share the weight's columns
+    grid = dim3((unsigned)(max_tiles(p) * (kTcBM / BM)), (N + BNu - 1) / BNu);
   return launch_pdl_c(kPdlGemm, k_gated_simt<OP, T, ACT, TM, TN>, grid, kThreads, 0, s, p);
 }
 
 // 128 x 128 tiles where they give every SM a block and rows to fill them, else
-// 32 x 64.
+// 64 x 64 (517 rows of 130 through 6 experts of 234: 23 us a layer 1 with tiles
+// of 32 x 64, whose threads hold 2 x 4 and spend their instructions on loads).
 bool wide_tiles(const moe_config &c, int max_rows, int op) {
-  const bool weight = op == kW1 || op == kW3 || op == kW2;
-  const bool to_d = op == kF2 || op == kB2 || op == kW2;
-  const int N = (op == kF1 ? 2 : 1) * (to_d ? c.d : c.d_ff);
-  const int M = op == kW2 ? c.d_ff : c.d;
-  const long long row_blocks = weight ? (long long)c.E * ((M + 127) / 128)
-                                      : ((long long)max_rows + 127) / 128;
-  return row_blocks * ((N + 127) / 128) >= sm_count() && (weight || max_rows >= 64 * c.E);
+  if (op == kW)
+    return 3ll * c.E * ((c.d + 127) / 128) * ((c.d_ff + 127) / 128) >= 2 * sm_count() &&
+           max_rows >= 64 * c.E;
+  const int N = (op == kF1 ? 2 : 1) * (op == kF2 || op == kB2 ? c.d : c.d_ff);
+  return ((long long)max_rows + 127) / 128 * ((N + 127) / 128) >= 2 * sm_count() &&
+         max_rows >= 64 * c.E;
 }
 
 template <int OP, typename T, int ACT>
 cudaError_t run_op(const GatedSimt &p, cudaStream_t s) {
   return wide_tiles(p.c, p.max_rows, OP) ? run_one<OP, T, ACT, 8, 8>(p, s)
-                                         : run_one<OP, T, ACT, 2, 4>(p, s);
+                                         : run_one<OP, T, ACT, 4, 4>(p, s);
 }
 
 template <typename T>
@@ -336,16 +347,13 @@ cudaError_t forward(const GatedSimt &p, cudaStream_t s) {
 }
 
 template <typename T>
-cudaError_t backward(const GatedSimt &p, cudaStream_t s) {
-  cudaError_t err = launch_pdl(k_gated_dy_rows<T>, (unsigned)((p.max_rows + 7) / 8), 256, 0, s, p);
-  if (err == cudaSuccess)
-    err = gated_dispatch(p.activation, [&](auto act) {
-      return run_op<kB1, T, decltype(act)::value>(p, s);
-    });
-  if (err == cudaSuccess) err = run_op<kB2, T, MOE_ACT_RELU>(p, s);
-  if (err == cudaSuccess) err = run_op<kW1, T, MOE_ACT_RELU>(p, s);
-  if (err == cudaSuccess) err = run_op<kW3, T, MOE_ACT_RELU>(p, s);
-  return err != cudaSuccess ? err : run_op<kW2, T, MOE_ACT_RELU>(p, s);
+cudaError_t backward_front(const GatedSimt &p, cudaStream_t s) {
+  const cudaError_t err =
+      launch_pdl(k_gated_rows<T>, (unsigned)((p.max_rows + 7ll) / 8), 256, 0, s, p);
+  if (err != cudaSuccess) return err;
+  return gated_dispatch(p.activation, [&](auto act) {
+    return run_op<kB1, T, decltype(act)::value>(p, s);
+  });
 }
 
 }  // namespace
@@ -359,8 +367,19 @@ cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s) {
   return p.c.act_dtype == MOE_BF16 ? forward<__nv_bfloat16>(p, s) : forward<float>(p, s);
 }
 
-cudaError_t launch_gated_simt_backward(const GatedSimt &p, cudaStream_t s) {
-  return p.c.act_dtype == MOE_BF16 ? backward<__nv_bfloat16>(p, s) : backward<float>(p, s);
+cudaError_t launch_gated_simt_front(const GatedSimt &p, cudaStream_t s) {
+  return p.c.act_dtype == MOE_BF16 ? backward_front<__nv_bfloat16>(p, s)
+                                   : backward_front<float>(p, s);
+}
+
+cudaError_t launch_gated_simt_dx(const GatedSimt &p, cudaStream_t s) {
+  return p.c.act_dtype == MOE_BF16 ? run_op<kB2, __nv_bfloat16, MOE_ACT_RELU>(p, s)
+                                   : run_op<kB2, float, MOE_ACT_RELU>(p, s);
+}
+
+cudaError_t launch_gated_simt_weights(const GatedSimt &p, cudaStream_t s) {
+  return p.c.act_dtype == MOE_BF16 ? run_op<kW, __nv_bfloat16, MOE_ACT_RELU>(p, s)
+                                   : run_op<kW, float, MOE_ACT_RELU>(p, s);
 }
 
 }  // namespace moe
