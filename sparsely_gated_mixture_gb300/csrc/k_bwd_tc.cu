@@ -91,17 +91,17 @@ struct BExtra<4> {
 
 // Mode 3 has the heaviest epilogue (two operands read, three written, an
 // exponential and a reciprocal an element): eight warps instead of four, each
-// with three staging tiles of 2 KB, at the price of one or two stages of the ring.
+// with two staging tiles of 2 KB, at the price of a stage of the one-CTA kernel's ring.
 template <int MODE>
 __host__ __device__ constexpr int epi_warps() { return MODE == 3 ? 8 : 4; }
 template <int MODE>
 __host__ __device__ constexpr int threads_of() { return 64 + 32 * epi_warps<MODE>(); }
 template <int MODE>
 __host__ __device__ constexpr int stages_of(bool pair) {
-  return pair ? (MODE == 3 ? 5 : 6) : (MODE == 3 ? 3 : 4);
+  return pair ? 6 : (MODE == 3 ? 3 : 4);
 }
 constexpr int G_TILE = 32 * 32 / 2;             // a staging tile of bf16, counted in floats
-constexpr int G_STG_BYTES = 8 * 3 * G_TILE * 4;  // mode 3
+constexpr int G_STG_BYTES = 8 * 2 * G_TILE * 4;  // mode 3
 
 // The CTA-pair kernel's tile ring, as in the forward expert GEMM: tile
 // indices from the even CTA's producer to the MMA issuer, both CTAs'
@@ -319,8 +319,8 @@ __device__ __forceinline__ void epilogue_rows(const BParams &p, const BTile &t, 
 // the accumulator was waited for. Global memory is read and written four lanes to a
 // row (a lane to a row would touch 32 lines an instruction); p1 and p3 of the
 // next 32 columns are fetched while these are worked on. They change to a lane's
-// own row through two of the warp's three staging tiles, where dP1 and dP3 take
-// their places, and h the third's, on the way back. Warp-collective.
+// own row through the warp's two staging tiles, where dP1 and dP3 and then h take
+// their places on the way back. Warp-collective.
 struct GatedPre {
   uint4 v[2][4];  // p1, p3: 8 columns of rows lane / 4 + 8 i
   // Columns n .. n + 31 of the warp's rows from m0 on; zero past the expert's.
@@ -370,6 +370,7 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
       for (int i = 0; i < 4; ++i) tile[w * kTile + piece(i)] = pre.v[w][i];
     __syncwarp();
     if (c + 1 < c0 + BN / 64) pre.fetch(p, ex, t, m0, n + 32);
+    uint4 hidden[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       uint4 *const at = tile + lane * 4 + (w ^ x);
@@ -394,8 +395,9 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
       }
       if (!real) o[0][0] = o[0][1] = o[0][2] = o[0][3] = o[1][0] = o[1][1] = o[1][2] = o[1][3] = 0;
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
+      for (int q = 0; q < 2; ++q)
         at[q * kTile] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+      hidden[w] = make_uint4(o[2][0], o[2][1], o[2][2], o[2][3]);
     }
     __syncwarp();
 #pragma unroll
@@ -404,9 +406,17 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
       const size_t at = (pr - lane + row) * p.N + n + quarter * 8;
       *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at) = tile[piece(i)];
       *reinterpret_cast<uint4 *>(ex.dP3 + at) = tile[kTile + piece(i)];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) tile[lane * 4 + (w ^ x)] = hidden[w];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = sub + 8 * i;
       if (m0 + row < t.rows)
         *reinterpret_cast<uint4 *>(ex.h + (size_t)(q0 + row) * p.N + n + quarter * 8) =
-            tile[2 * kTile + piece(i)];
+            tile[piece(i)];
     }
     __syncwarp();  // read before the next columns are written
   }
@@ -595,7 +605,7 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)(buf * BN);
       if constexpr (MODE == 3)
         epilogue_gated<ACT>(p, ex, t, m - lane, (warp - 2) >> 2, lane_addr,
-                            stg_all + (warp - 2) * 3 * G_TILE, pre);
+                            stg_all + (warp - 2) * 2 * G_TILE, pre);
       else
         epilogue_rows<MODE, OB>(p, t, m, lane_addr);
       tc_fence_before();
@@ -984,8 +994,8 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
     const int r_in_tile = quad * 32 + lane;
     const uint32_t acc_empty_leader0 = mapa(smem_u32(&acc_empty[0]), 0);
     const uint32_t acc_empty_leader1 = mapa(smem_u32(&acc_empty[1]), 0);
-    // This warp's two tiles (mode 3: three smaller ones).
-    float *stg = stg_all + (size_t)(warp - 2) * (MODE == 3 ? 3 * G_TILE : 2 * P_STG_TILE);
+    // This warp's two tiles (mode 3: of half the size).
+    float *stg = stg_all + (size_t)(warp - 2) * (MODE == 3 ? 2 * G_TILE : 2 * P_STG_TILE);
     uint32_t stg_cnt = 0;
     for (int local = 0;; ++local) {
       const int slot = local % kRing;
