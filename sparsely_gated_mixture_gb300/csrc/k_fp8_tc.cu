@@ -266,9 +266,11 @@ k_fp8_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           }
         }
       }
-      const uint32_t issued = it;  // copies have landed once their MMAs are done
+      // Copies in flight land first. The odd CTA's count on the even one's barriers:
+      // they have landed once their MMAs are done.
+      const uint32_t issued = it;
       for (uint32_t q = issued > (uint32_t)STAGES ? issued - STAGES : 0; q < issued; ++q)
-        mbar_drain(&empty[q % STAGES], (q / STAGES) & 1u);
+        mbar_drain(leader ? &full[q % STAGES] : &empty[q % STAGES], (q / STAGES) & 1u);
     }
     __syncwarp();
     pdl_trigger();

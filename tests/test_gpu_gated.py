@@ -437,6 +437,31 @@ def test_fp8_non_finite_and_bad_indexes(T):
     assert int(o["pos"][0, 1]) == -1 and int(o["keep"][0, 1]) == 0
 
 
+@pytest.mark.parametrize("T", [1, 24, 400])
+def test_fp8_non_finite_weight(T):
+    """An Inf in a weight makes its expert's outputs NaN, and no other's."""
+    s = inputs(T, 200, 4, 256, 1, BF16)
+    s["idx"][:, 0] = torch.arange(T) % 4
+    cfg, g = config(s, 4.0), dev(s)
+    good = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+    ref = run_fp8(cfg, R.SILU, g, good)
+    for w in range(3):
+        W = g[("W1", "W3", "W2")[w]].clone()
+        W[0, 130, 7] = float("inf")
+        E, K, N = W.shape
+        n8, ns = B.moe_weights_fp8_size(E, K, N)
+        q, sc, ws = buf(n8), buf(ns), buf(256, 0)
+        B.moe_weights_fp8(E, K, N, B.MOE_BF16, W, q, sc, ws)
+        assert B.moe_last_device_status(ws)[0] == 4
+        w8 = list(good)
+        w8[w] = (q.view(E, N, -1), sc.view(E, R.blocks(N), R.blocks(K)))
+        o = run_fp8(cfg, R.SILU, g, w8)
+        assert B.moe_last_device_status(o["ws"])[0] == 4
+        first = s["idx"][:, 0] == 0
+        assert torch.equal(o["y"].cpu()[~first], ref["y"].cpu()[~first])
+        assert bool(torch.isnan(o["y"].cpu()[first]).any(1).all())
+
+
 @pytest.mark.parametrize("T", [2, 300])
 def test_fp8_streams_and_graphs(T):
     s = inputs(T, 256, 5, 384, 2, BF16)
@@ -501,3 +526,154 @@ def test_a_training_step_and_serving():
     w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
     o8 = run_fp8(cfg, R.SILU, g, w8)
     check_forward(cfg, R.SILU, s, o8, reference8(cfg, R.SILU, s, w8))
+
+
+# ----------------------------------------------------------------------------- borders
+def sampled(s, at):
+    """The same call on some of its tokens (weights shared)."""
+    return {n: v if v is None or n not in ("x", "idx", "gate", "dy") else v[at].contiguous()
+            for n, v in s.items()}
+
+
+@pytest.mark.parametrize("T,E,k,cf", [(8192, 16, 4, 0.9), (8193, 16, 4, 0.9), (10000, 1024, 4, 1.0),
+                                      (8192, 1024, 4, 0.7), (2048, 3, 2, 0.5)])
+def test_routing_of_long_batches(T, E, k, cf):
+    """pos and keep on both sides of the one-launch routing (32768 choices), under
+    tight capacities; y for some tokens."""
+    s = inputs(T, 64, E, 64, k, BF16, seed=T + E, skew=1.0)
+    s["idx"][5] = s["idx"][5, 0]  # one expert in all of a token's choices
+    s["idx"][7, 0] = E
+    cfg, g = config(s, cf), dev(s)
+    pos, keep, _ = R.slots(s["idx"], E, cap(cfg))
+    o = run_forward(cfg, R.SILU, g, keeps=False)
+    assert B.moe_last_device_status(o["ws"])[0] == 6
+    assert torch.equal(o["pos"].cpu(), pos) and torch.equal(o["keep"].cpu(), keep)
+    at = [t for t in (0, 5, 6, T // 2, T - 1) if bool(keep[t].all())] + [0]
+    sub = sampled(s, at)
+    sub["gate"] = sub["gate"] * keep[at]
+    want = R.forward(R.SILU, sub["x"], sub["idx"], sub["gate"], s["W1"], s["b1"], s["W3"], s["b3"],
+                     s["W2"], s["b2"], T * k)
+    close("y", o["y"][at], want["y"], want["y_err"])
+
+
+@pytest.mark.parametrize("T,k,E,min_cap,fp8", [
+    (64, 8, 40, 1, False), (64, 8, 40, 1, True),    # 512 choices
+    (57, 9, 64, 1, False), (57, 9, 64, 1, True),    # 513
+    (64, 2, 2, 1, False), (64, 2, 2, 1, True),      # 64 rows an expert
+    (40, 2, 3, 100, False), (40, 2, 3, 100, True),  # more slots than tokens
+    (17, 16, 1024, 1, False), (17, 16, 1024, 1, True), (31, 1, 1, 1, False), (48, 3, 7, 1, True)])
+def test_few_rows_borders(T, k, E, min_cap, fp8):
+    s = inputs(T, 128, E, 192, k, BF16, seed=T * k)
+    s["idx"][0] = s["idx"][0, 0]  # one expert in all of a token's choices
+    cfg, g = config(s, float(E)), dev(s)
+    cfg.min_capacity = min_cap
+    if fp8:
+        w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+        check_forward(cfg, R.SILU, s, run_fp8(cfg, R.SILU, g, w8), reference8(cfg, R.SILU, s, w8))
+    else:
+        o = run_forward(cfg, R.SILU, g)
+        check_forward(cfg, R.SILU, s, o, reference(cfg, R.SILU, s))
+
+
+@pytest.mark.parametrize("dt,T,d,F", [(BF16, 160000, 64, 14336), (F32, 80000, 9, 30001)])
+def test_rows_past_32_bits(dt, T, d, F):
+    """Hidden rows of more than 2^31 values: y, pre-activations and gradients of
+    tokens on both sides, forward, backward and in 8 bits."""
+    s = inputs(T, d, 2, F, 1, dt, biases=False)
+    cfg, g = config(s, 2.0), dev(s)
+    order = torch.argsort(s["idx"][:, 0], stable=True)  # the packed rows' tokens
+    at = torch.cat([order[:5], order[(1 << 31) // F - 2:(1 << 31) // F + 3], order[-20:]])
+    sub = sampled(s, at)
+    want = R.forward(R.SILU, sub["x"], sub["idx"], sub["gate"], s["W1"], None, s["W3"], None,
+                     s["W2"], None, T)
+    o = run_forward(cfg, R.SILU, g)
+    assert B.moe_last_device_status(o["ws"])[0] == 0
+    close("y", o["y"][at.cuda()], want["y"], want["y_err"])
+    rows = torch.empty(T, dtype=torch.long)
+    rows[order] = torch.arange(T)
+    by = torch.argsort(sub["idx"][:, 0], stable=True)  # the sample's packed order
+    for q, n in enumerate(("p1", "p3")):
+        close(n, o[n][rows[at[by]].cuda()], want["pre"][q], want["pre_err"][q])
+    # Only the sample's tokens have a gradient, so the weights' come from them.
+    dy = torch.zeros_like(s["dy"])
+    dy[at] = s["dy"][at]
+    g["dy"] = dy.cuda()
+    del o["ws"]
+    b = run_backward(cfg, R.SILU, g, o["p1"], o["p3"])
+    assert B.moe_last_device_status(b["ws"])[0] == 0
+    p = [o[n][rows[at[by]].cuda()].cpu() for n in ("p1", "p3")]
+    wb, eb = R.backward(R.SILU, sub["x"], sub["idx"], sub["gate"], p[0], p[1], s["W1"], s["W3"],
+                        s["W2"], None, sub["dy"], T)
+    for n in ("dx", "dgate"):
+        close(n, b[n][at.cuda()], wb[n], eb[n])
+    for n in ("dW1", "dW3", "dW2"):
+        close(n, b[n], wb[n], eb[n])
+    del b, o
+    if dt == BF16:
+        w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+        o = run_fp8(cfg, R.SILU, g, w8)
+        q, sc = zip(*w8)
+        want = R.forward(R.SILU, sub["x"], sub["idx"], sub["gate"], q[0], None, q[1], None, q[2],
+                         None, T, weights8=sc)
+        close("y8", o["y"][at.cuda()], want["y"], want["y_err"])
+
+
+@pytest.mark.parametrize("T", [3, 600])
+def test_weights_past_32_bits(T):
+    """Weights of more than 2^31 values: the last experts, in bf16 and 8 bits."""
+    E, d, F, k = 1024, 512, 4608, 2
+    gen = torch.Generator("cuda").manual_seed(T)
+
+    def normal(*shape, std):
+        return torch.randn(shape, generator=gen, device="cuda", dtype=BF16).mul_(std)
+    s = inputs(T, d, 8, 64, k, BF16, biases=False)
+    s["idx"] = 1016 + s["idx"]
+    s["idx"][0, 0] = 0
+    g = dict(x=s["x"].cuda(), idx=s["idx"].cuda(), gate=s["gate"].cuda(), b1=None, b3=None,
+             b2=None, W1=normal(E, d, F, std=d ** -0.5), W3=normal(E, d, F, std=d ** -0.5),
+             W2=normal(E, F, d, std=F ** -0.5))
+    cfg = B.config(T, d, E, F, k, float(E))
+    at = list(range(0, T, max(1, T // 5)))
+    # The experts in use, renumbered, for the reference.
+    used = sorted(set(s["idx"].flatten().tolist()))
+    idx = torch.tensor([[used.index(e) for e in r] for r in s["idx"].tolist()], dtype=torch.int32)
+    few = {n: g[n][used].cpu() for n in ("W1", "W3", "W2")}
+    o = run_forward(cfg, R.SILU, g, keeps=False)
+    want = R.forward(R.SILU, s["x"][at], idx[at], s["gate"][at], few["W1"], None, few["W3"], None,
+                     few["W2"], None, T)
+    close("y", o["y"][at], want["y"], want["y_err"])
+    w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+    o = run_fp8(cfg, R.SILU, g, w8)
+    q = [v[used] for v, _ in w8]
+    sc = [v[used] for _, v in w8]
+    want = R.forward(R.SILU, s["x"][at], idx[at], s["gate"][at], q[0], None, q[1], None, q[2],
+                     None, T, weights8=sc)
+    close("y8", o["y"][at], want["y"], want["y_err"])
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_waits_that_run_out(T, monkeypatch):
+    """With no time to wait, the kernels report MOE_ERR_TIMEOUT and end; the next
+    call on the same workspace is right."""
+    s = inputs(T, 512, 4, 768, 2, BF16)
+    cfg, g = config(s, 4.0), dev(s)
+    w8 = [quantise(g, n, BF16) for n in ("W1", "W3", "W2")]
+    good = run_forward(cfg, R.SILU, g)
+    back = run_backward(cfg, R.SILU, g, good["p1"], good["p3"])
+    good8 = run_fp8(cfg, R.SILU, g, w8)
+    monkeypatch.setenv("MOE_WAIT_LIMIT_NS", "0")
+    codes = []
+    for call, ws in ((lambda w: run_forward(cfg, R.SILU, g, ws=w), good["ws"]),
+                     (lambda w: run_backward(cfg, R.SILU, g, good["p1"], good["p3"], ws=w),
+                      back["ws"]),
+                     (lambda w: run_fp8(cfg, R.SILU, g, w8, ws=w), good8["ws"])):
+        call(ws)
+        codes.append(B.moe_last_device_status(ws)[0])
+    assert codes[0] == 5 and codes[1] == 5 and codes[2] == 5, codes
+    monkeypatch.delenv("MOE_WAIT_LIMIT_NS")
+    o = run_forward(cfg, R.SILU, g, ws=good["ws"])
+    assert torch.equal(o["y"], good["y"])
+    b = run_backward(cfg, R.SILU, g, good["p1"], good["p3"], ws=back["ws"])
+    for n in ("dx", "dgate", "dW1", "dW3", "dW2", "db1", "db3", "db2"):
+        assert torch.equal(b[n], back[n]), n
+    assert torch.equal(run_fp8(cfg, R.SILU, g, w8, ws=good8["ws"])["y"], good8["y"])
