@@ -256,6 +256,12 @@ struct GatedFew {
 cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s);
 
 // k_gated.cu: what surrounds the products of the backward.
+// The backward's rows in bf16 (d a multiple of 64): xbuf = x in packed rows, dY =
+// dy and dU = gate * dy in padded blocks, pad rows zero; and zero rows behind the
+// last packed ones of xbuf and h, which the weight gradients' K tails read.
+cudaError_t launch_gated_gather(const moe_config &c, long long P_max, const GatedRows &rows,
+                                const int32_t *poff, const void *x, const void *dy, void *xbuf,
+                                void *h, void *dY, void *dU, cudaStream_t s);
 // dgate [T,k] = sum of a kept choice's dgpart row plus <dy, b2>; 0 for the others.
 // dgpart's row of assignment (t, j) is base[e] + pos[t,j].
 cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t *idx,

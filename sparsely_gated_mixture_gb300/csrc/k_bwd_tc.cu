@@ -28,8 +28,8 @@
 //   modes 0, 1: A K-major [128 rows x 64 K]; B K-major [256 rows x 64 K]: the
 //               weight's own rows (W2[e] is [d_ff, d]: row f holds K = d
 //               contiguous values; W1[e] is [d, d_ff]: row i holds d_ff).
-//   mode 2:     A MN-major (M contiguous) as two [64 K x 64 M] boxes, B
-//               MN-major as four [64 K x 64 N] boxes; the instruction
+//   mode 2:     A MN-major (M contiguous) as two [64 K x 64 M] blocks, B
+//               MN-major as four [64 K x 64 N] blocks, a load each; the instruction
 //               descriptor's transpose bits select MN-major for both.
 // Warp roles, the 4-stage ring, two TMEM accumulators and the bounded waits
 // are those of the forward kernel: warp 0 TMA producer, warp 1 TMEM owner and
@@ -523,14 +523,8 @@ k_bwd_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
             tma_load_2d(sB + s * B_BYTES, tb, &full[s], kx, t.e * p.N + t.nb * BN);
           } else {
             const int arow = p.offset[t.e] + kb * BK, brow = t.prow0 + kb * BK;
-#pragma unroll
-            for (int j = 0; j < BM / 64; ++j)
-              tma_load_2d(sA + s * A_BYTES + j * (BK * 128), &tmA, &full[s], t.mb * BM + j * 64,
-                          arow);
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(sB + s * B_BYTES + j * (BK * 128), &tmB, &full[s], t.nb * BN + j * 64,
-                          brow);
+            tma_load_blocks(sA + s * A_BYTES, &tmA, &full[s], arow, t.mb * (BM / 64));
+            tma_load_blocks(sB + s * B_BYTES, &tmB, &full[s], brow, t.nb * (BN / 64));
           }
         }
       }
@@ -913,14 +907,8 @@ k_bwd_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
             const int arow = p.offset[t.e] + kx, brow = t.prow0 + kx;
             const int mcol = t.mb * 2 * BM + (int)rank * BM;
             const int ncol = t.nb * BN + (int)rank * (BN / 2);
-#pragma unroll
-            for (int q = 0; q < BM / 64; ++q)
-              tma_load_2d_pair(sA + s * P_A_BYTES + q * (BK * 128), &tmA, full_leader,
-                               mcol + q * 64, arow);
-#pragma unroll
-            for (int q = 0; q < (BN / 2) / 64; ++q)
-              tma_load_2d_pair(sB + s * P_B_BYTES + q * (BK * 128), &tmB, full_leader,
-                               ncol + q * 64, brow);
+            tma_load_blocks_pair(sA + s * P_A_BYTES, &tmA, full_leader, arow, mcol / 64);
+            tma_load_blocks_pair(sB + s * P_B_BYTES, &tmB, full_leader, brow, ncol / 64);
           }
         }
       }
@@ -1164,7 +1152,8 @@ bool bwd_tc_supported(const moe_config &c) {
 // MOE_BWD_TC_VARIANT=single or =pair forces one kernel (read at each call);
 // otherwise the CTA pair runs where its reduction is long (K >= 1024; for the
 // weight gradient, the rows per expert, bounded by the capacity) and it has
-// at least four waves of 256 x 256 tiles.
+// at least pair_waves (four, unless the caller measured otherwise) waves of 256 x
+// 256 tiles.
 static int bwd_variant() {
   const char *v = getenv("MOE_BWD_TC_VARIANT");
   if (!v || !*v) return 0;
@@ -1178,7 +1167,7 @@ static int pick_pair(const BwdGemm &g, long long k_len, long long tiles) {
   const int clusters = pair_clusters_bwd<MODE>(bwd_smem_bytes_pair<MODE>(g.E));
   if (clusters <= 0) return 0;
   if (force == 2) return clusters;
-  return (k_len >= 1024 && tiles >= 4LL * clusters) ? clusters : 0;
+  return (k_len >= 1024 && tiles >= (long long)g.pair_waves * clusters) ? clusters : 0;
 }
 
 cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) {
@@ -1212,13 +1201,13 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
   const long long nb = (g.N + BN - 1) / BN;
   if (g.mode == 2) {
     // A: the forward's packed rows [a_rows, M]; B: padded rows [b_rows, N].
-    if (!make_map(&ta, g.A, (uint64_t)g.a_rows, (uint64_t)g.M, 64) ||
-        !make_map(&tb, g.B, (uint64_t)g.b_rows, (uint64_t)g.N, 64))
-      return cudaErrorInvalidValue;
-    const int cl = pick_pair<2>(g, g.k_len, (long long)g.E * ((g.M + 255) / 256) * nb);
     CUtensorMap to;
-    if (cl > 0 && (uintptr_t)g.out % 16 == 0 &&
-        make_out_map3(&to, g.out, g.E, g.M, g.N, g.out_bf16))
+    int cl = pick_pair<2>(g, g.k_len, (long long)g.E * ((g.M + 255) / 256) * nb);
+    if ((uintptr_t)g.out % 16 != 0 || !make_out_map3(&to, g.out, g.E, g.M, g.N, g.out_bf16)) cl = 0;
+    if (!make_blocks_map(&ta, g.A, (uint64_t)g.a_rows, (uint64_t)g.M, 64, BM / 64) ||
+        !make_blocks_map(&tb, g.B, (uint64_t)g.b_rows, (uint64_t)g.N, 64, cl > 0 ? 2 : 4))
+      return cudaErrorInvalidValue;
+    if (cl > 0)
       return g.out_bf16 ? launch_mode_pair<2, true>(ta, tb, to, p, cl, s)
                         : launch_mode_pair<2>(ta, tb, to, p, cl, s);
     return g.out_bf16 ? launch_mode<2, true>(ta, tb, p, s) : launch_mode<2>(ta, tb, p, s);

@@ -10,9 +10,11 @@
 //
 // Design (one persistent CTA per SM, 6 warps):
 //   warp 0     TMA producer: A tile [128 rows x 64 K] (K-major, 128B swizzle)
-//              and B tile [64 K x 256 N] as four [64 x 64] boxes (N-major,
-//              i.e. the weights' own row-major layout, 128B swizzle) into a
-//              4-stage shared-memory ring, completion on mbarriers.
+//              and B tile [64 K x 256 N] as four [64 x 64] blocks (N-major,
+//              i.e. the weights' own row-major layout, 128B swizzle) of one
+//              load (four loads take the issuing thread longer than a stage's
+//              MMAs: 120 cycles each) into a 4-stage shared-memory ring,
+//              completion on mbarriers.
 //   warp 1     allocates 512 TMEM columns (two 128 x 256 fp32 accumulators)
 //              and one lane issues tcgen05.mma kind::f16 (bf16 x bf16 -> fp32)
 //              M=128 N=256 K=16, four per stage; tcgen05.commit frees the
@@ -287,18 +289,10 @@ k_ffn_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtens
           }
           mbar_expect_tx(&full[s], STAGE_BYTES);
           tma_load_2d(sA + s * A_BYTES, &tmA, &full[s], kb * BK, arow);
-#pragma unroll
-          for (int j = 0; j < BN / 64; ++j) {
-            const CUtensorMap *tm = &tmB;
-            int n = n0 + j * 64;
-            if constexpr (LAYER == kGated) {
-              if (j >= kGatedBN / 64) {
-                tm = &ex.b;
-                n -= kGatedBN;
-              }
-            }
-            tma_load_2d(sB + s * B_BYTES + j * (BK * 128), tm, &full[s], n, brow + kb * BK);
-          }
+          tma_load_blocks(sB + s * B_BYTES, &tmB, &full[s], brow + kb * BK, n0 / 64);
+          if constexpr (LAYER == kGated)
+            tma_load_blocks(sB + s * B_BYTES + B_BYTES / 2, &ex.b, &full[s], brow + kb * BK,
+                            n0 / 64);
         }
       }
       // Copies in flight complete before the CTA leaves (bounded).
@@ -690,10 +684,7 @@ k_ffn_tc_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ C
           const uint32_t full_leader = mapa(smem_u32(&full[s]), 0);
           if (leader) mbar_expect_tx(&full[s], 2 * P_STAGE_BYTES);
           tma_load_2d_pair(sA + s * P_A_BYTES, &tmA, full_leader, kx, arow);
-#pragma unroll
-          for (int q = 0; q < P_BN_HALF / 64; ++q)
-            tma_load_2d_pair(sB + s * P_B_BYTES + q * (BK * 128), tmb, full_leader,
-                             ncol + q * 64, brow + kx);
+          tma_load_blocks_pair(sB + s * P_B_BYTES, tmb, full_leader, brow + kx, ncol / 64);
         }
       }
       // This CTA's copies have landed once the MMAs that read them are done.
@@ -937,6 +928,17 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, ui
   return r == CUDA_SUCCESS;
 }
 
+bool make_blocks_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
+                     uint32_t box_rows, uint32_t blocks) {
+  auto fn = encode_fn();
+  if (!fn || cols % 64 != 0) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64}, strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, blocks}, one[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2-D tensor [rows, cols] (cols % 8 == 0, 16-byte-aligned base) of bf16 or
 // fp32: an expert GEMM's output, box [32 rows, 32 columns] in the 64-byte
 // (bf16) or 128-byte (fp32) swizzle, for the CTA-pair kernel's TMA stores.
@@ -1137,13 +1139,14 @@ static cudaError_t launch_ffn_layer1(const moe_config &c, int C, const void *xbu
                                      cudaStream_t s) {
   const uint64_t A = (uint64_t)c.T * c.k;
   CUtensorMap ta, tb, to;
-  if (!make_map(&ta, xbuf, A, c.d, BM) || !make_map(&tb, W1, (uint64_t)c.E * c.d, c.d_ff, BK))
-    return cudaErrorInvalidValue;
   const int n_blocks = (c.d_ff + BN - 1) / BN;
+  const int clusters = pair_for(c, C, c.d, n_blocks);
+  if (!make_map(&ta, xbuf, A, c.d, BM) ||
+      !make_blocks_map(&tb, W1, (uint64_t)c.E * c.d, c.d_ff, BK, BN / 64 / (clusters ? 2 : 1)))
+    return cudaErrorInvalidValue;
   Params p = layer_params(c.d, c.d_ff, n_blocks, c.E, offset, row_gate, b1, hbuf, st);
   p.tma_out = make_rows_map(&to, hbuf, A, c.d_ff, false) ? 1 : 0;
   if (!p.tma_out) to = ta;  // unused
-  const int clusters = pair_for(c, C, c.d, n_blocks);
   return clusters ? launch_layer_pair<1>(ta, tb, to, p, clusters, s)
                   : launch_layer<1>(ta, tb, to, p, s);
 }
@@ -1154,12 +1157,13 @@ cudaError_t launch_ffn_layer2(const moe_config &c, int C, long long max_rows, co
                               cudaStream_t s) {
   const uint64_t A = (uint64_t)max_rows;
   CUtensorMap ta, tb, to;
-  if (!make_map(&ta, hbuf, A, c.d_ff, BM) || !make_map(&tb, W2, (uint64_t)c.E * c.d_ff, c.d, BK))
-    return cudaErrorInvalidValue;
   const int n_blocks = (c.d + BN - 1) / BN;
+  const int clusters = pair_for(c, C, c.d_ff, n_blocks);
+  if (!make_map(&ta, hbuf, A, c.d_ff, BM) ||
+      !make_blocks_map(&tb, W2, (uint64_t)c.E * c.d_ff, c.d, BK, BN / 64 / (clusters ? 2 : 1)))
+    return cudaErrorInvalidValue;
   Params p = layer_params(c.d_ff, c.d, n_blocks, c.E, offset, row_gate, b2, zbuf, st);
   p.z_bf16 = z_bf16 ? 1 : 0;
-  const int clusters = pair_for(c, C, c.d_ff, n_blocks);
   // The CTA-pair kernel's output box is [32 rows, 32 columns]; the one-CTA
   // kernel stores fp32 Z in 16-column boxes (its staging tiles are 2 KB).
   p.tma_out = (clusters || z_bf16 ? make_rows_map(&to, zbuf, A, c.d, !z_bf16)
@@ -1190,8 +1194,8 @@ cudaError_t launch_gated_tc_layer1(const moe_config &c, int C, int activation, l
   const uint64_t A = (uint64_t)max_rows, wrows = (uint64_t)c.E * c.d;
   CUtensorMap ta, tb, to;
   Extra<kGated> ex{};
-  if (!make_map(&ta, xbuf, A, c.d, BM) || !make_map(&tb, W1, wrows, c.d_ff, BK) ||
-      !make_map(&ex.b, W3, wrows, c.d_ff, BK))
+  if (!make_map(&ta, xbuf, A, c.d, BM) || !make_blocks_map(&tb, W1, wrows, c.d_ff, BK, 2) ||
+      !make_blocks_map(&ex.b, W3, wrows, c.d_ff, BK, 2))
     return cudaErrorInvalidValue;
   const int n_blocks = (c.d_ff + kGatedBN - 1) / kGatedBN;
   Params p = layer_params(c.d, c.d_ff, n_blocks, c.E, offset, nullptr, b1, hbuf, st);

@@ -209,6 +209,62 @@ k_gated_dgate(long long A, int E, int k, int d, int n_blocks, const int32_t *__r
   if (lane == 0) dgate[a] = s;
 }
 
+// One warp per padded row, then one per zero row: 16 bytes a lane, four in flight
+// of each operand.
+__global__ void __launch_bounds__(256)
+k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__restrict__ offset,
+               const int32_t *__restrict__ poff, const int32_t *__restrict__ row_token,
+               const float *__restrict__ row_gate, const uint4 *__restrict__ x,
+               const uint4 *__restrict__ dy, uint4 *__restrict__ xbuf, uint4 *__restrict__ h,
+               uint4 *__restrict__ dY, uint4 *__restrict__ dU) {
+  pdl_wait();
+  pdl_trigger();
+  const long long w = (blockIdx.x * 256ll + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  if (w >= P_max) {  // a row behind the last packed one
+    const size_t r = (size_t)offset[E] + (w - P_max);
+    for (int i = lane; i < nv; i += 32) xbuf[r * nv + i] = z;
+    for (int i = lane; i < fv; i += 32) h[r * fv + i] = z;
+    return;
+  }
+  if (w >= poff[E]) return;
+  int lo = 0, hi = E;  // largest e with poff[e] <= w
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (poff[mid] <= w) lo = mid;
+    else hi = mid;
+  }
+  const int m = (int)(w - poff[lo]), q = offset[lo] + m;
+  uint4 *oy = dY + w * nv, *ou = dU + w * nv;
+  if (q >= offset[lo + 1]) {
+    for (int i = lane; i < nv; i += 32) oy[i] = ou[i] = z;
+    return;
+  }
+  const size_t t = (size_t)(row_token[q] / k) * nv;
+  const float2 g = both(row_gate[q]);
+  uint4 *ox = xbuf + (size_t)q * nv;
+  constexpr int N = 4;
+  for (int i0 = lane; i0 < nv; i0 += 32 * N) {
+    uint4 a[N], b[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = i0 + 32 * j;
+      a[j] = i < nv ? x[t + i] : z;
+      b[j] = i < nv ? dy[t + i] : z;
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = i0 + 32 * j;
+      if (i >= nv) break;
+      ox[i] = a[j];
+      oy[i] = b[j];
+      ou[i] = make_uint4(pack_bf16x2(mul2(unpack2(b[j].x), g)), pack_bf16x2(mul2(unpack2(b[j].y), g)),
+                         pack_bf16x2(mul2(unpack2(b[j].z), g)), pack_bf16x2(mul2(unpack2(b[j].w), g)));
+    }
+  }
+}
+
 // The bias gradients: column sums of each expert's rows, a block for 64 columns
 // and an expert. Eight warps take rows in turn, 16 bytes a lane and eight of
 // them in flight (widths of an odd size: a value a lane); lanes, then warps,
@@ -324,6 +380,16 @@ k_gated_dx(int T_, int E, int k, int d, const int32_t *__restrict__ idx,
 cudaError_t launch_gated_route(const GatedRouteArgs &a, cudaStream_t s) {
   return launch_pdl(k_gated_route, (a.A + kRouteChunk - 1) / kRouteChunk, kRouteChunk,
                     ((2 * (size_t)route_copies(a.E) + 1) * a.E + 1) * 4, s, a);
+}
+
+cudaError_t launch_gated_gather(const moe_config &c, long long P_max, const GatedRows &rows,
+                                const int32_t *poff, const void *x, const void *dy, void *xbuf,
+                                void *h, void *dY, void *dU, cudaStream_t s) {
+  const long long warps = P_max + kBwdRowPad;
+  return launch_pdl(k_gated_gather, (unsigned)((warps + 7) / 8), 256, 0, s, P_max, c.E, c.k,
+                    c.d / 8, c.d_ff / 8, rows.offset, poff, rows.row_token, rows.row_gate,
+                    (const uint4 *)x, (const uint4 *)dy, (uint4 *)xbuf, (uint4 *)h, (uint4 *)dY,
+                    (uint4 *)dU);
 }
 
 cudaError_t launch_gated_begin(DeviceStatus *st, cudaStream_t s) {

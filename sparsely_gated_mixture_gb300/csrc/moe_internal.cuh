@@ -346,6 +346,7 @@ struct BwdGemm {
   int activation = 0;
   const void *pre1 = nullptr, *pre3 = nullptr, *A3 = nullptr, *B3 = nullptr;
   void *out3 = nullptr, *h = nullptr;
+  int pair_waves = 4;  // waves of 256 x 256 tiles from which the CTA pairs run
 };
 bool bwd_tc_supported(const moe_config &cfg);
 cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s);

@@ -15,6 +15,12 @@ namespace moe {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 // 2-D bf16 tensor [rows, cols] (cols contiguous), box [box_rows, 64 cols], 128B swizzle.
 bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// The same for an operand whose columns are not the reduction (cols % 64 == 0),
+// seen as [cols / 64, rows, 64]: box [blocks, box_rows, 64], so that one load brings
+// `blocks` swizzled column blocks side by side. A thread issues a load every 120
+// cycles or so, and a stage's MMAs take 512.
+bool make_blocks_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols,
+                     uint32_t box_rows, uint32_t blocks);
 // 2-D bf16 or fp32 tensor [rows, cols] (cols % 8 == 0, 16-byte-aligned base), box
 // [32 rows, 32 columns], 64-byte (bf16) or 128-byte (fp32) swizzle: a GEMM's
 // output for stage_store_bf16 / stage_store_f32. False if it cannot be made.
@@ -123,6 +129,16 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, u
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Column blocks from `block` on, rows from y on, of a make_blocks_map tensor.
+__device__ __forceinline__ void tma_load_blocks(void *dst, const CUtensorMap *map, uint64_t *bar,
+                                                int y, int block) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(smem_u32(bar)), "r"(0), "r"(y), "r"(block)
       : "memory");
 }
 
@@ -334,6 +350,14 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
       "l"((uint64_t)map), "r"(bar_cluster_addr), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_blocks_pair(void *dst, const CUtensorMap *map,
+                                                     uint32_t bar_cluster_addr, int y, int block) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"((uint64_t)map), "r"(bar_cluster_addr), "r"(0), "r"(y), "r"(block)
       : "memory");
 }
 // Arrives on the barrier at this offset in every CTA of `mask` (bit = cluster rank).
