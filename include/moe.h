@@ -624,8 +624,9 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
  * again from these, so nothing else is kept), dy [T,d] act_dtype. Outputs: dx
  * [T,d], dW1, dW3 [E,d,d_ff], dW2 [E,d_ff,d], db1, db3 [E,d_ff], db2 [E,d] in
  * act_dtype (fp32 sums rounded once; an expert without rows gets zeros), dgate
- * [T,k] fp32; db1, db3 and db2 may each be NULL. In bf16 layers dP1, dP3, g dy
- * and h are bf16 operands of the products. No output may overlap an input. ws:
+ * [T,k] fp32; db1, db3 and db2 may each be NULL. In bf16 layers dP1, dP3 and g h
+ * are bf16 operands of the products (dW2 = (g h)^T dy), and tensor-core sums cut
+ * instead of rounding, which leaves dgate off as moe_backward's. No output may overlap an input. ws:
  * moe_gated_backward_workspace_size bytes, scratch, its status word cleared
  * first; after MOE_ERR_NONFINITE no expert's gradients are to be used.
  */

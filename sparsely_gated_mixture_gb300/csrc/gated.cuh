@@ -257,23 +257,25 @@ cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s);
 
 // k_gated.cu: what surrounds the products of the backward.
 // The backward's rows in bf16 (d a multiple of 64): xbuf = x in packed rows, dY =
-// dy and dU = gate * dy in padded blocks, pad rows zero; and zero rows behind the
-// last packed ones of xbuf and h, which the weight gradients' K tails read.
+// dy in padded blocks, pad rows zero; and zero rows behind the last packed ones of
+// xbuf and h, which the weight gradients' K tails read.
 cudaError_t launch_gated_gather(const moe_config &c, long long P_max, const GatedRows &rows,
                                 const int32_t *poff, const void *x, const void *dy, void *xbuf,
-                                void *h, void *dY, void *dU, cudaStream_t s);
+                                void *h, void *dY, cudaStream_t s);
 // dgate [T,k] = sum of a kept choice's dgpart row plus <dy, b2>; 0 for the others.
 // dgpart's row of assignment (t, j) is base[e] + pos[t,j].
 cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t *idx,
                                const int32_t *pos, const uint8_t *keep, const int32_t *base,
                                const float *dgpart, const void *dy, const void *b2, float *dgate,
                                cudaStream_t s);
-// The bias gradients (each may be null) db2 = the column sums of dU [rows, d],
-// db1 and db3 of dP1 and dP3 [rows, d_ff], over each expert's rows from base[e]
-// on; rows in act_dtype, or fp32 (src_f32), sums in act_dtype.
+// The bias gradients (each may be null) db2 = the column sums of dY [rows, d],
+// each row times its gate (row_gate null: of dY as it is), db1 and db3 of dP1 and
+// dP3 [rows, d_ff], over each expert's rows from base[e] on; rows in act_dtype, or
+// fp32 (src_f32), sums in act_dtype.
 cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t *offset,
-                                const int32_t *base, const void *dU, void *db2, const void *dP1,
-                                void *db1, const void *dP3, void *db3, cudaStream_t s);
+                                const int32_t *base, const void *dY, const float *row_gate,
+                                void *db2, const void *dP1, void *db1, const void *dP3, void *db3,
+                                cudaStream_t s);
 // dx = dy + the kept choices' rows base[e] + pos of dX.
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                             const uint8_t *keep, const int32_t *base, const float *dX,

@@ -132,8 +132,9 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
 }
 
 // Tensor cores: xbuf and h are packed rows (64 more than there can be, for the
-// zeroed tail that the weight gradients read), dY, dU, dP1, dP3 and dX rows of
-// padded blocks (offsets poff). CUDA cores: fp32 packed rows, no dY.
+// zeroed tail that the weight gradients read; h's are gate * h), dY, dP1, dP3 and
+// dX rows of padded blocks (offsets poff). CUDA cores: fp32 packed rows, dU = gate *
+// dy in dY's place.
 struct GatedBwdLayout {
   GatedRoute r;
   size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, total;
@@ -153,7 +154,7 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   L.xbuf = take(tc ? (R + kBwdRowPad) * d * 2 : R * d * 4);
   L.h = take((R + (tc ? kBwdRowPad : 0)) * F * eb);
   L.dY = take(tc ? P * d * 2 : 0);
-  L.dU = take(P * d * eb);
+  L.dU = take(tc ? 0 : P * d * 4);
   L.dP1 = take(P * F * eb);
   L.dP3 = take(P * F * eb);
   L.dX = take(P * d * 4);
@@ -217,11 +218,11 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   const uint8_t *keep = ws_at<uint8_t>(ws, L.r.keep);
   const int32_t *poff = ws_at<int32_t>(ws, L.poff);
   void *xbuf = ws_at<char>(ws, L.xbuf), *h = ws_at<char>(ws, L.h);
-  void *dY = ws_at<char>(ws, L.dY), *dU = ws_at<char>(ws, L.dU);
+  void *dY = ws_at<char>(ws, L.dY);
   void *dP1 = ws_at<char>(ws, L.dP1), *dP3 = ws_at<char>(ws, L.dP3);
   float *dX = ws_at<float>(ws, L.dX), *dgpart = ws_at<float>(ws, L.dgpart);
   const long long R = gated_max_rows(c), cap = host_capacity(c);
-  MOE_CUDA(launch_gated_gather(c, L.P_max, rows, poff, q.x, q.dy, xbuf, h, dY, dU, s));
+  MOE_CUDA(launch_gated_gather(c, L.P_max, rows, poff, q.x, q.dy, xbuf, h, dY, s));
   BwdGemm g{3, c.d, c.d_ff, 0, c.E, L.P_max, 0, 0, dY, q.W2, rows.offset, poff, rows.row_gate,
             nullptr, dP1, dgpart, false};
   g.activation = q.activation;
@@ -239,7 +240,8 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   if (r != MOE_OK) return r;
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
                               fs));
-  MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dU, q.db2, dP1, q.db1, dP3, q.db3, fs));
+  MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dY, rows.row_gate, q.db2, dP1, q.db1,
+                               dP3, q.db3, fs));
   BwdGemm gx{4, c.d_ff, c.d, 0, c.E, L.P_max, 0, 0, dP1, q.W1, rows.offset, poff, nullptr, nullptr,
              dX, nullptr, false};
   gx.A3 = dP3;
@@ -254,7 +256,7 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
     w.pair_waves = 1;
     return launch_bwd_gemm(w, st, s);
   };
-  MOE_CUDA(wgrad(h, c.d_ff, dU, c.d, q.dW2));
+  MOE_CUDA(wgrad(h, c.d_ff, dY, c.d, q.dW2));
   MOE_CUDA(wgrad(xbuf, c.d, dP1, c.d_ff, q.dW1));
   MOE_CUDA(wgrad(xbuf, c.d, dP3, c.d_ff, q.dW3));
   if (side) {
@@ -446,7 +448,7 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   MOE_CUDA(launch_gated_simt_dx(p, s));
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, expert_idx, pos, keep, off, p.dgpart, dy, b2, dgate,
                               s));
-  MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, db2, p.dP1, db1, p.dP3, db3, fs));
+  MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, nullptr, db2, p.dP1, db1, p.dP3, db3, fs));
   MOE_CUDA(launch_gated_dx(c, expert_idx, pos, keep, off, p.dX, dy, dx, s));
   if (side) {
     MOE_CUDA(cudaEventRecord(side->join, side->s));

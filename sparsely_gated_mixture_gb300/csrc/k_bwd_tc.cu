@@ -12,8 +12,9 @@
 //       dW2: A = h rows, B = g * dY rows;  dW1: A = x rows, B = dpre rows
 //   gated dgrad through W2 (mode 3): D as in mode 0; with the kept
 //       pre-activations p1, p3 of the row, a = act(p1), h = a * p3:
-//       dP1 = g D p3 act'(p1), dP3 = g D a (bf16, padded rows), h (bf16, packed
-//       rows: the weight gradient's operand) and the dgate partial <D, h>
+//       dP1 = g D p3 act'(p1), dP3 = g D a (bf16, padded rows), g h (bf16, packed
+//       rows: the weight gradient dW2 = (g h)^T dY's operand, so that only one of
+//       its two is rounded) and the dgate partial <D, h>
 //   gated dgrad (mode 4): dX_rows = dP1 W1[e]^T + dP3 W3[e]^T, as mode 1 with a
 //       reduction that runs over both pairs
 //
@@ -82,7 +83,7 @@ struct BExtra {};
 template <>
 struct BExtra<3> {
   const __nv_bfloat16 *pre1, *pre3;  // [packed rows, N]
-  __nv_bfloat16 *dP3, *h;
+  __nv_bfloat16 *dP3, *h;            // h: g h
 };
 template <>
 struct BExtra<4> {
@@ -391,7 +392,7 @@ __device__ __forceinline__ void epilogue_gated(const BParams &p, const BExtra<3>
         odd = fma2(d1, both(0.f), fma2(d3, both(0.f), odd));
         o[0][j] = pack_bf16x2(d1);
         o[1][j] = pack_bf16x2(d3);
-        o[2][j] = pack_bf16x2(h);
+        o[2][j] = pack_bf16x2(mul2(h, both(g)));
       }
       if (!real) o[0][0] = o[0][1] = o[0][2] = o[0][3] = o[1][0] = o[1][1] = o[1][2] = o[1][3] = 0;
 #pragma unroll

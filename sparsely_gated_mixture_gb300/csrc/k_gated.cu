@@ -5,10 +5,12 @@
 namespace moe {
 namespace {
 
-// Up to three arrays of rows and what their column sums are.
+// Up to three arrays of rows and what their column sums are; weight: by packed
+// row, or null.
 template <typename S, typename O>
 struct GatedColumns {
   const S *src[3];
+  const float *weight[3];
   O *out[3];
   int cols[3], blocks[3];
 };
@@ -214,9 +216,8 @@ k_gated_dgate(long long A, int E, int k, int d, int n_blocks, const int32_t *__r
 __global__ void __launch_bounds__(256)
 k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__restrict__ offset,
                const int32_t *__restrict__ poff, const int32_t *__restrict__ row_token,
-               const float *__restrict__ row_gate, const uint4 *__restrict__ x,
-               const uint4 *__restrict__ dy, uint4 *__restrict__ xbuf, uint4 *__restrict__ h,
-               uint4 *__restrict__ dY, uint4 *__restrict__ dU) {
+               const uint4 *__restrict__ x, const uint4 *__restrict__ dy, uint4 *__restrict__ xbuf, uint4 *__restrict__ h,
+               uint4 *__restrict__ dY) {
   pdl_wait();
   pdl_trigger();
   const long long w = (blockIdx.x * 256ll + threadIdx.x) >> 5;
@@ -236,13 +237,12 @@ k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__r
     else hi = mid;
   }
   const int m = (int)(w - poff[lo]), q = offset[lo] + m;
-  uint4 *oy = dY + w * nv, *ou = dU + w * nv;
+  uint4 *oy = dY + w * nv;
   if (q >= offset[lo + 1]) {
-    for (int i = lane; i < nv; i += 32) oy[i] = ou[i] = z;
+    for (int i = lane; i < nv; i += 32) oy[i] = z;
     return;
   }
   const size_t t = (size_t)(row_token[q] / k) * nv;
-  const float2 g = both(row_gate[q]);
   uint4 *ox = xbuf + (size_t)q * nv;
   constexpr int N = 4;
   for (int i0 = lane; i0 < nv; i0 += 32 * N) {
@@ -259,8 +259,6 @@ k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__r
       if (i >= nv) break;
       ox[i] = a[j];
       oy[i] = b[j];
-      ou[i] = make_uint4(pack_bf16x2(mul2(unpack2(b[j].x), g)), pack_bf16x2(mul2(unpack2(b[j].y), g)),
-                         pack_bf16x2(mul2(unpack2(b[j].z), g)), pack_bf16x2(mul2(unpack2(b[j].w), g)));
     }
   }
 }
@@ -284,6 +282,7 @@ k_gated_colsum(const int32_t *__restrict__ offset, const int32_t *__restrict__ b
   const int rows = offset[e + 1] - offset[e];
   const int c0 = cb * 64 + (lane % LANES) * V;
   const S *src = p.src[job] + (size_t)base[e] * cols;
+  const float *weight = p.weight[job] ? p.weight[job] + offset[e] : nullptr;
   float acc[Q][V] = {};
   for (int r0 = warp * PER + lane / LANES; r0 < rows; r0 += 64 * PER) {
 #pragma unroll
@@ -299,9 +298,12 @@ k_gated_colsum(const int32_t *__restrict__ offset, const int32_t *__restrict__ b
                           : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 8; ++i) {
+          const float w = weight ? weight[min(r0 + i * 8 * PER, rows - 1)] : 1.f;
 #pragma unroll
-          for (int v = 0; v < V; ++v) acc[q][v] += ld(reinterpret_cast<const S *>(&u[i]), v);
+          for (int v = 0; v < V; ++v)
+            acc[q][v] = fmaf(w, ld(reinterpret_cast<const S *>(&u[i]), v), acc[q][v]);
+        }
       } else {
         float u[8];
 #pragma unroll
@@ -310,7 +312,9 @@ k_gated_colsum(const int32_t *__restrict__ offset, const int32_t *__restrict__ b
           u[i] = r < rows ? ld(src, (size_t)r * cols + c) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[q][0] += u[i];
+        for (int i = 0; i < 8; ++i)
+          acc[q][0] =
+              fmaf(weight ? weight[min(r0 + i * 8 * PER, rows - 1)] : 1.f, u[i], acc[q][0]);
       }
     }
   }
@@ -384,12 +388,11 @@ cudaError_t launch_gated_route(const GatedRouteArgs &a, cudaStream_t s) {
 
 cudaError_t launch_gated_gather(const moe_config &c, long long P_max, const GatedRows &rows,
                                 const int32_t *poff, const void *x, const void *dy, void *xbuf,
-                                void *h, void *dY, void *dU, cudaStream_t s) {
+                                void *h, void *dY, cudaStream_t s) {
   const long long warps = P_max + kBwdRowPad;
   return launch_pdl(k_gated_gather, (unsigned)((warps + 7) / 8), 256, 0, s, P_max, c.E, c.k,
-                    c.d / 8, c.d_ff / 8, rows.offset, poff, rows.row_token, rows.row_gate,
-                    (const uint4 *)x, (const uint4 *)dy, (uint4 *)xbuf, (uint4 *)h, (uint4 *)dY,
-                    (uint4 *)dU);
+                    c.d / 8, c.d_ff / 8, rows.offset, poff, rows.row_token, (const uint4 *)x,
+                    (const uint4 *)dy, (uint4 *)xbuf, (uint4 *)h, (uint4 *)dY);
 }
 
 cudaError_t launch_gated_begin(DeviceStatus *st, cudaStream_t s) {
@@ -412,14 +415,15 @@ cudaError_t launch_gated_dgate(const moe_config &c, int n_blocks, const int32_t 
 
 template <typename S, typename O>
 static cudaError_t run_colsum(int E, const int32_t *offset, const int32_t *base,
-                              const void *const (&src)[3], void *const (&out)[3],
-                              const int (&cols)[3], cudaStream_t s) {
+                              const void *const (&src)[3], const float *weight,
+                              void *const (&out)[3], const int (&cols)[3], cudaStream_t s) {
   GatedColumns<S, O> p{};
   int n = 0, blocks = 0;
   bool vec = true;
   for (int j = 0; j < 3; ++j) {
     if (!out[j]) continue;
     p.src[n] = static_cast<const S *>(src[j]);
+    p.weight[n] = j == 0 ? weight : nullptr;
     p.out[n] = static_cast<O *>(out[j]);
     p.cols[n] = cols[j];
     p.blocks[n] = (cols[j] + 63) / 64;
@@ -433,14 +437,15 @@ static cudaError_t run_colsum(int E, const int32_t *offset, const int32_t *base,
 }
 
 cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t *offset,
-                                const int32_t *base, const void *dU, void *db2, const void *dP1,
-                                void *db1, const void *dP3, void *db3, cudaStream_t s) {
-  const void *const src[3] = {dU, dP1, dP3};
+                                const int32_t *base, const void *dY, const float *row_gate,
+                                void *db2, const void *dP1, void *db1, const void *dP3, void *db3,
+                                cudaStream_t s) {
+  const void *const src[3] = {dY, dP1, dP3};
   void *const out[3] = {db2, db1, db3};
   const int cols[3] = {c.d, c.d_ff, c.d_ff};
-  if (c.act_dtype == MOE_F32) return run_colsum<float, float>(c.E, offset, base, src, out, cols, s);
-  if (src_f32) return run_colsum<float, __nv_bfloat16>(c.E, offset, base, src, out, cols, s);
-  return run_colsum<__nv_bfloat16, __nv_bfloat16>(c.E, offset, base, src, out, cols, s);
+  if (c.act_dtype == MOE_F32) return run_colsum<float, float>(c.E, offset, base, src, row_gate, out, cols, s);
+  if (src_f32) return run_colsum<float, __nv_bfloat16>(c.E, offset, base, src, row_gate, out, cols, s);
+  return run_colsum<__nv_bfloat16, __nv_bfloat16>(c.E, offset, base, src, row_gate, out, cols, s);
 }
 
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,

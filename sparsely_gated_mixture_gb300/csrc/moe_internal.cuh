@@ -340,7 +340,7 @@ struct BwdGemm {
   bool out_bf16;  // mode 2: the weight gradient in bf16
   const uint8_t *h8 = nullptr, *hscale = nullptr;  // mode 0: hbuf's values in 8 bits instead
   // Gated experts. Mode 3, mode 0's product: from pre1, pre3 [packed rows, N] to
-  // dP1 (out) and dP3 (out3) [padded rows, N] and h [packed rows, N];
+  // dP1 (out) and dP3 (out3) [padded rows, N] and gate * h (h) [packed rows, N];
   // dgpart has two columns for each 256 of N. Mode 4, mode 1's product for two
   // pairs at once: A B^T + A3 B3^T.
   int activation = 0;
