@@ -626,7 +626,8 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
  * act_dtype (fp32 sums rounded once; an expert without rows gets zeros), dgate
  * [T,k] fp32; db1, db3 and db2 may each be NULL. In bf16 layers dP1, dP3 and g h
  * are bf16 operands of the products (dW2 = (g h)^T dy), and tensor-core sums cut
- * instead of rounding, which leaves dgate off as moe_backward's. No output may overlap an input. ws:
+ * instead of rounding, which leaves dgate off as moe_backward's. No output may
+ * overlap an input. ws:
  * moe_gated_backward_workspace_size bytes, scratch, its status word cleared
  * first; after MOE_ERR_NONFINITE no expert's gradients are to be used.
  */

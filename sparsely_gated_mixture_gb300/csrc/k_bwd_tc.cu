@@ -1115,7 +1115,8 @@ cudaError_t launch_mode_pair(const CUtensorMap &a, const CUtensorMap &b, const C
 }
 
 template <int MODE, bool OB = false, int ACT = 0>
-cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p, cudaStream_t s, const BExtra<MODE> &ex = {}) {
+cudaError_t launch_mode(const CUtensorMap &a, const CUtensorMap &b, const BParams &p,
+                        cudaStream_t s, const BExtra<MODE> &ex = {}) {
   const size_t smem = bwd_smem_bytes<MODE>(p.E);
   cudaError_t err = allow_smem(k_bwd_tc<MODE, OB, ACT>);
   if (err != cudaSuccess) return err;
@@ -1222,7 +1223,8 @@ cudaError_t launch_bwd_gemm(const BwdGemm &g, DeviceStatus *st, cudaStream_t s) 
                                : pick_pair<4>(g, 2ll * g.K, tiles);
   const uint64_t rows = (uint64_t)g.a_rows, wrows = (uint64_t)g.E * g.N;
   const uint32_t box_b = cl > 0 ? BN / 2 : BN;
-  if (!make_map(&ta, g.A, rows, (uint64_t)g.K, BM) || !make_map(&tb, g.B, wrows, (uint64_t)g.K, box_b))
+  if (!make_map(&ta, g.A, rows, (uint64_t)g.K, BM) ||
+      !make_map(&tb, g.B, wrows, (uint64_t)g.K, box_b))
     return cudaErrorInvalidValue;
   CUtensorMap to = ta;  // unused unless p.tma_out
   if (g.mode == 3) {

@@ -176,8 +176,8 @@ cudaError_t launch_fp8_rows(int max_rows, int K, int k, const int32_t *count,
                             uint8_t *scale, cudaStream_t s) {
   const int KB = (int)fp8_blocks(K);
   const auto run = [&](auto kernel) {
-    return launch_pdl(kernel, (unsigned)((max_rows + 7ll) / 8), 256, 0, s, max_rows, K, KB, k, count,
-                      row_token, (const __nv_bfloat16 *)src, q, scale);
+    return launch_pdl(kernel, (unsigned)((max_rows + 7ll) / 8), 256, 0, s, max_rows, K, KB, k,
+                      count, row_token, (const __nv_bfloat16 *)src, q, scale);
   };
   return K % 4 == 0 ? run(k_fp8_rows<true>) : run(k_fp8_rows<false>);
 }

@@ -199,7 +199,8 @@ k_gated_dgate(long long A, int E, int k, int d, int n_blocks, const int32_t *__r
           const uint4 w = *reinterpret_cast<const uint4 *>(b + i);
 #pragma unroll
           for (int j = 0; j < V; ++j)
-            s = fmaf(ld(reinterpret_cast<const T *>(&u), j), ld(reinterpret_cast<const T *>(&w), j), s);
+            s = fmaf(ld(reinterpret_cast<const T *>(&u), j), ld(reinterpret_cast<const T *>(&w), j),
+                     s);
         }
       } else {
         for (int i = lane; i < d; i += 32) s = fmaf(ld(y, i), ld(b, i), s);
@@ -216,8 +217,8 @@ k_gated_dgate(long long A, int E, int k, int d, int n_blocks, const int32_t *__r
 __global__ void __launch_bounds__(256)
 k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__restrict__ offset,
                const int32_t *__restrict__ poff, const int32_t *__restrict__ row_token,
-               const uint4 *__restrict__ x, const uint4 *__restrict__ dy, uint4 *__restrict__ xbuf, uint4 *__restrict__ h,
-               uint4 *__restrict__ dY) {
+               const uint4 *__restrict__ x, const uint4 *__restrict__ dy,
+               uint4 *__restrict__ xbuf, uint4 *__restrict__ h, uint4 *__restrict__ dY) {
   pdl_wait();
   pdl_trigger();
   const long long w = (blockIdx.x * 256ll + threadIdx.x) >> 5;
@@ -443,9 +444,12 @@ cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t
   const void *const src[3] = {dY, dP1, dP3};
   void *const out[3] = {db2, db1, db3};
   const int cols[3] = {c.d, c.d_ff, c.d_ff};
-  if (c.act_dtype == MOE_F32) return run_colsum<float, float>(c.E, offset, base, src, row_gate, out, cols, s);
-  if (src_f32) return run_colsum<float, __nv_bfloat16>(c.E, offset, base, src, row_gate, out, cols, s);
-  return run_colsum<__nv_bfloat16, __nv_bfloat16>(c.E, offset, base, src, row_gate, out, cols, s);
+  const auto run = [&](auto kernel) {
+    return kernel(c.E, offset, base, src, row_gate, out, cols, s);
+  };
+  if (c.act_dtype == MOE_F32) return run(run_colsum<float, float>);
+  return src_f32 ? run(run_colsum<float, __nv_bfloat16>)
+                 : run(run_colsum<__nv_bfloat16, __nv_bfloat16>);
 }
 
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,

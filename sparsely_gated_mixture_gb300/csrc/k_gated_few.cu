@@ -394,7 +394,8 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // Lane l < 8: half l / 4's byte of chunk l % 4 of a group of four.
         const int half = (lane >> 2) & 1;
         const int nb = LAYER == 1 ? g.nt : min(2 * g.nt + half, p.NB - 1);
-        const uint8_t *sb = (LAYER == 1 && half ? p.sb3 : p.sb) + ((size_t)who.x * p.NB + nb) * p.KC;
+        const uint8_t *sb =
+            (LAYER == 1 && half ? p.sb3 : p.sb) + ((size_t)who.x * p.NB + nb) * p.KC;
         for (int k0 = g.kb0 & ~3; k0 < g.kb1; k0 += 4, ++g4) {
           uint32_t a[4];
 #pragma unroll
@@ -546,7 +547,8 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
               for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                  w[q][i] = i0 + i < rows && q < halves ? __ldcg(in + (i0 + i) * 256 + q * 128) : 0.f;
+                  w[q][i] =
+                      i0 + i < rows && q < halves ? __ldcg(in + (i0 + i) * 256 + q * 128) : 0.f;
 #pragma unroll
               for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -618,8 +620,10 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const size_t r = (size_t)row0 + i0 + i;
                 const float u = (v[q][i] + c) * p.row_gate[r];
                 if (!isfinite(u)) record_error(p.st, MOE_ERR_NONFINITE, (long long)r);
-                if (p.z_bf16) static_cast<__nv_bfloat16 *>(p.z)[r * p.N + n] = __float2bfloat16_rn(u);
-                else static_cast<float *>(p.z)[r * p.N + n] = u;
+                if (p.z_bf16)
+                  static_cast<__nv_bfloat16 *>(p.z)[r * p.N + n] = __float2bfloat16_rn(u);
+                else
+                  static_cast<float *>(p.z)[r * p.N + n] = u;
               }
             }
           }

@@ -40,7 +40,7 @@ def test_bad_config(lib, name, field, value, status):
 
 def test_sizes(lib):
     for name in SIZES:
-        small, large = (size(lib, name, B.config(T, 64, 8, 128, 2, 1.0)) for T in (16, 4096))
+        small, large = (size(lib, name, B.config(T, 64, 8, 128, 2, 1.0)) for T in (600, 4096))
         assert small[0] == large[0] == 0 and 0 < small[1] < large[1]
         assert getattr(lib, name)(ctypes.byref(B.config(16, 64, 8, 128, 2, 1.0)), None) == 1
     # Too many warps of 128 columns.

@@ -148,7 +148,8 @@ def test_forward_and_backward(shape, kind):
 
 
 # Row counts around the tiles of 128 (a CTA) and 256 (a pair of CTAs).
-VARIANT_SHAPES = [(300, 128, 3, 320, 1, 3.0), (1100, 192, 4, 256, 1, 4.0), (700, 256, 2, 576, 2, 2.0)]
+VARIANT_SHAPES = [(300, 128, 3, 320, 1, 3.0), (1100, 192, 4, 256, 1, 4.0),
+                  (700, 256, 2, 576, 2, 2.0)]
 
 
 @pytest.mark.parametrize("variant", ["single", "pair"])
