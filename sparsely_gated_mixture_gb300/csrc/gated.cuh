@@ -255,6 +255,24 @@ struct GatedFew {
 };
 cudaError_t launch_gated_few(const GatedFew &q, cudaStream_t s);
 
+// k_gated_few_simt.cu: both products and the combine for few rows on the CUDA
+// cores, after routing. part, part2: gated_few_simt_part bytes for the layers.
+struct GatedFewSimt {
+  moe_config c;
+  int activation, max_rows;
+  GatedRows rows;
+  const void *x;
+  const int32_t *idx, *pos;
+  const uint8_t *keep;
+  const float *gate;
+  const void *W1, *b1, *W3, *b3, *W2, *b2;
+  void *h, *pre1, *pre3, *y;
+  float *part, *part2;
+  DeviceStatus *st;
+};
+size_t gated_few_simt_part(const moe_config &c, int max_rows, int layer);
+cudaError_t launch_gated_few_simt(const GatedFewSimt &p, cudaStream_t s);
+
 // k_gated.cu: what surrounds the products of the backward.
 // The backward's rows in bf16 (d a multiple of 64): xbuf = x in packed rows, dY =
 // dy in padded blocks, pad rows zero; and zero rows behind the last packed ones of
@@ -276,6 +294,12 @@ cudaError_t launch_gated_colsum(const moe_config &c, bool src_f32, const int32_t
                                 const int32_t *base, const void *dY, const float *row_gate,
                                 void *db2, const void *dP1, void *db1, const void *dP3, void *db3,
                                 cudaStream_t s);
+// y = x + the kept choices' rows of z, for widths that launch_combine reads a value
+// at a time.
+cudaError_t launch_gated_combine(const moe_config &c, const void *x, const float *z,
+                                 const int32_t *idx, const int32_t *pos, const uint8_t *keep,
+                                 const int32_t *offset, void *y, DeviceStatus *st,
+                                 cudaStream_t s);
 // dx = dy + the kept choices' rows base[e] + pos of dX.
 cudaError_t launch_gated_dx(const moe_config &c, const int32_t *idx, const int32_t *pos,
                             const uint8_t *keep, const int32_t *base, const float *dX,

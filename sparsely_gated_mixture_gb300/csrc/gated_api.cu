@@ -93,7 +93,7 @@ static GatedFewLayout gated_few_layout(const moe_config &c, GatedTake &take) {
 struct GatedLayout {
   GatedRoute r;
   GatedFewLayout few;
-  size_t xbuf, h, z, total;
+  size_t xbuf, h, z, part, part2, total;
 };
 static GatedLayout gated_layout(const moe_config &c) {
   GatedLayout L{};
@@ -103,7 +103,12 @@ static GatedLayout gated_layout(const moe_config &c) {
   L.xbuf = take(gated_tc_shape(c) ? R * c.d * 2 : 0);
   L.h = take(R * c.d_ff * elem_bytes(c.act_dtype));
   L.z = take(R * c.d * (gated_z_bf16(c) ? 2 : 4));
-  if (gated_tc_shape(c)) L.few = gated_few_layout(c, take);
+  if (gated_tc_shape(c)) {
+    L.few = gated_few_layout(c, take);
+  } else if (gated_few_toks(c)) {
+    L.part = take(gated_few_simt_part(c, (int)R, 1));
+    L.part2 = take(gated_few_simt_part(c, (int)R, 2));
+  }
   L.total = take.off;
   return L;
 }
@@ -365,6 +370,28 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
     MOE_CUDA(launch_combine(c, x, z, zb, ps, kp, expert_idx, rows.offset, y, st, s));
     return MOE_OK;
   }
+  if (gated_few_toks(c)) {
+    GatedFewSimt p{};
+    p.c = c;
+    p.activation = activation;
+    p.max_rows = (int)R;
+    p.rows = gated_rows(L.r, ws);
+    p.x = x;
+    p.idx = expert_idx;
+    p.pos = ps;
+    p.keep = kp;
+    p.gate = gate;
+    p.W1 = W1; p.b1 = b1; p.W3 = W3; p.b3 = b3; p.W2 = W2; p.b2 = b2;
+    p.h = ws_at<char>(ws, L.h);
+    p.pre1 = pre1;
+    p.pre3 = pre3;
+    p.y = y;
+    p.part = ws_at<float>(ws, L.part);
+    p.part2 = ws_at<float>(ws, L.part2);
+    p.st = st;
+    MOE_CUDA(launch_gated_few_simt(p, s));
+    return MOE_OK;
+  }
   GatedSimt p{};
   p.c = c;
   p.activation = activation;
@@ -378,7 +405,10 @@ int moe_experts_gated(const moe_config *cfg, int32_t activation, const void *x,
   p.z = static_cast<float *>(z);
   p.st = st;
   MOE_CUDA(launch_gated_simt_forward(p, s));
-  MOE_CUDA(launch_combine(c, x, p.z, false, ps, kp, expert_idx, p.rows.offset, y, st, s));
+  if (c.d % 4 == 0)
+    MOE_CUDA(launch_combine(c, x, p.z, false, ps, kp, expert_idx, p.rows.offset, y, st, s));
+  else
+    MOE_CUDA(launch_gated_combine(c, x, p.z, expert_idx, ps, kp, p.rows.offset, y, st, s));
   return MOE_OK;
 }
 

@@ -8,7 +8,9 @@
 //   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
 // One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
 // block of 256 threads, TM x TN a thread, K in chunks whose next one is fetched
-// while this one is multiplied, packed fp32 multiply-adds (two a lane and
+// while this one is multiplied (small tiles: of 64 in the forward, whose blocks are
+// few and wait for each, 75 -> 61 us for 517 rows of 130 through 6 experts of 234;
+// of 16 in the backward, whose launches share the SMs: 108 -> 98), packed fp32 multiply-adds (two a lane and
 // instruction). Both projections of forward 1 share a block's columns, so that a
 // thread holds p1 and p3 of the same places; the three weight gradients are one
 // launch. Sums run over K in order.
@@ -48,12 +50,12 @@ __global__ void __launch_bounds__(kThreads)
 k_gated_simt(const GatedSimt p) {
   pdl_wait();
   pdl_trigger();
-  constexpr int BM = 16 * TM, BN = 16 * TN, BK = TM == 8 ? 16 : 32;
+  constexpr int BM = 16 * TM, BN = 16 * TN, BK = TM == 8 ? 16 : OP == kF1 || OP == kF2 ? 64 : 16;
   constexpr int KL = BK, KR = kThreads / BK;  // K-contiguous operands: lanes along K, rows a pass
   constexpr bool kWeight = OP == kW;
   constexpr int LA = BM * BK / kThreads, LB = BN * BK / kThreads;
-  __shared__ __align__(16) float As[BK][BM + 4];
-  __shared__ __align__(16) float Bs[BK][BN + 4];
+  __shared__ __align__(16) float As[BK][BM + (TM == 8 ? 4 : 2)];
+  __shared__ __align__(16) float Bs[BK][BN + (TN == 8 ? 4 : 2)];
   const int E = p.c.E, d = p.c.d, F = p.c.d_ff, k = p.c.k;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 

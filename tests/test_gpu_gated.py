@@ -147,6 +147,17 @@ def test_forward_and_backward(shape, kind):
     check_backward(cfg, kind, s, o["p1"], o["p3"], run_backward(cfg, kind, g, o["p1"], o["p3"]))
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_a_thousand_experts(dt):
+    """1024 experts, most of them with a row or two, some with none."""
+    s = inputs(900, 64, 1024, 64, 2, dt, skew=1.0)
+    cfg, g = config(s, 64.0), dev(s)
+    o = run_forward(cfg, R.SILU, g)
+    check_forward(cfg, R.SILU, s, o, reference(cfg, R.SILU, s))
+    check_backward(cfg, R.SILU, s, o["p1"], o["p3"],
+                   run_backward(cfg, R.SILU, g, o["p1"], o["p3"]))
+
+
 # Row counts around the tiles of 128 (a CTA) and 256 (a pair of CTAs).
 VARIANT_SHAPES = [(300, 128, 3, 320, 1, 3.0), (1100, 192, 4, 256, 1, 4.0),
                   (700, 256, 2, 576, 2, 2.0)]
@@ -574,6 +585,20 @@ def test_few_rows_borders(T, k, E, min_cap, fp8):
     else:
         o = run_forward(cfg, R.SILU, g)
         check_forward(cfg, R.SILU, s, o, reference(cfg, R.SILU, s))
+
+
+@pytest.mark.parametrize("dt,T,d,F,E,k,min_cap", [
+    (F32, 1, 3, 2000, 5, 2, 1), (F32, 1, 2000, 3, 5, 2, 1), (BF16, 3, 770, 1030, 24, 1, 1),
+    (F32, 17, 514, 1025, 7, 4, 1), (F32, 64, 36, 40, 2, 2, 1), (BF16, 40, 72, 100, 3, 2, 100),
+    (F32, 64, 20, 24, 600, 8, 1), (F32, 57, 20, 24, 64, 9, 1)])
+def test_few_rows_on_cuda_cores(dt, T, d, F, E, k, min_cap):
+    s = inputs(T, d, E, F, k, dt, seed=T + d)
+    s["idx"][0] = s["idx"][0, 0]
+    cfg, g = config(s, float(E)), dev(s)
+    cfg.min_capacity = min_cap
+    for kind in (R.SILU, R.GELU, R.RELU):
+        o = run_forward(cfg, kind, g)
+        check_forward(cfg, kind, s, o, reference(cfg, kind, s))
 
 
 @pytest.mark.parametrize("dt,T,d,F", [(BF16, 160000, 64, 14336), (F32, 80000, 9, 30001)])
