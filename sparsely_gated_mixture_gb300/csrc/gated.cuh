@@ -176,6 +176,7 @@ struct GatedSimt {
   const void *dy;     // backward
   float *xf, *hf, *dU, *dP1, *dP3, *dX, *dgpart;  // backward: fp32 rows
   void *dW1, *dW3, *dW2;                     // act_dtype
+  float *wpart;  // backward: gated_simt_wpart bytes, the weight gradients by slices of rows
   DeviceStatus *st;
 };
 cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s);
@@ -183,6 +184,7 @@ cudaError_t launch_gated_simt_forward(const GatedSimt &p, cudaStream_t s);
 cudaError_t launch_gated_simt_front(const GatedSimt &p, cudaStream_t s);
 cudaError_t launch_gated_simt_dx(const GatedSimt &p, cudaStream_t s);
 cudaError_t launch_gated_simt_weights(const GatedSimt &p, cudaStream_t s);
+size_t gated_simt_wpart(const moe_config &c, int max_rows);
 int gated_simt_dg_blocks(const moe_config &c, int max_rows);  // columns of dgpart [rows, ..]
 
 // k_ffn_tc.cu: the gated first layer on the tensor cores (ffn_tc_supported

@@ -142,7 +142,7 @@ static GatedFp8Layout gated_fp8_layout(const moe_config &c) {
 // dy in dY's place.
 struct GatedBwdLayout {
   GatedRoute r;
-  size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, total;
+  size_t poff, xbuf, h, dY, dU, dP1, dP3, dX, dgpart, wpart, total;
   long long P_max;
   int dg_blocks;
 };
@@ -164,6 +164,7 @@ static GatedBwdLayout gated_bwd_layout(const moe_config &c) {
   L.dP3 = take(P * F * eb);
   L.dX = take(P * d * 4);
   L.dgpart = take(P * L.dg_blocks * 4);
+  L.wpart = take(tc ? 0 : gated_simt_wpart(c, (int)R));
   L.total = take.off;
   return L;
 }
@@ -464,6 +465,7 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   p.dP3 = ws_at<float>(ws, L.dP3);
   p.dX = ws_at<float>(ws, L.dX);
   p.dgpart = ws_at<float>(ws, L.dgpart);
+  p.wpart = ws_at<float>(ws, L.wpart);
   p.dW1 = dW1; p.dW3 = dW3; p.dW2 = dW2;
   p.st = ws_at<DeviceStatus>(ws, L.r.status);
   MOE_CUDA(launch_gated_simt_front(p, s));

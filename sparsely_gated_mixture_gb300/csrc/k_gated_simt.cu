@@ -7,19 +7,26 @@
 //   backward 2: dX = dP1 W1^T + dP3 W3^T
 //   backward 3: dW1 = x^T dP1, dW3 = x^T dP3, dW2 = h^T (g dy)
 // One tiled product with these operands and epilogues: 16 TM x 16 TN outputs a
-// block of 256 threads, TM x TN a thread, K in chunks whose next one is fetched
-// while this one is multiplied (small tiles: of 64 in the forward, whose blocks are
-// few and wait for each, 75 -> 61 us for 517 rows of 130 through 6 experts of 234;
-// of 16 in the backward, whose launches share the SMs: 108 -> 98), packed fp32 multiply-adds (two a lane and
-// instruction). Both projections of forward 1 share a block's columns, so that a
-// thread holds p1 and p3 of the same places; the three weight gradients are one
-// launch. Sums run over K in order.
+// block of 256 threads, TM x TN a thread, packed fp32 multiply-adds (two a lane and
+// instruction), K in chunks whose next one is fetched while this one is multiplied.
+// Tiles of 128 x 128: chunks of 16, two in shared memory, two blocks an SM (bound by
+// the multiply-adds: 5019 tokens, top-4 of 5 experts of 181 x 683, layer 1 249 us
+// with that pipe active 66% of the time). Tiles of 64 x 64: chunks of 64 in the
+// forward, whose blocks are few and wait for each (75 -> 61 us for 517 rows of 130
+// through 6 experts of 234); of 16 in the backward, whose launches share the SMs
+// (108 -> 98). Both projections of forward 1 share a block's columns, so that a
+// thread holds p1 and p3 of the same places. The three weight gradients are one
+// launch; where their tiles are fewer than four an SM, slices of an expert's rows
+// go to fp32 sums that a second launch adds in order (4246 tokens, top-3 of 3
+// experts of 96 x 208: the backward 425 -> 188 us).
 #include "gated.cuh"
+
+#include <algorithm>
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kSliceRows = 256;
 
 template <typename T>
 __device__ __forceinline__ float ld(const T *p, size_t i) {
@@ -46,7 +53,7 @@ __device__ __forceinline__ unsigned long long pack2(float a, float b) {
 }
 
 template <int OP, typename T, int ACT, int TM, int TN>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, TM == 8 ? 2 : 1)
 k_gated_simt(const GatedSimt p) {
   pdl_wait();
   pdl_trigger();
@@ -54,8 +61,9 @@ k_gated_simt(const GatedSimt p) {
   constexpr int KL = BK, KR = kThreads / BK;  // K-contiguous operands: lanes along K, rows a pass
   constexpr bool kWeight = OP == kW;
   constexpr int LA = BM * BK / kThreads, LB = BN * BK / kThreads;
-  __shared__ __align__(16) float As[BK][BM + (TM == 8 ? 4 : 2)];
-  __shared__ __align__(16) float Bs[BK][BN + (TN == 8 ? 4 : 2)];
+  constexpr int NB = TM == 8 ? 2 : 1;  // chunks in shared memory
+  __shared__ __align__(16) float As[NB][BK][BM + (TM == 8 ? 4 : 2)];
+  __shared__ __align__(16) float Bs[NB][BK][BN + (TN == 8 ? 4 : 2)];
   const int E = p.c.E, d = p.c.d, F = p.c.d_ff, k = p.c.k;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
 
@@ -93,7 +101,11 @@ k_gated_simt(const GatedSimt p) {
   if (!kWeight && m0 >= rows) return;
   const int M = kWeight ? (which == 2 ? F : d) : rows;
   const int N = kWeight ? (which == 2 ? d : F) : OP == kF1 || OP == kB1 ? F : d;
-  const int K = kWeight ? rows : OP == kF1 || OP == kB1 ? d : OP == kF2 ? F : 2 * F;
+  // A weight gradient's slice of the rows (along z): [kbeg, kbeg + K).
+  const int slice = kWeight ? ((rows + (int)gridDim.z - 1) / (int)gridDim.z + BK - 1) / BK * BK : 0;
+  const int kbeg = kWeight ? min(rows, (int)blockIdx.z * slice) : 0;
+  const int K = kWeight ? min(rows - kbeg, slice)
+                        : OP == kF1 || OP == kB1 ? d : OP == kF2 ? F : 2 * F;
   const size_t we = (size_t)e * d * F;  // this expert's place in each weight
 
   // A: rows (K contiguous; K in lanes) or, for a weight gradient, columns of
@@ -114,11 +126,11 @@ k_gated_simt(const GatedSimt p) {
   // A weight gradient's rows [rows, M] and [rows, N].
   const float *wa = nullptr, *wb = nullptr;
   if constexpr (kWeight) {
-    wa = (which == 2 ? p.hf : p.xf) + (size_t)r0 * M;
-    wb = (which == 0 ? p.dP1 : which == 1 ? p.dP3 : p.dU) + (size_t)r0 * N;
+    wa = (which == 2 ? p.hf : p.xf) + (size_t)(r0 + kbeg) * M;
+    wb = (which == 0 ? p.dP1 : which == 1 ? p.dP3 : p.dU) + (size_t)(r0 + kbeg) * N;
   }
 
-  float ra[LA], rb[LB];
+  float ra[LA] = {}, rb[LB] = {};
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
@@ -159,16 +171,16 @@ k_gated_simt(const GatedSimt p) {
       rb[i] = v;
     }
   };
-  auto stage = [&] {
+  auto stage = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
-      if (kWeight) As[tid / BM + i * (kThreads / BM)][tid % BM] = ra[i];
-      else As[tid % KL][tid / KL + KR * i] = ra[i];
+      if (kWeight) As[buf][tid / BM + i * (kThreads / BM)][tid % BM] = ra[i];
+      else As[buf][tid % KL][tid / KL + KR * i] = ra[i];
     }
 #pragma unroll
     for (int i = 0; i < LB; ++i) {
-      if (OP == kB1 || OP == kB2) Bs[tid % KL][tid / KL + KR * i] = rb[i];
-      else Bs[tid / BN + i * (kThreads / BN)][tid % BN] = rb[i];
+      if (OP == kB1 || OP == kB2) Bs[buf][tid % KL][tid / KL + KR * i] = rb[i];
+      else Bs[buf][tid / BN + i * (kThreads / BN)][tid % BN] = rb[i];
     }
   };
 
@@ -177,10 +189,17 @@ k_gated_simt(const GatedSimt p) {
   // second half of its columns is W3's.
   constexpr int HM = TM / 2, HN = TN / 2;
   unsigned long long acc[TM][TN / 2] = {};
+  int buf = 0;
   if (K > 0) fetch(0);
-  for (int k0 = 0; k0 < K; k0 += BK) {
-    stage();
+  if (NB == 2) {
+    stage(0);
     __syncthreads();
+  }
+  for (int k0 = 0; k0 < K; k0 += BK) {
+    if (NB == 1) {
+      stage(0);
+      __syncthreads();
+    }
     if (k0 + BK < K) fetch(k0 + BK);
 #pragma unroll 16
     for (int kk = 0; kk < BK; ++kk) {
@@ -188,7 +207,7 @@ k_gated_simt(const GatedSimt p) {
       unsigned long long b[TN / 2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float *row = &As[kk][h * (BM / 2) + ty * HM];
+        const float *row = &As[buf][kk][h * (BM / 2) + ty * HM];
         if constexpr (HM == 4)
           *reinterpret_cast<float4 *>(&a[4 * h]) = *reinterpret_cast<const float4 *>(row);
         else
@@ -196,7 +215,7 @@ k_gated_simt(const GatedSimt p) {
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float *row = &Bs[kk][h * (BN / 2) + tx * HN];
+        const float *row = &Bs[buf][kk][h * (BN / 2) + tx * HN];
         if constexpr (HN == 4) {
           const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(row);
           b[2 * h] = u.x;
@@ -212,6 +231,7 @@ k_gated_simt(const GatedSimt p) {
         for (int j = 0; j < TN / 2; ++j) fma_pair(acc[i][j], aa, b[j]);
       }
     }
+    if (NB == 2 && k0 + BK < K) stage(buf ^= 1);
     __syncthreads();
   }
 
@@ -276,6 +296,9 @@ k_gated_simt(const GatedSimt p) {
           p.z[r * d + n] = u;
         } else if constexpr (OP == kB2) {
           p.dX[r * d + n] = u;
+        } else if (gridDim.z > 1) {
+          p.wpart[((size_t)blockIdx.z * 3 + which) * E * d * F + we + (size_t)m * N + n] = u;
+          continue;
         } else {
           void *out = which == 0 ? p.dW1 : which == 1 ? p.dW3 : p.dW2;
           put(static_cast<T *>(out), we + (size_t)m * N + n, u);
@@ -304,9 +327,45 @@ __global__ void __launch_bounds__(256) k_gated_rows(const GatedSimt p) {
   }
 }
 
+// The weight gradients from their slices' sums, in order; grid (elements of one, 3).
+template <typename T>
+__global__ void __launch_bounds__(256) k_gated_wsum(const GatedSimt p, int slices) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t n = (size_t)p.c.E * p.c.d * p.c.d_ff, i = blockIdx.x * (size_t)256 + threadIdx.x;
+  if (i >= n) return;
+  const int which = blockIdx.y;
+  const float *src = p.wpart + which * n + i;
+  float v = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < slices; ++s) v += src[(size_t)s * 3 * n];
+  void *out = which == 0 ? p.dW1 : which == 1 ? p.dW3 : p.dW2;
+  put(static_cast<T *>(out), i, v);
+  if (!isfinite(v))
+    record_error(p.st, MOE_ERR_NONFINITE,
+                 (long long)(i % ((size_t)p.c.d * p.c.d_ff) / (which == 2 ? p.c.d : p.c.d_ff)));
+}
+
 // Rows in 128-row tiles at most: every expert's last one may be short.
 long long max_tiles(const GatedSimt &p) {
   return ((long long)p.max_rows + kTcBM - 1) / kTcBM + (p.c.E < p.max_rows ? p.c.E : p.max_rows);
+}
+
+// The weight gradients' tiles, and the slices of an expert's rows that give every
+// SM four blocks where the tiles alone do not.
+// Slices of kSliceRows rows at least, at uniform loads (of 128: the same times).
+struct WeightSplit {
+  bool wide;
+  int slices;
+};
+WeightSplit weight_split(const moe_config &c, int max_rows) {
+  const auto blocks = [&](int t) {
+    return 3ll * c.E * ((c.d + t - 1) / t) * ((c.d_ff + t - 1) / t);
+  };
+  const long long most = std::min(16, std::max(1, max_rows / c.E / kSliceRows));
+  const bool wide = max_rows >= 64 * c.E && blocks(128) * most >= 2 * sm_count();
+  const long long b = blocks(wide ? 128 : 64);
+  return {wide, (int)std::min(most, (4ll * sm_count() + b - 1) / b)};
 }
 
 template <int OP, typename T, int ACT, int TM, int TN>
@@ -316,7 +375,8 @@ cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
   const int BNu = OP == kF1 ? BN / 2 : BN;
   dim3 grid;
   if (OP == kW)
-    grid = dim3(3 * ((p.c.d + BM - 1) / BM) * ((p.c.d_ff + BM - 1) / BM), p.c.E);
+    grid = dim3(3 * ((p.c.d + BM - 1) / BM) * ((p.c.d_ff + BM - 1) / BM), p.c.E,
+                weight_split(p.c, p.max_rows).slices);
   else  // row blocks fastest: they share the weight's columns
     grid = dim3((unsigned)(max_tiles(p) * (kTcBM / BM)), (N + BNu - 1) / BNu);
   return launch_pdl_c(kPdlGemm, k_gated_simt<OP, T, ACT, TM, TN>, grid, kThreads, 0, s, p);
@@ -326,9 +386,7 @@ cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
 // 64 x 64 (517 rows of 130 through 6 experts of 234: 23 us a layer 1 with tiles
 // of 32 x 64, whose threads hold 2 x 4 and spend their instructions on loads).
 bool wide_tiles(const moe_config &c, int max_rows, int op) {
-  if (op == kW)
-    return 3ll * c.E * ((c.d + 127) / 128) * ((c.d_ff + 127) / 128) >= 2 * sm_count() &&
-           max_rows >= 64 * c.E;
+  if (op == kW) return weight_split(c, max_rows).wide;
   const int N = (op == kF1 ? 2 : 1) * (op == kF2 || op == kB2 ? c.d : c.d_ff);
   return ((long long)max_rows + 127) / 128 * ((N + 127) / 128) >= 2 * sm_count() &&
          max_rows >= 64 * c.E;
@@ -336,8 +394,13 @@ bool wide_tiles(const moe_config &c, int max_rows, int op) {
 
 template <int OP, typename T, int ACT>
 cudaError_t run_op(const GatedSimt &p, cudaStream_t s) {
-  return wide_tiles(p.c, p.max_rows, OP) ? run_one<OP, T, ACT, 8, 8>(p, s)
-                                         : run_one<OP, T, ACT, 4, 4>(p, s);
+  if (!wide_tiles(p.c, p.max_rows, OP)) return run_one<OP, T, ACT, 4, 4>(p, s);
+  // Columns that leave half a tile empty (5019 tokens through 5 experts of 181 x
+  // 683: 505 -> 470 us; from 256 columns on the half tiles cost what they save).
+  if constexpr (OP == kF2 || OP == kB2) {
+    if (p.c.d < 256 && (p.c.d + 63) / 64 % 2) return run_one<OP, T, ACT, 8, 4>(p, s);
+  }
+  return run_one<OP, T, ACT, 8, 8>(p, s);
 }
 
 template <typename T>
@@ -379,9 +442,22 @@ cudaError_t launch_gated_simt_dx(const GatedSimt &p, cudaStream_t s) {
                                    : run_op<kB2, float, MOE_ACT_RELU>(p, s);
 }
 
+size_t gated_simt_wpart(const moe_config &c, int max_rows) {
+  const int slices = weight_split(c, max_rows).slices;
+  return slices > 1 ? 12ull * slices * c.E * c.d * c.d_ff : 0;
+}
+
+template <typename T>
+static cudaError_t weights(const GatedSimt &p, cudaStream_t s) {
+  const cudaError_t err = run_op<kW, T, MOE_ACT_RELU>(p, s);
+  const int slices = weight_split(p.c, p.max_rows).slices;
+  if (err != cudaSuccess || slices == 1) return err;
+  const size_t n = (size_t)p.c.E * p.c.d * p.c.d_ff;
+  return launch_pdl(k_gated_wsum<T>, dim3((unsigned)((n + 255) / 256), 3), 256, 0, s, p, slices);
+}
+
 cudaError_t launch_gated_simt_weights(const GatedSimt &p, cudaStream_t s) {
-  return p.c.act_dtype == MOE_BF16 ? run_op<kW, __nv_bfloat16, MOE_ACT_RELU>(p, s)
-                                   : run_op<kW, float, MOE_ACT_RELU>(p, s);
+  return p.c.act_dtype == MOE_BF16 ? weights<__nv_bfloat16>(p, s) : weights<float>(p, s);
 }
 
 }  // namespace moe

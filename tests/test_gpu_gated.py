@@ -158,6 +158,21 @@ def test_a_thousand_experts(dt):
                    run_backward(cfg, R.SILU, g, o["p1"], o["p3"]))
 
 
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("d,F,skew", [(72, 100, 0.0), (33, 1, 2.0), (181, 300, 1.0)])
+def test_weight_gradients_by_slices_of_rows(dt, d, F, skew):
+    """Many rows through few small experts on the CUDA cores: the rows' sums in slices,
+    some of them empty where the experts' loads differ."""
+    s = inputs(2300, d, 4, F, 2, dt, skew=skew)
+    cfg, g = config(s, 4.0), dev(s)
+    o = run_forward(cfg, R.GELU, g)
+    check_forward(cfg, R.GELU, s, o, reference(cfg, R.GELU, s))
+    a = run_backward(cfg, R.GELU, g, o["p1"], o["p3"])
+    check_backward(cfg, R.GELU, s, o["p1"], o["p3"], a)
+    b = run_backward(cfg, R.GELU, g, o["p1"], o["p3"])
+    assert all(torch.equal(a[n], b[n]) for n in ("dW1", "dW3", "dW2"))
+
+
 # Row counts around the tiles of 128 (a CTA) and 256 (a pair of CTAs).
 VARIANT_SHAPES = [(300, 128, 3, 320, 1, 3.0), (1100, 192, 4, 256, 1, 4.0),
                   (700, 256, 2, 576, 2, 2.0)]
