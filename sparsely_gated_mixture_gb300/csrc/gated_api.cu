@@ -229,6 +229,8 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   float *dX = ws_at<float>(ws, L.dX), *dgpart = ws_at<float>(ws, L.dgpart);
   const long long R = gated_max_rows(c), cap = host_capacity(c);
   MOE_CUDA(launch_gated_gather(c, L.P_max, rows, poff, q.x, q.dy, xbuf, h, dY, s));
+  // dgate's partials are of D as the tensor cores sum it: in fp32, cut at each add of
+  // 16 products, some 5e-6 too small at d = 4096 (moe_backward's dL/dgate alike).
   BwdGemm g{3, c.d, c.d_ff, 0, c.E, L.P_max, 0, 0, dY, q.W2, rows.offset, poff, rows.row_gate,
             nullptr, dP1, dgpart, false};
   g.activation = q.activation;

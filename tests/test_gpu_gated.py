@@ -169,8 +169,22 @@ def test_weight_gradients_by_slices_of_rows(dt, d, F, skew):
     check_forward(cfg, R.GELU, s, o, reference(cfg, R.GELU, s))
     a = run_backward(cfg, R.GELU, g, o["p1"], o["p3"])
     check_backward(cfg, R.GELU, s, o["p1"], o["p3"], a)
-    b = run_backward(cfg, R.GELU, g, o["p1"], o["p3"])
-    assert all(torch.equal(a[n], b[n]) for n in ("dW1", "dW3", "dW2"))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    ws = a["ws"].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        b = run_backward(cfg, R.GELU, g, o["p1"], o["p3"], ws=ws)
+    for _ in range(2):
+        ws.fill_(255)
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], b[n]) for n in ("dx", "dgate", "dW1", "dW3", "dW2"))
+    g["x"][0, 0] = float("nan")  # read by dW1 and dW3 alone: pre1 and pre3 are given
+    c = run_backward(cfg, R.GELU, g, o["p1"], o["p3"])
+    torch.cuda.synchronize()
+    assert B.moe_last_device_status(c["ws"])[0] == 4
 
 
 # Row counts around the tiles of 128 (a CTA) and 256 (a pair of CTAs).
