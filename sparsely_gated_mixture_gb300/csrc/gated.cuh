@@ -107,8 +107,12 @@ __device__ __forceinline__ float2 gated_act2(float2 v, float2 *slope) {
                                      v.y < 0.f ? tail.y : 1.f - tail.y);
       *slope = fma2(g, make_float2(exp2_fast(zz.x), exp2_fast(zz.y)), phi);
     }
-    // v Phi(v) = max(v, 0) - |v| Phi(-|v|)
-    return fma2(make_float2(-m.x, -m.y), tail, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+    // v Phi(v) = max(v, 0) - |v| Phi(-|v|). At +Inf the second term is finite * 0, so
+    // that the value is Inf, as the CUDA cores' form has it (Inf * 0 would be a NaN);
+    // at -Inf both are a NaN, and a NaN is one by its tail.
+    constexpr float kMost = 3.402823466e38f;
+    const float2 w = make_float2(-fabsf(fminf(v.x, kMost)), -fabsf(fminf(v.y, kMost)));
+    return fma2(w, tail, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
   } else {
     if constexpr (SLOPE) *slope = make_float2(v.x > 0.f ? 1.f : 0.f, v.y > 0.f ? 1.f : 0.f);
     return make_float2(max_nan(v.x, 0.f), max_nan(v.y, 0.f));
