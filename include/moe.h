@@ -28,7 +28,8 @@
  *   stream capture, see one ordered forward); moe_backward forks its gate
  *   branch onto the side stream and joins it back before its last kernel, as
  *   moe_backward_checkpoint does that and part of what it rebuilds, and
- *   moe_experts_gated_backward dgate and the bias gradients.
+ *   moe_experts_gated_backward dgate and the bias gradients (layers on the CUDA
+ *   cores: the weights' and biases' gradients).
  *   Each device has a pool of 8 side streams, made on the first such call
  *   that is not under stream capture (make one call before capturing if the
  *   captured graph should keep the overlap) and kept; each serves one caller
@@ -45,9 +46,9 @@
  *   gates and zbuf are always fp32.
  * Errors.  A bad argument returns MOE_ERR_ARG (or MOE_ERR_UNSUPPORTED) before
  *   anything is enqueued. A failed launch returns MOE_ERR_CUDA; work enqueued
- *   before the failure (on `stream` and, in moe_forward and the backwards, on
- *   the library's side stream) may still run, so synchronise the device before
- *   reusing the call's buffers. Conditions found
+ *   before the failure may still run on `stream`, and what went to a side stream
+ *   is joined back into `stream` before the call returns, so buffers may be freed
+ *   or reused in stream order. Conditions found
  *   on the device -- a non-finite router logit, expert output or layer output
  *   (the Switch page raises on each), an index out of range, or a bounded wait
  *   that ran out -- are recorded in a status word inside `ws`;

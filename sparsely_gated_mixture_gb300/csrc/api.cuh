@@ -58,4 +58,54 @@ struct SideStream {
 };
 SideStream *side_stream(std::unique_lock<std::mutex> &lock, cudaStream_t caller);
 
+// Work of one call on a side stream beside the caller's stream s. However the call
+// ends, with an error half-way too, what s gets later follows what the side
+// stream got: else freeing or reusing the call's buffers in stream order would race
+// with it, and a captured side stream would stay unjoined. Declared after the lock,
+// so that the join is enqueued under it.
+class SideFork {
+ public:
+  SideFork() = default;
+  SideFork(const SideFork &) = delete;
+  SideFork &operator=(const SideFork &) = delete;
+  ~SideFork() {
+    if (open_) join();
+  }
+  // side null: everything runs on s.
+  void use(SideStream *side, cudaStream_t s) {
+    side_ = side;
+    s_ = s;
+  }
+  cudaStream_t stream() const { return side_ ? side_->s : s_; }
+  // What stream() gets from here on follows what s got so far.
+  int fork() {
+    if (!side_) return MOE_OK;
+    MOE_CUDA(cudaEventRecord(side_->fork, s_));
+    MOE_CUDA(cudaStreamWaitEvent(side_->s, side_->fork, 0));
+    open_ = true;
+    return MOE_OK;
+  }
+  // The end of what stream() got so far, for await().
+  int mark() {
+    if (side_) MOE_CUDA(cudaEventRecord(side_->join, side_->s));
+    return MOE_OK;
+  }
+  // What s gets from here on follows the last mark().
+  int await() {
+    if (side_) MOE_CUDA(cudaStreamWaitEvent(s_, side_->join, 0));
+    return MOE_OK;
+  }
+  int join() {
+    const int r = mark();
+    if (r != MOE_OK) return r;
+    open_ = false;
+    return await();
+  }
+
+ private:
+  SideStream *side_ = nullptr;
+  cudaStream_t s_ = nullptr;
+  bool open_ = false;
+};
+
 }  // namespace moe

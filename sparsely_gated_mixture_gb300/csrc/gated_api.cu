@@ -197,15 +197,6 @@ static GatedRows gated_rows(const GatedRoute &L, void *ws) {
           ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate)};
 }
 
-// Work enqueued on fs from here follows that on s (fs: the side stream, or s).
-static int gated_fork(SideStream *side, cudaStream_t s, cudaStream_t &fs) {
-  if (!side) return MOE_OK;
-  MOE_CUDA(cudaEventRecord(side->fork, s));
-  MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
-  fs = side->s;
-  return MOE_OK;
-}
-
 // The backward's products on the tensor cores, dx included.
 struct GatedBwdCall {
   int activation;
@@ -242,10 +233,11 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   // Beside the products that follow, on the library's side stream: dL/dgate and
   // the bias gradients, whose small blocks fit next to the GEMMs' one an SM.
   std::unique_lock<std::mutex> side_lock;
-  SideStream *side = side_stream(side_lock, s);
-  cudaStream_t fs = s;
-  const int r = gated_fork(side, s, fs);
+  SideFork side;
+  side.use(side_stream(side_lock, s), s);
+  const int r = side.fork();
   if (r != MOE_OK) return r;
+  const cudaStream_t fs = side.stream();
   MOE_CUDA(launch_gated_dgate(c, L.dg_blocks, q.idx, pos, keep, poff, dgpart, q.dy, q.b2, q.dgate,
                               fs));
   MOE_CUDA(launch_gated_colsum(c, false, rows.offset, poff, dY, rows.row_gate, q.db2, dP1, q.db1,
@@ -267,10 +259,7 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   MOE_CUDA(wgrad(h, c.d_ff, dY, c.d, q.dW2));
   MOE_CUDA(wgrad(xbuf, c.d, dP1, c.d_ff, q.dW1));
   MOE_CUDA(wgrad(xbuf, c.d, dP3, c.d_ff, q.dW3));
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->join, side->s));
-    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
-  }
+  if (side.join() != MOE_OK) return MOE_ERR_CUDA;
   MOE_CUDA(launch_bwd_dx(c, q.idx, pos, keep, poff, dX, nullptr, q.dy, q.dx, s));
   return MOE_OK;
 }
@@ -473,10 +462,11 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
   MOE_CUDA(launch_gated_simt_front(p, s));
   // The weight gradients beside all that dx needs, and the small sums.
   std::unique_lock<std::mutex> side_lock;
-  SideStream *side = side_stream(side_lock, s);
-  cudaStream_t fs = s;
-  r = gated_fork(side, s, fs);
+  SideFork side;
+  side.use(side_stream(side_lock, s), s);
+  r = side.fork();
   if (r != MOE_OK) return r;
+  const cudaStream_t fs = side.stream();
   const int32_t *off = p.rows.offset;
   MOE_CUDA(launch_gated_simt_weights(p, fs));
   MOE_CUDA(launch_gated_simt_dx(p, s));
@@ -484,11 +474,7 @@ int moe_experts_gated_backward(const moe_config *cfg, int32_t activation, const 
                               s));
   MOE_CUDA(launch_gated_colsum(c, true, off, off, p.dU, nullptr, db2, p.dP1, db1, p.dP3, db3, fs));
   MOE_CUDA(launch_gated_dx(c, expert_idx, pos, keep, off, p.dX, dy, dx, s));
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->join, side->s));
-    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
-  }
-  return MOE_OK;
+  return side.join();
 }
 
 int moe_weights_fp8_size(int32_t E, int32_t K, int32_t N, size_t *w8_bytes,

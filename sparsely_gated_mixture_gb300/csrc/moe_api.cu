@@ -598,27 +598,19 @@ int moe_forward(const moe_config *cfg, const void *x, const float *Wg, const flo
   // The balancing finalize needs only the gate's partial sums: it runs on the
   // side stream beside dispatch, the expert GEMMs and combine (on `stream`
   // itself if no side stream could be made).
-  SideStream *side = nullptr;
   std::unique_lock<std::mutex> side_lock;
+  SideFork side;
   if (aux_out3) {
-    side = side_stream(side_lock, s);
-    cudaStream_t fs = s;
-    if (side) {
-      MOE_CUDA(cudaEventRecord(side->fork, s));
-      MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
-      fs = side->s;
-    }
+    side.use(side_stream(side_lock, s), s);
+    r = side.fork();
+    if (r != MOE_OK) return r;
     MOE_CUDA(launch_aux_finalize(c, ws_at<float>(ws, L.partials), L.n_aux_blocks, aux_out3,
-                                 nullptr, nullptr, ws_at<float2>(ws, L.aux_vec), st, fs));
+                                 nullptr, nullptr, ws_at<float2>(ws, L.aux_vec), st,
+                                 side.stream()));
   }
   r = expert_path(c, L, ws, x, idx, g, ps, kp, W1, b1, W2, b2, y, st, s);
   if (r != MOE_OK) return r;
-  if (side) {
-    // Join: work enqueued on `stream` after this call also waits for the losses.
-    MOE_CUDA(cudaEventRecord(side->join, side->s));
-    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
-  }
-  return MOE_OK;
+  return side.join();  // work enqueued on `stream` after this call also waits for the losses
 }
 
 int moe_expert_counts(const moe_config *cfg, const int32_t *expert_idx, int32_t *expert_count,
@@ -1038,24 +1030,17 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
   const BwdSimt sp{B.P_max, offset, poff, row_token, row_gate, q.dy, q.W1, q.W2, q.b2, xbuf,
                    hbuf, static_cast<float *>(dY), static_cast<float *>(dU), static_cast<float *>(dP),
                    dX, dgpart, q.dW1, q.dW2, st, q.dw_bf16};
-  SideStream *side = nullptr;
   std::unique_lock<std::mutex> side_lock;
-  cudaStream_t fs = s;
-  const auto fork = [&]() -> int {  // work enqueued on fs from here follows that on s
-    if (!side) return MOE_OK;
-    MOE_CUDA(cudaEventRecord(side->fork, s));
-    MOE_CUDA(cudaStreamWaitEvent(side->s, side->fork, 0));
-    return MOE_OK;
-  };
+  SideFork side;
   if (ck) {
     // From a checkpoint: the choices' slots first. Beside them and the first
     // GEMM, on the side stream, what only later steps read: the router, the
     // packed x rows and the hidden rows in the layer's type (the tensor-core
     // dgrad reads them in 8 bits).
-    side = side_stream(side_lock, s);
-    if (side) fs = side->s;
+    side.use(side_stream(side_lock, s), s);
+    const cudaStream_t fs = side.stream();
     MOE_CUDA(launch_checkpoint_begin(st, s));
-    int r = fork();
+    int r = side.fork();
     if (r == MOE_OK) r = ckpt_router(c, L, B, q, *ck, fs);
     if (r != MOE_OK) return r;
     MOE_CUDA(launch_slots(c, host_capacity(c), ck->expert_idx, q.gate, ws_at<int32_t>(ws, L.hist),
@@ -1064,13 +1049,14 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
                           ws_at<int32_t>(ws, L.pos), ws_at<uint8_t>(ws, L.keep),
                           ws_at<int32_t>(ws, L.row_token), ws_at<float>(ws, L.row_gate),
                           L.n_chunks, st, s));
-    r = fork();
+    r = side.fork();
     if (r != MOE_OK) return r;
     MOE_CUDA(launch_gather(c, q.x, offset, row_token, xbuf, st, fs));
     MOE_CUDA(launch_checkpoint_load(c.act_dtype == MOE_BF16, checkpoint_rows(c), c.d_ff,
                                     offset + c.E, ck->h8, ck->hscale, hbuf, tc ? fs : s));
     if (tc) MOE_CUDA(launch_bwd_tail_zero(c, offset, xbuf, hbuf, fs));
-    if (side) MOE_CUDA(cudaEventRecord(side->join, side->s));
+    r = side.mark();
+    if (r != MOE_OK) return r;
   }
   // 1. Padded row blocks, finite K tails, the dy rows (plain and gate-scaled);
   // 2. through W2: D = dY W2^T, the gate partials <D, h> and dpre = g D [h > 0].
@@ -1095,11 +1081,11 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
   // load and Switch terms, the router's weight gradients and its share of dx
   // -- and the bias column sums. Their small kernels fit beside the
   // persistent GEMM CTAs of the other branch, which stays on `stream`.
-  if (!ck) side = side_stream(side_lock, s);
-  if (side) fs = side->s;
-  int r = fork();
+  if (!ck) side.use(side_stream(side_lock, s), s);
+  int r = side.fork();
+  if (r == MOE_OK && ck) r = side.await();  // the packed rows
   if (r != MOE_OK) return r;
-  if (ck && side) MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));  // the packed rows
+  const cudaStream_t fs = side.stream();
   if (tc)
     MOE_CUDA(launch_bwd_dg(c, B.n_blocks2, offset, poff, row_token, dgpart, q.dy, q.b2, dg,
                            fs));
@@ -1126,10 +1112,8 @@ static int backward_impl(const moe_config &c, const WsLayout &L, const BwdCall &
   } else {
     MOE_CUDA(launch_bwd_simt_back(c, sp, s));
   }
-  if (side) {
-    MOE_CUDA(cudaEventRecord(side->join, side->s));
-    MOE_CUDA(cudaStreamWaitEvent(s, side->join, 0));
-  }
+  r = side.join();
+  if (r != MOE_OK) return r;
   // 4. dx = dy + the router's share + the kept experts' rows.
   if (tc)
     MOE_CUDA(launch_bwd_dx(c, q.idx, q.pos, q.keep, poff, dX, dxr, q.dy, q.dx, s));
