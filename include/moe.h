@@ -477,7 +477,8 @@ int moe_forward_threshold_few(const moe_config *cfg, const void *x, const float 
  * be NULL); dW1 [E,d,d_ff]; db1 [E,d_ff] (may be NULL); dW2 [E,d_ff,d]; db2
  * [E,d] (may be NULL); dgate [T,k] (may be NULL) = dL/dgate of each selected
  * gate value (<dy_t, U_e(x_t)> for a kept choice plus the Importance term).
- * bws is the backward's own workspace, moe_backward_workspace_size bytes,
+ * bws is the backward's own workspace, moe_backward_workspace_size bytes (asked
+ * for in a process that sees the GPU: one that sees none is told less),
  * 256-byte aligned. Device-side errors (a non-finite gradient, a bounded wait
  * that ran out) go to the status word of `ws`. After MOE_ERR_NONFINITE no
  * expert's gradients are to be used: on the tensor cores a non-finite x or hidden

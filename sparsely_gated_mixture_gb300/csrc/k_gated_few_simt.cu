@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256) k_few_simt_combine(const GatedFewSimt p, 
 int slice_of(const moe_config &c, int K, int N) {
   const long long A = (long long)c.T * c.k, used = A < c.E ? A : c.E;
   const long long tiles = used * ((N + kCols - 1) / kCols);
-  long long slices = (8ll * 152 + tiles - 1) / tiles;
+  long long slices = (8ll * kPlanSms + tiles - 1) / tiles;
   long long s = (K + slices - 1) / slices;
   s = s < 64 ? 64 : s > kMaxSlice ? kMaxSlice : s;
   return (int)((s + kFlight - 1) / kFlight * kFlight);

@@ -352,7 +352,8 @@ long long max_tiles(const GatedSimt &p) {
 }
 
 // The weight gradients' tiles, and the slices of an expert's rows that give every
-// SM four blocks where the tiles alone do not.
+// SM four blocks where the tiles alone do not. Workspaces are sized by these, so
+// they count on kPlanSms.
 // Slices of kSliceRows rows at least, at uniform loads (of 128: the same times).
 struct WeightSplit {
   bool wide;
@@ -363,9 +364,9 @@ WeightSplit weight_split(const moe_config &c, int max_rows) {
     return 3ll * c.E * ((c.d + t - 1) / t) * ((c.d_ff + t - 1) / t);
   };
   const long long most = std::min(16, std::max(1, max_rows / c.E / kSliceRows));
-  const bool wide = max_rows >= 64 * c.E && blocks(128) * most >= 2 * sm_count();
+  const bool wide = max_rows >= 64 * c.E && blocks(128) * most >= 2 * kPlanSms;
   const long long b = blocks(wide ? 128 : 64);
-  return {wide, (int)std::min(most, (4ll * sm_count() + b - 1) / b)};
+  return {wide, (int)std::min(most, (4ll * kPlanSms + b - 1) / b)};
 }
 
 template <int OP, typename T, int ACT, int TM, int TN>
@@ -388,7 +389,7 @@ cudaError_t run_one(const GatedSimt &p, cudaStream_t s) {
 bool wide_tiles(const moe_config &c, int max_rows, int op) {
   if (op == kW) return weight_split(c, max_rows).wide;
   const int N = (op == kF1 ? 2 : 1) * (op == kF2 || op == kB2 ? c.d : c.d_ff);
-  return ((long long)max_rows + 127) / 128 * ((N + 127) / 128) >= 2 * sm_count() &&
+  return ((long long)max_rows + 127) / 128 * ((N + 127) / 128) >= 2 * kPlanSms &&
          max_rows >= 64 * c.E;
 }
 

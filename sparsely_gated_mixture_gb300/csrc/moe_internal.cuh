@@ -375,6 +375,9 @@ cudaError_t launch_bwd_simt_dx(const moe_config &c, const BwdSimt &p, const int3
 
 // k_bwd.cu: the CUDA-core kernels of the backward.
 int sm_count();  // multiprocessors of the current device (k_ffn_tc.cu)
+// GB300's, for what workspaces are sized by: a size may be asked for in a process
+// that sees no device (sm_count() is 1 there) and used in one that does.
+constexpr int kPlanSms = 152;
 int xtd_splits(int T, int d, int NC);
 int colsum_chunks(int C);
 cudaError_t launch_bwd_offsets(int E, const int32_t *offset, int32_t *poff, cudaStream_t s);
