@@ -20,7 +20,8 @@ struct Eight {
         u[i] = n + i * 4 < N ? *reinterpret_cast<const uint4 *>(row + n + i * 4)
                              : make_uint4(0, 0, 0, 0);
     } else {
-      T t[8];
+      __align__(16) T t[8];
+      static_assert(__alignof__(t) % alignof(uint4) == 0, "read as uint4");
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[j] = n + j < N ? row[n + j] : T(0.f);
 #pragma unroll
@@ -50,7 +51,8 @@ k_fp8_weights(int K, int N, int KB, const T *__restrict__ W, uint8_t *__restrict
               uint8_t *__restrict__ scale, DeviceStatus *st) {
   pdl_wait();
   pdl_trigger();
-  __shared__ uint2 tile[B * 16];
+  __shared__ __align__(16) uint2 tile[B * 16];
+  static_assert(__alignof__(tile) % alignof(uint4) == 0, "read as uint4");
   __shared__ float tops[8];
   const int nb = blockIdx.x, kb = blockIdx.y, e = blockIdx.z;
   const int tid = threadIdx.x, v = tid & 15, q = tid >> 4;
