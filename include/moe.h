@@ -584,7 +584,8 @@ int moe_backward_checkpoint(const moe_config *cfg, const void *x, const float *W
  * and their gate values are the caller's: moe_gate's, or any router's; an
  * expert may stand twice in a token's choices. Uses T, d, E, d_ff, k,
  * capacity_factor, min_capacity and act_dtype of cfg; E <= 1024, k <= 16, d and
- * d_ff at most MOE_GATED_MAX_WIDTH, and rows * ceil(max(d, d_ff) / 128) under
+ * d_ff at most MOE_GATED_MAX_WIDTH, at most 2^31 - 1024 rows (T*k, or what the
+ * capacities hold if that is less) and rows * ceil(max(d, d_ff) / 128) under
  * 2^32, else MOE_ERR_UNSUPPORTED.
  *
  * x [T,d], W1, W3 [E,d,d_ff], b1, b3 [E,d_ff] (NULL = 0), W2 [E,d_ff,d], b2

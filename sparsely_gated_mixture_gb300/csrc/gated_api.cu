@@ -15,9 +15,10 @@ static int check_gated(const moe_config *c) {
   const int r = check_cfg(c);
   if (r != MOE_OK) return r;
   if (c->d > MOE_GATED_MAX_WIDTH || c->d_ff > MOE_GATED_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-  // Kernels count warps of 128 columns of a row in 32 bits.
-  const long long w = fp8_blocks(c->d > c->d_ff ? c->d : c->d_ff);
-  return gated_max_rows(*c) * w < (1ll << 32) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  // Kernels count warps of 128 columns of a row in 32 bits, and step over rows, a
+  // few hundred at a time, in as many with a sign.
+  const long long w = fp8_blocks(c->d > c->d_ff ? c->d : c->d_ff), rows = gated_max_rows(*c);
+  return rows * w < (1ll << 32) && rows <= (1ll << 31) - 1024 ? MOE_OK : MOE_ERR_UNSUPPORTED;
 }
 
 // What routing needs, at the start of every gated workspace.
