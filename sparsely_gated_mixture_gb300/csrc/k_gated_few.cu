@@ -271,6 +271,12 @@ __device__ __forceinline__ void few_scales(uint32_t tmem, uint32_t smem) {
                      (uint64_t)1 << 46;
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
+// The routing's results, from L2. Layer 2 reads them before it waits for layer 1: all of
+// layer 1's threads wait for the routing launch before they let layer 2 start, and
+// a launch that was waited for has its writes performed for the whole GPU, so L2 has
+// them; only a copy in an SM's L1 could be older, which these loads do not read.
+__device__ __forceinline__ int experts_in_use(const FewParams &p) { return __ldcg(p.counters); }
+__device__ __forceinline__ int4 expert_of(const FewParams &p, int j) { return __ldcg(p.list + j); }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // tmA, tmA3: weights (bf16: [E, K, N], box [1, 64, 64]; e4m3: [E, N, K], box [1,
@@ -317,10 +323,9 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // The list is complete: layer 1 follows the routing, and layer 2 starts once
-  // every block of layer 1 has waited for it.
+  // The list is complete: layer 1 follows the routing, layer 2 starts after that.
   if (LAYER == 1) pdl_wait();
-  const Run run(p.counters[0], p.NT, p.KC);
+  const Run run(experts_in_use(p), p.NT, p.KC);
   tc_fence_before();
   __syncthreads();
   pdl_trigger();  // this block has its TMEM: a dependent one cannot keep it from it
@@ -359,14 +364,14 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       if (LAYER == 2) {
         uint32_t i = 0;
         for (Seg g(run); g.more() && i < ahead; g.next(run)) {
-          const int4 who = p.list[g.j];
+          const int4 who = expert_of(p, g.j);
           for (int kb = g.kb0; kb < g.kb1 && i < ahead; ++kb, ++i) weights(g, who, kb, i);
         }
         pdl_wait();
       }
       bool ok = true;
       for (Seg g(run); ok && g.more(); g.next(run)) {
-        const int4 who = p.list[g.j];
+        const int4 who = expert_of(p, g.j);
         for (int kb = g.kb0; kb < g.kb1; ++kb, ++it) {
           const int s = it % S;
           if (it >= ahead) {
@@ -390,7 +395,7 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
       uint32_t g4 = 0;
       bool ok = true;
       for (Seg g(run); ok && g.more(); g.next(run)) {
-        const int4 who = p.list[g.j];
+        const int4 who = expert_of(p, g.j);
         // Lane l < 8: half l / 4's byte of chunk l % 4 of a group of four.
         const int half = (lane >> 2) & 1;
         const int nb = LAYER == 1 ? g.nt : min(2 * g.nt + half, p.NB - 1);
@@ -433,7 +438,7 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (!mbar_wait(&acc_empty[buf], ((local >> 1) & 1u) ^ 1u, abort_flag, p.st, 133, p.wait_ns))
           break;
         tc_fence_after();
-        const int n = (p.list[g.j].z + 15) / 16 * 16, halves = halves_of(g.nt);
+        const int n = (expert_of(p, g.j).z + 15) / 16 * 16, halves = halves_of(g.nt);
         const uint32_t d0 = tmem + (uint32_t)buf * acc_cols;
         uint32_t sft = 0;
         for (int kb = g.kb0; kb < g.kb1; ++kb, ++it) {
@@ -497,7 +502,7 @@ k_gated_few(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
           : "memory");
       if (!go) break;
       tc_fence_after();
-      const int4 who = p.list[g.j];
+      const int4 who = expert_of(p, g.j);
       const int e = who.x, row0 = who.y, rows = who.z, halves = halves_of(g.nt);
       const uint32_t acc = lanes + (uint32_t)buf * acc_cols;
       const bool whole = g.kb0 == 0 && g.kb1 == run.KC;
