@@ -225,6 +225,7 @@ k_gated_gather(long long P_max, int E, int k, int nv, int fv, const int32_t *__r
   const int lane = threadIdx.x & 31;
   const uint4 z = make_uint4(0, 0, 0, 0);
   if (w >= P_max) {  // a row behind the last packed one
+    if (w >= P_max + kBwdRowPad) return;  // the grid's last block has warps to spare
     const size_t r = (size_t)offset[E] + (w - P_max);
     for (int i = lane; i < nv; i += 32) xbuf[r * nv + i] = z;
     for (int i = lane; i < fv; i += 32) h[r * fv + i] = z;
