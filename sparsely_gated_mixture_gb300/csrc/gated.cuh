@@ -140,7 +140,7 @@ inline cudaError_t gated_dispatch(int activation, F &&f) {
 // ----------------------------------------------------------------------------- 8-bit blocks
 // e4m3 values v / 2^e, e the smallest exponent (at least -124) with 448 * 2^e
 // >= the block's largest magnitude; scale byte e + 127, 255 for a block that
-// holds an Inf or a NaN (its product is NaN then).
+// holds an Inf or a NaN (its product is a NaN by that byte, whatever its values).
 constexpr int kFp8Block = 128;
 constexpr int kFp8Low = -124;
 __device__ __forceinline__ uint32_t fp8_scale_byte(float amax) {
@@ -149,7 +149,8 @@ __device__ __forceinline__ uint32_t fp8_scale_byte(float amax) {
   const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
   return (uint32_t)(max(e, kFp8Low) + 127);
 }
-// What values are multiplied by: 2^-e (a NaN for byte 255: its values are not used).
+// What values are multiplied by: 2^-e; for byte 255 2^127, which leaves zeros, NaNs and
+// +-448.
 __device__ __forceinline__ float fp8_inverse(uint32_t byte) {
   return __uint_as_float((254u - (byte == 255u ? 0u : byte)) << 23);
 }

@@ -73,7 +73,10 @@ static int gated_few_toks(const moe_config &c) {
 // through 8 large experts 419 us against 437) once the experts in use, at
 // uniform choices, have tiles of layer 2 for three quarters of the SMs; with
 // fewer they leave most of them idle (one token 227 us against 127). In 8 bits
-// they do not (64 tokens 257 us against 242).
+// they do not (64 tokens 253 us against 235; 64 tokens through 16 experts of 512 x 1024
+// 36 either way). Many narrow experts do better by these kernels beyond the rule too
+// (top-8 of experts of 2048 x 1024, bf16: 64 tokens through 64 of them 178 us against
+// 147, through 256 409 against 385).
 static bool gated_few_pays(const moe_config &c) {
   if (!gated_few_toks(c)) return false;
   const double used = c.E * (1.0 - pow(1.0 - (double)c.k / c.E, (double)c.T));
@@ -248,7 +251,11 @@ static int gated_backward_tc(const moe_config &c, const GatedBwdLayout &L, const
   gx.A3 = dP3;
   gx.B3 = q.W3;
   // The pairs' lower traffic pays from one wave on (top-4 layer's backward 229 us
-  // with none of them, 219 with dX's and the weight gradients', 226 with all).
+  // with none of them, 219 with dX's and the weight gradients', 226 with all; none,
+  // all and by this rule, top-2 of 8 experts: 4096 tokens of 1024 x 2048 259, 251,
+  // 243; 8192 of 768 x 2048 365, 346, 331; 8192 of 2048 x 4096 1238, 1105, 1104; 1024 of
+  // 4096 x 14336, whose weight gradients have short sums, 2077, 1761, 1959; 2048
+  // tokens, top-2 of 32 of 1024 x 2048: 310, 313, 297).
   gx.pair_waves = 1;
   MOE_CUDA(launch_bwd_gemm(gx, st, s));
   const auto wgrad = [&](const void *A, int M, const void *B, int N, void *out) {

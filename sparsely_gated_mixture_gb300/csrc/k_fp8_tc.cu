@@ -641,6 +641,10 @@ cudaError_t launch_fp8_tc(const Fp8Layer &q, cudaStream_t s) {
   if (q.layer == 2)
     p.tma_out = q.z_bf16 ? make_rows_map(&to, q.z, (uint64_t)q.max_rows, (uint64_t)N, false)
                          : make_rows_map16(&to, q.z, (uint64_t)q.max_rows, (uint64_t)N);
+  // The CTA pairs where the bf16 layers take theirs. Here they gain nothing: a stage
+  // holds twice the K (8192 tokens, top-2 of 8 experts, one CTA and pairs forced: d =
+  // d_ff = 1024 119 and 123 us, 1536 190 and 192, 2048 247 and 251, 4096 684 and 690;
+  // 4096 x 14336 2049 and 2071).
   const long long tiles = (q.max_rows / 256) * (long long)p.n_blocks;
   const int pairs = forced() == 1 ? 0 : pair_units();
   const bool pair = pairs > 0 && (forced() == 2 || (K >= 2048 && tiles >= 4ll * pairs));
